@@ -43,6 +43,10 @@ __all__ = [
     "fno_linear_conv2d",
     "fno_linear_conv1d_prepare",
     "fno_linear_conv1d",
+    "fno_group_norm",
+    "fno_group_norm_backward",
+    "fno_grad_norm",
+    "fno_clip_grad_norm",
     "fno_workspace_size_2d",
     "fno_workspace_size_1d",
     "fno_forward2d",
@@ -64,6 +68,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _S = ctypes.c_size_t
+_F = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/fno.h
 _SIGNATURES = {
@@ -97,6 +102,12 @@ _SIGNATURES = {
     "fno_linear_conv2d": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "fno_linear_conv1d_prepare": (_I, [_P, _P, _I, _I, _I, _I, _P]),
     "fno_linear_conv1d": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "fno_group_norm_workspace_size": (_S, [_I, _I, _I, _I]),
+    "fno_group_norm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _I, _I, _I, _P, _S, _P]),
+    "fno_group_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _S, _P]),
+    "fno_grad_norm_workspace_size": (_S, [_I]),
+    "fno_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _S, _P]),
+    "fno_clip_grad_norm": (_I, [_P, _P, _P, _P, _I, _F, _P, _P, _P, _S, _P]),
     "fno_set_timing_events": (_I, [ctypes.POINTER(ctypes.c_void_p), _I]),
     "fno_last_kernel_count": (_I, []),
     "fno_last_kernel_name": (ctypes.c_char_p, [_I]),
@@ -531,6 +542,217 @@ def fno_spectral_conv1d_backward(x, w, grad_out, modes: int, need_x: bool = True
                                                   b, cin, cout, n, modes, _stream_ptr(x.device)),
                "fno_spectral_conv1d_backward")
     return gx, gw
+
+
+_ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
+_types = {}
+
+
+def _type_code(t, name, complex_too=False):
+    """The ABI's element type (enum fno_type) of a tensor."""
+    if not _types:
+        torch = _torch()
+        _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.complex64: 3})
+    code = _types.get(t.dtype, -1)
+    if code < 0 or (code == 3 and not complex_too):
+        raise TypeError(f"{name} must be float32, bfloat16{', float16 or complex64' if complex_too else ' or float16'}"
+                        f", got {t.dtype}")
+    return code
+
+
+def _need_field(t, name, device=None):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a GPU device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return _type_code(t, name)
+
+
+def _group_norm_args(x, groups, weight, bias, act, channels_last, out_channels_last):
+    torch = _torch()
+    x_type = _need_field(x, "x")
+    if x.dim() < 2:
+        raise ValueError(f"x must have a batch and a channel axis, got shape {tuple(x.shape)}")
+    if act not in _ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, got {act!r}")
+    shape = tuple(x.shape)
+    c = shape[-1] if channels_last else shape[1]
+    grid = shape[1:-1] if channels_last else shape[2:]
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, torch.float32, 1, name)
+            if t.shape[0] != c or t.device != x.device:
+                raise ValueError(f"{name} must be [{c}] on {x.device}")
+    if out_channels_last is None:
+        out_channels_last = channels_last
+    out_shape = (shape[0],) + grid + (c,) if out_channels_last else (shape[0], c) + grid
+    p = 1
+    for n in grid:
+        p *= n
+    if shape[0] > 0x7fffffff or c > 0x7fffffff or p > 0x7fffffff:
+        raise ValueError(f"x is too large: shape {shape}")
+    # (B, C, P, groups), (act, x_last, out_last, x_type)
+    dims = (shape[0], c, p, int(groups))
+    return dims, (_ACTIVATIONS[act], int(bool(channels_last)), int(bool(out_channels_last)), x_type), out_shape
+
+
+def _group_norm_workspace(x, dims):
+    # from torch's allocator, on the current stream: every call, and every captured graph, has its own
+    return _torch().empty(max(1, int(lib().fno_group_norm_workspace_size(*dims))), dtype=_torch().uint8,
+                          device=x.device)
+
+
+def _opt(t):
+    return ctypes.c_void_p(t.data_ptr() if t is not None else 0)
+
+
+def fno_group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: str = "none",
+                   channels_last: bool = False, out_channels_last=None, out_dtype=None, out=None, stats=None):
+    """Group norm and activation of a field; returns (out, stats).
+
+    x is [B, C, *grid], or [B, *grid, C] with channels_last (a torch.channels_last tensor:
+    x.permute(0, 2, 3, 1)), of float32, bfloat16 or float16.  out has x's layout unless
+    out_channels_last says otherwise (out_channels_last=False gives the channels-first field the
+    transforms read), and x's type or float32 (out_dtype, or that of `out`).  weight, bias [C]
+    float32 are optional; act is "none", "gelu" (the exact erf form) or "silu".  stats
+    [B, groups, 2] float32 holds (mean, 1 / deviation) for fno_group_norm_backward."""
+    torch = _torch()
+    dims, opts, out_shape = _group_norm_args(x, groups, weight, bias, act, channels_last, out_channels_last)
+    if out is None:
+        out = torch.empty(out_shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    out_type = _need_field(out, "out", x.device)
+    if tuple(out.shape) != out_shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {out_shape}")
+    stats_shape = (dims[0], max(dims[3], 0), 2)
+    if stats is None:
+        stats = torch.empty(stats_shape, dtype=torch.float32, device=x.device)
+    _need(stats, torch.float32, 3, "stats")
+    if tuple(stats.shape) != stats_shape or stats.device != x.device:
+        raise ValueError(f"stats must be {stats_shape} on {x.device}")
+    with _on_device(x):
+        ws = _group_norm_workspace(x, dims)
+        _check(lib().fno_group_norm(_ptr(x), _opt(weight), _opt(bias), _ptr(out), _ptr(stats), *dims, eps, *opts,
+                                    out_type, _ptr(ws), ws.numel(), _stream_ptr(x.device)), "fno_group_norm")
+    return out, stats
+
+
+def fno_group_norm_backward(x, stats, grad_out, groups: int, weight=None, bias=None, act: str = "none",
+                            channels_last: bool = False, out_channels_last=None, need_x: bool = True,
+                            need_w: bool = True, grad_x=None, grad_weight=None, grad_bias=None):
+    """Gradients (grad_x, grad_weight, grad_bias) through fno_group_norm, given its x, stats, weight, bias
+    and options, and grad_out of its output's layout and type.  need_x / need_w choose the field's and the
+    parameters' gradients; those not asked for, or of a parameter that is None, are returned as None."""
+    torch = _torch()
+    dims, opts, out_shape = _group_norm_args(x, groups, weight, bias, act, channels_last, out_channels_last)
+    out_type = _need_field(grad_out, "grad_out", x.device)
+    if tuple(grad_out.shape) != out_shape:
+        raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, expected {out_shape}")
+    _need(stats, torch.float32, 3, "stats")
+    if tuple(stats.shape) != (dims[0], dims[3], 2) or stats.device != x.device:
+        raise ValueError(f"stats must be {(dims[0], dims[3], 2)} on {x.device}")
+    if not (need_x or (need_w and (weight is not None or bias is not None))):
+        raise ValueError("ask for at least one gradient")
+
+    def target(given, like, wanted, name):
+        if not wanted or like is None:
+            return None
+        if given is None:
+            return torch.empty_like(like)
+        _need(given, like.dtype, like.dim(), name)
+        if given.shape != like.shape or given.device != like.device:
+            raise ValueError(f"{name} must match {tuple(like.shape)} on {like.device}")
+        return given
+
+    gx = target(grad_x, x, need_x, "grad_x")
+    gw = target(grad_weight, weight, need_w, "grad_weight")
+    gb = target(grad_bias, bias, need_w, "grad_bias")
+    with _on_device(x):
+        ws = _group_norm_workspace(x, dims)
+        _check(lib().fno_group_norm_backward(_ptr(x), _opt(weight), _opt(bias), _ptr(stats), _ptr(grad_out), _opt(gx),
+                                             _opt(gw), _opt(gb), *dims, *opts, out_type, _ptr(ws), ws.numel(),
+                                             _stream_ptr(x.device)), "fno_group_norm_backward")
+    return gx, gw, gb
+
+
+def _tensor_table(tensors, name):
+    """Host arrays (pointers, element counts, types) of a list of tensors, and their device."""
+    torch = _torch()
+    tensors = list(tensors)
+    n = len(tensors)
+    device = tensors[0].device if n and isinstance(tensors[0], torch.Tensor) else None
+    types = []
+    for t in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be torch tensors")
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{name} must live on one GPU device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        types.append(_type_code(t, name, complex_too=True))
+        if types[-1] == 3 and t.is_conj():
+            raise ValueError(f"{name} must not be lazily conjugated (call resolve_conj())")
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
+    numels = (ctypes.c_longlong * n)(*[t.numel() for t in tensors])
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return tensors, ptrs, numels, (ctypes.c_int * n)(*types), device
+
+
+def _norm_scalar(norm, device, name):
+    torch = _torch()
+    if norm is None:
+        return torch.empty((), dtype=torch.float32, device=device)
+    _need(norm, torch.float32, 0, name)
+    if norm.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return norm
+
+
+def _grad_workspace(count, device):
+    return _torch().empty(int(lib().fno_grad_norm_workspace_size(count)), dtype=_torch().uint8, device=device)
+
+
+def fno_grad_norm(grads, out=None):
+    """Euclidean norm of all values of a list of gradients (float32, bfloat16, float16, complex64, mixed):
+    a float32 scalar on their device."""
+    grads, ptrs, numels, types, device = _tensor_table(grads, "grads")
+    out = _norm_scalar(out, device, "out")
+    with _on_device(out):
+        ws = _grad_workspace(len(grads), device)
+        _check(lib().fno_grad_norm(ptrs, numels, types, len(grads), _ptr(out), _ptr(ws), ws.numel(),
+                                   _stream_ptr(device)), "fno_grad_norm")
+    return out
+
+
+def fno_clip_grad_norm(grads, max_norm: float, norm=None, out=None):
+    """Scale a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out`
+    (of the same shapes and types); returns their norm, a float32 scalar on their device.  `norm`, if given,
+    is used as the norm (one reduced over several GPUs, say) and returned.  Nothing is copied to the host."""
+    grads, ptrs, numels, types, device = _tensor_table(grads, "grads")
+    outs = ptrs
+    if out is not None:
+        out, outs, _, out_types, out_device = _tensor_table(out, "out")
+        if len(out) != len(grads) or any(o.shape != g.shape for o, g in zip(out, grads)):
+            raise ValueError("out must hold a tensor of each gradient's shape")
+        if any(a != b for a, b in zip(out_types, types)):
+            raise TypeError("out must have the gradients' types")
+        if out_device != device:
+            raise ValueError(f"out must be on {device}")
+    given = norm is not None
+    norm = _norm_scalar(norm, device, "norm")
+    with _on_device(norm):
+        ws = _grad_workspace(len(grads), device)
+        _check(lib().fno_clip_grad_norm(ptrs, outs, numels, types, len(grads), max_norm,
+                                        _ptr(norm) if given else None, None if given else _ptr(norm), _ptr(ws),
+                                        ws.numel(), _stream_ptr(device)), "fno_clip_grad_norm")
+    return norm
 
 
 def fno_forward2d(x, mx: int, my: int, xh=None):

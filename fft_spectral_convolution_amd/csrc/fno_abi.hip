@@ -8,6 +8,7 @@
 // half spectrum).  Everything is checked before anything is enqueued.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -1065,6 +1066,162 @@ int backward1d_common(const float* x, const void* w, const float* g, float* gx, 
     return rec_end(hs, run());
 }
 
+// ---------------------------------------------------------------------------
+// group norm, gradient norm and clipping: scratch always comes from the
+// caller, so these calls never allocate
+// ---------------------------------------------------------------------------
+
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+// Every output against every input and every other output.
+bool any_overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+        if (!o->p) continue;
+        for (const Span& i : inputs)
+            if (i.p && overlap(o->p, o->bytes, i.p, i.bytes)) return true;
+        for (const Span* q = o + 1; q != outputs.end(); ++q)
+            if (q->p && overlap(o->p, o->bytes, q->p, q->bytes)) return true;
+    }
+    return false;
+}
+
+size_t type_bytes(int type) { return type == FNO_C64 ? 8 : type == FNO_F32 ? 4 : 2; }
+
+bool off_grain(const void* p, size_t grain) { return reinterpret_cast<uintptr_t>(p) % grain != 0; }
+
+int check_group_norm(const GroupNorm& g) {
+    if (g.B < 1 || g.C < 1 || g.P < 1 || g.groups < 1 || g.C % g.groups != 0) return FNO_ERR_SHAPE;
+    // one workgroup an item and channel at the most; a field that no device holds
+    if (g.B * g.C > INT32_MAX || g.B * g.C > (INT64_C(1) << 40) / g.P) return FNO_ERR_SHAPE;
+    if (g.act < FNO_ACT_NONE || g.act > FNO_ACT_SILU) return FNO_ERR_VALUE;
+    if (g.x_type < FNO_F32 || g.x_type > FNO_F16) return FNO_ERR_VALUE;
+    if (g.out_type != g.x_type && g.out_type != FNO_F32) return FNO_ERR_VALUE;
+    return FNO_OK;
+}
+
+int group_norm_common(const GroupNorm& g, const GroupNormArgs& a, bool backward, size_t ws_bytes, void* stream) {
+    const size_t n = (size_t)(g.B * g.C * g.P), cbytes = (size_t)g.C * 4;
+    const size_t xb = n * type_bytes(g.x_type), ob = n * type_bytes(g.out_type);
+    const size_t sb = (size_t)(g.B * g.groups) * 8;
+    if (!a.x || !a.stats || !a.out) return FNO_ERR_NULL;
+    if (backward && !a.grad_x && !a.grad_weight && !a.grad_bias) return FNO_ERR_NULL;
+    if (off_grain(a.x, type_bytes(g.x_type)) || off_grain(a.out, type_bytes(g.out_type)) || off_grain(a.stats, 4) ||
+        off_grain(a.weight, 4) || off_grain(a.bias, 4) || off_grain(a.grad_x, type_bytes(g.x_type)) ||
+        off_grain(a.grad_weight, 4) || off_grain(a.grad_bias, 4))
+        return FNO_ERR_ALIGN;
+    const Span x{a.x, xb}, w{a.weight, cbytes}, b{a.bias, cbytes}, st{a.stats, sb}, o{a.out, ob};
+    const Span ws{a.ws, ws_bytes};
+    if (backward ? any_overlap({{a.grad_x, xb}, {a.grad_weight, cbytes}, {a.grad_bias, cbytes}, ws}, {x, w, b, st, o})
+                 : any_overlap({o, st, ws}, {x, w, b}))
+        return FNO_ERR_ALIAS;
+    if (!a.ws || ws_bytes < group_norm_workspace(g)) return FNO_ERR_WORKSPACE;
+    if (off_grain(a.ws, 256)) return FNO_ERR_ALIGN;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    auto run = [&]() -> int {
+        const char* names[4] = {};
+        const int count = group_norm_kernels(g, backward, a.grad_x != nullptr, names);
+        for (int k = 0; k < count; ++k) {
+            rec_kernel(names[k], hs);
+            const hipError_t e = launch_group_norm(g, a, backward, k, hs);
+            if (e != hipSuccess) return hip_fail(e);
+        }
+        return FNO_OK;
+    };
+    rec_begin();
+    return rec_end(hs, run());
+}
+
+int check_grads(const void* const* grads, const long long* numels, const int* types, int count) {
+    if (count < 0) return FNO_ERR_SHAPE;
+    if (count && (!grads || !numels || !types)) return FNO_ERR_NULL;
+    for (int i = 0; i < count; ++i) {
+        if (types[i] < FNO_F32 || types[i] > FNO_C64) return FNO_ERR_VALUE;
+        if (numels[i] < 0 || numels[i] > (1LL << 40)) return FNO_ERR_SHAPE;
+        if (numels[i] && !grads[i]) return FNO_ERR_NULL;
+        if (numels[i] && off_grain(grads[i], types[i] == FNO_C64 ? 4 : type_bytes(types[i]))) return FNO_ERR_ALIGN;
+    }
+    return FNO_OK;
+}
+
+// Nothing a clipping call writes may overlap anything else that it reads or
+// writes, but for a tensor clipped in place: sorted by address, each span
+// must end before the next that either side writes.
+bool grads_overlap(const void* const* grads, void* const* outs, const long long* numels, const int* types, int count,
+                   std::initializer_list<Span> others) {
+    struct Piece {
+        uintptr_t at, end;
+        bool written;
+    };
+    std::vector<Piece> v;
+    v.reserve(2 * (size_t)count + others.size());
+    auto add = [&](const void* p, size_t bytes, bool written) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (p && bytes) v.push_back({a, a + bytes, written});
+    };
+    for (int i = 0; i < count; ++i) {
+        const size_t bytes = (size_t)numels[i] * type_bytes(types[i]);
+        if (outs[i] != grads[i]) add(grads[i], bytes, false);
+        add(outs[i], bytes, true);
+    }
+    for (const Span& o : others) add(o.p, o.bytes, true);
+    std::sort(v.begin(), v.end(), [](const Piece& a, const Piece& b) { return a.at < b.at; });
+    uintptr_t read_end = 0, write_end = 0;   // ends of what lies before, by kind
+    for (const Piece& p : v) {
+        if (p.at < write_end || (p.written && p.at < read_end)) return true;
+        (p.written ? write_end : read_end) = std::max(p.written ? write_end : read_end, p.end);
+    }
+    return false;
+}
+
+// outs null: the norm alone.
+int grad_norm_common(const void* const* grads, void* const* outs, const long long* numels, const int* types, int count,
+                     float max_norm, const float* given, float* norm, void* ws, size_t ws_bytes, void* stream) {
+    if (!ws || ws_bytes < grad_norm_workspace(count)) return FNO_ERR_WORKSPACE;
+    if (off_grain(ws, 256) || off_grain(norm, 4) || off_grain(given, 4)) return FNO_ERR_ALIGN;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    float* coef = static_cast<float*>(ws);
+    double* part = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
+    auto fill = [&](GradTable& t, int at) {
+        const int m = std::min(count - at, kGradTable);
+        t = GradTable{};
+        for (int i = 0; i < m; ++i) {
+            t.src[i] = grads[at + i];
+            t.dst[i] = outs ? outs[at + i] : nullptr;
+            t.n[i] = numels[at + i] * (types[at + i] == FNO_C64 ? 2 : 1);
+            t.type[i] = (uint8_t)types[at + i];
+        }
+        return grad_table_chunks(t, m);
+    };
+    auto run = [&]() -> int {
+        GradTable t;
+        int nparts = 0;
+        for (int at = 0; !given && at < count; at += kGradTable) {
+            const uint32_t chunks = fill(t, at);
+            if (!chunks) continue;
+            rec_kernel("grad_sumsq", hs);
+            const hipError_t e = launch_grad_sumsq(t, chunks, part + nparts, hs);
+            if (e != hipSuccess) return hip_fail(e);
+            nparts += grad_sumsq_blocks(chunks);
+        }
+        rec_kernel("grad_finish", hs);
+        const hipError_t e = launch_grad_finish(part, nparts, given, max_norm, norm, outs ? coef : nullptr, hs);
+        if (e != hipSuccess) return hip_fail(e);
+        for (int at = 0; outs && at < count; at += kGradTable) {
+            const uint32_t chunks = fill(t, at);
+            if (!chunks) continue;
+            rec_kernel("grad_scale", hs);
+            const hipError_t e2 = launch_grad_scale(t, chunks, coef, hs);
+            if (e2 != hipSuccess) return hip_fail(e2);
+        }
+        return FNO_OK;
+    };
+    rec_begin();
+    return rec_end(hs, run());
+}
+
 }  // namespace
 
 LaunchEvents take_launch_events() {
@@ -1094,6 +1251,7 @@ const char* fno_status_string(int status) {
         case FNO_ERR_CAPTURE: return "a table or workspace would have to be allocated while the stream is captured";
         case FNO_ERR_TOO_LARGE: return "the shape needs more scratch than the fixed device array of the no-allocation call holds";
         case FNO_ERR_NOT_INIT: return "fno_init has not been called on this device";
+        case FNO_ERR_VALUE: return "an option, type or scalar argument is not one the call takes";
         default: return "unknown status";
     }
 }
@@ -1355,6 +1513,61 @@ int fno_inverse1d(const void* yh, float* out, int B, int C, int N, int modes, vo
     hipError_t e = rows_inv_n(static_cast<const float2*>(yh), out, (int64_t)B * C, N, modes, modes,
                                    scale, st->twiddle, hs);
     return rec_end(hs, e == hipSuccess ? FNO_OK : hip_fail(e));
+}
+
+size_t fno_group_norm_workspace_size(int B, int C, int P, int groups) {
+    const GroupNorm g{B, C, P, groups, 0.0f, FNO_ACT_NONE, false, false, FNO_F32, FNO_F32};
+    return check_group_norm(g) == FNO_OK ? group_norm_workspace(g) : 0;
+}
+
+int fno_group_norm(const void* x, const float* weight, const float* bias, void* out, float* stats, int B, int C, int P,
+                   int groups, float eps, int act, int x_last, int out_last, int x_type, int out_type, void* workspace,
+                   size_t ws_bytes, void* stream) {
+    if ((x_last & ~1) || (out_last & ~1) || !(eps > 0.0f) || !std::isfinite(eps)) return FNO_ERR_VALUE;
+    const GroupNorm g{B, C, P, groups, eps, act, x_last != 0, out_last != 0, x_type, out_type};
+    const int rc = check_group_norm(g);
+    if (rc) return rc;
+    const GroupNormArgs a{x, weight, bias, stats, out, nullptr, nullptr, nullptr, workspace};
+    return group_norm_common(g, a, false, ws_bytes, stream);
+}
+
+int fno_group_norm_backward(const void* x, const float* weight, const float* bias, const float* stats,
+                            const void* grad_out, void* grad_x, float* grad_weight, float* grad_bias, int B, int C,
+                            int P, int groups, int act, int x_last, int out_last, int x_type, int out_type,
+                            void* workspace, size_t ws_bytes, void* stream) {
+    if ((x_last & ~1) || (out_last & ~1)) return FNO_ERR_VALUE;
+    const GroupNorm g{B, C, P, groups, 0.0f, act, x_last != 0, out_last != 0, x_type, out_type};
+    const int rc = check_group_norm(g);
+    if (rc) return rc;
+    const GroupNormArgs a{x, weight, bias, const_cast<float*>(stats), const_cast<void*>(grad_out), grad_x, grad_weight,
+                          grad_bias, workspace};
+    return group_norm_common(g, a, true, ws_bytes, stream);
+}
+
+size_t fno_grad_norm_workspace_size(int count) { return count < 0 ? 0 : grad_norm_workspace(count); }
+
+int fno_grad_norm(const void* const* grads, const long long* numels, const int* types, int count, float* norm,
+                  void* workspace, size_t ws_bytes, void* stream) {
+    const int rc = check_grads(grads, numels, types, count);
+    if (rc) return rc;
+    if (!norm) return FNO_ERR_NULL;
+    return grad_norm_common(grads, nullptr, numels, types, count, 0.0f, nullptr, norm, workspace, ws_bytes, stream);
+}
+
+int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long long* numels, const int* types,
+                       int count, float max_norm, const float* given_norm, float* norm, void* workspace,
+                       size_t ws_bytes, void* stream) {
+    int rc = check_grads(grads, numels, types, count);
+    if (rc) return rc;
+    if (count && !outs) return FNO_ERR_NULL;
+    rc = check_grads(const_cast<const void* const*>(outs), numels, types, count);
+    if (rc) return rc;
+    if (!given_norm && !norm) return FNO_ERR_NULL;
+    if (!(max_norm >= 0.0f)) return FNO_ERR_VALUE;
+    if (grads_overlap(grads, outs, numels, types, count,
+                      {{norm, 4}, {given_norm == norm ? nullptr : given_norm, 4}, {workspace, ws_bytes}}))
+        return FNO_ERR_ALIAS;
+    return grad_norm_common(grads, outs, numels, types, count, max_norm, given_norm, norm, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -289,4 +289,52 @@ hipError_t launch_weight_grad(const float2* xh, const SpecLayout& lx, const floa
 hipError_t launch_weight_grad_reduce(const void* ws, float2* gw, int64_t Cin, int64_t Cout, int64_t M, int splits,
                                      int my, int nyq, hipStream_t s);
 
+// ---- group norm (fno_groupnorm.hip) -----------------------------------------
+constexpr int kTypeF32 = 0, kTypeBf16 = 1, kTypeF16 = 2, kTypeC64 = 3;   // enum fno_type
+constexpr int kActNone = 0, kActGelu = 1, kActSilu = 2;                  // enum fno_activation
+
+// A field of B items, P positions and C channels in `groups` groups; x and
+// out are channels last [B][P][C] or channels first [B][C][P].
+struct GroupNorm {
+    int64_t B, C, P, groups;
+    float eps;
+    int act;
+    bool x_last, out_last;
+    int x_type, out_type;
+};
+struct GroupNormArgs {
+    const void* x;
+    const float *weight, *bias;   // null: ones, zeros
+    float* stats;                 // [B][groups][2]: mean, 1 / deviation (backward: input)
+    void* out;                    // backward: grad_out
+    void* grad_x;                 // backward only, null where not asked for
+    float *grad_weight, *grad_bias;
+    void* ws;
+};
+// A call is a list of kernels, launched one after the other.
+int group_norm_kernels(const GroupNorm& g, bool backward, bool need_x, const char** names);
+size_t group_norm_workspace(const GroupNorm& g);
+hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s);
+
+// ---- gradient norm and clipping (fno_gradnorm.hip) ----------------------------
+// Tensors of one launch, passed by value (3.7 KiB of the 4 KiB of kernel
+// arguments).  n counts floats (two a complex value); first is a tensor's
+// first chunk (grad_table_chunks fills it and returns the chunk count).
+constexpr int kGradTable = 128;
+struct GradTable {
+    const void* src[kGradTable];
+    void* dst[kGradTable];
+    int64_t n[kGradTable];
+    uint32_t first[kGradTable];
+    uint8_t type[kGradTable];
+};
+uint32_t grad_table_chunks(GradTable& t, int count);
+int grad_sumsq_blocks(uint32_t nchunks);                // partial sums launch_grad_sumsq writes
+size_t grad_norm_workspace(int64_t count);
+hipError_t launch_grad_sumsq(const GradTable& t, uint32_t nchunks, double* part, hipStream_t s);
+// norm and / or coef may be null; given (if not null) stands for the norm
+hipError_t launch_grad_finish(const double* part, int nparts, const float* given, float max_norm, float* norm,
+                              float* coef, hipStream_t s);
+hipError_t launch_grad_scale(const GradTable& t, uint32_t nchunks, const float* coef, hipStream_t s);
+
 }  // namespace fno

@@ -2,7 +2,7 @@
  * libfno -- Fourier-neural-operator spectral convolution on MI355X (gfx950).
  *
  * C ABI.  Every pointer argument named x, w, out, xh, yh, grad_out, grad_x,
- * grad_w, bias, branch, mask, k, wspec or workspace is DEVICE memory on the current HIP
+ * grad_w, bias, branch, mask, k, wspec, weight, stats, norm or workspace is DEVICE memory on the current HIP
  * device, owned by the caller; the library never frees caller memory.  `stream` is a hipStream_t passed as void*
  * (NULL = the null stream).  All calls only enqueue work on `stream` and
  * return without synchronising; a kernel fault shows up at the caller's next
@@ -64,8 +64,16 @@ enum fno_status {
     FNO_ERR_CAPTURE = -9,    /* a table or workspace would have to be allocated while
                                 the stream is being captured into a graph */
     FNO_ERR_TOO_LARGE = -10, /* shape needs more than fno_spectral_conv2d_noalloc's fixed scratch */
-    FNO_ERR_NOT_INIT = -11   /* fno_init has not been called on the current device */
+    FNO_ERR_NOT_INIT = -11,  /* fno_init has not been called on the current device */
+    FNO_ERR_VALUE = -12      /* an option, type or scalar argument is not one the call takes */
 };
+
+/* Element types of the calls that take more than float32 (complex64 as
+ * interleaved float32 pairs). */
+enum fno_type { FNO_F32 = 0, FNO_BF16 = 1, FNO_F16 = 2, FNO_C64 = 3 };
+
+/* gelu(z) = z (1 + erf(z / sqrt 2)) / 2, silu(z) = z / (1 + e^-z). */
+enum fno_activation { FNO_ACT_NONE = 0, FNO_ACT_GELU = 1, FNO_ACT_SILU = 2 };
 
 /* Library version as major*10000 + minor*100 + patch. */
 int fno_version(void);
@@ -317,6 +325,82 @@ int fno_linear_conv1d_prepare(const float* k, void* wspec, int Cin, int Cout, in
                               void* stream);
 int fno_linear_conv1d(const float* x, const void* wspec, float* out, int B, int Cin, int Cout,
                       int N, int K, int crop, int No, void* stream);
+
+/*
+ * Group norm with an activation, between the layers.  x is a field of B
+ * items, P positions (H W of a 2D grid, N of a sequence) and C channels, in
+ * `groups` groups of D = C / groups neighbouring channels; with n = P D,
+ *
+ *   mean[b,g] = sum x / n,  rstd[b,g] = (sum (x - mean)^2 / n + eps)^-1/2
+ *   out = act((x - mean) rstd weight[c] + bias[c])
+ *
+ * x_last / out_last: 1 where that field is channels last [B][P][C] (as
+ * channel products read it), 0 where it is channels first [B][C][P] (as the
+ * transforms do).  x_type is FNO_F32, FNO_BF16 or FNO_F16, out_type the same
+ * or FNO_F32; weight, bias (float32 [C], NULL for ones and zeros) and all
+ * arithmetic are float32, a 16-bit output is rounded once.  stats float32
+ * [B][groups][2] receives (mean, rstd), which the backward call reads.
+ *
+ * eps must be positive and finite, C a multiple of groups, 1 <= B, C, P,
+ * B C < 2^31.  Fields need the alignment of their elements only.  Nothing
+ * written may overlap anything else (FNO_ERR_ALIAS).  A NaN or infinity
+ * makes its group NaN, no other.
+ *
+ * Scratch is the caller's: `workspace`, 256-byte aligned, at least
+ * fno_group_norm_workspace_size bytes (0 for invalid sizes), free again when
+ * the call's kernels have run.  Nothing is allocated, so the calls can be
+ * captured into graphs at any time; graphs that may run at the same time
+ * need a workspace each.
+ */
+size_t fno_group_norm_workspace_size(int B, int C, int P, int groups);
+int fno_group_norm(const void* x, const float* weight, const float* bias, void* out, float* stats,
+                   int B, int C, int P, int groups, float eps, int act, int x_last, int out_last,
+                   int x_type, int out_type, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Backward pass of fno_group_norm: with grad_out = dL/dout (out's layout and
+ * type), xh = (x - mean) rstd and g = grad_out act'(xh weight + bias),
+ *
+ *   grad_weight[c] = sum_{b,p} g xh,  grad_bias[c] = sum_{b,p} g
+ *   grad_x = rstd (g weight - s1 - xh s2)      (x's layout and type)
+ *
+ * s1, s2 the means of g weight and g weight xh over the group.  Each of
+ * grad_x, grad_weight and grad_bias may be NULL, not all; they are
+ * overwritten.  Sums run in a fixed order: equal inputs give equal bits.
+ */
+int fno_group_norm_backward(const void* x, const float* weight, const float* bias, const float* stats,
+                            const void* grad_out, void* grad_x, float* grad_weight, float* grad_bias,
+                            int B, int C, int P, int groups, int act, int x_last, int out_last,
+                            int x_type, int out_type, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Global norm of `count` gradients, and clipping by it:
+ *
+ *   norm = sqrt(sum over all values of |g|^2)
+ *   outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6))
+ *
+ * grads, outs (device pointers), numels (elements, 0 allowed) and types
+ * (enum fno_type) are host arrays, read before the call returns; they may
+ * mix types.  Squares are summed in float64.  norm is one float32 in device
+ * memory: nothing is copied to the host or waited for.
+ *
+ * fno_clip_grad_norm: outs[i] == grads[i] clips in place; otherwise nothing
+ * written may overlap anything else, the same tensor given twice included
+ * (FNO_ERR_ALIAS).  In place and with norm + 1e-6 <= max_norm nothing is
+ * written.  given_norm (device, float32), if not NULL, stands for the norm,
+ * as where it was reduced over several GPUs; norm is then optional.  A NaN
+ * norm makes every output NaN, an infinite one zero (NaN where the gradient
+ * is not finite).  max_norm >= 0.
+ *
+ * `workspace`: as for fno_group_norm, fno_grad_norm_workspace_size(count)
+ * bytes.
+ */
+size_t fno_grad_norm_workspace_size(int count);
+int fno_grad_norm(const void* const* grads, const long long* numels, const int* types, int count,
+                  float* norm, void* workspace, size_t ws_bytes, void* stream);
+int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long long* numels,
+                       const int* types, int count, float max_norm, const float* given_norm,
+                       float* norm, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Per-kernel timing for benchmarks and profilers.  While `events` is non-NULL,

@@ -1,0 +1,141 @@
+"""Host-side checks of the group norm and gradient clipping calls (no GPU):
+bad arguments are refused before the device is touched.  Pointers are fake
+addresses."""
+import ctypes
+import os
+
+import pytest
+
+import fft_spectral_convolution_amd as fno
+
+NULL, SHAPE, ALIAS, ALIGN, WORKSPACE, VALUE = -1, -2, -4, -5, -8, -12
+
+X, W, B, O, S, G = (0x10000000 * k for k in range(1, 7))
+GW, GB, WS = 0x70000000, 0x71000000, 0x72000000
+BIG = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(fno.library_path()):
+        pytest.skip("libfno.so not built (run __graft_entry__.build())")
+    return fno.lib()
+
+
+def norm(lib, x=X, w=W, b=B, out=O, stats=S, dims=(2, 8, 10, 4), eps=1e-5, act=0, x_last=1, out_last=1, x_type=0,
+         out_type=0, ws=WS, ws_bytes=BIG):
+    return lib.fno_group_norm(x, w, b, out, stats, *dims, eps, act, x_last, out_last, x_type, out_type, ws, ws_bytes,
+                              None)
+
+
+def back(lib, x=X, w=W, b=B, stats=S, dy=O, gx=G, gw=GW, gb=GB, dims=(2, 8, 10, 4), act=0, x_last=1, out_last=1,
+         x_type=0, out_type=0, ws=WS, ws_bytes=BIG):
+    return lib.fno_group_norm_backward(x, w, b, stats, dy, gx, gw, gb, *dims, act, x_last, out_last, x_type, out_type,
+                                       ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [norm, back])
+def test_group_norm_sizes_and_options(lib, call):
+    for dims in ((0, 8, 10, 4), (2, 0, 10, 4), (2, 8, 0, 4), (2, 8, 10, 0), (2, 8, 10, 3), (2, 8, 10, 16),
+                 (-1, 8, 10, 4), (2, 8, -10, 4), (65536, 65536, 1, 1), (1 << 20, 1 << 10, 1 << 20, 1)):
+        assert call(lib, dims=dims) == SHAPE, dims
+        assert fno.lib().fno_group_norm_workspace_size(*dims) == 0
+    assert call(lib, act=3) == VALUE and call(lib, act=-1) == VALUE
+    assert call(lib, x_last=2) == VALUE and call(lib, out_last=-1) == VALUE
+    assert call(lib, x_type=3) == VALUE and call(lib, x_type=-1) == VALUE
+    assert call(lib, x_type=0, out_type=1) == VALUE          # float32 in, bfloat16 out
+    assert call(lib, x_type=1, out_type=2) == VALUE
+    assert call(lib, ws=None) == WORKSPACE and call(lib, ws_bytes=8) == WORKSPACE
+    assert call(lib, ws=WS + 16) == ALIGN
+
+
+def test_group_norm_eps(lib):
+    for eps in (0.0, -1e-5, float("nan"), float("inf")):
+        assert norm(lib, eps=eps) == VALUE
+
+
+def test_group_norm_pointers(lib):
+    for k in ("x", "out", "stats"):
+        assert norm(lib, **{k: None}) == NULL
+    assert norm(lib, x=X + 2) == ALIGN and norm(lib, out=O + 1, x_type=1, out_type=1) == ALIGN
+    assert norm(lib, w=W + 2) == ALIGN and norm(lib, b=B + 1) == ALIGN and norm(lib, stats=S + 2) == ALIGN
+    n = 2 * 8 * 10 * 4
+    assert norm(lib, out=X) == ALIAS and norm(lib, out=X + n - 4) == ALIAS and norm(lib, out=X - n + 4) == ALIAS
+    assert norm(lib, out=W - n + 8) == ALIAS and norm(lib, stats=B) == ALIAS and norm(lib, stats=O + 64) == ALIAS
+    assert norm(lib, ws=X, ws_bytes=BIG) == ALIAS and norm(lib, out=WS + 4096) == ALIAS
+
+
+def test_group_norm_backward_pointers(lib):
+    for k in ("x", "dy", "stats"):
+        assert back(lib, **{k: None}) == NULL
+    assert back(lib, gx=None, gw=None, gb=None) == NULL
+    assert back(lib, gx=G + 2) == ALIGN and back(lib, gw=GW + 2) == ALIGN and back(lib, gb=GB + 3) == ALIGN
+    assert back(lib, gx=X) == ALIAS and back(lib, gx=O) == ALIAS and back(lib, gw=W) == ALIAS
+    assert back(lib, gw=GW, gb=GW + 4) == ALIAS and back(lib, gb=S) == ALIAS
+
+
+def table(entries):
+    n = len(entries)
+    return ((ctypes.c_void_p * n)(*[e[0] for e in entries]), (ctypes.c_longlong * n)(*[e[1] for e in entries]),
+            (ctypes.c_int * n)(*[e[2] for e in entries]))
+
+
+def clip(lib, entries, outs=None, limit=1.0, given=None, n=O, ws=WS, ws_bytes=BIG, count=None):
+    p, m, t = table(entries)
+    q = p if outs is None else (ctypes.c_void_p * len(outs))(*outs)
+    return lib.fno_clip_grad_norm(p, q, m, t, len(entries) if count is None else count, limit, given, n, ws, ws_bytes,
+                                  None)
+
+
+def total(lib, entries, n=O, ws=WS, ws_bytes=BIG, count=None):
+    p, m, t = table(entries)
+    return lib.fno_grad_norm(p, m, t, len(entries) if count is None else count, n, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [total, clip])
+def test_grad_norm_refusals(lib, call):
+    assert call(lib, [(X, 10, 0)], count=-1) == SHAPE
+    assert call(lib, [(X, -1, 0)]) == SHAPE
+    assert call(lib, [(X, 10, 4)]) == VALUE and call(lib, [(X, 10, -1)]) == VALUE
+    assert call(lib, [(None, 10, 0)]) == NULL
+    assert call(lib, [(X + 2, 10, 0)]) == ALIGN and call(lib, [(X + 1, 10, 1)]) == ALIGN
+    assert call(lib, [(X, 10, 0)], n=None) == NULL
+    assert call(lib, [(X, 10, 0)], n=O + 2) == ALIGN
+    assert call(lib, [(X, 10, 0)], ws=None) == WORKSPACE and call(lib, [(X, 10, 0)], ws_bytes=64) == WORKSPACE
+    assert call(lib, [(X, 10, 0)], ws=WS + 8) == ALIGN
+    assert lib.fno_grad_norm(None, None, None, 1, O, WS, BIG, None) == NULL
+    assert lib.fno_grad_norm_workspace_size(-1) == 0
+
+
+def test_clip_refusals(lib):
+    one = [(X, 100, 0)]
+    for limit in (-1.0, float("nan")):
+        assert clip(lib, one, limit=limit) == VALUE
+    assert clip(lib, one, outs=[None]) == NULL
+    assert clip(lib, one, outs=[G + 1]) == ALIGN
+    assert clip(lib, one, outs=[X + 4]) == ALIAS                       # not in place, not apart
+    assert clip(lib, one, outs=[X + 396]) == ALIAS
+    assert clip(lib, [(X, 100, 0), (X, 100, 0)]) == ALIAS              # one tensor twice, in place
+    assert clip(lib, [(X, 100, 0), (X + 200, 4, 0)]) == ALIAS          # a part of another
+    assert clip(lib, [(X, 100, 0), (G, 100, 0)], outs=[GW, GW + 396]) == ALIAS
+    assert clip(lib, [(X, 100, 0), (G, 100, 0)], outs=[G, X]) == ALIAS # swapped
+    assert clip(lib, one, n=X + 40) == ALIAS
+    assert clip(lib, one, n=None, given=X + 40) == ALIAS
+    assert clip(lib, one, ws=X - 256) == ALIAS
+
+
+def test_binding_refuses_before_the_device():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros((1, 4, 8))
+    with pytest.raises(ValueError):
+        fno.fno_group_norm(x, 2)
+    with pytest.raises(ValueError):
+        fno.fno_group_norm_backward(x, torch.zeros(1, 2, 2), x, 2)
+    with pytest.raises(ValueError):
+        fno.fno_grad_norm([x])
+    with pytest.raises(ValueError):
+        fno.fno_clip_grad_norm([x], 1.0)
+    with pytest.raises(TypeError):
+        fno.fno_grad_norm([1.0])
+    with pytest.raises(TypeError):
+        fno.fno_group_norm([1.0], 1)
