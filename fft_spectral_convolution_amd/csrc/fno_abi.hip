@@ -1094,8 +1094,9 @@ bool off_grain(const void* p, size_t grain) { return reinterpret_cast<uintptr_t>
 
 int check_group_norm(const GroupNorm& g) {
     if (g.B < 1 || g.C < 1 || g.P < 1 || g.groups < 1 || g.C % g.groups != 0) return FNO_ERR_SHAPE;
-    // one workgroup an item and channel at the most; a field that no device holds
-    if (g.B * g.C > INT32_MAX || g.B * g.C > (INT64_C(1) << 40) / g.P) return FNO_ERR_SHAPE;
+    // positions and channels of an item are indexed in 32 bits, and no device holds more than 2^40 values
+    if (g.P > 1 << 30 || g.C > 1 << 24 || g.B * g.C > INT32_MAX || g.B * g.C > (INT64_C(1) << 40) / g.P)
+        return FNO_ERR_SHAPE;
     if (g.act < FNO_ACT_NONE || g.act > FNO_ACT_SILU) return FNO_ERR_VALUE;
     if (g.x_type < FNO_F32 || g.x_type > FNO_F16) return FNO_ERR_VALUE;
     if (g.out_type != g.x_type && g.out_type != FNO_F32) return FNO_ERR_VALUE;
@@ -1122,7 +1123,7 @@ int group_norm_common(const GroupNorm& g, const GroupNormArgs& a, bool backward,
     hipStream_t hs = static_cast<hipStream_t>(stream);
     auto run = [&]() -> int {
         const char* names[4] = {};
-        const int count = group_norm_kernels(g, backward, a.grad_x != nullptr, names);
+        const int count = group_norm_kernels(g, a, backward, names);
         for (int k = 0; k < count; ++k) {
             rec_kernel(names[k], hs);
             const hipError_t e = launch_group_norm(g, a, backward, k, hs);

@@ -1,205 +1,656 @@
-// Group norm with an activation, and its backward pass.
-//
-// With n = P D values in a group (D = C / groups channels of all P positions):
+// Group norm with an activation:
 //   mean = sum x / n,  var = sum (x - mean)^2 / n,  rstd = (var + eps)^-1/2
-//   xh = (x - mean) rstd,  z = xh w_c + b_c,  out = act(z)
-// and, for grad_out = dL/dout, g = grad_out act'(z):
-//   grad_b_c = sum_{b,p} g,  grad_w_c = sum_{b,p} g xh
-//   s1 = sum_group g w_c / n,  s2 = sum_group g w_c xh / n
-//   grad_x = rstd (g w_c - s1 - xh s2)
-// (the last from differentiating mean and rstd, which both depend on x).
-#include "fno_fields.hpp"
+//   out = act((x - mean) rstd w_c + b_c)
+// over the n = P D values of a group (D = C / groups channels of all P
+// positions).
+//
+// A group that fits a workgroup's registers is read once (k_gn_fused_*): mean,
+// then the squares about it, then the output from the kept values.  A larger
+// one is read twice: k_gn_stats_* leaves (mean, sum of squares about it) of
+// each chunk, k_gn_finish joins them (Chan, Golub and LeVeque's pairwise
+// update, all chunks at once), and k_gn_apply_* writes the output.
+#include "fno_groupnorm.hpp"
 
 namespace fno {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kHeld = 8;              // vectors a thread keeps in the one-pass kernels
+constexpr int kFusedThreads = 1024;
 
-struct View {
-    int64_t B, C, P, G;
-    bool last;
-    __device__ __forceinline__ int64_t at(int64_t b, int64_t c, int64_t p) const {
-        return last ? (b * P + p) * C + c : (b * C + c) * P + p;
+// ---- one pass, channels last -----------------------------------------------------
+// Workgroup (item, slice of cs channels).
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __restrict__ x,
+                                                                const float* __restrict__ w,
+                                                                const float* __restrict__ bias,
+                                                                TY* __restrict__ out, float* __restrict__ stats,
+                                                                LastRows r, int slices, int64_t blocks, float eps) {
+    constexpr int V = kVec<TX>;
+    extern __shared__ float lds[];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    float* buf = lds;
+    float* mean = lds + r.threads * V;
+    const int groups = r.cs / r.D;
+    float* rstd = mean + groups;
+    const int64_t b = id / slices;
+    const int c0 = (int)(id % slices) * r.cs;
+    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const bool on = row < r.q;
+    const int64_t base = b * r.P * r.C + c0 + slot * V;
+    const float n_group = (float)r.P * (float)r.D, inv_n = 1.0f / n_group;
+
+    Raw<TX, V> held[kHeld];
+    float sum[V] = {};
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int s = row + i * r.q;
+        held[i].load(x + base + (int64_t)s * r.stride(), on ? last_valid<V>(r, s, slot) : 0);
     }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += held[i][j];
+    last_sums(sum, buf, mean, r, r.D);
+    float m[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        m[j] = mean[(slot * V + j) % r.cs / r.D] / n_group;
+        sum[j] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int n = on ? last_valid<V>(r, row + i * r.q, slot) : 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = held[i][j] - m[j];
+            sum[j] = fmaf(j < n ? d : 0.0f, d, sum[j]);
+        }
+    }
+    last_sums(sum, buf, rstd, r, r.D);
+    for (int g = t; g < groups; g += blockDim.x) {
+        float* st = stats + 2 * (b * (r.C / r.D) + c0 / r.D + g);
+        st[0] = mean[g] / n_group;
+        st[1] = rsqrtf(fmaf(rstd[g], inv_n, eps));
+    }
+    if (!on) return;
+    float a[V], o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (slot * V + j) % r.cs;
+        a[j] = rsqrtf(fmaf(rstd[c / r.D], inv_n, eps)) * or_one(w, c0 + c);
+        o[j] = or_zero(bias, c0 + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int s = row + i * r.q, n = last_valid<V>(r, s, slot);
+        if (n == 0) break;
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = act_value<ACT>(fmaf(held[i][j] - m[j], a[j], o[j]));
+        store_part(out + base + (int64_t)s * r.stride(), n, y);
+    }
+}
+
+// ---- one pass, channels first ------------------------------------------------------
+// Workgroup (item, group): D rows of P values, one run of memory.
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kFusedThreads) void k_gn_fused_first(const TX* __restrict__ x,
+                                                                 const float* __restrict__ w,
+                                                                 const float* __restrict__ bias,
+                                                                 TY* __restrict__ out, float* __restrict__ stats,
+                                                                 int D, int P, int groups, FastDiv by_p, int64_t blocks,
+                                                                 float eps) {
+    constexpr int V = kVec<TX>;
+    __shared__ float red[16];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int n = D * P, t = threadIdx.x, step = blockDim.x * V;
+    const int c0 = (int)(id % groups) * D;
+    const int64_t base = id * n;
+    const float inv_n = 1.0f / (float)n;
+
+    Raw<TX, V> held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int e = i * step + t * V;
+        held[i].load(x + base + e, max(0, min(V, n - e)));
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += held[i][j];
+    const float mean = block_sum(sum, red) / (float)n;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int left = n - (i * step + t * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = held[i][j] - mean;
+            sum = fmaf(j < left ? d : 0.0f, d, sum);
+        }
+    }
+    const float rstd = rsqrtf(fmaf(block_sum(sum, red), inv_n, eps));
+    if (t == 0) {
+        stats[2 * id] = mean;
+        stats[2 * id + 1] = rstd;
+    }
+    const bool whole = P % V == 0;        // a vector lies in one channel
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int e = i * step + t * V, left = n - e;
+        if (left <= 0) break;
+        float y[V];
+        int c = c0 + div_by(e, by_p);
+        float a = rstd * or_one(w, c), o = or_zero(bias, c);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (!whole && j && j < left) {
+                c = c0 + div_by(e + j, by_p);
+                a = rstd * or_one(w, c);
+                o = or_zero(bias, c);
+            }
+            y[j] = act_value<ACT>(fmaf(held[i][j] - mean, a, o));
+        }
+        store_part(out + base + e, min(V, left), y);
+    }
+}
+
+// ---- statistics of chunks ------------------------------------------------------------
+// A thread sums its values less the first of them, and their squares: what
+// is subtracted lies within the spread of the thread's own values, so the
+// squares lose nothing to a level far from zero.
+struct Running {
+    float pivot, s, q;
+    __device__ __forceinline__ void add(float v) {
+        const float d = v - pivot;
+        s += d;
+        q = fmaf(d, d, q);
+    }
+    __device__ __forceinline__ float mean(float n) const { return pivot + s / n; }
+    __device__ __forceinline__ float squares(float n) const { return fmaxf(q - s * (s / n), 0.0f); }
 };
 
-// One workgroup per (item, group): mean first, then the squares about it.
+// Workgroup (item, chunk of `per` super-rows); part[(b chunks + chunk) groups + g].
 template <typename TX>
-__global__ __launch_bounds__(kThreads) void k_gn_stats(const TX* __restrict__ x, float* __restrict__ stats, View v,
-                                                       float eps) {
-    __shared__ float red[16];
-    const int64_t b = blockIdx.x / v.G, g = blockIdx.x % v.G, D = v.C / v.G, n = D * v.P;
-    float sum = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t d = v.last ? i % D : i / v.P, p = v.last ? i / D : i % v.P;
-        sum += (float)x[v.at(b, g * D + d, p)];
+__global__ __launch_bounds__(kMaxSlots) void k_gn_stats_last(const TX* __restrict__ x, float2* __restrict__ part,
+                                                             LastRows r, int per, int chunks, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    extern __shared__ float lds[];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    float* buf = lds;
+    float* mean = lds + r.threads * V;
+    const int groups = r.C / r.D;
+    float* sq = mean + groups;
+    const int64_t b = id / chunks;
+    const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
+    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const bool on = row < r.q;
+    const TX* p = x + b * r.P * r.C + slot * V;
+    // positions of this chunk
+    const float n = (float)min((int64_t)per * r.R, r.P - (int64_t)first * r.R) * (float)r.D;
+
+    Running run[V] = {};
+    float cnt = 0.0f;
+    int s = first + row;
+    const int full = min(last, r.P / r.R);
+    if (on && s < full) {
+        float v[V];
+        load_vec<V>(p + (int64_t)s * r.stride(), v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) run[j] = Running{v[j], 0.0f, 0.0f};
+        cnt = 1.0f;
+        for (s += r.q; s + 3 * r.q < full; s += 4 * r.q) {
+            float u[4][V];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_vec<V>(p + (int64_t)(s + i * r.q) * r.stride(), u[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) run[j].add(u[i][j]);
+            cnt += 4.0f;
+        }
+        for (; s < full; s += r.q) {
+            load_vec<V>(p + (int64_t)s * r.stride(), v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) run[j].add(v[j]);
+            cnt += 1.0f;
+        }
     }
+    // the incomplete super-row: values that some of the vector's places lack
+    float num[V];
+    const int tail = on && s < last && s >= full ? last_valid<V>(r, s, slot) : 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        num[j] = cnt;
+        if (j < tail) {
+            const float v = (float)p[(int64_t)s * r.stride() + j];
+            if (cnt == 0.0f) run[j] = Running{v, 0.0f, 0.0f};
+            else run[j].add(v);
+            num[j] += 1.0f;
+        }
+    }
+    float val[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) val[j] = num[j] > 0.0f ? num[j] * run[j].mean(num[j]) : 0.0f;
+    last_sums(val, buf, mean, r, r.D);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float d = num[j] > 0.0f ? run[j].mean(num[j]) - mean[(slot * V + j) % r.C / r.D] / n : 0.0f;
+        val[j] = num[j] > 0.0f ? fmaf(num[j] * d, d, run[j].squares(num[j])) : 0.0f;
+    }
+    last_sums(val, buf, sq, r, r.D);
+    for (int g = t; g < groups; g += blockDim.x) part[id * groups + g] = make_float2(mean[g] / n, sq[g]);
+}
+
+// Workgroup (group's run of memory, chunk of `per` values); part[run chunks + chunk].
+template <typename TX>
+__global__ __launch_bounds__(kGnThreads) void k_gn_stats_first(const TX* __restrict__ x, float2* __restrict__ part,
+                                                               int64_t run_len, int per, int chunks, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    __shared__ float red[16];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t run_id = id / chunks, at = (id % chunks) * per;
+    const int n = (int)min((int64_t)per, run_len - at);
+    const TX* p = x + run_id * run_len + at;
+    constexpr int kStep = kGnThreads * V;
+    const int t = threadIdx.x, full = n / kStep * kStep;
+    Running run{};
+    float cnt = 0.0f;
+    if (t < n) run.pivot = (float)p[min(t * V, n - 1)];
+    int e = t * V;
+    for (; e + 3 * kStep < full; e += 4 * kStep) {
+        float u[4][V];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_vec<V>(p + e + i * kStep, u[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) run.add(u[i][j]);
+        cnt += 4.0f * V;
+    }
+    for (; e < n; e += kStep) {
+        float u[V];
+        const int m = min(V, n - e);
+        load_part<V>(p + e, m, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < m) run.add(u[j]);
+        cnt += (float)m;
+    }
+    const float mine = cnt > 0.0f ? run.mean(cnt) : 0.0f;
+    const float mean = block_sum(cnt * mine, red) / (float)n;
+    const float d = mine - mean;
+    const float sq = block_sum(cnt > 0.0f ? fmaf(cnt * d, d, run.squares(cnt)) : 0.0f, red);
+    if (t == 0) part[id] = make_float2(mean, sq);
+}
+
+// One wave a group: joins its chunks' statistics.  Chunk i of group (b, g) is
+// part[(b G + g) chunks + i] (channels first) or part[(b chunks + i) G + g];
+// all chunks hold `per` values but the last.
+__global__ __launch_bounds__(kGnThreads) void k_gn_finish(const float2* __restrict__ part, float* __restrict__ stats,
+                                                          int64_t total, int groups, int chunks, bool last, int64_t per,
+                                                          int64_t n, float eps) {
+    const int64_t i = block_id() * (kGnThreads / 64) + (threadIdx.x >> 6);
+    if (i >= total) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t base = last ? i / groups * chunks * groups + i % groups : i * chunks;
+    const int64_t step = last ? groups : 1;
+    float sum = 0.0f;
+    for (int k = lane; k < chunks; k += 64)
+        sum = fmaf((float)min(per, n - k * per), part[base + k * step].x, sum);
+    const float mean = wave_sum(sum) / (float)n;
+    float sq = 0.0f;
+    for (int k = lane; k < chunks; k += 64) {
+        const float2 q = part[base + k * step];
+        const float d = q.x - mean;
+        sq += fmaf((float)min(per, n - k * per) * d, d, q.y);
+    }
+    sq = wave_sum(sq);
+    if (lane == 0) {
+        stats[2 * i] = mean;
+        stats[2 * i + 1] = rsqrtf(sq / (float)n + eps);
+    }
+}
+
+// ---- output, the layout kept ------------------------------------------------------------
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kMaxSlots) void k_gn_apply_last(const TX* __restrict__ x, const float* __restrict__ w,
+                                                             const float* __restrict__ bias,
+                                                             const float* __restrict__ stats, TY* __restrict__ out,
+                                                             LastRows r, int per, int chunks, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / chunks;
+    const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
+    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    if (row >= r.q) return;
+    const int64_t base = b * r.P * r.C + slot * V;
+    const float* st = stats + 2 * b * (r.C / r.D);
+    float m[V], a[V], o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (slot * V + j) % r.C, g = c / r.D;
+        m[j] = st[2 * g];
+        a[j] = st[2 * g + 1] * or_one(w, c);
+        o[j] = or_zero(bias, c);
+    }
+    int s = first + row;
+    for (; s + r.q < min(last, r.P / r.R); s += 2 * r.q) {
+        float u[2][V], y[V];
+        const int64_t e = base + (int64_t)s * r.stride(), f = e + (int64_t)r.q * r.stride();
+        load_vec<V>(x + e, u[0]);
+        load_vec<V>(x + f, u[1]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = act_value<ACT>(fmaf(u[0][j] - m[j], a[j], o[j]));
+        store_vec<V>(out + e, y);
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = act_value<ACT>(fmaf(u[1][j] - m[j], a[j], o[j]));
+        store_vec<V>(out + f, y);
+    }
+    for (; s < last; s += r.q) {
+        float u[V];
+        const int n = last_valid<V>(r, s, slot);
+        const int64_t e = base + (int64_t)s * r.stride();
+        load_part<V>(x + e, n, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = act_value<ACT>(fmaf(u[j] - m[j], a[j], o[j]));
+        store_part(out + e, n, u);
+    }
+}
+
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_apply_first(const TX* __restrict__ x, const float* __restrict__ w,
+                                                               const float* __restrict__ bias,
+                                                               const float* __restrict__ stats, TY* __restrict__ out,
+                                                               FirstRows r, int C, int D, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t row = id / r.chunks * (kGnThreads / r.team) + threadIdx.x / r.team;
+    if (row >= r.rows) return;
+    const int at = (int)(id % r.chunks) * r.piece, end = min(at + r.piece, r.P);
+    const int c = (int)(row % C);
+    const float* st = stats + 2 * (row / D);
+    const float m = st[0], a = st[1] * or_one(w, c), o = or_zero(bias, c);
+    const int64_t base = row * r.P;
+    for (int p = at + (threadIdx.x & (r.team - 1)) * V; p < end; p += r.team * V) {
+        float u[V];
+        const int n = min(V, end - p);
+        load_part<V>(x + base + p, n, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = act_value<ACT>(fmaf(u[j] - m, a, o));
+        store_part(out + base + p, n, u);
+    }
+}
+
+// ---- output in the other layout -----------------------------------------------------------
+// One tile a workgroup: read along x's rows, turned in LDS, written along
+// out's.
+template <int ACT, bool XLAST, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_apply_cross(const TX* __restrict__ x, const float* __restrict__ w,
+                                                               const float* __restrict__ bias,
+                                                               const float* __restrict__ stats, TY* __restrict__ out,
+                                                               Tiles q, int C, int P, int D, int64_t blocks) {
+    constexpr int V = kVec<TX>, VY = kVec<TY>;
+    __shared__ float tile[kTileLds];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / q.tiles_c / q.tiles_p;
+    const int r0 = (int)(id % ((int64_t)q.tiles_c * q.tiles_p));
+    const int c0 = r0 % q.tiles_c << q.log2c, p0 = r0 / q.tiles_c * q.tp();
+    const int ld = q.tp() + 1, t = threadIdx.x;
+    const int nc = min(q.tc(), C - c0), np = min(q.tp(), P - p0);
+    const float* st = stats + 2 * b * (C / D);
+    const int64_t item = b * (int64_t)P * C;
+    if constexpr (XLAST) {
+        const int lv = q.log2c - (V == 4 ? 2 : 3);           // log2 of vectors a row
+        const int c = (t & ((1 << lv) - 1)) * V, n = max(0, min(V, nc - c));
+        float m[V], a[V], o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int ch = min(c0 + c + j, C - 1);
+            m[j] = st[2 * (ch / D)];
+            a[j] = st[2 * (ch / D) + 1] * or_one(w, ch);
+            o[j] = or_zero(bias, ch);
+        }
+#pragma unroll
+        for (int i = 0; i < kTile / V / kGnThreads; ++i) {
+            const int p = (i * kGnThreads + t) >> lv;
+            float u[V];
+            load_part<V>(x + item + (int64_t)(p0 + p) * C + c0 + c, p < np ? n : 0, u);
+#pragma unroll
+            for (int j = 0; j < V; ++j) tile[(c + j) * ld + p] = act_value<ACT>(fmaf(u[j] - m[j], a[j], o[j]));
+        }
+    } else {
+        const int lv = 12 - q.log2c - (V == 4 ? 2 : 3);
+#pragma unroll
+        for (int i = 0; i < kTile / V / kGnThreads; ++i) {
+            const int v = i * kGnThreads + t, c = v >> lv, p = (v & ((1 << lv) - 1)) * V;
+            const int ch = min(c0 + c, C - 1);
+            const float m = st[2 * (ch / D)], a = st[2 * (ch / D) + 1] * or_one(w, ch), o = or_zero(bias, ch);
+            float u[V];
+            load_part<V>(x + item + (int64_t)(c0 + c) * P + p0 + p, c < nc ? max(0, min(V, np - p)) : 0, u);
+#pragma unroll
+            for (int j = 0; j < V; ++j) tile[c * ld + p + j] = act_value<ACT>(fmaf(u[j] - m, a, o));
+        }
+    }
+    __syncthreads();
+    if constexpr (XLAST) {
+        const int lv = 12 - q.log2c - (VY == 4 ? 2 : 3);
+#pragma unroll
+        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
+            const int v = i * kGnThreads + t, c = v >> lv, p = (v & ((1 << lv) - 1)) * VY;
+            if (c >= nc || p >= np) continue;
+            float u[VY];
+#pragma unroll
+            for (int j = 0; j < VY; ++j) u[j] = tile[c * ld + p + j];
+            store_part(out + item + (int64_t)(c0 + c) * P + p0 + p, min(VY, np - p), u);
+        }
+    } else {
+        const int lv = q.log2c - (VY == 4 ? 2 : 3);
+#pragma unroll
+        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
+            const int v = i * kGnThreads + t, p = v >> lv, c = (v & ((1 << lv) - 1)) * VY;
+            if (c >= nc || p >= np) continue;
+            float u[VY];
+#pragma unroll
+            for (int j = 0; j < VY; ++j) u[j] = tile[(c + j) * ld + p];
+            store_part(out + item + (int64_t)(p0 + p) * C + c0 + c, min(VY, nc - c), u);
+        }
+    }
+}
+
+// ---- channels last, too wide for a workgroup ------------------------------------------------
+// Workgroup (item, group), reading P short runs of D values: right for any C.
+template <typename TX>
+__global__ __launch_bounds__(kGnThreads) void k_gn_stats_wide(const TX* __restrict__ x, float* __restrict__ stats,
+                                                              int64_t C, int D, int64_t P, int64_t blocks, float eps) {
+    __shared__ float red[16];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t G = C / D, b = id / G, n = P * D;
+    const TX* p = x + b * P * C + id % G * D;
+    float sum = 0.0f;
+    for (int64_t i = threadIdx.x; i < n; i += kGnThreads) sum += (float)p[i / D * C + i % D];
     const float mean = block_sum(sum, red) / (float)n;
     float sq = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t d = v.last ? i % D : i / v.P, p = v.last ? i / D : i % v.P;
-        const float t = (float)x[v.at(b, g * D + d, p)] - mean;
-        sq = fmaf(t, t, sq);
+    for (int64_t i = threadIdx.x; i < n; i += kGnThreads) {
+        const float d = (float)p[i / D * C + i % D] - mean;
+        sq = fmaf(d, d, sq);
     }
     sq = block_sum(sq, red);
     if (threadIdx.x == 0) {
-        stats[2 * blockIdx.x] = mean;
-        stats[2 * blockIdx.x + 1] = rsqrtf(sq / (float)n + eps);
+        stats[2 * id] = mean;
+        stats[2 * id + 1] = rsqrtf(sq / (float)n + eps);
     }
 }
 
+// Workgroup (row): C values of one position.
 template <int ACT, typename TX, typename TY>
-__global__ __launch_bounds__(kThreads) void k_gn_apply(const TX* __restrict__ x, const float* __restrict__ w,
-                                                       const float* __restrict__ bias,
-                                                       const float* __restrict__ stats, TY* __restrict__ out, View v,
-                                                       bool out_last) {
-    const int64_t total = v.B * v.C * v.P;
-    View o = v;
-    o.last = out_last;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t b = i / (v.C * v.P), r = i % (v.C * v.P);
-        const int64_t c = out_last ? r % v.C : r / v.P, p = out_last ? r / v.C : r % v.P;
-        const float* st = stats + 2 * (b * v.G + c / (v.C / v.G));
-        const float xh = ((float)x[v.at(b, c, p)] - st[0]) * st[1];
-        out[i] = (TY)act_value<ACT>(fmaf(xh, w ? w[c] : 1.0f, bias ? bias[c] : 0.0f));
+__global__ __launch_bounds__(kGnThreads) void k_gn_apply_wide(const TX* __restrict__ x, const float* __restrict__ w,
+                                                              const float* __restrict__ bias,
+                                                              const float* __restrict__ stats, TY* __restrict__ out,
+                                                              int64_t C, int D, int64_t P, int64_t blocks) {
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const float* st = stats + 2 * (id / P) * (C / D);
+    for (int64_t c = threadIdx.x; c < C; c += kGnThreads) {
+        const int64_t g = c / D;
+        const float xh = ((float)x[id * C + c] - st[2 * g]) * st[2 * g + 1];
+        out[id * C + c] = (TY)act_value<ACT>(fmaf(xh, or_one(w, c), or_zero(bias, c)));
     }
 }
 
-// One workgroup per (item, channel): part[b][c] = (sum g, sum g xh).
-template <int ACT, typename TX, typename TY>
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(const TX* __restrict__ x, const TY* __restrict__ dy,
-                                                          const float* __restrict__ w,
-                                                          const float* __restrict__ bias,
-                                                          const float* __restrict__ stats, float2* __restrict__ part,
-                                                          View v, bool out_last) {
-    __shared__ float red[16];
-    const int64_t b = blockIdx.x / v.C, c = blockIdx.x % v.C;
-    const float* st = stats + 2 * (b * v.G + c / (v.C / v.G));
-    const float wc = w ? w[c] : 1.0f, bc = bias ? bias[c] : 0.0f;
-    View o = v;
-    o.last = out_last;
-    float sg = 0.0f, sgx = 0.0f;
-    for (int64_t p = threadIdx.x; p < v.P; p += kThreads) {
-        const float xh = ((float)x[v.at(b, c, p)] - st[0]) * st[1];
-        const float g = (float)dy[o.at(b, c, p)] * act_slope<ACT>(fmaf(xh, wc, bc));
-        sg += g;
-        sgx = fmaf(g, xh, sgx);
-    }
-    sg = block_sum(sg, red);
-    sgx = block_sum(sgx, red);
-    if (threadIdx.x == 0) part[blockIdx.x] = make_float2(sg, sgx);
-}
+// ---- schedules ------------------------------------------------------------------------------
+enum Stats { kFusedLast, kFusedFirst, kSplitLast, kSplitFirst, kWide };
+struct Plan {
+    Stats how;
+    LastRows rows;                // fused or split, channels last
+    int slices;                   // fused, channels last
+    int threads;                  // fused, channels first
+    int per, chunks;              // split: super-rows or values a chunk
+    int64_t parts;                // float2 of workspace
+};
 
-// Items B G: gsum[b][g] = (s1, s2).  Items B G + c: grad_weight, grad_bias.
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_reduce(const float2* __restrict__ part,
-                                                            const float* __restrict__ w, float2* __restrict__ gsum,
-                                                            float* __restrict__ gw, float* __restrict__ gb, View v) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i < v.B * v.G) {
-        const int64_t b = i / v.G, g = i % v.G, D = v.C / v.G;
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int64_t c = g * D; c < (g + 1) * D; ++c) {
-            const float2 q = part[b * v.C + c];
-            const float wc = w ? w[c] : 1.0f;
-            s1 = fmaf(wc, q.x, s1);
-            s2 = fmaf(wc, q.y, s2);
+Plan plan_forward(const GroupNorm& g) {
+    const int V = vec_of(g);
+    const int64_t D = g.C / g.groups, n = D * g.P;
+    const int64_t capacity = (int64_t)kFusedThreads * kHeld * V;
+    const bool same = g.x_last == g.out_last || g.P == 1;
+    const bool last = g.x_last || g.P == 1;       // [B][C][1] is [B][1][C]
+    Plan p{};
+    if (!last) {
+        if (same && n <= capacity) {
+            p.how = kFusedFirst;
+            const int64_t vectors = (n + V - 1) / V;
+            p.threads = 64;
+            while (p.threads < kFusedThreads && p.threads * kHeld < vectors) p.threads *= 2;
+            return p;
         }
-        const float inv = 1.0f / ((float)D * (float)v.P);
-        gsum[i] = make_float2(s1 * inv, s2 * inv);
-    } else if (i < v.B * v.G + v.C) {
-        const int64_t c = i - v.B * v.G;
-        float sg = 0.0f, sgx = 0.0f;
-        for (int64_t b = 0; b < v.B; ++b) {
-            const float2 q = part[b * v.C + c];
-            sg += q.x;
-            sgx += q.y;
+        p.how = kSplitFirst;
+        split_chunks(g.B * g.groups, n, 4 * kGnThreads * V, 64 * kGnThreads * V, &p.per, &p.chunks);
+        p.parts = g.B * g.groups * p.chunks;
+        return p;
+    }
+    if (!last_rows_ok(g.C, V)) {
+        p.how = kWide;
+        return p;
+    }
+    if (same) {
+        // the narrowest slice of whole groups that is a run of 64 bytes or more, or the whole rows
+        int64_t cs = D;
+        while (cs < g.C && (g.C % cs != 0 || cs % V != 0 || cs * 16 / V < 64)) cs += D;
+        const LastRows r = last_rows(g.C, cs, D, g.P, V, kGnThreads);
+        const int64_t vectors = (int64_t)r.ns * r.cv;
+        if (vectors <= (int64_t)kFusedThreads * kHeld) {
+            int threads = 64;
+            while (threads < kFusedThreads && (threads < r.cv || (int64_t)(threads / r.cv) * kHeld < r.ns)) threads *= 2;
+            p.rows = last_rows(g.C, cs, D, g.P, V, threads);
+            if ((int64_t)p.rows.q * kHeld >= p.rows.ns && p.rows.threads <= kFusedThreads) {
+                p.how = kFusedLast;
+                p.slices = (int)(g.C / cs);
+                return p;
+            }
         }
-        if (gw) gw[c] = sgx;
-        if (gb) gb[c] = sg;
     }
-}
-
-template <int ACT, typename TX, typename TY>
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(const TX* __restrict__ x, const TY* __restrict__ dy,
-                                                           const float* __restrict__ w,
-                                                           const float* __restrict__ bias,
-                                                           const float* __restrict__ stats,
-                                                           const float2* __restrict__ gsum, TX* __restrict__ gx,
-                                                           View v, bool out_last) {
-    const int64_t total = v.B * v.C * v.P;
-    View o = v;
-    o.last = out_last;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t b = i / (v.C * v.P), r = i % (v.C * v.P);
-        const int64_t c = v.last ? r % v.C : r / v.P, p = v.last ? r / v.C : r % v.P;
-        const int64_t gi = b * v.G + c / (v.C / v.G);
-        const float rstd = stats[2 * gi + 1], wc = w ? w[c] : 1.0f;
-        const float xh = ((float)x[i] - stats[2 * gi]) * rstd;
-        const float g = (float)dy[o.at(b, c, p)] * act_slope<ACT>(fmaf(xh, wc, bias ? bias[c] : 0.0f));
-        const float2 s = gsum[gi];
-        gx[i] = (TX)(rstd * (fmaf(g, wc, -s.x) - xh * s.y));
-    }
-}
-
-template <typename F>
-hipError_t with_types(const GroupNorm& g, F&& f) {
-    switch (g.x_type * 4 + g.out_type) {
-        case kTypeF32 * 4 + kTypeF32: return f(float{}, float{});
-        case kTypeBf16 * 4 + kTypeBf16: return f(bf16{}, bf16{});
-        case kTypeBf16 * 4 + kTypeF32: return f(bf16{}, float{});
-        case kTypeF16 * 4 + kTypeF16: return f(f16{}, f16{});
-        default: return f(f16{}, float{});
-    }
-}
-template <typename F>
-hipError_t with_act(int act, F&& f) {
-    switch (act) {
-        case kActGelu: return f(std::integral_constant<int, kActGelu>{});
-        case kActSilu: return f(std::integral_constant<int, kActSilu>{});
-        default: return f(std::integral_constant<int, kActNone>{});
-    }
+    p.how = kSplitLast;
+    p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
+    split_chunks(g.B, p.rows.ns, 4 * p.rows.q, 64 * p.rows.q, &p.per, &p.chunks);
+    p.parts = g.B * p.chunks * g.groups;
+    return p;
 }
 
 }  // namespace
 
-int group_norm_kernels(const GroupNorm&, bool backward, bool need_x, const char** names) {
-    names[0] = backward ? "gn_bwd_sums" : "gn_stats";
-    names[1] = backward ? "gn_bwd_reduce" : "gn_apply";
-    names[2] = "gn_bwd_apply";
-    return backward && need_x ? 3 : 2;
+size_t gn_forward_workspace(const GroupNorm& g) { return sizeof(float2) * (size_t)plan_forward(g).parts; }
+
+int gn_forward_kernels(const GroupNorm& g, const char** names) {
+    const Plan p = plan_forward(g);
+    const bool same = g.x_last == g.out_last || g.P == 1;
+    const char* apply = same ? "gn_apply" : "gn_apply_cross";
+    if (p.how == kFusedLast || p.how == kFusedFirst) {
+        names[0] = "gn_fused";
+        return 1;
+    }
+    names[0] = p.how == kWide ? "gn_stats_wide" : "gn_stats";
+    names[1] = p.how == kWide ? apply : "gn_finish";
+    names[2] = apply;
+    return p.how == kWide ? 2 : 3;
 }
 
-size_t group_norm_workspace(const GroupNorm& g) { return sizeof(float2) * (size_t)(g.B * g.C + g.B * g.groups); }
-
-hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s) {
-    const View v{g.B, g.C, g.P, g.groups, g.x_last};
-    const unsigned flat = (unsigned)std::min<int64_t>((g.B * g.C * g.P + kThreads - 1) / kThreads, 8192);
+hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int kernel, hipStream_t s) {
+    const Plan p = plan_forward(g);
+    const int D = (int)(g.C / g.groups), C = (int)g.C, P = (int)g.P;
+    const int64_t n = (int64_t)D * P, runs = g.B * g.groups;
     float2* part = static_cast<float2*>(a.ws);
-    float2* gsum = part + g.B * g.C;
     return with_types(g, [&](auto tx, auto ty) {
         using TX = decltype(tx);
         using TY = decltype(ty);
+        constexpr int V = kVec<TX>;
         const TX* x = static_cast<const TX*>(a.x);
-        TY* o = static_cast<TY*>(a.out);
+        TY* out = static_cast<TY*>(a.out);
+        const float* stats = a.stats;
+        const size_t lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * (D ? p.rows.cs / D : 0));
+        if (kernel == 0 && p.how == kSplitLast) {
+            const int64_t blocks = g.B * p.chunks;
+            return launch_kernel(k_gn_stats_last<TX>, grid_of(blocks), dim3(p.rows.threads), lds, s, x, part, p.rows,
+                                 p.per, p.chunks, blocks);
+        }
+        if (kernel == 0 && p.how == kSplitFirst) {
+            const int64_t blocks = runs * p.chunks;
+            return launch_kernel(k_gn_stats_first<TX>, grid_of(blocks), dim3(kGnThreads), 0, s, x, part, n, p.per,
+                                 p.chunks, blocks);
+        }
+        if (kernel == 0 && p.how == kWide)
+            return launch_kernel(k_gn_stats_wide<TX>, grid_of(runs), dim3(kGnThreads), 0, s, x, a.stats, g.C, D, g.P,
+                                 runs, g.eps);
+        if (kernel == 1 && p.how != kWide) {
+            const bool last = p.how == kSplitLast;
+            const int64_t per = last ? (int64_t)p.per * p.rows.R * D : p.per;
+            return launch_kernel(k_gn_finish, grid_of((runs + 3) / 4), dim3(kGnThreads), 0, s, (const float2*)part,
+                                 a.stats, runs, (int)g.groups, p.chunks, last, per, n, g.eps);
+        }
         return with_act(g.act, [&](auto act) {
             constexpr int ACT = decltype(act)::value;
-            if (!backward && kernel == 0)
-                return launch_kernel(k_gn_stats<TX>, dim3((unsigned)(g.B * g.groups)), dim3(kThreads), 0, s, x,
-                                     a.stats, v, g.eps);
-            if (!backward)
-                return launch_kernel(k_gn_apply<ACT, TX, TY>, dim3(flat), dim3(kThreads), 0, s, x, a.weight, a.bias,
-                                     (const float*)a.stats, o, v, g.out_last);
-            if (kernel == 0)
-                return launch_kernel(k_gn_bwd_sums<ACT, TX, TY>, dim3((unsigned)(g.B * g.C)), dim3(kThreads), 0, s, x,
-                                     (const TY*)o, a.weight, a.bias, (const float*)a.stats, part, v, g.out_last);
-            if (kernel == 1)
-                return launch_kernel(k_gn_bwd_reduce,
-                                     dim3((unsigned)((g.B * g.groups + g.C + kThreads - 1) / kThreads)),
-                                     dim3(kThreads), 0, s, (const float2*)part, a.weight, gsum, a.grad_weight,
-                                     a.grad_bias, v);
-            return launch_kernel(k_gn_bwd_apply<ACT, TX, TY>, dim3(flat), dim3(kThreads), 0, s, x, (const TY*)o,
-                                 a.weight, a.bias, (const float*)a.stats, (const float2*)gsum,
-                                 static_cast<TX*>(a.grad_x), v, g.out_last);
+            if (p.how == kFusedLast) {
+                const int64_t blocks = g.B * p.slices;
+                return launch_kernel(k_gn_fused_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), lds, s, x,
+                                     a.weight, a.bias, out, a.stats, p.rows, p.slices, blocks, g.eps);
+            }
+            if (p.how == kFusedFirst)
+                return launch_kernel(k_gn_fused_first<ACT, TX, TY>, grid_of(runs), dim3(p.threads), 0, s, x, a.weight,
+                                     a.bias, out, a.stats, D, P, (int)g.groups, fast_div(P), runs, g.eps);
+            if (g.x_last != g.out_last && g.P > 1) {
+                const Tiles q = tiles_of(C, P);
+                const int64_t blocks = g.B * q.tiles_c * q.tiles_p;
+                if (g.x_last)
+                    return launch_kernel(k_gn_apply_cross<ACT, true, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s,
+                                         x, a.weight, a.bias, stats, out, q, C, P, D, blocks);
+                return launch_kernel(k_gn_apply_cross<ACT, false, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
+                                     a.weight, a.bias, stats, out, q, C, P, D, blocks);
+            }
+            if (p.how == kSplitLast) {
+                // eight vectors a thread: 32 KiB of a 16-byte-vector field a workgroup
+                const int per = std::min(8 * p.rows.q, p.rows.ns), chunks = (p.rows.ns + per - 1) / per;
+                const int64_t blocks = g.B * chunks;
+                return launch_kernel(k_gn_apply_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), 0, s, x,
+                                     a.weight, a.bias, stats, out, p.rows, per, chunks, blocks);
+            }
+            if (p.how == kSplitFirst) {
+                const FirstRows r = first_rows(g.B * g.C, g.P, V, 8);
+                const int64_t blocks = first_blocks(r);
+                return launch_kernel(k_gn_apply_first<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
+                                     a.weight, a.bias, stats, out, r, C, D, blocks);
+            }
+            const int64_t blocks = g.B * g.P;
+            return launch_kernel(k_gn_apply_wide<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x, a.weight,
+                                 a.bias, stats, out, g.C, D, g.P, blocks);
         });
     });
 }

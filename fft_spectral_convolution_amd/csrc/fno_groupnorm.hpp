@@ -1,0 +1,240 @@
+// Shared by the forward and backward group norm kernels: how a field is cut
+// into vectors, rows and chunks, and the sums over a workgroup's part of it.
+#pragma once
+
+#include <algorithm>
+
+#include "fno_fields.hpp"
+
+namespace fno {
+
+constexpr int kGnThreads = 256;
+
+// Vector width of a field: 16 bytes.
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// Workgroups are counted in up to two grid dimensions: a dimension holds
+// fewer than 2^32 threads, and a field may have more groups than that.
+inline dim3 grid_of(int64_t blocks) {
+    constexpr int64_t kRow = 1 << 20;
+    return blocks <= kRow ? dim3((unsigned)blocks) : dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
+}
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+// ---- channels last ------------------------------------------------------------
+// An item is P rows of C channels.  A workgroup covers `cs` neighbouring
+// channels (all C of them, or a slice of whole groups).  Where C is no
+// multiple of the vector width V, rows are taken R = V / gcd(C, V) at a time:
+// R rows are a whole number of vectors, and a vector at place `slot` of such a
+// super-row holds the channels (slot V + j) mod C whatever the super-row, so
+// that each thread keeps its slot, and the constants of its channels stay in
+// registers.  Only the last super-row of an item can be incomplete.
+struct LastRows {
+    int C, cs, D;          // channels, those of a slice, those of a group
+    int P;                 // positions
+    int R;                 // rows of a super-row (1 where cs < C)
+    int cv;                // vectors of a super-row
+    int q;                 // super-rows a workgroup takes at a time
+    int threads;           // cv q, rounded up to whole waves
+    int ns;                // super-rows of an item
+    __host__ __device__ int stride() const { return cs < C ? C : C * R; }   // elements from one to the next
+};
+
+inline int gcd_of(int a, int b) {
+    while (b) {
+        const int t = a % b;
+        a = b;
+        b = t;
+    }
+    return a;
+}
+
+inline LastRows last_rows(int64_t C, int64_t cs, int64_t D, int64_t P, int V, int threads) {
+    LastRows r;
+    r.C = (int)C;
+    r.cs = (int)cs;
+    r.D = (int)D;
+    r.P = (int)P;
+    const int g = gcd_of((int)std::min<int64_t>(cs, INT32_MAX), V);
+    r.R = V / g;
+    r.cv = (int)(cs / g);
+    r.q = std::max(1, threads / r.cv);
+    r.threads = (r.cv * r.q + 63) / 64 * 64;
+    r.ns = (int)((P + r.R - 1) / r.R);
+    return r;
+}
+
+constexpr int kMaxSlots = 512;    // slots a workgroup covers; wider items take the one-group-a-workgroup kernels
+inline bool last_rows_ok(int64_t C, int V) { return C / gcd_of((int)std::min<int64_t>(C, INT32_MAX), V) <= kMaxSlots; }
+
+// Elements of a thread's vector in super-row s that exist (all V but in the
+// last super-row).
+template <int V>
+__device__ __forceinline__ int last_valid(const LastRows& r, int s, int slot) {
+    if (s >= r.ns) return 0;
+    if (r.R == 1) return V;
+    const int64_t left = (int64_t)r.P * r.C - ((int64_t)s * r.R * r.C + slot * V);
+    return left >= V ? V : left > 0 ? (int)left : 0;
+}
+
+// Loads n <= N elements, zeros beyond.
+template <int N, typename T>
+__device__ __forceinline__ void load_part(const T* p, int n, float (&v)[N]) {
+    if (n == N) {
+        load_vec<N>(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = j < n ? (float)p[j] : 0.0f;
+    }
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_part(T* p, int n, const float (&v)[N]) {
+    if (n == N) {
+        store_vec<N>(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < n) p[j] = (T)v[j];
+    }
+}
+
+// A vector as it lies in memory: values kept in registers between the passes
+// of a kernel stay in their own type.
+template <typename T, int N>
+struct Raw {
+    typename VecOf<T, N>::type q;
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if (n == N) {
+            q = *reinterpret_cast<const typename VecOf<T, N>::type*>(p);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) q[j] = j < n ? p[j] : (T)0.0f;
+        }
+    }
+    __device__ __forceinline__ float operator[](int j) const { return (float)q[j]; }
+};
+
+// Sums of `val` (V values a thread) over the rows of a workgroup's super-rows
+// and over `width` neighbouring channels: res[c / width].  width is D for
+// group sums, 1 for channel sums.  buf holds threads * V floats.  Lanes
+// `parts` at a time share a result and are added by shuffles, in an order
+// that depends on the sizes alone.  buf may be reused after the next barrier,
+// res is complete on return.
+template <int V>
+__device__ __forceinline__ void last_sums(const float (&val)[V], float* buf, float* res, const LastRows& r, int width) {
+    const int t = threadIdx.x, active = r.cv * r.q;
+    __syncthreads();
+    if (t < active) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) buf[t * V + j] = val[j];
+    }
+    __syncthreads();
+    const int count = r.cs / width, rows = r.q * r.R;
+    int parts = 1;
+    while (parts < 64 && 2 * parts * count <= (int)blockDim.x) parts *= 2;
+    const int part = t & (parts - 1);
+    const int entries = rows * width;
+    for (int g = t / parts; g < count; g += (int)blockDim.x / parts) {
+        float s = 0.0f;
+        for (int k = part; k < entries; k += parts) {
+            const int row = width == 1 ? k : k / width;
+            s += buf[row * r.cs + g * width + (width == 1 ? 0 : k - row * width)];
+        }
+        for (int m = parts >> 1; m; m >>= 1) s += __shfl_xor(s, m, 64);
+        if (part == 0) res[g] = s;
+    }
+    __syncthreads();
+}
+
+// Chunks of a two-pass reduction over items of `units` each: about 2048
+// workgroups in all, of min_per to max_per units.  The upper end bounds the
+// chain of additions in a thread to a few hundred.
+inline void split_chunks(int64_t items, int64_t units, int64_t min_per, int64_t max_per, int* per, int* chunks) {
+    const int64_t want = std::max<int64_t>(1, 2048 / items);
+    const int64_t p = std::min(std::min(std::max((units + want - 1) / want, min_per), max_per), units);
+    *per = (int)p;
+    *chunks = (int)((units + p - 1) / p);
+}
+
+// ---- channels first ------------------------------------------------------------
+// Rows (b, c) of P positions.  A team of `team` threads (a power of two, at
+// most the workgroup) takes a row, or one of its `chunks` pieces.
+struct FirstRows {
+    int64_t rows;          // B C
+    int P, team, chunks, piece;
+};
+inline FirstRows first_rows(int64_t rows, int64_t P, int V, int vectors) {
+    FirstRows r{rows, (int)P, 1, 1, (int)P};
+    while (r.team < 64 && (int64_t)2 * r.team * V * 2 <= P) r.team *= 2;
+    if (P >= (int64_t)2 * kGnThreads * V) {
+        r.team = kGnThreads;
+        r.piece = (int)std::min<int64_t>(P, (int64_t)kGnThreads * V * vectors);
+        r.chunks = (int)((P + r.piece - 1) / r.piece);
+    }
+    return r;
+}
+inline int64_t first_blocks(const FirstRows& r) {
+    const int per = kGnThreads / r.team;
+    return (r.rows + per - 1) / per * r.chunks;
+}
+
+// Quotient by a small divisor without a division: exact for n d < 2^32.
+struct FastDiv {
+    uint32_t d, m;
+};
+inline FastDiv fast_div(int d) { return FastDiv{(uint32_t)d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) { return f.m ? (int)__umulhi((uint32_t)n, f.m) : n; }
+
+// ---- one layout to the other ----------------------------------------------------
+// Tiles of 4096 values: 2^log2c channels times 4096 / 2^log2c positions,
+// turned in LDS.  The row length is odd, so that both the writes (lanes along
+// channels) and the reads (lanes along positions) fall on different banks.
+constexpr int kTile = 4096;
+struct Tiles {
+    int log2c;
+    int tiles_p, tiles_c;
+    __host__ __device__ int tc() const { return 1 << log2c; }
+    __host__ __device__ int tp() const { return kTile >> log2c; }
+};
+inline Tiles tiles_of(int64_t C, int64_t P) {
+    Tiles t{4, 0, 0};
+    while (t.log2c < 6 && (1 << t.log2c) < C) ++t.log2c;
+    t.tiles_p = (int)((P + t.tp() - 1) / t.tp());
+    t.tiles_c = (int)((C + t.tc() - 1) / t.tc());
+    return t;
+}
+constexpr int kTileLds = kTile + 256;     // tc (tp + 1) <= 4096 + 64
+
+__device__ __forceinline__ float or_one(const float* w, int64_t c) { return w ? w[c] : 1.0f; }
+__device__ __forceinline__ float or_zero(const float* b, int64_t c) { return b ? b[c] : 0.0f; }
+
+template <typename F>
+hipError_t with_types(const GroupNorm& g, F&& f) {
+    switch (g.x_type * 4 + g.out_type) {
+        case kTypeF32 * 4 + kTypeF32: return f(float{}, float{});
+        case kTypeBf16 * 4 + kTypeBf16: return f(bf16{}, bf16{});
+        case kTypeBf16 * 4 + kTypeF32: return f(bf16{}, float{});
+        case kTypeF16 * 4 + kTypeF16: return f(f16{}, f16{});
+        default: return f(f16{}, float{});
+    }
+}
+template <typename F>
+hipError_t with_act(int act, F&& f) {
+    switch (act) {
+        case kActGelu: return f(std::integral_constant<int, kActGelu>{});
+        case kActSilu: return f(std::integral_constant<int, kActSilu>{});
+        default: return f(std::integral_constant<int, kActNone>{});
+    }
+}
+inline int vec_of(const GroupNorm& g) { return g.x_type == kTypeF32 ? 4 : 8; }
+
+// Forward and backward halves of launch_group_norm and its queries.
+int gn_forward_kernels(const GroupNorm& g, const char** names);
+size_t gn_forward_workspace(const GroupNorm& g);
+hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int kernel, hipStream_t s);
+int gn_backward_kernels(const GroupNorm& g, bool need_x, bool need_w, const char** names);
+size_t gn_backward_workspace(const GroupNorm& g);
+hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int kernel, hipStream_t s);
+
+}  // namespace fno

@@ -1,0 +1,894 @@
+// Backward pass of the group norm with an activation.  With xh = (x - mean)
+// rstd, z = xh w_c + b_c and g = grad_out act'(z):
+//   grad_b_c = sum_{b,p} g,  grad_w_c = sum_{b,p} g xh
+//   s1 = sum_group g w_c / n,  s2 = sum_group g w_c xh / n
+//   grad_x = rstd (g w_c - s1 - xh s2)
+// (mean and rstd depend on every x of the group: the two means take that
+// back out.)  All of it follows from the sums of g and g xh over each item's
+// channel, so those are what a workgroup forms:
+// k_gn_bwd_fused_* keep x and grad_out in registers between the sums and
+// grad_x, both read once; larger groups take k_gn_bwd_sums_* (partial sums of
+// chunks), k_gn_bwd_finish (s1, s2 and the parameters' gradients) and
+// k_gn_bwd_apply_*.
+#include "fno_groupnorm.hpp"
+
+namespace fno {
+namespace {
+
+constexpr int kHeld = 4;              // vectors of x and of grad_out a thread keeps
+constexpr int kFusedThreads = 1024;
+constexpr size_t kLdsMax = 65536;
+
+template <int ACT>
+__device__ __forceinline__ float slope_times(float dy, float xh, float w, float b) {
+    return dy * act_slope<ACT>(fmaf(xh, w, b));
+}
+
+// s1, s2 (not yet divided by n) of `groups` groups of D channels from the
+// channels' sums; res[g] and res[groups + g].
+__device__ __forceinline__ void group_means(const float* cg, const float* cx, const float* w, int64_t c0, int D,
+                                            int groups, float* res) {
+    const int t = threadIdx.x;
+    int parts = 1;
+    while (parts < 64 && 2 * parts * groups <= (int)blockDim.x && parts < D) parts *= 2;
+    for (int g = t / parts; g < groups; g += (int)blockDim.x / parts) {
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int d = t & (parts - 1); d < D; d += parts) {
+            const float wc = or_one(w, c0 + g * D + d);
+            s1 = fmaf(wc, cg[g * D + d], s1);
+            s2 = fmaf(wc, cx[g * D + d], s2);
+        }
+        for (int m = parts >> 1; m; m >>= 1) {
+            s1 += __shfl_xor(s1, m, 64);
+            s2 += __shfl_xor(s2, m, 64);
+        }
+        if ((t & (parts - 1)) == 0) {
+            res[g] = s1;
+            res[groups + g] = s2;
+        }
+    }
+    __syncthreads();
+}
+
+// ---- one pass, channels last: workgroup (item, slice of cs channels) ------------
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
+    const TX* __restrict__ x, const TY* __restrict__ dy, const float* __restrict__ w, const float* __restrict__ bias,
+    const float* __restrict__ stats, TX* __restrict__ gx, float2* __restrict__ part, LastRows r, int slices,
+    int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    extern __shared__ float lds[];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    float* buf = lds;
+    float* cg = lds + r.threads * V;
+    float* cx = cg + r.cs;
+    float* res = cx + r.cs;
+    const int groups = r.cs / r.D;
+    const int64_t b = id / slices;
+    const int c0 = (int)(id % slices) * r.cs;
+    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const bool on = row < r.q;
+    const int64_t base = b * r.P * r.C + c0 + slot * V;
+    const float* st = stats + 2 * (b * (r.C / r.D) + c0 / r.D);
+
+    Raw<TX, V> hx[kHeld];
+    Raw<TY, V> hy[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int s = row + i * r.q, n = on ? last_valid<V>(r, s, slot) : 0;
+        const int64_t e = base + (int64_t)s * r.stride();
+        hx[i].load(x + e, n);
+        hy[i].load(dy + e, n);
+    }
+    float m[V], k[V], a[V], o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (slot * V + j) % r.cs;
+        m[j] = st[2 * (c / r.D)];
+        k[j] = st[2 * (c / r.D) + 1];
+        a[j] = or_one(w, c0 + c);
+        o[j] = or_zero(bias, c0 + c);
+    }
+    // an element that does not exist reads grad_out 0 and adds nothing; its x is set to the mean, so
+    // that xh is 0 however large the mean
+    float sg[V] = {}, sx[V] = {};
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int n = on ? last_valid<V>(r, row + i * r.q, slot) : 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = j < n ? (hx[i][j] - m[j]) * k[j] : 0.0f;
+            const float g = j < n ? slope_times<ACT>(hy[i][j], xh, a[j], o[j]) : 0.0f;
+            sg[j] += g;
+            sx[j] = fmaf(g, xh, sx[j]);
+        }
+    }
+    last_sums(sg, buf, cg, r, 1);
+    last_sums(sx, buf, cx, r, 1);
+    if (part)
+        for (int c = t; c < r.cs; c += blockDim.x) part[b * r.C + c0 + c] = make_float2(cg[c], cx[c]);
+    if (!gx) return;
+    group_means(cg, cx, w, c0, r.D, groups, res);
+    if (!on) return;
+    const float inv_n = 1.0f / ((float)r.P * (float)r.D);
+    float s1[V], s2[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int g = (slot * V + j) % r.cs / r.D;
+        s1[j] = res[g] * inv_n;
+        s2[j] = res[groups + g] * inv_n;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int s = row + i * r.q, n = last_valid<V>(r, s, slot);
+        if (n == 0) break;
+        float u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = (hx[i][j] - m[j]) * k[j];
+            const float g = slope_times<ACT>(hy[i][j], xh, a[j], o[j]);
+            u[j] = k[j] * (fmaf(g, a[j], -s1[j]) - xh * s2[j]);
+        }
+        store_part(gx + base + (int64_t)s * r.stride(), n, u);
+    }
+}
+
+// ---- one pass, channels first: workgroup (item, group) ----------------------------
+// Every vector leaves its sums of g and g xh in LDS, for its first channel
+// and, where the row length is no multiple of V, for the next one (a row is
+// at least a vector long); the vectors of each channel are then added in order.
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
+    const TX* __restrict__ x, const TY* __restrict__ dy, const float* __restrict__ w, const float* __restrict__ bias,
+    const float* __restrict__ stats, TX* __restrict__ gx, float2* __restrict__ part, int D, int P, int groups,
+    FastDiv by_p, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    extern __shared__ float lds[];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int n = D * P, t = threadIdx.x, step = blockDim.x * V, nv = (n + V - 1) / V;
+    const bool whole = P % V == 0;
+    float2* head = reinterpret_cast<float2*>(lds);
+    float2* next = head + nv;
+    float* cg = reinterpret_cast<float*>(whole ? next : next + nv);
+    float* cx = cg + D;
+    float* res = cx + D;
+    const int c0 = (int)(id % groups) * D;
+    const int64_t base = id * n;
+    const float mean = stats[2 * id], rstd = stats[2 * id + 1];
+
+    Raw<TX, V> hx[kHeld];
+    Raw<TY, V> hy[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int e = i * step + t * V, m = max(0, min(V, n - e));
+        hx[i].load(x + base + e, m);
+        hy[i].load(dy + base + e, m);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int e = i * step + t * V;
+        if (e >= n) break;
+        const int d = div_by(e, by_p), cut = (d + 1) * P - e;      // places of the vector in channel d
+        float2 s = make_float2(0.0f, 0.0f), u = make_float2(0.0f, 0.0f);
+        const int c1 = min(d + 1, D - 1);
+        const float w0 = or_one(w, c0 + d), b0 = or_zero(bias, c0 + d);
+        const float w1 = or_one(w, c0 + c1), b1 = or_zero(bias, c0 + c1);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (j >= n - e) break;
+            const float xh = (hx[i][j] - mean) * rstd;
+            const float g = slope_times<ACT>(hy[i][j], xh, j < cut ? w0 : w1, j < cut ? b0 : b1);
+            if (j < cut) {
+                s.x += g;
+                s.y = fmaf(g, xh, s.y);
+            } else {
+                u.x += g;
+                u.y = fmaf(g, xh, u.y);
+            }
+        }
+        head[e / V] = s;
+        if (!whole) next[e / V] = u;
+    }
+    __syncthreads();
+    int parts = 1;
+    while (parts < 64 && 2 * parts * D <= (int)blockDim.x) parts *= 2;
+    for (int d = t / parts; d < D; d += (int)blockDim.x / parts) {
+        const int lo = d * P / V, hi = ((d + 1) * P + V - 1) / V;
+        float2 s = make_float2(0.0f, 0.0f);
+        for (int v = lo + (t & (parts - 1)); v < hi; v += parts) {
+            const float2 q = v * V < d * P ? next[v] : head[v];
+            s.x += q.x;
+            s.y += q.y;
+        }
+        for (int m = parts >> 1; m; m >>= 1) {
+            s.x += __shfl_xor(s.x, m, 64);
+            s.y += __shfl_xor(s.y, m, 64);
+        }
+        if ((t & (parts - 1)) == 0) {
+            cg[d] = s.x;
+            cx[d] = s.y;
+            if (part) part[id * D + d] = s;
+        }
+    }
+    if (!gx) return;
+    __syncthreads();
+    group_means(cg, cx, w, c0, D, 1, res);
+    const float inv_n = 1.0f / (float)n, s1 = res[0] * inv_n, s2 = res[1] * inv_n;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int e = i * step + t * V;
+        if (e >= n) break;
+        const int d = div_by(e, by_p), cut = (d + 1) * P - e;
+        const int c1 = min(d + 1, D - 1);
+        const float w0 = or_one(w, c0 + d), b0 = or_zero(bias, c0 + d);
+        const float w1 = or_one(w, c0 + c1), b1 = or_zero(bias, c0 + c1);
+        float u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = (hx[i][j] - mean) * rstd, wc = j < cut ? w0 : w1;
+            const float g = slope_times<ACT>(hy[i][j], xh, wc, j < cut ? b0 : b1);
+            u[j] = rstd * (fmaf(g, wc, -s1) - xh * s2);
+        }
+        store_part(gx + base + e, min(V, n - e), u);
+    }
+}
+
+// ---- partial sums of chunks ----------------------------------------------------------
+// Channels last: workgroup (item, chunk); part[(b chunks + chunk) C + c].
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_sums_last(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                const float* __restrict__ w,
+                                                                const float* __restrict__ bias,
+                                                                const float* __restrict__ stats,
+                                                                float2* __restrict__ part, LastRows r, int per,
+                                                                int chunks, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    extern __shared__ float lds[];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    float* buf = lds;
+    float* cg = lds + r.threads * V;
+    float* cx = cg + r.C;
+    const int64_t b = id / chunks;
+    const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
+    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int64_t base = b * r.P * r.C + slot * V;
+    const float* st = stats + 2 * b * (r.C / r.D);
+    float m[V], k[V], a[V], o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (slot * V + j) % r.C;
+        m[j] = st[2 * (c / r.D)];
+        k[j] = st[2 * (c / r.D) + 1];
+        a[j] = or_one(w, c);
+        o[j] = or_zero(bias, c);
+    }
+    float sg[V] = {}, sx[V] = {};
+    auto take = [&](const float (&u)[V], const float (&v)[V], int n) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = (u[j] - m[j]) * k[j];
+            const float g = slope_times<ACT>(v[j], xh, a[j], o[j]);
+            if (j < n) {
+                sg[j] += g;
+                sx[j] = fmaf(g, xh, sx[j]);
+            }
+        }
+    };
+    if (row < r.q) {
+        int s = first + row;
+        const int full = min(last, r.P / r.R);
+        for (; s + r.q < full; s += 2 * r.q) {
+            float u[2][V], v[2][V];
+            const int64_t e = base + (int64_t)s * r.stride(), f = e + (int64_t)r.q * r.stride();
+            load_vec<V>(x + e, u[0]);
+            load_vec<V>(dy + e, v[0]);
+            load_vec<V>(x + f, u[1]);
+            load_vec<V>(dy + f, v[1]);
+            take(u[0], v[0], V);
+            take(u[1], v[1], V);
+        }
+        for (; s < last; s += r.q) {
+            float u[V], v[V];
+            const int n = last_valid<V>(r, s, slot);
+            const int64_t e = base + (int64_t)s * r.stride();
+            load_part<V>(x + e, n, u);
+            load_part<V>(dy + e, n, v);
+            take(u, v, n);
+        }
+    }
+    last_sums(sg, buf, cg, r, 1);
+    last_sums(sx, buf, cx, r, 1);
+    for (int c = t; c < r.C; c += blockDim.x) part[id * r.C + c] = make_float2(cg[c], cx[c]);
+}
+
+// Channels first: a team takes a row or a piece of it; part[row chunks + piece].
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                  const float* __restrict__ w,
+                                                                  const float* __restrict__ bias,
+                                                                  const float* __restrict__ stats,
+                                                                  float2* __restrict__ part, FirstRows r, int C, int D,
+                                                                  int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    __shared__ float red[16];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t row = id / r.chunks * (kGnThreads / r.team) + threadIdx.x / r.team;
+    const int piece = (int)(id % r.chunks);
+    float sg = 0.0f, sx = 0.0f;
+    if (row < r.rows) {
+        const int at = piece * r.piece, end = min(at + r.piece, r.P);
+        const int c = (int)(row % C);
+        const float* st = stats + 2 * (row / D);
+        const float m = st[0], k = st[1], a = or_one(w, c), o = or_zero(bias, c);
+        const int64_t base = row * r.P;
+        for (int p = at + (threadIdx.x & (r.team - 1)) * V; p < end; p += r.team * V) {
+            float u[V], v[V];
+            const int n = min(V, end - p);
+            load_part<V>(x + base + p, n, u);
+            load_part<V>(dy + base + p, n, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xh = (u[j] - m) * k;
+                const float g = slope_times<ACT>(v[j], xh, a, o);
+                if (j < n) {
+                    sg += g;
+                    sx = fmaf(g, xh, sx);
+                }
+            }
+        }
+    }
+    if (r.team == kGnThreads) {
+        sg = block_sum(sg, red);
+        sx = block_sum(sx, red);
+    } else {
+        for (int q = r.team >> 1; q; q >>= 1) {
+            sg += __shfl_xor(sg, q, 64);
+            sx += __shfl_xor(sx, q, 64);
+        }
+    }
+    if ((threadIdx.x & (r.team - 1)) == 0 && row < r.rows) part[row * r.chunks + piece] = make_float2(sg, sx);
+}
+
+// x and grad_out of different layouts: workgroup (item, channel tile, chunk
+// of `per` position tiles); grad_out is turned in LDS, x read in its own
+// order.  part as that of x's layout.
+template <typename TY>
+__device__ __forceinline__ void load_turned(const TY* dy, float* tile, const Tiles& q, bool dy_last, int64_t item,
+                                            int c0, int p0, int nc, int np, int C, int P) {
+    constexpr int VY = kVec<TY>;
+    const int ld = q.tp() + 1, t = threadIdx.x;
+    if (dy_last) {
+        const int lv = q.log2c - (VY == 4 ? 2 : 3);
+#pragma unroll
+        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
+            const int v = i * kGnThreads + t, p = v >> lv, c = (v & ((1 << lv) - 1)) * VY;
+            float u[VY];
+            load_part<VY>(dy + item + (int64_t)(p0 + p) * C + c0 + c, p < np ? max(0, min(VY, nc - c)) : 0, u);
+#pragma unroll
+            for (int j = 0; j < VY; ++j) tile[(c + j) * ld + p] = u[j];
+        }
+    } else {
+        const int lv = 12 - q.log2c - (VY == 4 ? 2 : 3);
+#pragma unroll
+        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
+            const int v = i * kGnThreads + t, c = v >> lv, p = (v & ((1 << lv) - 1)) * VY;
+            float u[VY];
+            load_part<VY>(dy + item + (int64_t)(c0 + c) * P + p0 + p, c < nc ? max(0, min(VY, np - p)) : 0, u);
+#pragma unroll
+            for (int j = 0; j < VY; ++j) tile[c * ld + p + j] = u[j];
+        }
+    }
+}
+
+template <int ACT, bool XLAST, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                  const float* __restrict__ w,
+                                                                  const float* __restrict__ bias,
+                                                                  const float* __restrict__ stats,
+                                                                  float2* __restrict__ part, Tiles q, int C, int P,
+                                                                  int D, int per, int chunks, int64_t blocks) {
+    constexpr int V = kVec<TX>, N = kTile / V / kGnThreads;
+    __shared__ float tile[kTileLds];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / chunks / q.tiles_c;
+    const int chunk = (int)(id / q.tiles_c % chunks), c0 = (int)(id % q.tiles_c) << q.log2c;
+    const int first = chunk * per, last = min(first + per, q.tiles_p);
+    const int ld = q.tp() + 1, t = threadIdx.x, nc = min(q.tc(), C - c0);
+    const int lv = (XLAST ? q.log2c : 12 - q.log2c) - (V == 4 ? 2 : 3);      // log2 of vectors along x's rows
+    const float* st = stats + 2 * b * (C / D);
+    const int64_t item = b * (int64_t)P * C;
+    // sums of a channel for each place of the vector (x channels last), or for
+    // each of the thread's N vectors (x channels first)
+    constexpr int S = XLAST ? V : N;
+    float sg[S] = {}, sx[S] = {}, m[S], k[S], a[S], o[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const int c = XLAST ? (t & ((1 << lv) - 1)) * V + j : (j * kGnThreads + t) >> lv;
+        const int ch = min(c0 + c, C - 1);
+        m[j] = st[2 * (ch / D)];
+        k[j] = st[2 * (ch / D) + 1];
+        a[j] = or_one(w, ch);
+        o[j] = or_zero(bias, ch);
+    }
+    for (int pt = first; pt < last; ++pt) {
+        const int p0 = pt * q.tp(), np = min(q.tp(), P - p0);
+        __syncthreads();
+        load_turned(dy, tile, q, !XLAST, item, c0, p0, nc, np, C, P);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = i * kGnThreads + t;
+            const int along = (v & ((1 << lv) - 1)) * V, across = v >> lv;
+            const int n = XLAST ? (across < np ? max(0, min(V, nc - along)) : 0)
+                                : (across < nc ? max(0, min(V, np - along)) : 0);
+            const int64_t e = XLAST ? item + (int64_t)(p0 + across) * C + c0 + along
+                                    : item + (int64_t)(c0 + across) * P + p0 + along;
+            float u[V];
+            load_part<V>(x + e, n, u);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int h = XLAST ? j : i;
+                const float d = XLAST ? tile[(along + j) * ld + across] : tile[across * ld + along + j];
+                const float xh = (u[j] - m[h]) * k[h];
+                const float g = slope_times<ACT>(d, xh, a[h], o[h]);
+                if (j < n) {
+                    sg[h] += g;
+                    sx[h] = fmaf(g, xh, sx[h]);
+                }
+            }
+        }
+    }
+    if constexpr (XLAST) {
+        // threads 2^lv apart hold the same channels
+        __syncthreads();
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) tile[(pass * kGnThreads + t) * V + j] = pass ? sx[j] : sg[j];
+        }
+        __syncthreads();
+        const int c = t, rows = kGnThreads >> lv, width = V << lv;
+        if (c < nc) {
+            float s = 0.0f, z = 0.0f;
+            for (int i = 0; i < rows; ++i) {
+                s += tile[i * width + c];
+                z += tile[kGnThreads * V + i * width + c];
+            }
+            part[(b * chunks + chunk) * C + c0 + c] = make_float2(s, z);
+        }
+    } else {
+        const int lanes = min(64, 1 << lv);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float s = sg[i], z = sx[i];
+            for (int h = lanes >> 1; h; h >>= 1) {
+                s += __shfl_xor(s, h, 64);
+                z += __shfl_xor(z, h, 64);
+            }
+            const int c = (i * kGnThreads + t) >> lv;
+            if ((t & (lanes - 1)) == 0 && c < nc) part[(b * C + c0 + c) * chunks + chunk] = make_float2(s, z);
+        }
+    }
+}
+
+// Channels last, any width: workgroup (item, chunk of positions), threads along
+// the channels; part[(b chunks + chunk) C + c].
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                 const float* __restrict__ w,
+                                                                 const float* __restrict__ bias,
+                                                                 const float* __restrict__ stats,
+                                                                 float2* __restrict__ part, int C, int P, int D,
+                                                                 int per, int chunks, int64_t blocks) {
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / chunks;
+    const int first = (int)(id % chunks) * per, last = min(first + per, P);
+    for (int c = threadIdx.x; c < C; c += kGnThreads) {
+        const float* st = stats + 2 * (b * (C / D) + c / D);
+        const float m = st[0], k = st[1], a = or_one(w, c), o = or_zero(bias, c);
+        float sg = 0.0f, sx = 0.0f;
+        for (int p = first; p < last; ++p) {
+            const int64_t e = (b * P + p) * C + c;
+            const float xh = ((float)x[e] - m) * k;
+            const float g = slope_times<ACT>((float)dy[e], xh, a, o);
+            sg += g;
+            sx = fmaf(g, xh, sx);
+        }
+        part[id * C + c] = make_float2(sg, sx);
+    }
+}
+
+// ---- joining the partial sums -----------------------------------------------------------
+// One wave a result: first (with gsum) the B G groups' (s1, s2), then the C
+// channels' gradients, each a sum over items and chunks.
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(const float2* __restrict__ part,
+                                                              const float* __restrict__ w, float2* __restrict__ gsum,
+                                                              float* __restrict__ gw, float* __restrict__ gb, int64_t B,
+                                                              int C, int D, int chunks, bool last, float inv_n,
+                                                              int64_t ngroups) {
+    const int64_t i = block_id() * (kGnThreads / 64) + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    float s = 0.0f, z = 0.0f;
+    if (i < ngroups) {
+        const int64_t b = i / (C / D);
+        const int c0 = (int)(i % (C / D)) * D;
+        for (int64_t k = lane; k < (int64_t)D * chunks; k += 64) {
+            const int d = last ? (int)(k % D) : (int)(k / chunks), ch = last ? (int)(k / D) : (int)(k % chunks);
+            const float2 q = part[last ? (b * chunks + ch) * C + c0 + d : (b * C + c0 + d) * chunks + ch];
+            const float wc = or_one(w, c0 + d);
+            s = fmaf(wc, q.x, s);
+            z = fmaf(wc, q.y, z);
+        }
+        s = wave_sum(s);
+        z = wave_sum(z);
+        if (lane == 0) gsum[i] = make_float2(s * inv_n, z * inv_n);
+    } else if (i < ngroups + C) {
+        const int64_t c = i - ngroups;
+        for (int64_t k = lane; k < B * chunks; k += 64) {
+            const float2 q = part[last ? k * C + c : (k / chunks * C + c) * chunks + k % chunks];
+            s += q.x;
+            z += q.y;
+        }
+        s = wave_sum(s);
+        z = wave_sum(z);
+        if (lane == 0) {
+            if (gb) gb[c] = s;
+            if (gw) gw[c] = z;
+        }
+    }
+}
+
+// ---- grad_x --------------------------------------------------------------------------------
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_apply_last(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                 const float* __restrict__ w,
+                                                                 const float* __restrict__ bias,
+                                                                 const float* __restrict__ stats,
+                                                                 const float2* __restrict__ gsum, TX* __restrict__ gx,
+                                                                 LastRows r, int per, int chunks, int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / chunks;
+    const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
+    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    if (row >= r.q) return;
+    const int64_t base = b * r.P * r.C + slot * V;
+    const float* st = stats + 2 * b * (r.C / r.D);
+    const float2* gs = gsum + b * (r.C / r.D);
+    float m[V], k[V], a[V], o[V], s1[V], s2[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (slot * V + j) % r.C, g = c / r.D;
+        m[j] = st[2 * g];
+        k[j] = st[2 * g + 1];
+        a[j] = or_one(w, c);
+        o[j] = or_zero(bias, c);
+        s1[j] = gs[g].x;
+        s2[j] = gs[g].y;
+    }
+    for (int s = first + row; s < last; s += r.q) {
+        float u[V], v[V];
+        const int n = last_valid<V>(r, s, slot);
+        const int64_t e = base + (int64_t)s * r.stride();
+        load_part<V>(x + e, n, u);
+        load_part<V>(dy + e, n, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = (u[j] - m[j]) * k[j];
+            const float g = slope_times<ACT>(v[j], xh, a[j], o[j]);
+            u[j] = k[j] * (fmaf(g, a[j], -s1[j]) - xh * s2[j]);
+        }
+        store_part(gx + e, n, u);
+    }
+}
+
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_first(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                   const float* __restrict__ w,
+                                                                   const float* __restrict__ bias,
+                                                                   const float* __restrict__ stats,
+                                                                   const float2* __restrict__ gsum,
+                                                                   TX* __restrict__ gx, FirstRows r, int C, int D,
+                                                                   int64_t blocks) {
+    constexpr int V = kVec<TX>;
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t row = id / r.chunks * (kGnThreads / r.team) + threadIdx.x / r.team;
+    if (row >= r.rows) return;
+    const int at = (int)(id % r.chunks) * r.piece, end = min(at + r.piece, r.P);
+    const int c = (int)(row % C);
+    const float* st = stats + 2 * (row / D);
+    const float2 gs = gsum[row / D];
+    const float m = st[0], k = st[1], a = or_one(w, c), o = or_zero(bias, c);
+    const int64_t base = row * r.P;
+    for (int p = at + (threadIdx.x & (r.team - 1)) * V; p < end; p += r.team * V) {
+        float u[V], v[V];
+        const int n = min(V, end - p);
+        load_part<V>(x + base + p, n, u);
+        load_part<V>(dy + base + p, n, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = (u[j] - m) * k;
+            const float g = slope_times<ACT>(v[j], xh, a, o);
+            u[j] = k * (fmaf(g, a, -gs.x) - xh * gs.y);
+        }
+        store_part(gx + base + p, n, u);
+    }
+}
+
+template <int ACT, bool XLAST, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_cross(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                   const float* __restrict__ w,
+                                                                   const float* __restrict__ bias,
+                                                                   const float* __restrict__ stats,
+                                                                   const float2* __restrict__ gsum,
+                                                                   TX* __restrict__ gx, Tiles q, int C, int P, int D,
+                                                                   int64_t blocks) {
+    constexpr int V = kVec<TX>, N = kTile / V / kGnThreads;
+    __shared__ float tile[kTileLds];
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / q.tiles_c / q.tiles_p;
+    const int r0 = (int)(id % ((int64_t)q.tiles_c * q.tiles_p));
+    const int c0 = r0 % q.tiles_c << q.log2c, p0 = r0 / q.tiles_c * q.tp();
+    const int ld = q.tp() + 1, t = threadIdx.x;
+    const int nc = min(q.tc(), C - c0), np = min(q.tp(), P - p0);
+    const int lv = (XLAST ? q.log2c : 12 - q.log2c) - (V == 4 ? 2 : 3);
+    const float* st = stats + 2 * b * (C / D);
+    const float2* gs = gsum + b * (C / D);
+    const int64_t item = b * (int64_t)P * C;
+    load_turned(dy, tile, q, !XLAST, item, c0, p0, nc, np, C, P);
+    constexpr int S = XLAST ? V : N;
+    float m[S], k[S], a[S], o[S], s1[S], s2[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const int c = XLAST ? (t & ((1 << lv) - 1)) * V + j : (j * kGnThreads + t) >> lv;
+        const int ch = min(c0 + c, C - 1), g = ch / D;
+        m[j] = st[2 * g];
+        k[j] = st[2 * g + 1];
+        a[j] = or_one(w, ch);
+        o[j] = or_zero(bias, ch);
+        s1[j] = gs[g].x;
+        s2[j] = gs[g].y;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = i * kGnThreads + t;
+        const int along = (v & ((1 << lv) - 1)) * V, across = v >> lv;
+        const int n = XLAST ? (across < np ? max(0, min(V, nc - along)) : 0)
+                            : (across < nc ? max(0, min(V, np - along)) : 0);
+        const int64_t e = XLAST ? item + (int64_t)(p0 + across) * C + c0 + along
+                                : item + (int64_t)(c0 + across) * P + p0 + along;
+        float u[V];
+        load_part<V>(x + e, n, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int h = XLAST ? j : i;
+            const float d = XLAST ? tile[(along + j) * ld + across] : tile[across * ld + along + j];
+            const float xh = (u[j] - m[h]) * k[h];
+            const float g = slope_times<ACT>(d, xh, a[h], o[h]);
+            u[j] = k[h] * (fmaf(g, a[h], -s1[h]) - xh * s2[h]);
+        }
+        store_part(gx + e, n, u);
+    }
+}
+
+template <int ACT, typename TX, typename TY>
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_wide(const TX* __restrict__ x, const TY* __restrict__ dy,
+                                                                  const float* __restrict__ w,
+                                                                  const float* __restrict__ bias,
+                                                                  const float* __restrict__ stats,
+                                                                  const float2* __restrict__ gsum,
+                                                                  TX* __restrict__ gx, int C, int P, int D,
+                                                                  int64_t blocks) {
+    const int64_t id = block_id();
+    if (id >= blocks) return;
+    const int64_t b = id / P;
+    for (int c = threadIdx.x; c < C; c += kGnThreads) {
+        const int64_t g = b * (C / D) + c / D, e = id * C + c;
+        const float k = stats[2 * g + 1], a = or_one(w, c);
+        const float xh = ((float)x[e] - stats[2 * g]) * k;
+        const float v = slope_times<ACT>((float)dy[e], xh, a, or_zero(bias, c));
+        gx[e] = (TX)(k * (fmaf(v, a, -gsum[g].x) - xh * gsum[g].y));
+    }
+}
+
+// ---- schedules ------------------------------------------------------------------------------
+enum How { kFusedLast, kFusedFirst, kSplitLast, kSplitFirst, kCross, kWide };
+struct Plan {
+    How how;
+    bool last;                    // layout of the partial sums
+    LastRows rows;
+    FirstRows frows;
+    Tiles tiles;
+    int slices, threads, per, chunks;
+    size_t lds;
+};
+
+Plan plan_backward(const GroupNorm& g) {
+    const int V = vec_of(g);
+    const int64_t D = g.C / g.groups, n = D * g.P;
+    const int64_t capacity = (int64_t)kFusedThreads * kHeld;      // vectors
+    Plan p{};
+    p.chunks = 1;
+    const bool same = g.x_last == g.out_last || g.P == 1;
+    p.last = g.x_last || g.P == 1;
+    if (!same) {
+        p.how = kCross;
+        p.tiles = tiles_of(g.C, g.P);
+        split_chunks(g.B * p.tiles.tiles_c, p.tiles.tiles_p, 1, 32, &p.per, &p.chunks);
+        return p;
+    }
+    if (!p.last) {
+        const int64_t vectors = (n + V - 1) / V;
+        p.lds = (size_t)vectors * sizeof(float2) * (g.P % V ? 2 : 1) + sizeof(float) * (size_t)(2 * D + 2);
+        if (g.P >= V && vectors <= capacity && p.lds <= kLdsMax) {
+            p.how = kFusedFirst;
+            p.threads = 64;
+            while (p.threads < kFusedThreads && p.threads * kHeld < vectors) p.threads *= 2;
+            return p;
+        }
+        p.how = kSplitFirst;
+        p.frows = first_rows(g.B * g.C, g.P, V, 16);
+        p.chunks = p.frows.chunks;
+        return p;
+    }
+    if (!last_rows_ok(g.C, V)) {
+        p.how = kWide;
+        split_chunks(g.B, g.P, 1, 256, &p.per, &p.chunks);
+        return p;
+    }
+    // the narrowest slice of whole groups that is a run of 64 bytes or more, or the whole rows
+    int64_t cs = D;
+    while (cs < g.C && (g.C % cs != 0 || cs % V != 0 || cs * 16 / V < 64)) cs += D;
+    const LastRows r = last_rows(g.C, cs, D, g.P, V, kGnThreads);
+    if ((int64_t)r.ns * r.cv <= capacity) {
+        int threads = 64;
+        while (threads < kFusedThreads && (threads < r.cv || (int64_t)(threads / r.cv) * kHeld < r.ns)) threads *= 2;
+        p.rows = last_rows(g.C, cs, D, g.P, V, threads);
+        p.lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * cs + 2 * (cs / D));
+        if ((int64_t)p.rows.q * kHeld >= p.rows.ns && p.rows.threads <= kFusedThreads && p.lds <= kLdsMax) {
+            p.how = kFusedLast;
+            p.slices = (int)(g.C / cs);
+            return p;
+        }
+    }
+    p.how = kSplitLast;
+    p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
+    split_chunks(g.B, p.rows.ns, 4 * p.rows.q, 64 * p.rows.q, &p.per, &p.chunks);
+    p.lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * g.C);
+    return p;
+}
+
+bool fused(const Plan& p) { return p.how == kFusedLast || p.how == kFusedFirst; }
+
+}  // namespace
+
+size_t gn_backward_workspace(const GroupNorm& g) {
+    return sizeof(float2) * (size_t)(g.B * g.C * plan_backward(g).chunks + g.B * g.groups);
+}
+
+int gn_backward_kernels(const GroupNorm& g, bool need_x, bool need_w, const char** names) {
+    const Plan p = plan_backward(g);
+    int k = 0;
+    names[k++] = fused(p) ? "gn_bwd_fused" : p.how == kCross ? "gn_bwd_sums_cross" : "gn_bwd_sums";
+    if (need_w || !fused(p)) names[k++] = "gn_bwd_finish";
+    if (need_x && !fused(p)) names[k++] = p.how == kCross ? "gn_bwd_apply_cross" : "gn_bwd_apply";
+    return k;
+}
+
+hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int kernel, hipStream_t s) {
+    const Plan p = plan_backward(g);
+    const int D = (int)(g.C / g.groups), C = (int)g.C, P = (int)g.P;
+    const int64_t runs = g.B * g.groups;
+    float2* part = static_cast<float2*>(a.ws);
+    float2* gsum = part + g.B * g.C * p.chunks;
+    if (kernel == 1) {
+        const bool need_groups = !fused(p) && a.grad_x, need_w = a.grad_weight || a.grad_bias;
+        const int64_t ngroups = need_groups ? runs : 0, results = ngroups + (need_w ? C : 0);
+        return launch_kernel(k_gn_bwd_finish, grid_of((results + 3) / 4), dim3(kGnThreads), 0, s, (const float2*)part,
+                             a.weight, gsum, a.grad_weight, a.grad_bias, g.B, C, D, p.chunks, p.last,
+                             1.0f / ((float)D * (float)P), ngroups);
+    }
+    return with_types(g, [&](auto tx, auto ty) {
+        using TX = decltype(tx);
+        using TY = decltype(ty);
+        const TX* x = static_cast<const TX*>(a.x);
+        const TY* dy = static_cast<const TY*>(a.out);
+        const float* stats = a.stats;
+        TX* gx = static_cast<TX*>(a.grad_x);
+        return with_act(g.act, [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
+            if (fused(p)) {
+                float2* mine = a.grad_weight || a.grad_bias ? part : nullptr;
+                if (p.how == kFusedLast) {
+                    const int64_t blocks = g.B * p.slices;
+                    return launch_kernel(k_gn_bwd_fused_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), p.lds,
+                                         s, x, dy, a.weight, a.bias, stats, gx, mine, p.rows, p.slices, blocks);
+                }
+                return launch_kernel(k_gn_bwd_fused_first<ACT, TX, TY>, grid_of(runs), dim3(p.threads), p.lds, s, x, dy,
+                                     a.weight, a.bias, stats, gx, mine, D, P, (int)g.groups, fast_div(P), runs);
+            }
+            if (kernel == 0) {
+                if (p.how == kSplitLast) {
+                    const int64_t blocks = g.B * p.chunks;
+                    return launch_kernel(k_gn_bwd_sums_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), p.lds,
+                                         s, x, dy, a.weight, a.bias, stats, part, p.rows, p.per, p.chunks, blocks);
+                }
+                if (p.how == kSplitFirst) {
+                    const int64_t blocks = first_blocks(p.frows);
+                    return launch_kernel(k_gn_bwd_sums_first<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
+                                         dy, a.weight, a.bias, stats, part, p.frows, C, D, blocks);
+                }
+                if (p.how == kWide) {
+                    const int64_t blocks = g.B * p.chunks;
+                    return launch_kernel(k_gn_bwd_sums_wide<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
+                                         dy, a.weight, a.bias, stats, part, C, P, D, p.per, p.chunks, blocks);
+                }
+                const int64_t blocks = g.B * p.chunks * p.tiles.tiles_c;
+                if (g.x_last)
+                    return launch_kernel(k_gn_bwd_sums_cross<ACT, true, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0,
+                                         s, x, dy, a.weight, a.bias, stats, part, p.tiles, C, P, D, p.per, p.chunks,
+                                         blocks);
+                return launch_kernel(k_gn_bwd_sums_cross<ACT, false, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s,
+                                     x, dy, a.weight, a.bias, stats, part, p.tiles, C, P, D, p.per, p.chunks, blocks);
+            }
+            const float2* gs = gsum;
+            if (p.how == kSplitLast) {
+                const int per = std::min(8 * p.rows.q, p.rows.ns), chunks = (p.rows.ns + per - 1) / per;
+                const int64_t blocks = g.B * chunks;
+                return launch_kernel(k_gn_bwd_apply_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), 0, s, x,
+                                     dy, a.weight, a.bias, stats, gs, gx, p.rows, per, chunks, blocks);
+            }
+            if (p.how == kSplitFirst) {
+                const FirstRows r = first_rows(g.B * g.C, g.P, kVec<TX>, 8);
+                const int64_t blocks = first_blocks(r);
+                return launch_kernel(k_gn_bwd_apply_first<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x, dy,
+                                     a.weight, a.bias, stats, gs, gx, r, C, D, blocks);
+            }
+            if (p.how == kWide) {
+                const int64_t blocks = g.B * g.P;
+                return launch_kernel(k_gn_bwd_apply_wide<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x, dy,
+                                     a.weight, a.bias, stats, gs, gx, C, P, D, blocks);
+            }
+            const int64_t blocks = g.B * p.tiles.tiles_c * p.tiles.tiles_p;
+            if (g.x_last)
+                return launch_kernel(k_gn_bwd_apply_cross<ACT, true, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s,
+                                     x, dy, a.weight, a.bias, stats, gs, gx, p.tiles, C, P, D, blocks);
+            return launch_kernel(k_gn_bwd_apply_cross<ACT, false, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
+                                 dy, a.weight, a.bias, stats, gs, gx, p.tiles, C, P, D, blocks);
+        });
+    });
+}
+
+// ---- both directions ---------------------------------------------------------------------------
+int group_norm_kernels(const GroupNorm& g, const GroupNormArgs& a, bool backward, const char** names) {
+    return backward ? gn_backward_kernels(g, a.grad_x, a.grad_weight || a.grad_bias, names)
+                    : gn_forward_kernels(g, names);
+}
+size_t group_norm_workspace(const GroupNorm& g) {
+    // either type's vector width: the query knows no type
+    size_t bytes = 256;
+    for (int type : {kTypeF32, kTypeF16})
+        for (bool x_last : {false, true})
+            for (bool out_last : {false, true}) {
+                GroupNorm h = g;
+                h.x_type = h.out_type = type;
+                h.x_last = x_last;
+                h.out_last = out_last;
+                bytes = std::max(bytes, std::max(gn_forward_workspace(h), gn_backward_workspace(h)));
+            }
+    return bytes;
+}
+hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s) {
+    return backward ? gn_backward_launch(g, a, kernel, s) : gn_forward_launch(g, a, kernel, s);
+}
+
+}  // namespace fno

@@ -312,8 +312,8 @@ struct GroupNormArgs {
     void* ws;
 };
 // A call is a list of kernels, launched one after the other.
-int group_norm_kernels(const GroupNorm& g, bool backward, bool need_x, const char** names);
-size_t group_norm_workspace(const GroupNorm& g);
+int group_norm_kernels(const GroupNorm& g, const GroupNormArgs& a, bool backward, const char** names);
+size_t group_norm_workspace(const GroupNorm& g);     // enough for either direction
 hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s);
 
 // ---- gradient norm and clipping (fno_gradnorm.hip) ----------------------------

@@ -341,8 +341,8 @@ int fno_linear_conv1d(const float* x, const void* wspec, float* out, int B, int 
  * arithmetic are float32, a 16-bit output is rounded once.  stats float32
  * [B][groups][2] receives (mean, rstd), which the backward call reads.
  *
- * eps must be positive and finite, C a multiple of groups, 1 <= B, C, P,
- * B C < 2^31.  Fields need the alignment of their elements only.  Nothing
+ * eps must be positive and finite, C a multiple of groups, 1 <= B,
+ * 1 <= C <= 2^24, 1 <= P <= 2^30, B C < 2^31, B C P <= 2^40.  Fields need the alignment of their elements only.  Nothing
  * written may overlap anything else (FNO_ERR_ALIAS).  A NaN or infinity
  * makes its group NaN, no other.
  *
