@@ -12,8 +12,11 @@ cannot be loaded, every call raises; there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
+import functools
+import math
 import os
 import threading
 
@@ -102,7 +105,7 @@ _SIGNATURES = {
     "fno_linear_conv2d": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "fno_linear_conv1d_prepare": (_I, [_P, _P, _I, _I, _I, _I, _P]),
     "fno_linear_conv1d": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
-    "fno_group_norm_workspace_size": (_S, [_I, _I, _I, _I]),
+    "fno_group_norm_workspace_size": (_S, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "fno_group_norm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _I, _I, _I, _P, _S, _P]),
     "fno_group_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _S, _P]),
     "fno_grad_norm_workspace_size": (_S, [_I]),
@@ -545,70 +548,90 @@ def fno_spectral_conv1d_backward(x, w, grad_out, modes: int, need_x: bool = True
 
 
 _ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
-_types = {}
+_types = {}         # torch dtype -> enum fno_type
 
 
-def _type_code(t, name, complex_too=False):
-    """The ABI's element type (enum fno_type) of a tensor."""
+def _element_types():
     if not _types:
         torch = _torch()
         _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.complex64: 3})
-    code = _types.get(t.dtype, -1)
-    if code < 0 or (code == 3 and not complex_too):
-        raise TypeError(f"{name} must be float32, bfloat16{', float16 or complex64' if complex_too else ' or float16'}"
-                        f", got {t.dtype}")
-    return code
+    return _types
 
 
-def _need_field(t, name, device=None):
-    torch = _torch()
+def _raw_stream(torch, index):
+    """The current stream's handle.  The calls below serve small tensors too, where building a
+    torch.cuda.Stream object for it (2 us) would be a fifth of the whole call."""
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _field_type(torch, t, name, device=None):
+    """Checks a field and returns its ABI element type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
+    code = _element_types().get(t.dtype, 3)
+    if code == 3:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a GPU device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return _type_code(t, name)
+    return code
 
 
-def _group_norm_args(x, groups, weight, bias, act, channels_last, out_channels_last):
-    torch = _torch()
-    x_type = _need_field(x, "x")
-    if x.dim() < 2:
-        raise ValueError(f"x must have a batch and a channel axis, got shape {tuple(x.shape)}")
-    if act not in _ACTIVATIONS:
-        raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, got {act!r}")
-    shape = tuple(x.shape)
-    c = shape[-1] if channels_last else shape[1]
-    grid = shape[1:-1] if channels_last else shape[2:]
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _need(t, torch.float32, 1, name)
-            if t.shape[0] != c or t.device != x.device:
-                raise ValueError(f"{name} must be [{c}] on {x.device}")
-    if out_channels_last is None:
-        out_channels_last = channels_last
-    out_shape = (shape[0],) + grid + (c,) if out_channels_last else (shape[0], c) + grid
-    p = 1
-    for n in grid:
-        p *= n
-    if shape[0] > 0x7fffffff or c > 0x7fffffff or p > 0x7fffffff:
-        raise ValueError(f"x is too large: shape {shape}")
-    # (B, C, P, groups), (act, x_last, out_last, x_type)
-    dims = (shape[0], c, p, int(groups))
-    return dims, (_ACTIVATIONS[act], int(bool(channels_last)), int(bool(out_channels_last)), x_type), out_shape
+def _f32_ptr(torch, t, shape, device, name):
+    """Address of a float32 tensor of the given shape (0 for None)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 torch tensor")
+    if t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
 
 
-def _group_norm_workspace(x, dims):
-    # from torch's allocator, on the current stream: every call, and every captured graph, has its own
-    return _torch().empty(max(1, int(lib().fno_group_norm_workspace_size(*dims))), dtype=_torch().uint8,
-                          device=x.device)
+@functools.lru_cache(maxsize=4096)
+def _group_norm_workspace_size(*key):
+    return int(lib().fno_group_norm_workspace_size(*key))
 
 
-def _opt(t):
-    return ctypes.c_void_p(t.data_ptr() if t is not None else 0)
+class _GroupNormCall:
+    """What the forward and the backward call have in common: checked sizes and options."""
+
+    __slots__ = ("device", "sizes", "options", "out_shape", "stats_shape", "weight", "bias", "x_type")
+
+    def __init__(self, torch, x, groups, weight, bias, act, channels_last, out_channels_last):
+        self.x_type = _field_type(torch, x, "x")
+        shape = x.shape
+        if len(shape) < 2:
+            raise ValueError(f"x must have a batch and a channel axis, got shape {tuple(shape)}")
+        code = _ACTIVATIONS.get(act, -1)
+        if code < 0:
+            raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, got {act!r}")
+        out_channels_last = channels_last if out_channels_last is None else out_channels_last
+        b = shape[0]
+        c = shape[-1] if channels_last else shape[1]
+        grid = shape[1:-1] if channels_last else shape[2:]
+        p = math.prod(grid)
+        if max(b, c, p) > 0x7fffffff:
+            raise ValueError(f"x is too large: shape {tuple(shape)}")
+        groups = int(groups)
+        self.device = device = x.device
+        self.weight = _f32_ptr(torch, weight, (c,), device, "weight")
+        self.bias = _f32_ptr(torch, bias, (c,), device, "bias")
+        self.sizes = (b, c, p, groups)
+        self.options = (code, 1 if channels_last else 0, 1 if out_channels_last else 0)
+        self.out_shape = (b, *grid, c) if out_channels_last else (b, c, *grid)
+        self.stats_shape = (b, max(groups, 0), 2)
+
+    def workspace(self, torch, backward):
+        """Scratch of this call alone (so calls on other streams and captured graphs share none), or None."""
+        size = _group_norm_workspace_size(*self.sizes, self.options[1], self.options[2], self.x_type, backward)
+        return torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
 
 
 def fno_group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: str = "none",
@@ -622,24 +645,24 @@ def fno_group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, ac
     float32 are optional; act is "none", "gelu" (the exact erf form) or "silu".  stats
     [B, groups, 2] float32 holds (mean, 1 / deviation) for fno_group_norm_backward."""
     torch = _torch()
-    dims, opts, out_shape = _group_norm_args(x, groups, weight, bias, act, channels_last, out_channels_last)
+    call = _GroupNormCall(torch, x, groups, weight, bias, act, channels_last, out_channels_last)
+    device = call.device
     if out is None:
-        out = torch.empty(out_shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        out = torch.empty(call.out_shape, dtype=x.dtype if out_dtype is None else out_dtype, device=device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    out_type = _need_field(out, "out", x.device)
-    if tuple(out.shape) != out_shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {out_shape}")
-    stats_shape = (dims[0], max(dims[3], 0), 2)
+    out_type = _field_type(torch, out, "out", device)
+    if out.shape != call.out_shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {call.out_shape}")
     if stats is None:
-        stats = torch.empty(stats_shape, dtype=torch.float32, device=x.device)
-    _need(stats, torch.float32, 3, "stats")
-    if tuple(stats.shape) != stats_shape or stats.device != x.device:
-        raise ValueError(f"stats must be {stats_shape} on {x.device}")
+        stats = torch.empty(call.stats_shape, dtype=torch.float32, device=device)
+    stats_ptr = _f32_ptr(torch, stats, call.stats_shape, device, "stats")
     with _on_device(x):
-        ws = _group_norm_workspace(x, dims)
-        _check(lib().fno_group_norm(_ptr(x), _opt(weight), _opt(bias), _ptr(out), _ptr(stats), *dims, eps, *opts,
-                                    out_type, _ptr(ws), ws.numel(), _stream_ptr(x.device)), "fno_group_norm")
+        ws = call.workspace(torch, 0)
+        _check(lib().fno_group_norm(x.data_ptr(), call.weight, call.bias, out.data_ptr(), stats_ptr, *call.sizes, eps,
+                                    *call.options, call.x_type, out_type, 0 if ws is None else ws.data_ptr(),
+                                    0 if ws is None else ws.numel(), _raw_stream(torch, device.index)),
+               "fno_group_norm")
     return out, stats
 
 
@@ -650,84 +673,85 @@ def fno_group_norm_backward(x, stats, grad_out, groups: int, weight=None, bias=N
     and options, and grad_out of its output's layout and type.  need_x / need_w choose the field's and the
     parameters' gradients; those not asked for, or of a parameter that is None, are returned as None."""
     torch = _torch()
-    dims, opts, out_shape = _group_norm_args(x, groups, weight, bias, act, channels_last, out_channels_last)
-    out_type = _need_field(grad_out, "grad_out", x.device)
-    if tuple(grad_out.shape) != out_shape:
-        raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, expected {out_shape}")
-    _need(stats, torch.float32, 3, "stats")
-    if tuple(stats.shape) != (dims[0], dims[3], 2) or stats.device != x.device:
-        raise ValueError(f"stats must be {(dims[0], dims[3], 2)} on {x.device}")
+    call = _GroupNormCall(torch, x, groups, weight, bias, act, channels_last, out_channels_last)
+    device = call.device
+    out_type = _field_type(torch, grad_out, "grad_out", device)
+    if grad_out.shape != call.out_shape:
+        raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, expected {call.out_shape}")
+    if stats is None:
+        raise ValueError("stats must be what fno_group_norm returned")
+    stats_ptr = _f32_ptr(torch, stats, call.stats_shape, device, "stats")
     if not (need_x or (need_w and (weight is not None or bias is not None))):
         raise ValueError("ask for at least one gradient")
-
-    def target(given, like, wanted, name):
-        if not wanted or like is None:
-            return None
-        if given is None:
-            return torch.empty_like(like)
-        _need(given, like.dtype, like.dim(), name)
-        if given.shape != like.shape or given.device != like.device:
-            raise ValueError(f"{name} must match {tuple(like.shape)} on {like.device}")
-        return given
-
-    gx = target(grad_x, x, need_x, "grad_x")
-    gw = target(grad_weight, weight, need_w, "grad_weight")
-    gb = target(grad_bias, bias, need_w, "grad_bias")
+    gx = gw = gb = None
+    if need_x:
+        gx = torch.empty_like(x) if grad_x is None else grad_x
+        if _field_type(torch, gx, "grad_x", device) != call.x_type or gx.shape != x.shape:
+            raise ValueError(f"grad_x must match {tuple(x.shape)} {x.dtype}")
+    if need_w and weight is not None:
+        gw = torch.empty_like(weight) if grad_weight is None else grad_weight
+    if need_w and bias is not None:
+        gb = torch.empty_like(bias) if grad_bias is None else grad_bias
+    channels = (call.sizes[1],)
+    gw_ptr = _f32_ptr(torch, gw, channels, device, "grad_weight")
+    gb_ptr = _f32_ptr(torch, gb, channels, device, "grad_bias")
     with _on_device(x):
-        ws = _group_norm_workspace(x, dims)
-        _check(lib().fno_group_norm_backward(_ptr(x), _opt(weight), _opt(bias), _ptr(stats), _ptr(grad_out), _opt(gx),
-                                             _opt(gw), _opt(gb), *dims, *opts, out_type, _ptr(ws), ws.numel(),
-                                             _stream_ptr(x.device)), "fno_group_norm_backward")
+        ws = call.workspace(torch, 1)
+        _check(lib().fno_group_norm_backward(x.data_ptr(), call.weight, call.bias, stats_ptr, grad_out.data_ptr(),
+                                             0 if gx is None else gx.data_ptr(), gw_ptr, gb_ptr, *call.sizes,
+                                             *call.options, call.x_type, out_type, 0 if ws is None else ws.data_ptr(),
+                                             0 if ws is None else ws.numel(), _raw_stream(torch, device.index)),
+               "fno_group_norm_backward")
     return gx, gw, gb
 
 
-def _tensor_table(tensors, name):
-    """Host arrays (pointers, element counts, types) of a list of tensors, and their device."""
-    torch = _torch()
+def _tensor_table(torch, tensors, name):
+    """Host arrays (addresses, element counts, types) of a list of tensors, and their device.  Attribute by
+    attribute over the whole list: a model has hundreds of gradients, and this is most of a call's host time."""
     tensors = list(tensors)
-    n = len(tensors)
-    device = tensors[0].device if n and isinstance(tensors[0], torch.Tensor) else None
-    types = []
-    for t in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be torch tensors")
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"{name} must live on one GPU device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        types.append(_type_code(t, name, complex_too=True))
-        if types[-1] == 3 and t.is_conj():
-            raise ValueError(f"{name} must not be lazily conjugated (call resolve_conj())")
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-    numels = (ctypes.c_longlong * n)(*[t.numel() for t in tensors])
-    if device is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    return tensors, ptrs, numels, (ctypes.c_int * n)(*types), device
+    if not tensors:
+        return tensors, array.array("Q"), array.array("q"), array.array("i"), \
+            torch.device("cuda", torch.cuda.current_device())
+    if not all([isinstance(t, torch.Tensor) for t in tensors]):
+        raise TypeError(f"{name} must be torch tensors")
+    index = tensors[0].get_device()
+    if index < 0 or not all([t.get_device() == index for t in tensors]):
+        raise ValueError(f"{name} must live on one GPU device")
+    codes = _element_types()
+    try:
+        types = array.array("i", [codes[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise TypeError(f"{name} must be float32, bfloat16, float16 or complex64, got {e.args[0]}") from None
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous")
+    if 3 in types and any(t.is_conj() for t, k in zip(tensors, types) if k == 3):
+        raise ValueError(f"{name} must not be lazily conjugated (call resolve_conj())")
+    return (tensors, array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]),
+            types, tensors[0].device)
 
 
-def _norm_scalar(norm, device, name):
-    torch = _torch()
+def _norm_scalar(torch, norm, device, name):
     if norm is None:
         return torch.empty((), dtype=torch.float32, device=device)
-    _need(norm, torch.float32, 0, name)
-    if norm.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    _f32_ptr(torch, norm, (), device, name)
     return norm
 
 
-def _grad_workspace(count, device):
-    return _torch().empty(int(lib().fno_grad_norm_workspace_size(count)), dtype=_torch().uint8, device=device)
+def _grad_workspace(torch, count, device):
+    return torch.empty(int(lib().fno_grad_norm_workspace_size(count)), dtype=torch.uint8, device=device)
 
 
 def fno_grad_norm(grads, out=None):
     """Euclidean norm of all values of a list of gradients (float32, bfloat16, float16, complex64, mixed):
     a float32 scalar on their device."""
-    grads, ptrs, numels, types, device = _tensor_table(grads, "grads")
-    out = _norm_scalar(out, device, "out")
+    torch = _torch()
+    grads, ptrs, numels, types, device = _tensor_table(torch, grads, "grads")
+    out = _norm_scalar(torch, out, device, "out")
     with _on_device(out):
-        ws = _grad_workspace(len(grads), device)
-        _check(lib().fno_grad_norm(ptrs, numels, types, len(grads), _ptr(out), _ptr(ws), ws.numel(),
-                                   _stream_ptr(device)), "fno_grad_norm")
+        ws = _grad_workspace(torch, len(grads), device)
+        _check(lib().fno_grad_norm(ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], len(grads),
+                                   out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(torch, device.index)),
+               "fno_grad_norm")
     return out
 
 
@@ -735,23 +759,26 @@ def fno_clip_grad_norm(grads, max_norm: float, norm=None, out=None):
     """Scale a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out`
     (of the same shapes and types); returns their norm, a float32 scalar on their device.  `norm`, if given,
     is used as the norm (one reduced over several GPUs, say) and returned.  Nothing is copied to the host."""
-    grads, ptrs, numels, types, device = _tensor_table(grads, "grads")
+    torch = _torch()
+    grads, ptrs, numels, types, device = _tensor_table(torch, grads, "grads")
     outs = ptrs
     if out is not None:
-        out, outs, _, out_types, out_device = _tensor_table(out, "out")
-        if len(out) != len(grads) or any(o.shape != g.shape for o, g in zip(out, grads)):
+        out, outs, _, out_types, out_device = _tensor_table(torch, out, "out")
+        if len(out) != len(grads) or not all([o.shape == g.shape for o, g in zip(out, grads)]):
             raise ValueError("out must hold a tensor of each gradient's shape")
-        if any(a != b for a, b in zip(out_types, types)):
+        if out_types != types:
             raise TypeError("out must have the gradients' types")
         if out_device != device:
             raise ValueError(f"out must be on {device}")
     given = norm is not None
-    norm = _norm_scalar(norm, device, "norm")
+    norm = _norm_scalar(torch, norm, device, "norm")
     with _on_device(norm):
-        ws = _grad_workspace(len(grads), device)
-        _check(lib().fno_clip_grad_norm(ptrs, outs, numels, types, len(grads), max_norm,
-                                        _ptr(norm) if given else None, None if given else _ptr(norm), _ptr(ws),
-                                        ws.numel(), _stream_ptr(device)), "fno_clip_grad_norm")
+        ws = _grad_workspace(torch, len(grads), device)
+        at = norm.data_ptr()
+        _check(lib().fno_clip_grad_norm(ptrs.buffer_info()[0], outs.buffer_info()[0], numels.buffer_info()[0],
+                                        types.buffer_info()[0], len(grads), max_norm, at if given else 0,
+                                        0 if given else at, ws.data_ptr(), ws.numel(),
+                                        _raw_stream(torch, device.index)), "fno_clip_grad_norm")
     return norm
 
 

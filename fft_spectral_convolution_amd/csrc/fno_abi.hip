@@ -1118,7 +1118,8 @@ int group_norm_common(const GroupNorm& g, const GroupNormArgs& a, bool backward,
     if (backward ? any_overlap({{a.grad_x, xb}, {a.grad_weight, cbytes}, {a.grad_bias, cbytes}, ws}, {x, w, b, st, o})
                  : any_overlap({o, st, ws}, {x, w, b}))
         return FNO_ERR_ALIAS;
-    if (!a.ws || ws_bytes < group_norm_workspace(g)) return FNO_ERR_WORKSPACE;
+    const size_t need = group_norm_workspace(g, backward);
+    if (need && (!a.ws || ws_bytes < need)) return FNO_ERR_WORKSPACE;
     if (off_grain(a.ws, 256)) return FNO_ERR_ALIGN;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     auto run = [&]() -> int {
@@ -1516,9 +1517,11 @@ int fno_inverse1d(const void* yh, float* out, int B, int C, int N, int modes, vo
     return rec_end(hs, e == hipSuccess ? FNO_OK : hip_fail(e));
 }
 
-size_t fno_group_norm_workspace_size(int B, int C, int P, int groups) {
-    const GroupNorm g{B, C, P, groups, 0.0f, FNO_ACT_NONE, false, false, FNO_F32, FNO_F32};
-    return check_group_norm(g) == FNO_OK ? group_norm_workspace(g) : 0;
+size_t fno_group_norm_workspace_size(int B, int C, int P, int groups, int x_last, int out_last, int x_type,
+                                     int backward) {
+    if ((x_last & ~1) || (out_last & ~1) || (backward & ~1)) return 0;
+    const GroupNorm g{B, C, P, groups, 0.0f, FNO_ACT_NONE, x_last != 0, out_last != 0, x_type, x_type};
+    return check_group_norm(g) == FNO_OK ? group_norm_workspace(g, backward != 0) : 0;
 }
 
 int fno_group_norm(const void* x, const float* weight, const float* bias, void* out, float* stats, int B, int C, int P,

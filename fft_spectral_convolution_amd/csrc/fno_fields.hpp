@@ -93,10 +93,50 @@ __device__ __forceinline__ float act_slope(float z) {
     return 1.0f;
 }
 
-// ---- block sums -----------------------------------------------------------------
-// Sum over a wave in a fixed order, the same value in every lane.
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
+// ---- sums over lanes and blocks ---------------------------------------------------
+// Adding across a wave takes one or two vector instructions a step: data
+// moved within rows of 16 lanes by DPP, across them by the lane swaps (a
+// shuffle through LDS costs ten times that, which small calls feel).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+constexpr int kDppXor1 = 0xb1, kDppXor2 = 0x4e, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+// v plus the value of the lane 16 or 32 away: the swap exchanges the odd rows
+// (halves) of one register with the even ones of the other.  The results are
+// copied out before they are read as floats: a bit cast of a vector's element
+// itself reads the first one.
+template <int N>
+__device__ __forceinline__ float swap_add(float v) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    uint32_t x, y;
+    if constexpr (N == 16) {
+        const auto q = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+        x = q[0];
+        y = q[1];
+    } else {
+        const auto q = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+        x = q[0];
+        y = q[1];
+    }
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Sum over the lanes of each aligned team of `parts` (a power of two, at most
+// 64, the same in every lane), in every lane.
+__device__ __forceinline__ float team_sum(float v, int parts) {
+    if (parts > 1) v += dpp<kDppXor1>(v);
+    if (parts > 2) v += dpp<kDppXor2>(v);
+    if (parts > 4) v += dpp<kDppHalfMirror>(v);      // lanes of a quad hold the same value by now
+    if (parts > 8) v += dpp<kDppMirror>(v);
+    if (parts > 16) v = swap_add<16>(v);
+    if (parts > 32) v = swap_add<32>(v);
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) { return team_sum(v, 64); }
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
     return v;
@@ -114,5 +154,13 @@ __device__ __forceinline__ T block_sum(T v, T* red) {
     for (int i = 1; i < nw; ++i) s += red[i];
     return s;
 }
+
+// Quotient by a small divisor without a division: exact for n d < 2^32.
+struct FastDiv {
+    uint32_t d, m;
+};
+inline FastDiv fast_div(int d) { return FastDiv{(uint32_t)d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) { return f.m ? (int)__umulhi((uint32_t)n, f.m) : n; }
+__device__ __forceinline__ int mod_by(int n, const FastDiv& f) { return n - div_by(n, f) * (int)f.d; }
 
 }  // namespace fno

@@ -31,11 +31,11 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
     if (id >= blocks) return;
     float* buf = lds;
     float* mean = lds + r.threads * V;
-    const int groups = r.cs / r.D;
+    const int groups = div_by(r.cs, r.by_D);
     float* rstd = mean + groups;
     const int64_t b = id / slices;
     const int c0 = (int)(id % slices) * r.cs;
-    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
     const bool on = row < r.q;
     const int64_t base = b * r.P * r.C + c0 + slot * V;
     const float n_group = (float)r.P * (float)r.D, inv_n = 1.0f / n_group;
@@ -51,11 +51,17 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
     for (int i = 0; i < kHeld; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] += held[i][j];
-    last_sums(sum, buf, mean, r, r.D);
-    float m[V];
+    float m[V], a[V], o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        m[j] = mean[(slot * V + j) % r.cs / r.D] / n_group;
+        const int c = c0 + mod_by(slot * V + j, r.by_cs);
+        a[j] = or_one(w, c);
+        o[j] = or_zero(bias, c);
+    }
+    last_sums(sum, buf, mean, r, r.D);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        m[j] = mean[div_by(mod_by(slot * V + j, r.by_cs), r.by_D)] / n_group;
         sum[j] = 0.0f;
     }
 #pragma unroll
@@ -69,18 +75,14 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
     }
     last_sums(sum, buf, rstd, r, r.D);
     for (int g = t; g < groups; g += blockDim.x) {
-        float* st = stats + 2 * (b * (r.C / r.D) + c0 / r.D + g);
+        float* st = stats + 2 * (b * (div_by(r.C, r.by_D)) + div_by(c0, r.by_D) + g);
         st[0] = mean[g] / n_group;
         st[1] = rsqrtf(fmaf(rstd[g], inv_n, eps));
     }
     if (!on) return;
-    float a[V], o[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int c = (slot * V + j) % r.cs;
-        a[j] = rsqrtf(fmaf(rstd[c / r.D], inv_n, eps)) * or_one(w, c0 + c);
-        o[j] = or_zero(bias, c0 + c);
-    }
+    for (int j = 0; j < V; ++j)
+        a[j] *= rsqrtf(fmaf(rstd[div_by(mod_by(slot * V + j, r.by_cs), r.by_D)], inv_n, eps));
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int s = row + i * r.q, n = last_valid<V>(r, s, slot);
@@ -183,11 +185,11 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_stats_last(const TX* __restric
     if (id >= blocks) return;
     float* buf = lds;
     float* mean = lds + r.threads * V;
-    const int groups = r.C / r.D;
+    const int groups = div_by(r.C, r.by_D);
     float* sq = mean + groups;
     const int64_t b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
-    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
     const bool on = row < r.q;
     const TX* p = x + b * r.P * r.C + slot * V;
     // positions of this chunk
@@ -198,27 +200,28 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_stats_last(const TX* __restric
     int s = first + row;
     const int full = min(last, r.P / r.R);
     if (on && s < full) {
-        float v[V];
-        load_vec<V>(p + (int64_t)s * r.stride(), v);
+        // eight loads on their way at once; those past the end repeat the last and are not counted
+        bool fresh = true;
+        for (; s < full; s += 8 * r.q) {
+            Raw<TX, V> u[8];
 #pragma unroll
-        for (int j = 0; j < V; ++j) run[j] = Running{v[j], 0.0f, 0.0f};
-        cnt = 1.0f;
-        for (s += r.q; s + 3 * r.q < full; s += 4 * r.q) {
-            float u[4][V];
+            for (int i = 0; i < 8; ++i)
+                u[i].load(p + (int64_t)(s + i * r.q < full ? s + i * r.q : s) * r.stride(), V);
+            if (fresh) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_vec<V>(p + (int64_t)(s + i * r.q) * r.stride(), u[i]);
+                for (int j = 0; j < V; ++j) run[j].pivot = u[0][j];
+                fresh = false;
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
+                if (s + i * r.q < full) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) run[j].add(u[i][j]);
-            cnt += 4.0f;
+                    for (int j = 0; j < V; ++j) run[j].add(u[i][j]);
+                    cnt += 1.0f;
+                }
         }
-        for (; s < full; s += r.q) {
-            load_vec<V>(p + (int64_t)s * r.stride(), v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) run[j].add(v[j]);
-            cnt += 1.0f;
-        }
+        // where the loop would have gone next
+        s = first + row + (full - 1 - first - row) / r.q * r.q + r.q;
     }
     // the incomplete super-row: values that some of the vector's places lack
     float num[V];
@@ -239,7 +242,7 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_stats_last(const TX* __restric
     last_sums(val, buf, mean, r, r.D);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const float d = num[j] > 0.0f ? run[j].mean(num[j]) - mean[(slot * V + j) % r.C / r.D] / n : 0.0f;
+        const float d = num[j] > 0.0f ? run[j].mean(num[j]) - mean[div_by(mod_by(slot * V + j, r.by_cs), r.by_D)] / n : 0.0f;
         val[j] = num[j] > 0.0f ? fmaf(num[j] * d, d, run[j].squares(num[j])) : 0.0f;
     }
     last_sums(val, buf, sq, r, r.D);
@@ -328,14 +331,14 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_apply_last(const TX* __restric
     if (id >= blocks) return;
     const int64_t b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
-    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
     if (row >= r.q) return;
     const int64_t base = b * r.P * r.C + slot * V;
-    const float* st = stats + 2 * b * (r.C / r.D);
+    const float* st = stats + 2 * b * (div_by(r.C, r.by_D));
     float m[V], a[V], o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = (slot * V + j) % r.C, g = c / r.D;
+        const int c = mod_by(slot * V + j, r.by_cs), g = div_by(c, r.by_D);
         m[j] = st[2 * g];
         a[j] = st[2 * g + 1] * or_one(w, c);
         o[j] = or_zero(bias, c);

@@ -38,6 +38,7 @@ struct LastRows {
     int q;                 // super-rows a workgroup takes at a time
     int threads;           // cv q, rounded up to whole waves
     int ns;                // super-rows of an item
+    FastDiv by_cv, by_cs, by_D;
     __host__ __device__ int stride() const { return cs < C ? C : C * R; }   // elements from one to the next
 };
 
@@ -62,6 +63,9 @@ inline LastRows last_rows(int64_t C, int64_t cs, int64_t D, int64_t P, int V, in
     r.q = std::max(1, threads / r.cv);
     r.threads = (r.cv * r.q + 63) / 64 * 64;
     r.ns = (int)((P + r.R - 1) / r.R);
+    r.by_cv = fast_div(r.cv);
+    r.by_cs = fast_div(r.cs);
+    r.by_D = fast_div(r.D);
     return r;
 }
 
@@ -118,8 +122,8 @@ struct Raw {
 // Sums of `val` (V values a thread) over the rows of a workgroup's super-rows
 // and over `width` neighbouring channels: res[c / width].  width is D for
 // group sums, 1 for channel sums.  buf holds threads * V floats.  Lanes
-// `parts` at a time share a result and are added by shuffles, in an order
-// that depends on the sizes alone.  buf may be reused after the next barrier,
+// `parts` at a time share a result, in an order that depends on the sizes
+// alone.  buf may be reused after the next barrier,
 // res is complete on return.
 template <int V>
 __device__ __forceinline__ void last_sums(const float (&val)[V], float* buf, float* res, const LastRows& r, int width) {
@@ -130,18 +134,18 @@ __device__ __forceinline__ void last_sums(const float (&val)[V], float* buf, flo
         for (int j = 0; j < V; ++j) buf[t * V + j] = val[j];
     }
     __syncthreads();
-    const int count = r.cs / width, rows = r.q * r.R;
+    const FastDiv by_width = width == 1 ? FastDiv{1, 0} : r.by_D;
+    const int count = width == 1 ? r.cs : div_by(r.cs, r.by_D), entries = r.q * r.R * width;
     int parts = 1;
     while (parts < 64 && 2 * parts * count <= (int)blockDim.x) parts *= 2;
-    const int part = t & (parts - 1);
-    const int entries = rows * width;
-    for (int g = t / parts; g < count; g += (int)blockDim.x / parts) {
+    const int part = t & (parts - 1), step = (int)blockDim.x >> __builtin_ctz(parts);
+    for (int g = t >> __builtin_ctz(parts); g < count; g += step) {
         float s = 0.0f;
         for (int k = part; k < entries; k += parts) {
-            const int row = width == 1 ? k : k / width;
-            s += buf[row * r.cs + g * width + (width == 1 ? 0 : k - row * width)];
+            const int row = div_by(k, by_width);
+            s += buf[row * (r.cs - width) + g * width + k];
         }
-        for (int m = parts >> 1; m; m >>= 1) s += __shfl_xor(s, m, 64);
+        s = team_sum(s, parts);
         if (part == 0) res[g] = s;
     }
     __syncthreads();
@@ -178,13 +182,6 @@ inline int64_t first_blocks(const FirstRows& r) {
     const int per = kGnThreads / r.team;
     return (r.rows + per - 1) / per * r.chunks;
 }
-
-// Quotient by a small divisor without a division: exact for n d < 2^32.
-struct FastDiv {
-    uint32_t d, m;
-};
-inline FastDiv fast_div(int d) { return FastDiv{(uint32_t)d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
-__device__ __forceinline__ int div_by(int n, const FastDiv& f) { return f.m ? (int)__umulhi((uint32_t)n, f.m) : n; }
 
 // ---- one layout to the other ----------------------------------------------------
 // Tiles of 4096 values: 2^log2c channels times 4096 / 2^log2c positions,

@@ -38,10 +38,8 @@ __device__ __forceinline__ void group_means(const float* cg, const float* cx, co
             s1 = fmaf(wc, cg[g * D + d], s1);
             s2 = fmaf(wc, cx[g * D + d], s2);
         }
-        for (int m = parts >> 1; m; m >>= 1) {
-            s1 += __shfl_xor(s1, m, 64);
-            s2 += __shfl_xor(s2, m, 64);
-        }
+        s1 = team_sum(s1, parts);
+        s2 = team_sum(s2, parts);
         if ((t & (parts - 1)) == 0) {
             res[g] = s1;
             res[groups + g] = s2;
@@ -64,13 +62,13 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
     float* cg = lds + r.threads * V;
     float* cx = cg + r.cs;
     float* res = cx + r.cs;
-    const int groups = r.cs / r.D;
+    const int groups = div_by(r.cs, r.by_D);
     const int64_t b = id / slices;
     const int c0 = (int)(id % slices) * r.cs;
-    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
     const bool on = row < r.q;
     const int64_t base = b * r.P * r.C + c0 + slot * V;
-    const float* st = stats + 2 * (b * (r.C / r.D) + c0 / r.D);
+    const float* st = stats + 2 * (b * (div_by(r.C, r.by_D)) + div_by(c0, r.by_D));
 
     Raw<TX, V> hx[kHeld];
     Raw<TY, V> hy[kHeld];
@@ -84,9 +82,9 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
     float m[V], k[V], a[V], o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = (slot * V + j) % r.cs;
-        m[j] = st[2 * (c / r.D)];
-        k[j] = st[2 * (c / r.D) + 1];
+        const int c = mod_by(slot * V + j, r.by_cs);
+        m[j] = st[2 * (div_by(c, r.by_D))];
+        k[j] = st[2 * (div_by(c, r.by_D)) + 1];
         a[j] = or_one(w, c0 + c);
         o[j] = or_zero(bias, c0 + c);
     }
@@ -115,7 +113,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
     float s1[V], s2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int g = (slot * V + j) % r.cs / r.D;
+        const int g = div_by(mod_by(slot * V + j, r.by_cs), r.by_D);
         s1[j] = res[g] * inv_n;
         s2[j] = res[groups + g] * inv_n;
     }
@@ -202,10 +200,8 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
             s.x += q.x;
             s.y += q.y;
         }
-        for (int m = parts >> 1; m; m >>= 1) {
-            s.x += __shfl_xor(s.x, m, 64);
-            s.y += __shfl_xor(s.y, m, 64);
-        }
+        s.x = team_sum(s.x, parts);
+        s.y = team_sum(s.y, parts);
         if ((t & (parts - 1)) == 0) {
             cg[d] = s.x;
             cx[d] = s.y;
@@ -253,15 +249,15 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_sums_last(const TX* __rest
     float* cx = cg + r.C;
     const int64_t b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
-    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
     const int64_t base = b * r.P * r.C + slot * V;
-    const float* st = stats + 2 * b * (r.C / r.D);
+    const float* st = stats + 2 * b * (div_by(r.C, r.by_D));
     float m[V], k[V], a[V], o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = (slot * V + j) % r.C;
-        m[j] = st[2 * (c / r.D)];
-        k[j] = st[2 * (c / r.D) + 1];
+        const int c = mod_by(slot * V + j, r.by_cs);
+        m[j] = st[2 * (div_by(c, r.by_D))];
+        k[j] = st[2 * (div_by(c, r.by_D)) + 1];
         a[j] = or_one(w, c);
         o[j] = or_zero(bias, c);
     }
@@ -345,10 +341,8 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __re
         sg = block_sum(sg, red);
         sx = block_sum(sx, red);
     } else {
-        for (int q = r.team >> 1; q; q >>= 1) {
-            sg += __shfl_xor(sg, q, 64);
-            sx += __shfl_xor(sx, q, 64);
-        }
+        sg = team_sum(sg, r.team);
+        sx = team_sum(sx, r.team);
     }
     if ((threadIdx.x & (r.team - 1)) == 0 && row < r.rows) part[row * r.chunks + piece] = make_float2(sg, sx);
 }
@@ -464,11 +458,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
         const int lanes = min(64, 1 << lv);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float s = sg[i], z = sx[i];
-            for (int h = lanes >> 1; h; h >>= 1) {
-                s += __shfl_xor(s, h, 64);
-                z += __shfl_xor(z, h, 64);
-            }
+            const float s = team_sum(sg[i], lanes), z = team_sum(sx[i], lanes);
             const int c = (i * kGnThreads + t) >> lv;
             if ((t & (lanes - 1)) == 0 && c < nc) part[(b * C + c0 + c) * chunks + chunk] = make_float2(s, z);
         }
@@ -504,39 +494,54 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __res
 }
 
 // ---- joining the partial sums -----------------------------------------------------------
-// One wave a result: first (with gsum) the B G groups' (s1, s2), then the C
-// channels' gradients, each a sum over items and chunks.
+// First (with gsum) the B G groups' (s1, s2), a wave each; then the C channels'
+// gradients, a workgroup each, over items and chunks.  The partial sums come
+// from other XCDs' kernels and are far away (a microsecond), so a lane asks
+// for eight at a time.
+template <typename F>
+__device__ __forceinline__ void sum_parts(int64_t n, int first, int step, F&& at, float& s, float& z) {
+    for (int64_t k = first; k < n; k += 8 * step) {
+        float2 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = k + i * step < n ? at(k + i * step) : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s += q[i].x;
+            z += q[i].y;
+        }
+    }
+}
+
 __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(const float2* __restrict__ part,
                                                               const float* __restrict__ w, float2* __restrict__ gsum,
                                                               float* __restrict__ gw, float* __restrict__ gb, int64_t B,
                                                               int C, int D, int chunks, bool last, float inv_n,
                                                               int64_t ngroups) {
-    const int64_t i = block_id() * (kGnThreads / 64) + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
+    __shared__ float red[16];
+    const int64_t id = block_id(), gblocks = (ngroups + 3) / 4;
     float s = 0.0f, z = 0.0f;
-    if (i < ngroups) {
+    if (id < gblocks) {
+        const int64_t i = id * 4 + (threadIdx.x >> 6);
+        if (i >= ngroups) return;
         const int64_t b = i / (C / D);
         const int c0 = (int)(i % (C / D)) * D;
-        for (int64_t k = lane; k < (int64_t)D * chunks; k += 64) {
+        sum_parts((int64_t)D * chunks, threadIdx.x & 63, 64, [&](int64_t k) {
             const int d = last ? (int)(k % D) : (int)(k / chunks), ch = last ? (int)(k / D) : (int)(k % chunks);
             const float2 q = part[last ? (b * chunks + ch) * C + c0 + d : (b * C + c0 + d) * chunks + ch];
             const float wc = or_one(w, c0 + d);
-            s = fmaf(wc, q.x, s);
-            z = fmaf(wc, q.y, z);
-        }
+            return make_float2(wc * q.x, wc * q.y);
+        }, s, z);
         s = wave_sum(s);
         z = wave_sum(z);
-        if (lane == 0) gsum[i] = make_float2(s * inv_n, z * inv_n);
-    } else if (i < ngroups + C) {
-        const int64_t c = i - ngroups;
-        for (int64_t k = lane; k < B * chunks; k += 64) {
-            const float2 q = part[last ? k * C + c : (k / chunks * C + c) * chunks + k % chunks];
-            s += q.x;
-            z += q.y;
-        }
-        s = wave_sum(s);
-        z = wave_sum(z);
-        if (lane == 0) {
+        if ((threadIdx.x & 63) == 0) gsum[i] = make_float2(s * inv_n, z * inv_n);
+    } else if (id - gblocks < C) {
+        const int64_t c = id - gblocks;
+        sum_parts(B * chunks, threadIdx.x, kGnThreads, [&](int64_t k) {
+            return part[last ? k * C + c : (k / chunks * C + c) * chunks + k % chunks];
+        }, s, z);
+        s = block_sum(s, red);
+        z = block_sum(z, red);
+        if (threadIdx.x == 0) {
             if (gb) gb[c] = s;
             if (gw) gw[c] = z;
         }
@@ -556,15 +561,15 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_apply_last(const TX* __res
     if (id >= blocks) return;
     const int64_t b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
-    const int t = threadIdx.x, slot = t % r.cv, row = t / r.cv;
+    const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
     if (row >= r.q) return;
     const int64_t base = b * r.P * r.C + slot * V;
-    const float* st = stats + 2 * b * (r.C / r.D);
-    const float2* gs = gsum + b * (r.C / r.D);
+    const float* st = stats + 2 * b * (div_by(r.C, r.by_D));
+    const float2* gs = gsum + b * (div_by(r.C, r.by_D));
     float m[V], k[V], a[V], o[V], s1[V], s2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = (slot * V + j) % r.C, g = c / r.D;
+        const int c = mod_by(slot * V + j, r.by_cs), g = div_by(c, r.by_D);
         m[j] = st[2 * g];
         k[j] = st[2 * g + 1];
         a[j] = or_one(w, c);
@@ -792,8 +797,8 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
     float2* gsum = part + g.B * g.C * p.chunks;
     if (kernel == 1) {
         const bool need_groups = !fused(p) && a.grad_x, need_w = a.grad_weight || a.grad_bias;
-        const int64_t ngroups = need_groups ? runs : 0, results = ngroups + (need_w ? C : 0);
-        return launch_kernel(k_gn_bwd_finish, grid_of((results + 3) / 4), dim3(kGnThreads), 0, s, (const float2*)part,
+        const int64_t ngroups = need_groups ? runs : 0, blocks = (ngroups + 3) / 4 + (need_w ? C : 0);
+        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kGnThreads), 0, s, (const float2*)part,
                              a.weight, gsum, a.grad_weight, a.grad_bias, g.B, C, D, p.chunks, p.last,
                              1.0f / ((float)D * (float)P), ngroups);
     }
@@ -873,19 +878,8 @@ int group_norm_kernels(const GroupNorm& g, const GroupNormArgs& a, bool backward
     return backward ? gn_backward_kernels(g, a.grad_x, a.grad_weight || a.grad_bias, names)
                     : gn_forward_kernels(g, names);
 }
-size_t group_norm_workspace(const GroupNorm& g) {
-    // either type's vector width: the query knows no type
-    size_t bytes = 256;
-    for (int type : {kTypeF32, kTypeF16})
-        for (bool x_last : {false, true})
-            for (bool out_last : {false, true}) {
-                GroupNorm h = g;
-                h.x_type = h.out_type = type;
-                h.x_last = x_last;
-                h.out_last = out_last;
-                bytes = std::max(bytes, std::max(gn_forward_workspace(h), gn_backward_workspace(h)));
-            }
-    return bytes;
+size_t group_norm_workspace(const GroupNorm& g, bool backward) {
+    return backward ? gn_backward_workspace(g) : gn_forward_workspace(g);
 }
 hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s) {
     return backward ? gn_backward_launch(g, a, kernel, s) : gn_forward_launch(g, a, kernel, s);

@@ -347,12 +347,14 @@ int fno_linear_conv1d(const float* x, const void* wspec, float* out, int B, int 
  * makes its group NaN, no other.
  *
  * Scratch is the caller's: `workspace`, 256-byte aligned, at least
- * fno_group_norm_workspace_size bytes (0 for invalid sizes), free again when
- * the call's kernels have run.  Nothing is allocated, so the calls can be
+ * fno_group_norm_workspace_size bytes (backward: 1 for the backward call; 0
+ * where none is needed, NULL will do then, and for invalid arguments), free
+ * again when the call's kernels have run.  Nothing is allocated, so the calls can be
  * captured into graphs at any time; graphs that may run at the same time
  * need a workspace each.
  */
-size_t fno_group_norm_workspace_size(int B, int C, int P, int groups);
+size_t fno_group_norm_workspace_size(int B, int C, int P, int groups, int x_last, int out_last,
+                                     int x_type, int backward);
 int fno_group_norm(const void* x, const float* weight, const float* bias, void* out, float* stats,
                    int B, int C, int P, int groups, float eps, int act, int x_last, int out_last,
                    int x_type, int out_type, void* workspace, size_t ws_bytes, void* stream);

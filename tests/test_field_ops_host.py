@@ -39,14 +39,19 @@ def test_group_norm_sizes_and_options(lib, call):
     for dims in ((0, 8, 10, 4), (2, 0, 10, 4), (2, 8, 0, 4), (2, 8, 10, 0), (2, 8, 10, 3), (2, 8, 10, 16),
                  (-1, 8, 10, 4), (2, 8, -10, 4), (65536, 65536, 1, 1), (1 << 20, 1 << 10, 1 << 20, 1)):
         assert call(lib, dims=dims) == SHAPE, dims
-        assert fno.lib().fno_group_norm_workspace_size(*dims) == 0
+        assert lib.fno_group_norm_workspace_size(*dims, 1, 1, 0, 0) == 0
     assert call(lib, act=3) == VALUE and call(lib, act=-1) == VALUE
     assert call(lib, x_last=2) == VALUE and call(lib, out_last=-1) == VALUE
     assert call(lib, x_type=3) == VALUE and call(lib, x_type=-1) == VALUE
     assert call(lib, x_type=0, out_type=1) == VALUE          # float32 in, bfloat16 out
     assert call(lib, x_type=1, out_type=2) == VALUE
-    assert call(lib, ws=None) == WORKSPACE and call(lib, ws_bytes=8) == WORKSPACE
+    # float32 in the one layout, out or grad_out in the other: chunks' sums in the workspace
+    need = lib.fno_group_norm_workspace_size(2, 8, 10, 4, 1, 0, 0, int(call is back))
+    assert need > 0
+    assert call(lib, out_last=0, ws=None) == WORKSPACE and call(lib, out_last=0, ws_bytes=need - 1) == WORKSPACE
     assert call(lib, ws=WS + 16) == ALIGN
+    assert lib.fno_group_norm_workspace_size(2, 8, 10, 4, 1, 0, 3, 0) == 0
+    assert lib.fno_group_norm_workspace_size(2, 8, 10, 4, 2, 0, 0, 0) == 0
 
 
 def test_group_norm_eps(lib):
