@@ -1200,6 +1200,14 @@ int grad_norm_common(const void* const* grads, void* const* outs, const long lon
     auto run = [&]() -> int {
         GradTable t;
         int nparts = 0;
+        if (!given && count <= kGradTable) {
+            const uint32_t chunks = fill(t, 0);
+            if (chunks <= kGradSmallChunks) {
+                rec_kernel("grad_small", hs);
+                const hipError_t e = launch_grad_small(t, chunks, max_norm, outs != nullptr, norm, hs);
+                return e == hipSuccess ? FNO_OK : hip_fail(e);
+            }
+        }
         for (int at = 0; !given && at < count; at += kGradTable) {
             const uint32_t chunks = fill(t, at);
             if (!chunks) continue;

@@ -5,6 +5,8 @@
 // (kGradTable tensors a launch), cut into chunks of 16 KiB.  Squares are
 // summed in double: the square of a float neither overflows nor vanishes
 // there, and the norm of 10^9 values is as good as its inputs.
+#include <algorithm>
+
 #include "fno_fields.hpp"
 
 namespace fno {
@@ -28,33 +30,44 @@ __device__ __forceinline__ int tensor_of(const GradTable& t, uint32_t chunk) {
     return __builtin_amdgcn_readfirstlane(__popcll(lo) + __popcll(hi) - 1);
 }
 
+template <typename F>
+__device__ __forceinline__ void with_type(int type, F&& f) {
+    if (type == kTypeBf16) {
+        f(bf16{});
+    } else if (type == kTypeF16) {
+        f(f16{});
+    } else {
+        f(0.0f);          // complex values as pairs
+    }
+}
+
 template <typename T>
-__device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t n, int threads) {
+__device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t n, int t, int threads) {
     constexpr int V = 16 / sizeof(T);
     double s = 0.0;
     const int64_t nv = n / V;
-    for (int64_t i = threadIdx.x; i < nv; i += threads) {
+    for (int64_t i = t; i < nv; i += threads) {
         float v[V];
         load_vec<V>(p + i * V, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) s = fma((double)v[j], (double)v[j], s);
     }
-    for (int64_t i = nv * V + threadIdx.x; i < n; i += threads) s = fma((double)(float)p[i], (double)(float)p[i], s);
+    for (int64_t i = nv * V + t; i < n; i += threads) s = fma((double)(float)p[i], (double)(float)p[i], s);
     return s;
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_by(const T* p, T* q, int64_t n, float coef, int threads) {
+__device__ __forceinline__ void scale_by(const T* p, T* q, int64_t n, float coef, int t, int threads) {
     constexpr int V = 16 / sizeof(T);
     const int64_t nv = n / V;
-    for (int64_t i = threadIdx.x; i < nv; i += threads) {
+    for (int64_t i = t; i < nv; i += threads) {
         float v[V];
         load_vec<V>(p + i * V, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] *= coef;
         store_vec<V>(q + i * V, v);
     }
-    for (int64_t i = nv * V + threadIdx.x; i < n; i += threads) q[i] = (T)((float)p[i] * coef);
+    for (int64_t i = nv * V + t; i < n; i += threads) q[i] = (T)((float)p[i] * coef);
 }
 
 // part[blockIdx.x] = sum of squares of this block's chunks.
@@ -63,16 +76,11 @@ __global__ __launch_bounds__(kThreads) void k_grad_sumsq(GradTable t, uint32_t n
     double s = 0.0;
     for (uint32_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
         const int i = tensor_of(t, c);
-        const int type = t.type[i];
-        const int64_t ce = chunk_elems(type), at = (int64_t)(c - t.first[i]) * ce;
+        const int64_t ce = chunk_elems(t.type[i]), at = (int64_t)(c - t.first[i]) * ce;
         const int64_t n = min(ce, t.n[i] - at);
-        if (type == kTypeBf16) {
-            s += sum_squares(static_cast<const bf16*>(t.src[i]) + at, n, kThreads);
-        } else if (type == kTypeF16) {
-            s += sum_squares(static_cast<const f16*>(t.src[i]) + at, n, kThreads);
-        } else {
-            s += sum_squares(static_cast<const float*>(t.src[i]) + at, n, kThreads);
-        }
+        with_type(t.type[i], [&](auto e) {
+            s += sum_squares(static_cast<const decltype(e)*>(t.src[i]) + at, n, threadIdx.x, kThreads);
+        });
     }
     s = block_sum(s, red);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -99,22 +107,51 @@ __global__ __launch_bounds__(kThreads) void k_grad_finish(const double* __restri
     }
 }
 
+// Few chunks: everything in one workgroup, a wave a chunk.  The second read
+// comes from the caches.  at most kGradSmallChunks.
+__global__ __launch_bounds__(1024) void k_grad_small(GradTable t, uint32_t nchunks, float max_norm, bool scale,
+                                                     float* __restrict__ norm) {
+    __shared__ double red[16];
+    const uint32_t wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    double s = 0.0;
+    for (uint32_t c = wave; c < nchunks; c += 16) {
+        const int i = tensor_of(t, c);
+        const int64_t ce = chunk_elems(t.type[i]), at = (int64_t)(c - t.first[i]) * ce;
+        const int64_t n = min(ce, t.n[i] - at);
+        with_type(t.type[i], [&](auto e) {
+            s += sum_squares(static_cast<const decltype(e)*>(t.src[i]) + at, n, lane, 64);
+        });
+    }
+    const double v = sqrt(block_sum(s, red));
+    if (threadIdx.x == 0) *norm = (float)v;
+    if (!scale) return;
+    const float k = clip_coef(v, max_norm);
+    for (uint32_t c = wave; c < nchunks; c += 16) {
+        const int i = tensor_of(t, c);
+        if (k == 1.0f && t.src[i] == t.dst[i]) continue;
+        const int64_t ce = chunk_elems(t.type[i]), at = (int64_t)(c - t.first[i]) * ce;
+        const int64_t n = min(ce, t.n[i] - at);
+        with_type(t.type[i], [&](auto e) {
+            scale_by(static_cast<const decltype(e)*>(t.src[i]) + at, static_cast<decltype(e)*>(t.dst[i]) + at, n, k,
+                     lane, 64);
+        });
+    }
+}
+
 // One chunk a block.  A tensor clipped in place by a factor of 1 is left as
 // it is: every value times 1 is itself.
-__global__ __launch_bounds__(kThreads) void k_grad_scale(GradTable t, const float* __restrict__ coef) {
+__global__ __launch_bounds__(kThreads) void k_grad_scale(GradTable t, uint32_t nchunks, const float* __restrict__ coef) {
     const float k = *coef;
-    const uint32_t c = blockIdx.x;
-    const int i = tensor_of(t, c);
-    if (k == 1.0f && t.src[i] == t.dst[i]) return;
-    const int type = t.type[i];
-    const int64_t ce = chunk_elems(type), at = (int64_t)(c - t.first[i]) * ce;
-    const int64_t n = min(ce, t.n[i] - at);
-    if (type == kTypeBf16) {
-        scale_by(static_cast<const bf16*>(t.src[i]) + at, static_cast<bf16*>(t.dst[i]) + at, n, k, kThreads);
-    } else if (type == kTypeF16) {
-        scale_by(static_cast<const f16*>(t.src[i]) + at, static_cast<f16*>(t.dst[i]) + at, n, k, kThreads);
-    } else {
-        scale_by(static_cast<const float*>(t.src[i]) + at, static_cast<float*>(t.dst[i]) + at, n, k, kThreads);
+    for (uint32_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
+        const int i = tensor_of(t, c);
+        if (k == 1.0f && t.src[i] == t.dst[i]) continue;
+        const int64_t ce = chunk_elems(t.type[i]), at = (int64_t)(c - t.first[i]) * ce;
+        const int64_t n = min(ce, t.n[i] - at);
+        with_type(t.type[i], [&](auto e) {
+            scale_by(static_cast<const decltype(e)*>(t.src[i]) + at, static_cast<decltype(e)*>(t.dst[i]) + at, n, k,
+                     threadIdx.x, kThreads);
+        });
     }
 }
 
@@ -141,12 +178,18 @@ size_t grad_norm_workspace(int64_t count) {
 hipError_t launch_grad_sumsq(const GradTable& t, uint32_t nchunks, double* part, hipStream_t s) {
     return launch_kernel(k_grad_sumsq, dim3(grad_sumsq_blocks(nchunks)), dim3(kThreads), 0, s, t, nchunks, part);
 }
+hipError_t launch_grad_small(const GradTable& t, uint32_t nchunks, float max_norm, bool scale, float* norm,
+                             hipStream_t s) {
+    return launch_kernel(k_grad_small, dim3(1), dim3(1024), 0, s, t, nchunks, max_norm, scale, norm);
+}
 hipError_t launch_grad_finish(const double* part, int nparts, const float* given, float max_norm, float* norm,
                               float* coef, hipStream_t s) {
     return launch_kernel(k_grad_finish, dim3(1), dim3(kThreads), 0, s, part, nparts, given, max_norm, norm, coef);
 }
 hipError_t launch_grad_scale(const GradTable& t, uint32_t nchunks, const float* coef, hipStream_t s) {
-    return launch_kernel(k_grad_scale, dim3(nchunks), dim3(kThreads), 0, s, t, coef);
+    // one chunk a workgroup (a dimension of the grid holds fewer than 2^32 threads)
+    return launch_kernel(k_grad_scale, dim3(std::min<uint32_t>(nchunks, 1u << 22)), dim3(kThreads), 0, s, t, nchunks,
+                         coef);
 }
 
 }  // namespace fno

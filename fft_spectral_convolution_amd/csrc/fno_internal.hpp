@@ -332,6 +332,10 @@ uint32_t grad_table_chunks(GradTable& t, int count);
 int grad_sumsq_blocks(uint32_t nchunks);                // partial sums launch_grad_sumsq writes
 size_t grad_norm_workspace(int64_t count);
 hipError_t launch_grad_sumsq(const GradTable& t, uint32_t nchunks, double* part, hipStream_t s);
+// all in one kernel, for at most kGradSmallChunks chunks of one table
+constexpr uint32_t kGradSmallChunks = 32;
+hipError_t launch_grad_small(const GradTable& t, uint32_t nchunks, float max_norm, bool scale, float* norm,
+                             hipStream_t s);
 // norm and / or coef may be null; given (if not null) stands for the norm
 hipError_t launch_grad_finish(const double* part, int nparts, const float* given, float max_norm, float* norm,
                               float* coef, hipStream_t s);
