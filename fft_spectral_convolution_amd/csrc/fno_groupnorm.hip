@@ -292,32 +292,321 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_stats_first(const TX* __restr
     if (t == 0) part[id] = make_float2(mean, sq);
 }
 
-// One wave a group: joins its chunks' statistics.  Chunk i of group (b, g) is
-// part[(b G + g) chunks + i] (channels first) or part[(b chunks + i) G + g];
-// all chunks hold `per` values but the last.
+// One workgroup a group: joins its chunks' statistics.  Chunk i of group (b, g)
+// is part[(b G + g) chunks + i] (channels first) or part[(b chunks + i) G + g];
+// all chunks hold `per` values but the last.  A thread asks for eight pairs at
+// a time (they come from far away) and keeps the first eight for the squares.
 __global__ __launch_bounds__(kGnThreads) void k_gn_finish(const float2* __restrict__ part, float* __restrict__ stats,
                                                           int64_t total, int groups, int chunks, bool last, int64_t per,
                                                           int64_t n, float eps) {
-    const int64_t i = block_id() * (kGnThreads / 64) + (threadIdx.x >> 6);
+    __shared__ float red[16];
+    const int64_t i = block_id();
     if (i >= total) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t base = last ? i / groups * chunks * groups + i % groups : i * chunks;
-    const int64_t step = last ? groups : 1;
-    float sum = 0.0f;
-    for (int k = lane; k < chunks; k += 64)
-        sum = fmaf((float)min(per, n - k * per), part[base + k * step].x, sum);
-    const float mean = wave_sum(sum) / (float)n;
-    float sq = 0.0f;
-    for (int k = lane; k < chunks; k += 64) {
-        const float2 q = part[base + k * step];
-        const float d = q.x - mean;
-        sq += fmaf((float)min(per, n - k * per) * d, d, q.y);
+    const float2* p = part + (last ? i / groups * chunks * groups + i % groups : i * chunks);
+    const int step = last ? groups : 1;
+    const auto load = [&](int k0, float2(&q)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = k0 + e * kGnThreads;
+            q[e] = k < chunks ? p[(int64_t)k * step] : make_float2(0.0f, 0.0f);
+        }
+    };
+    const auto values = [&](int k) { return k < chunks ? (float)min(per, n - k * per) : 0.0f; };
+    const auto sums = [&](int k0, const float2(&q)[8]) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(values(k0 + e * kGnThreads), q[e].x, s);
+        return s;
+    };
+    const int t = threadIdx.x;
+    float2 q[8], far[8];
+    load(t, q);
+    float sum = sums(t, q);
+    for (int k = t + 8 * kGnThreads; k < chunks; k += 8 * kGnThreads) {
+        load(k, far);
+        sum += sums(k, far);
     }
-    sq = wave_sum(sq);
-    if (lane == 0) {
+    const float mean = block_sum(sum, red) / (float)n;
+    const auto squares = [&](int k0, const float2(&v)[8]) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = v[e].x - mean;
+            s += fmaf(values(k0 + e * kGnThreads) * d, d, v[e].y);
+        }
+        return s;
+    };
+    float sq = squares(t, q);
+    for (int k = t + 8 * kGnThreads; k < chunks; k += 8 * kGnThreads) {
+        load(k, far);
+        sq += squares(k, far);
+    }
+    sq = block_sum(sq, red);
+    if (t == 0) {
         stats[2 * i] = mean;
         stats[2 * i + 1] = rsqrtf(sq / (float)n + eps);
     }
+}
+
+// ---- one pass, items spread over workgroups ----------------------------------------------
+// Workgroup (item, chunk of q NV super-rows).  Vectors are whole (P is a
+// multiple of R); rows past the end of an item are read as the thread's last
+// one and left out.
+template <typename TX, typename TY>
+struct OnceArgs {
+    const TX* x;
+    const float *w, *bias;
+    TY* out;
+    float* stats;
+    uint64_t* slots;
+    LastRows r;
+    Once o;
+    float eps;
+    int spin;
+};
+
+template <int ACT, int NV, bool TURN, typename TX, typename TY>
+struct OnceLast {
+    static constexpr int V = kVec<TX>;
+    // TURN: out is channels first; kTurn vectors a thread go through LDS at a time, so that a channel's run in out is
+    // kTurn q positions long
+    static constexpr int kTurn = NV < 4 ? NV : 4;
+    typedef typename VecOf<TX, V>::type Vec;
+    const OnceArgs<TX, TY>& a;
+    const LastRows& r;
+    float *buf, *counts, *mean, *sq;
+    int* missing;
+    int t, row, slot, groups, chunk;
+    int64_t item, step;
+
+    __device__ __forceinline__ OnceLast(const OnceArgs<TX, TY>& args, float* lds, int* flag)
+        : a(args), r(args.r), buf(lds), missing(flag) {
+        t = threadIdx.x;
+        row = div_by(t, r.by_cv);
+        slot = t - row * r.cv;
+        groups = div_by(r.C, r.by_D);
+        counts = lds + once_buffer(r.threads, V, r.C, TURN ? kTurn : 0, r.q * r.R);
+        mean = counts + r.q;
+        sq = mean + groups;
+        item = blockIdx.x / a.o.chunks;
+        chunk = (int)(blockIdx.x - item * a.o.chunks);
+        step = (int64_t)r.q * r.stride();
+    }
+    __device__ __forceinline__ int per() const { return r.q * NV; }
+    __device__ __forceinline__ const TX* x_item() const { return a.x + item * r.P * r.C; }
+    __device__ __forceinline__ uint64_t* pairs() const { return a.slots + item * groups * a.o.chunks; }
+    __device__ __forceinline__ float values_of(int k) const {
+        return (float)min(per(), r.ns - k * per()) * (float)(r.R * r.D);
+    }
+    // rows of chunk k that this thread holds, and the element of the first
+    __device__ __forceinline__ int rows_of(int k) const {
+        return row < r.q ? max(0, min(NV, (r.ns - (k * per() + row) + r.q - 1) / r.q)) : 0;
+    }
+    __device__ __forceinline__ int64_t at_of(int k) const { return (int64_t)(k * per() + row) * r.stride() + slot * V; }
+    // Chunk k's mean and squares about it, of each group, to its slots.  `rows` vectors that `each` hands over one
+    // by one (twice): every thread leaves its own mean and squares in LDS; after one barrier a team of lanes joins a
+    // group's (their mean first, then the squares about that).
+    template <typename F>
+    __device__ __forceinline__ void put(int k, int rows, F&& each) const {
+        float m[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) m[j] = 0.0f;
+        each([&](const Vec& h) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] += (float)h[j];
+        });
+        const float inv_rows = rows ? __builtin_amdgcn_rcpf((float)rows) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            // the quotient to the last bit or so: the reciprocal's error is put right once
+            const float sum = m[j];
+            m[j] = sum * inv_rows;
+            m[j] = fmaf(fmaf(-(float)rows, m[j], sum), inv_rows, m[j]);
+            q[j] = 0.0f;
+        }
+        each([&](const Vec& h) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = (float)h[j] - m[j];
+                q[j] = fmaf(d, d, q[j]);
+            }
+        });
+        __syncthreads();
+        float* means = buf;
+        float* squares = buf + r.threads * V;
+        if (row < r.q) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                means[t * V + j] = m[j];
+                squares[t * V + j] = q[j];
+            }
+            if (slot == 0) counts[row] = (float)rows;
+        }
+        __syncthreads();
+        const int parts = a.o.parts, part = t & (parts - 1), g = t >> __builtin_ctz(parts);
+        if (g < groups) {
+            const int entries = r.q * r.R * r.D;
+            float sum = 0.0f;
+            for (int e = part; e < entries; e += parts) {
+                const int i = div_by(e, r.by_D);
+                sum = fmaf(counts[div_by(i, r.by_R)], means[i * (r.C - r.D) + g * r.D + e], sum);
+            }
+            const float mu = team_sum(sum, parts) / values_of(k);
+            sum = 0.0f;
+            for (int e = part; e < entries; e += parts) {
+                const int i = div_by(e, r.by_D), at = i * (r.C - r.D) + g * r.D + e;
+                const float d = means[at] - mu;
+                sum += fmaf(counts[div_by(i, r.by_R)] * d, d, squares[at]);
+            }
+            sum = team_sum(sum, parts);
+            if (part == 0) put_pair(pairs() + g * a.o.chunks + k, mu, sum);
+        }
+    }
+    // mean and 1 / deviation of the item's groups, in LDS, from all its chunks; the first chunk not there, or `chunks`
+    __device__ __forceinline__ int join(int looks) const {
+        const int chunks = a.o.chunks, parts = a.o.parts;
+        const int part = t & (parts - 1), g = t >> __builtin_ctz(parts);
+        __syncthreads();
+        if (t == 0) *missing = chunks;
+        __syncthreads();
+        if (g < groups) {
+            uint64_t v[kLooks];
+            const int lost = gather_pairs(pairs() + g * chunks, chunks, part, parts, looks, v);
+            if (lost < chunks) atomicMin(missing, lost);
+            const float n = (float)r.P * (float)r.D;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kLooks; ++i) {
+                const int k = part + i * parts;
+                if (k < chunks) sum = fmaf(values_of(k), unpack_pair(v[i]).x, sum);
+            }
+            const float mu = team_sum(sum, parts) / n;
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kLooks; ++i) {
+                const int k = part + i * parts;
+                const float2 q = unpack_pair(v[i]);
+                if (k < chunks) sum += fmaf(values_of(k) * (q.x - mu), q.x - mu, q.y);
+            }
+            sum = team_sum(sum, parts);
+            if (part == 0) {
+                mean[g] = mu;
+                sq[g] = rsqrtf(sum / n + a.eps);
+            }
+        }
+        __syncthreads();
+        return *missing;
+    }
+    // The output of this workgroup's chunk from its vectors: get(i) is vector i < rows.
+    template <typename F>
+    __device__ __forceinline__ void write(int64_t at, int rows, F&& get) const {
+        if (chunk == 0)
+            for (int i = t; i < groups; i += blockDim.x) {
+                a.stats[2 * (item * groups + i)] = mean[i];
+                a.stats[2 * (item * groups + i) + 1] = sq[i];
+            }
+        float m[V], k[V], c[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int ch = mod_by(slot * V + j, r.by_cs), gr = div_by(ch, r.by_D);
+            m[j] = mean[gr];
+            k[j] = sq[gr] * or_one(a.w, ch);
+            c[j] = or_zero(a.bias, ch);
+        }
+        if constexpr (!TURN) {
+            TY* y = a.out + item * r.P * r.C + at;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i < rows) {
+                    const Vec h = get(i);
+                    float u[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) u[j] = act_value<ACT>(fmaf((float)h[j] - m[j], k[j], c[j]));
+                    store_vec<V>(y + i * step, u);
+                }
+        } else {
+            constexpr int VY = kVec<TY>;
+            const int span = kTurn * r.q * r.R, ld = span + 1;       // positions in LDS at a time
+            int place[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = slot * V + j, ch = mod_by(e, r.by_cs);
+                place[j] = ch * ld + div_by(e, r.by_cs) + row * r.R;
+            }
+            TY* y = a.out + item * r.P * r.C;
+#pragma unroll
+            for (int i0 = 0; i0 < NV; i0 += kTurn) {
+                const int p0 = (chunk * per() + i0 * r.q) * r.R, np = min(span, r.P - p0);
+                if (np <= 0) break;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kTurn; ++i)
+                    if (i0 + i < rows) {
+                        const Vec h = get(i0 + i);
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            buf[place[j] + i * r.q * r.R] = act_value<ACT>(fmaf((float)h[j] - m[j], k[j], c[j]));
+                    }
+                __syncthreads();
+                const int runs = (np + VY - 1) / VY;                 // vectors of a channel
+                const FastDiv by_runs{(uint32_t)runs, runs == 1 ? 0u : 0xffffffffu / (uint32_t)runs + 1u};
+#pragma unroll 4
+                for (int e = t; e < r.C * runs; e += blockDim.x) {
+                    const int ch = div_by(e, by_runs), p = (e - ch * runs) * VY;
+                    float u[VY];
+#pragma unroll
+                    for (int j = 0; j < VY; ++j) u[j] = buf[ch * ld + p + j];
+                    store_part(y + (int64_t)ch * r.P + p0 + p, min(VY, np - p), u);
+                }
+            }
+        }
+    }
+};
+
+// Where others' sums stayed out: their chunks from memory, in the same order,
+// then this workgroup's own again.  A call that does not return to the
+// kernel's registers, which are thus not sized for it.
+template <int ACT, int NV, bool TURN, typename TX, typename TY>
+__device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float* lds, int* flag, int lost) {
+    typedef OnceLast<ACT, NV, TURN, TX, TY> F;
+    const F f(args, lds, flag);
+    do {
+        const TX* p = f.x_item() + f.at_of(lost);
+        const int n = f.rows_of(lost);
+        f.put(lost, n, [&](auto&& take) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) take(*reinterpret_cast<const typename F::Vec*>(p + i * f.step));
+        });
+        lost = f.join(0);
+    } while (lost < args.o.chunks);
+    const int64_t at = f.at_of(f.chunk);
+    f.write(at, f.rows_of(f.chunk),
+            [&](int i) { return *reinterpret_cast<const typename F::Vec*>(f.x_item() + at + i * f.step); });
+}
+
+template <int ACT, int NV, bool TURN, typename TX, typename TY>
+__global__ __launch_bounds__(kOnceThreads, 4) void k_gn_once_last(OnceArgs<TX, TY> args) {
+    typedef OnceLast<ACT, NV, TURN, TX, TY> F;
+    extern __shared__ float lds[];
+    __shared__ int missing;
+    const F f(args, lds, &missing);
+    typename F::Vec cur[NV];
+    const int rows = f.rows_of(f.chunk);
+    const int64_t at = rows ? f.at_of(f.chunk) : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        cur[i] = *reinterpret_cast<const typename F::Vec*>(f.x_item() + at + max(0, min(i, rows - 1)) * f.step);
+    f.put(f.chunk, rows, [&](auto&& take) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < rows) take(cur[i]);
+    });
+    const int lost = f.join(args.spin);
+    if (lost < args.o.chunks) {
+        once_late<ACT, NV, TURN, TX, TY>(args, lds, &missing, lost);
+        return;
+    }
+    f.write(at, rows, [&](int i) { return cur[i]; });
 }
 
 // ---- output, the layout kept ------------------------------------------------------------
@@ -511,7 +800,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_wide(const TX* __restri
 }
 
 // ---- schedules ------------------------------------------------------------------------------
-enum Stats { kFusedLast, kFusedFirst, kSplitLast, kSplitFirst, kWide };
+enum Stats { kFusedLast, kFusedFirst, kOnceLast, kSplitLast, kSplitFirst, kWide };
 struct Plan {
     Stats how;
     LastRows rows;                // fused or split, channels last
@@ -519,7 +808,14 @@ struct Plan {
     int threads;                  // fused, channels first
     int per, chunks;              // split: super-rows or values a chunk
     int64_t parts;                // float2 of workspace
+    Once once;
 };
+
+size_t once_lds(const GroupNorm& g, const Plan& p) {
+    const LastRows& r = p.rows;
+    const int turn = g.x_last != g.out_last && g.P > 1 ? std::min(p.once.nv, 4) : 0;
+    return sizeof(float) * (size_t)(once_buffer(r.threads, vec_of(g), r.C, turn, r.q * r.R) + r.q + 2 * g.groups);
+}
 
 Plan plan_forward(const GroupNorm& g) {
     const int V = vec_of(g);
@@ -562,6 +858,14 @@ Plan plan_forward(const GroupNorm& g) {
             }
         }
     }
+    p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
+    if (once_plan(g, p.rows, 16, &p.once)) {
+        if (once_lds(g, p) <= kLdsMax) {
+            p.how = kOnceLast;
+            p.parts = p.once.total * g.groups;
+            return p;
+        }
+    }
     p.how = kSplitLast;
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
     split_chunks(g.B, p.rows.ns, 4 * p.rows.q, 64 * p.rows.q, &p.per, &p.chunks);
@@ -580,6 +884,11 @@ int gn_forward_kernels(const GroupNorm& g, const char** names) {
     if (p.how == kFusedLast || p.how == kFusedFirst) {
         names[0] = "gn_fused";
         return 1;
+    }
+    if (p.how == kOnceLast) {
+        names[0] = "gn_clear";
+        names[1] = "gn_once";
+        return 2;
     }
     names[0] = p.how == kWide ? "gn_stats_wide" : "gn_stats";
     names[1] = p.how == kWide ? apply : "gn_finish";
@@ -600,6 +909,8 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
         TY* out = static_cast<TY*>(a.out);
         const float* stats = a.stats;
         const size_t lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * (D ? p.rows.cs / D : 0));
+        if (kernel == 0 && p.how == kOnceLast)
+            return launch_clear((uint64_t*)part, p.parts, s);
         if (kernel == 0 && p.how == kSplitLast) {
             const int64_t blocks = g.B * p.chunks;
             return launch_kernel(k_gn_stats_last<TX>, grid_of(blocks), dim3(p.rows.threads), lds, s, x, part, p.rows,
@@ -613,10 +924,10 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
         if (kernel == 0 && p.how == kWide)
             return launch_kernel(k_gn_stats_wide<TX>, grid_of(runs), dim3(kGnThreads), 0, s, x, a.stats, g.C, D, g.P,
                                  runs, g.eps);
-        if (kernel == 1 && p.how != kWide) {
+        if (kernel == 1 && p.how != kWide && p.how != kOnceLast) {
             const bool last = p.how == kSplitLast;
             const int64_t per = last ? (int64_t)p.per * p.rows.R * D : p.per;
-            return launch_kernel(k_gn_finish, grid_of((runs + 3) / 4), dim3(kGnThreads), 0, s, (const float2*)part,
+            return launch_kernel(k_gn_finish, grid_of(runs), dim3(kGnThreads), 0, s, (const float2*)part,
                                  a.stats, runs, (int)g.groups, p.chunks, last, per, n, g.eps);
         }
         return with_act(g.act, [&](auto act) {
@@ -626,6 +937,17 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
                 return launch_kernel(k_gn_fused_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), lds, s, x,
                                      a.weight, a.bias, out, a.stats, p.rows, p.slices, blocks, g.eps);
             }
+            if (p.how == kOnceLast)
+                return with_vectors(p.once.nv, [&](auto nv) {
+                    const OnceArgs<TX, TY> args{x,      a.weight, a.bias, out, a.stats, (uint64_t*)part,
+                                                p.rows, p.once,   g.eps,  once_spin()};
+                    constexpr int NV = decltype(nv)::value;
+                    const bool turn = g.x_last != g.out_last && g.P > 1;
+                    const auto kernel_of = turn ? k_gn_once_last<ACT, NV, true, TX, TY>
+                                                : k_gn_once_last<ACT, NV, false, TX, TY>;
+                    return launch_kernel(kernel_of, dim3((unsigned)p.once.total), dim3(p.rows.threads),
+                                         once_lds(g, p), s, args);
+                });
             if (p.how == kFusedFirst)
                 return launch_kernel(k_gn_fused_first<ACT, TX, TY>, grid_of(runs), dim3(p.threads), 0, s, x, a.weight,
                                      a.bias, out, a.stats, D, P, (int)g.groups, fast_div(P), runs, g.eps);

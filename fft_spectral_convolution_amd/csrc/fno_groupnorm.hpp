@@ -3,12 +3,14 @@
 #pragma once
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "fno_fields.hpp"
 
 namespace fno {
 
 constexpr int kGnThreads = 256;
+constexpr size_t kLdsMax = 65536;      // dynamic LDS of a workgroup, here
 
 // Vector width of a field: 16 bytes.
 template <typename T>
@@ -38,7 +40,7 @@ struct LastRows {
     int q;                 // super-rows a workgroup takes at a time
     int threads;           // cv q, rounded up to whole waves
     int ns;                // super-rows of an item
-    FastDiv by_cv, by_cs, by_D;
+    FastDiv by_cv, by_cs, by_D, by_R;
     __host__ __device__ int stride() const { return cs < C ? C : C * R; }   // elements from one to the next
 };
 
@@ -66,6 +68,7 @@ inline LastRows last_rows(int64_t C, int64_t cs, int64_t D, int64_t P, int V, in
     r.by_cv = fast_div(r.cv);
     r.by_cs = fast_div(r.cs);
     r.by_D = fast_div(r.D);
+    r.by_R = fast_div(r.R);
     return r;
 }
 
@@ -139,8 +142,10 @@ __device__ __forceinline__ void last_sums(const float (&val)[V], float* buf, flo
     int parts = 1;
     while (parts < 64 && 2 * parts * count <= (int)blockDim.x) parts *= 2;
     const int part = t & (parts - 1), step = (int)blockDim.x >> __builtin_ctz(parts);
+#pragma unroll 1
     for (int g = t >> __builtin_ctz(parts); g < count; g += step) {
         float s = 0.0f;
+#pragma unroll 2
         for (int k = part; k < entries; k += parts) {
             const int row = div_by(k, by_width);
             s += buf[row * (r.cs - width) + g * width + k];
@@ -159,6 +164,106 @@ inline void split_chunks(int64_t items, int64_t units, int64_t min_per, int64_t 
     const int64_t p = std::min(std::min(std::max((units + want - 1) / want, min_per), max_per), units);
     *per = (int)p;
     *chunks = (int)((units + p - 1) / p);
+}
+
+// ---- one pass over items larger than a workgroup ------------------------------------
+// An item's chunks are spread over workgroups that keep their values in
+// registers, exchange two numbers a group and chunk through memory, and then
+// write the output.  A pair travels as one 64-bit atomic, so nothing needs
+// ordering: a slot holds kEmpty until its pair is there.  A workgroup does
+// not depend on the others' progress: when a pair is not there after `spin`
+// looks, it forms that chunk's sums itself and stores them, the same bits.
+constexpr uint64_t kEmpty = ~0ull;
+constexpr int kOnceThreads = 512, kLooks = 8;
+
+__device__ __forceinline__ uint64_t pack_pair(float a, float b) {
+    // NaNs of any payload become the one that kEmpty is not
+    const uint32_t x = a == a ? __builtin_bit_cast(uint32_t, a) : 0x7fc00000u;
+    const uint32_t y = b == b ? __builtin_bit_cast(uint32_t, b) : 0x7fc00000u;
+    return (uint64_t)x << 32 | y;
+}
+__device__ __forceinline__ float2 unpack_pair(uint64_t v) {
+    return make_float2(__builtin_bit_cast(float, (uint32_t)(v >> 32)), __builtin_bit_cast(float, (uint32_t)v));
+}
+__device__ __forceinline__ void put_pair(uint64_t* slot, float a, float b) {
+    __hip_atomic_store(slot, pack_pair(a, b), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t look(const uint64_t* slot) {
+    return __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Fills v[i] with slots[part + i parts], i < kLooks, part + i parts < n;
+// returns the first of those places that stayed empty, or n.
+__device__ __forceinline__ int gather_pairs(const uint64_t* slots, int n, int part, int parts, int spin,
+                                            uint64_t (&v)[kLooks]) {
+#pragma unroll
+    for (int i = 0; i < kLooks; ++i) v[i] = kEmpty;
+    int missing = n;
+    for (int tries = 0; tries <= spin; ++tries) {
+        missing = n;
+#pragma unroll
+        for (int i = kLooks - 1; i >= 0; --i) {
+            const int k = part + i * parts;
+            if (k < n && v[i] == kEmpty) {
+                v[i] = look(slots + k);
+                if (v[i] == kEmpty) missing = k;
+            }
+        }
+        if (missing == n) break;
+        __builtin_amdgcn_s_sleep(4);
+    }
+    return missing;
+}
+
+// How an item is cut: `chunks` of q nv super-rows; `parts` lanes look for a
+// group's pairs.
+struct Once {
+    int nv, chunks, parts;
+    int64_t total;
+};
+
+// Whether a one-pass kernel serves the field, and how.  An item must fit the
+// workgroups that run at once, and its pairs the looks of a workgroup.
+inline bool once_plan(const GroupNorm& g, const LastRows& r, int vectors, Once* o) {
+    constexpr int kRunning = 1024;        // workgroups: four a CU
+    if (r.threads > kOnceThreads || r.P % r.R) return false;
+    // vectors a thread: as many as `vectors`, fewer where that would leave CUs without work
+    const auto chunks_of = [&](int nv) { return (r.ns + (int64_t)r.q * nv - 1) / ((int64_t)r.q * nv); };
+    o->nv = vectors;
+    while (o->nv > 2 && g.B * chunks_of(o->nv) < kRunning / 2) o->nv /= 2;
+    const int64_t chunks = chunks_of(o->nv);
+    if (chunks > kRunning / 2 || g.B * chunks >= 1 << 22) return false;
+    o->chunks = (int)chunks;
+    o->parts = 1;
+    while (o->parts < 64 && 2 * o->parts * g.groups <= r.threads) o->parts *= 2;
+    if (o->parts * g.groups > r.threads || (int64_t)o->parts * kLooks < chunks) return false;
+    o->total = g.B * chunks;
+    return true;
+}
+
+// Floats of LDS of k_gn_once_last's exchange: two values of each of a
+// workgroup's elements, or `turn` vectors a thread turned to channel rows.
+__host__ __device__ inline int once_buffer(int threads, int V, int C, int turn, int positions) {
+    const int pairs = 2 * threads * V, turned = turn ? C * (turn * positions + 1) : 0;
+    return pairs > turned ? pairs : turned;
+}
+
+template <typename F>
+hipError_t with_vectors(int nv, F&& f) {
+    switch (nv) {
+        case 16: return f(std::integral_constant<int, 16>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+        case 4: return f(std::integral_constant<int, 4>{});
+        default: return f(std::integral_constant<int, 2>{});
+    }
+}
+
+// Looks for another workgroup's sums before a workgroup forms them itself:
+// some milliseconds.  FNO_GN_SPIN sets another count (0: at once), which is how
+// that path is tested.
+inline int once_spin() {
+    const char* v = std::getenv("FNO_GN_SPIN");
+    return v ? std::max(0, std::atoi(v)) : 4096;
 }
 
 // ---- channels first ------------------------------------------------------------
@@ -225,6 +330,9 @@ hipError_t with_act(int act, F&& f) {
     }
 }
 inline int vec_of(const GroupNorm& g) { return g.x_type == kTypeF32 ? 4 : 8; }
+
+// Empties the slots of a one-pass kernel.
+hipError_t launch_clear(uint64_t* slots, int64_t n, hipStream_t s);
 
 // Forward and backward halves of launch_group_norm and its queries.
 int gn_forward_kernels(const GroupNorm& g, const char** names);

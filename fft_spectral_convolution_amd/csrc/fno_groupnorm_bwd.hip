@@ -17,7 +17,6 @@ namespace {
 
 constexpr int kHeld = 4;              // vectors of x and of grad_out a thread keeps
 constexpr int kFusedThreads = 1024;
-constexpr size_t kLdsMax = 65536;
 
 template <int ACT>
 __device__ __forceinline__ float slope_times(float dy, float xh, float w, float b) {
@@ -229,6 +228,243 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
         }
         store_part(gx + base + e, min(V, n - e), u);
     }
+}
+
+// ---- one pass, items spread over workgroups --------------------------------------------
+// Workgroup (item, chunk of q NV super-rows), as k_gn_once_last: x and
+// grad_out stay in registers while the chunks' (s1, s2) are exchanged.  Each
+// chunk's channel sums go to part[(item chunks + chunk) C + c].
+template <typename TX, typename TY>
+struct OnceArgs {
+    const TX* x;
+    const TY* dy;
+    const float *w, *bias, *stats;
+    TX* gx;
+    float2* part;
+    uint64_t* slots;
+    LastRows r;
+    Once o;
+    int spin;
+};
+
+template <int ACT, int NV, typename TX, typename TY>
+struct OnceLast {
+    static constexpr int V = kVec<TX>;
+    // float32 keeps g = grad_out act'(z) in the place of grad_out: the slope is not formed twice
+    static constexpr bool kKeep = std::is_same_v<TY, float>;
+    typedef typename VecOf<TX, V>::type VecX;
+    typedef typename VecOf<TY, V>::type VecY;
+    const OnceArgs<TX, TY>& a;
+    const LastRows& r;
+    float *buf, *w, *s1, *s2;
+    int* missing;
+    int t, row, slot, groups, chunk;
+    int64_t item, step;
+    float m[V], k[V], b[V];
+
+    __device__ __forceinline__ OnceLast(const OnceArgs<TX, TY>& args, float* lds, int* flag)
+        : a(args), r(args.r), buf(lds), missing(flag) {
+        t = threadIdx.x;
+        row = div_by(t, r.by_cv);
+        slot = t - row * r.cv;
+        groups = div_by(r.C, r.by_D);
+        w = lds + 2 * r.threads * V;
+        s1 = w + r.C;
+        s2 = s1 + groups;
+        item = blockIdx.x / a.o.chunks;
+        chunk = (int)(blockIdx.x - item * a.o.chunks);
+        step = (int64_t)r.q * r.stride();
+        for (int c = t; c < r.C; c += blockDim.x) w[c] = or_one(a.w, c);
+        const float* st = a.stats + 2 * item * groups;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = channel(j), g = div_by(c, r.by_D);
+            m[j] = st[2 * g];
+            k[j] = st[2 * g + 1];
+            b[j] = or_zero(a.bias, c);
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ int channel(int j) const { return mod_by(slot * V + j, r.by_cs); }
+    __device__ __forceinline__ int per() const { return r.q * NV; }
+    __device__ __forceinline__ int64_t base() const { return item * r.P * r.C; }
+    __device__ __forceinline__ uint64_t* pairs() const { return a.slots + item * groups * a.o.chunks; }
+    __device__ __forceinline__ int rows_of(int c) const {
+        return row < r.q ? max(0, min(NV, (r.ns - (c * per() + row) + r.q - 1) / r.q)) : 0;
+    }
+    __device__ __forceinline__ int64_t at_of(int c) const { return (int64_t)(c * per() + row) * r.stride() + slot * V; }
+
+    // The sums of chunk c, from the pairs of vectors that `each` hands over (g is left in the second where it fits).
+    template <typename F>
+    __device__ __forceinline__ void put(int c, bool own, F&& each) const {
+        float sg[V], sx[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) sg[j] = sx[j] = 0.0f;
+        each([&](const VecX& x, VecY& y) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xh = ((float)x[j] - m[j]) * k[j];
+                const float g = slope_times<ACT>((float)y[j], xh, w[channel(j)], b[j]);
+                sg[j] += g;
+                sx[j] = fmaf(g, xh, sx[j]);
+                if constexpr (kKeep) y[j] = g;
+            }
+        });
+        float* gs = buf;
+        float* xs = buf + r.threads * V;
+        __syncthreads();
+        if (row < r.q) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                gs[t * V + j] = sg[j];
+                xs[t * V + j] = sx[j];
+            }
+        }
+        __syncthreads();
+        const int rows = r.q * r.R;
+        {
+            const int parts = a.o.parts, part = t & (parts - 1), g = t >> __builtin_ctz(parts);
+            if (g < groups) {
+                float s = 0.0f, z = 0.0f;
+                for (int e = part; e < rows * r.D; e += parts) {
+                    const int i = div_by(e, r.by_D), ch = g * r.D + e - i * r.D;
+                    s = fmaf(w[ch], gs[i * r.C + ch], s);
+                    z = fmaf(w[ch], xs[i * r.C + ch], z);
+                }
+                s = team_sum(s, parts);
+                z = team_sum(z, parts);
+                if (part == 0) put_pair(pairs() + g * a.o.chunks + c, s, z);
+            }
+        }
+        if (own && a.part) {
+            int parts = 1;
+            while (parts < 64 && 2 * parts * r.C <= (int)blockDim.x) parts *= 2;
+            const int part = t & (parts - 1), step_c = (int)blockDim.x >> __builtin_ctz(parts);
+            for (int ch = t >> __builtin_ctz(parts); ch < r.C; ch += step_c) {
+                float s = 0.0f, z = 0.0f;
+                for (int i = part; i < rows; i += parts) {
+                    s += gs[i * r.C + ch];
+                    z += xs[i * r.C + ch];
+                }
+                s = team_sum(s, parts);
+                z = team_sum(z, parts);
+                if (part == 0) a.part[(item * a.o.chunks + c) * r.C + ch] = make_float2(s, z);
+            }
+        }
+    }
+    // s1 and s2 of the item's groups, in LDS; the first chunk not there, or `chunks`
+    __device__ __forceinline__ int join(int looks) const {
+        const int chunks = a.o.chunks, parts = a.o.parts;
+        const int part = t & (parts - 1), g = t >> __builtin_ctz(parts);
+        __syncthreads();
+        if (t == 0) *missing = chunks;
+        __syncthreads();
+        if (g < groups) {
+            uint64_t v[kLooks];
+            const int lost = gather_pairs(pairs() + g * chunks, chunks, part, parts, looks, v);
+            if (lost < chunks) atomicMin(missing, lost);
+            float s = 0.0f, z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kLooks; ++i)
+                if (part + i * parts < chunks) {
+                    const float2 q = unpack_pair(v[i]);
+                    s += q.x;
+                    z += q.y;
+                }
+            s = team_sum(s, parts);
+            z = team_sum(z, parts);
+            if (part == 0) {
+                const float inv = 1.0f / ((float)r.P * (float)r.D);
+                s1[g] = s * inv;
+                s2[g] = z * inv;
+            }
+        }
+        __syncthreads();
+        return *missing;
+    }
+    // grad_x of this workgroup's chunk; `kept`: the second vector holds g
+    template <bool KEPT, typename F>
+    __device__ __forceinline__ void write(int64_t at, F&& each) const {
+        float p[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int g = div_by(channel(j), r.by_D);
+            p[j] = s1[g];
+            q[j] = s2[g];
+        }
+        TX* out = a.gx + base() + at;
+        each([&](int i, const VecX& x, const VecY& y) {
+            float u[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xh = ((float)x[j] - m[j]) * k[j], wc = w[channel(j)];
+                const float g = KEPT ? (float)y[j] : slope_times<ACT>((float)y[j], xh, wc, b[j]);
+                u[j] = k[j] * (fmaf(g, wc, -p[j]) - xh * q[j]);
+            }
+            store_vec<V>(out + i * step, u);
+        });
+    }
+};
+
+template <int ACT, int NV, typename TX, typename TY>
+__device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float* lds, int* flag, int lost) {
+    typedef OnceLast<ACT, NV, TX, TY> F;
+    const F f(args, lds, flag);
+    const auto pair_at = [&](int64_t at, int i, auto&& use) {
+        const int64_t e = f.base() + at + i * f.step;
+        const typename F::VecX x = *reinterpret_cast<const typename F::VecX*>(args.x + e);
+        typename F::VecY y = *reinterpret_cast<const typename F::VecY*>(args.dy + e);
+        use(x, y);
+    };
+    do {
+        const int n = f.rows_of(lost);
+        const int64_t at = f.at_of(lost);
+        f.put(lost, false, [&](auto&& take) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) pair_at(at, i, take);
+        });
+        lost = f.join(0);
+    } while (lost < args.o.chunks);
+    const int64_t at = f.at_of(f.chunk);
+    f.template write<false>(at, [&](auto&& to) {
+#pragma unroll 1
+        for (int i = 0; i < f.rows_of(f.chunk); ++i)
+            pair_at(at, i, [&](const auto& x, const auto& y) { to(i, x, y); });
+    });
+}
+
+template <int ACT, int NV, typename TX, typename TY>
+__global__ __launch_bounds__(kOnceThreads, 4) void k_gn_bwd_once_last(OnceArgs<TX, TY> args) {
+    typedef OnceLast<ACT, NV, TX, TY> F;
+    extern __shared__ float lds[];
+    __shared__ int missing;
+    const F f(args, lds, &missing);
+    typename F::VecX x[NV];
+    typename F::VecY y[NV];
+    const int rows = f.rows_of(f.chunk);
+    const int64_t at = rows ? f.at_of(f.chunk) : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t e = f.base() + at + max(0, min(i, rows - 1)) * f.step;
+        x[i] = *reinterpret_cast<const typename F::VecX*>(args.x + e);
+        y[i] = *reinterpret_cast<const typename F::VecY*>(args.dy + e);
+    }
+    f.put(f.chunk, true, [&](auto&& take) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < rows) take(x[i], y[i]);
+    });
+    if (!args.gx) return;
+    const int lost = f.join(args.spin);
+    if (lost < args.o.chunks) {
+        once_late<ACT, NV, TX, TY>(args, lds, &missing, lost);
+        return;
+    }
+    f.template write<F::kKeep>(at, [&](auto&& to) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i < rows) to(i, x[i], y[i]);
+    });
 }
 
 // ---- partial sums of chunks ----------------------------------------------------------
@@ -495,7 +731,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __res
 
 // ---- joining the partial sums -----------------------------------------------------------
 // First (with gsum) the B G groups' (s1, s2), a wave each; then the C channels'
-// gradients, a workgroup each, over items and chunks.  The partial sums come
+// gradients, a workgroup for each or for eight, over items and chunks.  The partial sums come
 // from other XCDs' kernels and are far away (a microsecond), so a lane asks
 // for eight at a time.
 template <typename F>
@@ -518,6 +754,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(const float2* __re
                                                               int C, int D, int chunks, bool last, float inv_n,
                                                               int64_t ngroups) {
     __shared__ float red[16];
+    __shared__ float2 both[kGnThreads];
     const int64_t id = block_id(), gblocks = (ngroups + 3) / 4;
     float s = 0.0f, z = 0.0f;
     if (id < gblocks) {
@@ -534,11 +771,28 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(const float2* __re
         s = wave_sum(s);
         z = wave_sum(z);
         if ((threadIdx.x & 63) == 0) gsum[i] = make_float2(s * inv_n, z * inv_n);
+    } else if (last) {
+        // eight channels a workgroup: their pairs share a 64-byte piece of each chunk's row
+        const int64_t c = (id - gblocks) * 8 + (threadIdx.x & 7);
+        if (c < C)
+            sum_parts(B * chunks, threadIdx.x >> 3, kGnThreads / 8, [&](int64_t k) { return part[k * C + c]; }, s, z);
+        both[threadIdx.x] = make_float2(s, z);
+        __syncthreads();
+        for (int half = kGnThreads / 2; half >= 8; half >>= 1) {
+            if ((int)threadIdx.x < half) {
+                both[threadIdx.x].x += both[threadIdx.x + half].x;
+                both[threadIdx.x].y += both[threadIdx.x + half].y;
+            }
+            __syncthreads();
+        }
+        if (threadIdx.x < 8 && c < C) {
+            if (gb) gb[c] = both[threadIdx.x].x;
+            if (gw) gw[c] = both[threadIdx.x].y;
+        }
     } else if (id - gblocks < C) {
         const int64_t c = id - gblocks;
-        sum_parts(B * chunks, threadIdx.x, kGnThreads, [&](int64_t k) {
-            return part[last ? k * C + c : (k / chunks * C + c) * chunks + k % chunks];
-        }, s, z);
+        sum_parts(B * chunks, threadIdx.x, kGnThreads,
+                  [&](int64_t k) { return part[(k / chunks * C + c) * chunks + k % chunks]; }, s, z);
         s = block_sum(s, red);
         z = block_sum(z, red);
         if (threadIdx.x == 0) {
@@ -706,7 +960,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_wide(const TX* __re
 }
 
 // ---- schedules ------------------------------------------------------------------------------
-enum How { kFusedLast, kFusedFirst, kSplitLast, kSplitFirst, kCross, kWide };
+enum How { kFusedLast, kFusedFirst, kOnceLast, kSplitLast, kSplitFirst, kCross, kWide };
 struct Plan {
     How how;
     bool last;                    // layout of the partial sums
@@ -715,6 +969,7 @@ struct Plan {
     Tiles tiles;
     int slices, threads, per, chunks;
     size_t lds;
+    Once once;
 };
 
 Plan plan_backward(const GroupNorm& g) {
@@ -765,8 +1020,14 @@ Plan plan_backward(const GroupNorm& g) {
             return p;
         }
     }
-    p.how = kSplitLast;
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
+    p.lds = sizeof(float) * (size_t)(2 * p.rows.threads * V + g.C + 2 * g.groups);
+    if (p.lds <= kLdsMax && once_plan(g, p.rows, V == 4 || g.out_type != kTypeF32 ? 8 : 4, &p.once)) {
+        p.how = kOnceLast;
+        p.chunks = p.once.chunks;
+        return p;
+    }
+    p.how = kSplitLast;
     split_chunks(g.B, p.rows.ns, 4 * p.rows.q, 64 * p.rows.q, &p.per, &p.chunks);
     p.lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * g.C);
     return p;
@@ -774,15 +1035,27 @@ Plan plan_backward(const GroupNorm& g) {
 
 bool fused(const Plan& p) { return p.how == kFusedLast || p.how == kFusedFirst; }
 
+// (s1, s2) of each group, or the slots where chunks exchange theirs
+int64_t group_pairs(const GroupNorm& g, const Plan& p) {
+    return g.B * g.groups * (p.how == kOnceLast ? p.once.chunks : 1);
+}
+
 }  // namespace
 
 size_t gn_backward_workspace(const GroupNorm& g) {
-    return sizeof(float2) * (size_t)(g.B * g.C * plan_backward(g).chunks + g.B * g.groups);
+    const Plan p = plan_backward(g);
+    return sizeof(float2) * (size_t)(g.B * g.C * p.chunks + group_pairs(g, p));
 }
 
 int gn_backward_kernels(const GroupNorm& g, bool need_x, bool need_w, const char** names) {
     const Plan p = plan_backward(g);
     int k = 0;
+    if (p.how == kOnceLast) {
+        names[k++] = "gn_clear";
+        names[k++] = "gn_bwd_once";
+        if (need_w) names[k++] = "gn_bwd_finish";
+        return k;
+    }
     names[k++] = fused(p) ? "gn_bwd_fused" : p.how == kCross ? "gn_bwd_sums_cross" : "gn_bwd_sums";
     if (need_w || !fused(p)) names[k++] = "gn_bwd_finish";
     if (need_x && !fused(p)) names[k++] = p.how == kCross ? "gn_bwd_apply_cross" : "gn_bwd_apply";
@@ -795,9 +1068,11 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
     const int64_t runs = g.B * g.groups;
     float2* part = static_cast<float2*>(a.ws);
     float2* gsum = part + g.B * g.C * p.chunks;
-    if (kernel == 1) {
-        const bool need_groups = !fused(p) && a.grad_x, need_w = a.grad_weight || a.grad_bias;
-        const int64_t ngroups = need_groups ? runs : 0, blocks = (ngroups + 3) / 4 + (need_w ? C : 0);
+    if (p.how == kOnceLast && kernel == 0)
+        return launch_clear(reinterpret_cast<uint64_t*>(gsum), group_pairs(g, p), s);
+    if (kernel == (p.how == kOnceLast ? 2 : 1)) {
+        const bool need_groups = !fused(p) && p.how != kOnceLast && a.grad_x, need_w = a.grad_weight || a.grad_bias;
+        const int64_t ngroups = need_groups ? runs : 0, blocks = (ngroups + 3) / 4 + (!need_w ? 0 : p.last ? (C + 7) / 8 : C);
         return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kGnThreads), 0, s, (const float2*)part,
                              a.weight, gsum, a.grad_weight, a.grad_bias, g.B, C, D, p.chunks, p.last,
                              1.0f / ((float)D * (float)P), ngroups);
@@ -821,6 +1096,18 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
                 return launch_kernel(k_gn_bwd_fused_first<ACT, TX, TY>, grid_of(runs), dim3(p.threads), p.lds, s, x, dy,
                                      a.weight, a.bias, stats, gx, mine, D, P, (int)g.groups, fast_div(P), runs);
             }
+            if (p.how == kOnceLast)
+                return with_vectors(p.once.nv, [&](auto nv) {
+                    constexpr int NV = std::min(decltype(nv)::value, 8);
+                    const OnceArgs<TX, TY> args{x,  dy,
+                                                a.weight, a.bias,
+                                                stats, gx,
+                                                a.grad_weight || a.grad_bias ? part : nullptr,
+                                                reinterpret_cast<uint64_t*>(gsum),
+                                                p.rows, p.once, once_spin()};
+                    return launch_kernel(k_gn_bwd_once_last<ACT, NV, TX, TY>, dim3((unsigned)p.once.total),
+                                         dim3(p.rows.threads), p.lds, s, args);
+                });
             if (kernel == 0) {
                 if (p.how == kSplitLast) {
                     const int64_t blocks = g.B * p.chunks;
@@ -871,6 +1158,17 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
                                  dy, a.weight, a.bias, stats, gs, gx, p.tiles, C, P, D, blocks);
         });
     });
+}
+
+// ---- slots, empty ------------------------------------------------------------------------------
+namespace {
+__global__ __launch_bounds__(kGnThreads) void k_gn_clear(uint64_t* slots, int64_t n) {
+    const int64_t i = block_id() * kGnThreads + threadIdx.x;
+    if (i < n) slots[i] = kEmpty;
+}
+}  // namespace
+hipError_t launch_clear(uint64_t* slots, int64_t n, hipStream_t s) {
+    return launch_kernel(k_gn_clear, grid_of((n + kGnThreads - 1) / kGnThreads), dim3(kGnThreads), 0, s, slots, n);
 }
 
 // ---- both directions ---------------------------------------------------------------------------

@@ -424,6 +424,31 @@ def test_captured_and_replayed(b, c, grid, groups, last, out_last):
             assert all(torch.equal(p, q) for p, q in zip(got, want)), rep
 
 
+@pytest.mark.parametrize("b,c,grid,groups,dtype", [
+    (1, 32, (200, 200), 4, F32),       # one item over all workgroups
+    (5, 48, (64, 61), 6, F32),
+    (3, 30, (101, 67), 5, F16),        # incomplete super-rows
+    (32, 64, (128, 128), 8, F32),      # several rounds of items
+    (70, 32, (64, 64), 8, BF16),
+])
+@pytest.mark.parametrize("out_last", [True, False])
+def test_workgroups_that_do_not_wait(b, c, grid, groups, dtype, out_last, monkeypatch):
+    """Items spread over workgroups: one that does not see another's sums in
+    time forms them itself.  With no time at all, most do; the bits are the same."""
+    x = field((b, *grid, c), dtype, 180, 0.5)
+    w, bias = params(c, 180)
+    opts = dict(weight=w, bias=bias, act="gelu", channels_last=True, out_channels_last=out_last)
+    out, stats = fno.fno_group_norm(x, groups, **opts)
+    dy = field(out.shape, dtype, 181)
+    want = (out, stats, *fno.fno_group_norm_backward(x, stats, dy, groups, **opts))
+    for spin in ("0", "1"):
+        monkeypatch.setenv("FNO_GN_SPIN", spin)
+        out, stats = fno.fno_group_norm(x, groups, **opts)
+        got = (out, stats, *fno.fno_group_norm_backward(x, stats, dy, groups, **opts))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_streams_at_once():
     """Calls in flight on two streams share nothing."""
     cases = [(4, 64, (96, 96), 8, True, True), (4, 64, (96, 96), 8, False, True)]
