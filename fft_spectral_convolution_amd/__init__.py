@@ -17,6 +17,7 @@ import contextlib
 import ctypes
 import functools
 import math
+import operator
 import os
 import threading
 
@@ -599,39 +600,55 @@ def _group_norm_workspace_size(*key):
     return int(lib().fno_group_norm_workspace_size(*key))
 
 
-class _GroupNormCall:
-    """What the forward and the backward call have in common: checked sizes and options."""
+def _enqueue(torch, device, name, *args):
+    """Call a library function on the current stream of `device`."""
+    call = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = call(*args, _raw_stream(torch, device.index))
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, _raw_stream(torch, device.index))
+    if status:
+        _check(status, name)
 
-    __slots__ = ("device", "sizes", "options", "out_shape", "stats_shape", "weight", "bias", "x_type")
 
-    def __init__(self, torch, x, groups, weight, bias, act, channels_last, out_channels_last):
-        self.x_type = _field_type(torch, x, "x")
-        shape = x.shape
-        if len(shape) < 2:
-            raise ValueError(f"x must have a batch and a channel axis, got shape {tuple(shape)}")
-        code = _ACTIVATIONS.get(act, -1)
-        if code < 0:
-            raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, got {act!r}")
-        out_channels_last = channels_last if out_channels_last is None else out_channels_last
-        b = shape[0]
-        c = shape[-1] if channels_last else shape[1]
-        grid = shape[1:-1] if channels_last else shape[2:]
-        p = math.prod(grid)
-        if max(b, c, p) > 0x7fffffff:
-            raise ValueError(f"x is too large: shape {tuple(shape)}")
-        groups = int(groups)
-        self.device = device = x.device
-        self.weight = _f32_ptr(torch, weight, (c,), device, "weight")
-        self.bias = _f32_ptr(torch, bias, (c,), device, "bias")
-        self.sizes = (b, c, p, groups)
-        self.options = (code, 1 if channels_last else 0, 1 if out_channels_last else 0)
-        self.out_shape = (b, *grid, c) if out_channels_last else (b, c, *grid)
-        self.stats_shape = (b, max(groups, 0), 2)
+def _group_norm_args(torch, x, groups, weight, bias, act, channels_last, out_channels_last):
+    """Checked arguments of both directions: (weight, bias) addresses, (B, C, P, groups), (act, x_last, out_last,
+    x_type), out's shape and the statistics'."""
+    x_type = _field_type(torch, x, "x")
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError(f"x must have a batch and a channel axis, got shape {tuple(shape)}")
+    code = _ACTIVATIONS.get(act, -1)
+    if code < 0:
+        raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, got {act!r}")
+    if out_channels_last is None:
+        out_channels_last = channels_last
+    b = shape[0]
+    if channels_last:
+        c, grid = shape[-1], shape[1:-1]
+    else:
+        c, grid = shape[1], shape[2:]
+    p = math.prod(grid)
+    if b > 0x7fffffff or c > 0x7fffffff or p > 0x7fffffff:
+        raise ValueError(f"x is too large: shape {tuple(shape)}")
+    groups = int(groups)
+    device = x.device
+    params = (_f32_ptr(torch, weight, (c,), device, "weight"), _f32_ptr(torch, bias, (c,), device, "bias"))
+    out_shape = shape if bool(channels_last) == bool(out_channels_last) else \
+        (b, *grid, c) if out_channels_last else (b, c, *grid)
+    return (params, (b, c, p, groups), (code, 1 if channels_last else 0, 1 if out_channels_last else 0, x_type),
+            out_shape, (b, max(groups, 0), 2))
 
-    def workspace(self, torch, backward):
-        """Scratch of this call alone (so calls on other streams and captured graphs share none), or None."""
-        size = _group_norm_workspace_size(*self.sizes, self.options[1], self.options[2], self.x_type, backward)
-        return torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+
+def _group_norm_scratch(torch, x, sizes, options, backward):
+    """Scratch of one call alone (so calls on other streams and captured graphs share none): a tensor or None, its
+    address and size."""
+    size = _group_norm_workspace_size(*sizes, *options[1:], backward)
+    if not size:
+        return None, 0, 0
+    ws = x.new_empty(size, dtype=torch.uint8)
+    return ws, ws.data_ptr(), size
 
 
 def fno_group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: str = "none",
@@ -645,24 +662,26 @@ def fno_group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, ac
     float32 are optional; act is "none", "gelu" (the exact erf form) or "silu".  stats
     [B, groups, 2] float32 holds (mean, 1 / deviation) for fno_group_norm_backward."""
     torch = _torch()
-    call = _GroupNormCall(torch, x, groups, weight, bias, act, channels_last, out_channels_last)
-    device = call.device
+    params, sizes, options, out_shape, stats_shape = _group_norm_args(torch, x, groups, weight, bias, act,
+                                                                      channels_last, out_channels_last)
+    device = x.device
     if out is None:
-        out = torch.empty(call.out_shape, dtype=x.dtype if out_dtype is None else out_dtype, device=device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    out_type = _field_type(torch, out, "out", device)
-    if out.shape != call.out_shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {call.out_shape}")
+        out = x.new_empty(out_shape, dtype=out_dtype)
+        out_type = options[3] if out_dtype is None else _field_type(torch, out, "out")
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        out_type = _field_type(torch, out, "out", device)
+        if out.shape != out_shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(out_shape)}")
     if stats is None:
-        stats = torch.empty(call.stats_shape, dtype=torch.float32, device=device)
-    stats_ptr = _f32_ptr(torch, stats, call.stats_shape, device, "stats")
-    with _on_device(x):
-        ws = call.workspace(torch, 0)
-        _check(lib().fno_group_norm(x.data_ptr(), call.weight, call.bias, out.data_ptr(), stats_ptr, *call.sizes, eps,
-                                    *call.options, call.x_type, out_type, 0 if ws is None else ws.data_ptr(),
-                                    0 if ws is None else ws.numel(), _raw_stream(torch, device.index)),
-               "fno_group_norm")
+        stats = x.new_empty(stats_shape, dtype=torch.float32)
+        stats_ptr = stats.data_ptr()
+    else:
+        stats_ptr = _f32_ptr(torch, stats, stats_shape, device, "stats")
+    ws, ws_ptr, ws_size = _group_norm_scratch(torch, x, sizes, options, 0)
+    _enqueue(torch, device, "fno_group_norm", x.data_ptr(), *params, out.data_ptr(), stats_ptr, *sizes, eps, *options,
+             out_type, ws_ptr, ws_size)
     return out, stats
 
 
@@ -673,60 +692,66 @@ def fno_group_norm_backward(x, stats, grad_out, groups: int, weight=None, bias=N
     and options, and grad_out of its output's layout and type.  need_x / need_w choose the field's and the
     parameters' gradients; those not asked for, or of a parameter that is None, are returned as None."""
     torch = _torch()
-    call = _GroupNormCall(torch, x, groups, weight, bias, act, channels_last, out_channels_last)
-    device = call.device
+    params, sizes, options, out_shape, stats_shape = _group_norm_args(torch, x, groups, weight, bias, act,
+                                                                      channels_last, out_channels_last)
+    device = x.device
     out_type = _field_type(torch, grad_out, "grad_out", device)
-    if grad_out.shape != call.out_shape:
-        raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, expected {call.out_shape}")
+    if grad_out.shape != out_shape:
+        raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, expected {tuple(out_shape)}")
     if stats is None:
         raise ValueError("stats must be what fno_group_norm returned")
-    stats_ptr = _f32_ptr(torch, stats, call.stats_shape, device, "stats")
+    stats_ptr = _f32_ptr(torch, stats, stats_shape, device, "stats")
     if not (need_x or (need_w and (weight is not None or bias is not None))):
         raise ValueError("ask for at least one gradient")
     gx = gw = gb = None
+    gx_ptr = 0
     if need_x:
-        gx = torch.empty_like(x) if grad_x is None else grad_x
-        if _field_type(torch, gx, "grad_x", device) != call.x_type or gx.shape != x.shape:
-            raise ValueError(f"grad_x must match {tuple(x.shape)} {x.dtype}")
+        if grad_x is None:
+            gx = torch.empty_like(x)
+        else:
+            gx = grad_x
+            if _field_type(torch, gx, "grad_x", device) != options[3] or gx.shape != x.shape:
+                raise ValueError(f"grad_x must match {tuple(x.shape)} {x.dtype}")
+        gx_ptr = gx.data_ptr()
     if need_w and weight is not None:
         gw = torch.empty_like(weight) if grad_weight is None else grad_weight
     if need_w and bias is not None:
         gb = torch.empty_like(bias) if grad_bias is None else grad_bias
-    channels = (call.sizes[1],)
+    channels = (sizes[1],)
     gw_ptr = _f32_ptr(torch, gw, channels, device, "grad_weight")
     gb_ptr = _f32_ptr(torch, gb, channels, device, "grad_bias")
-    with _on_device(x):
-        ws = call.workspace(torch, 1)
-        _check(lib().fno_group_norm_backward(x.data_ptr(), call.weight, call.bias, stats_ptr, grad_out.data_ptr(),
-                                             0 if gx is None else gx.data_ptr(), gw_ptr, gb_ptr, *call.sizes,
-                                             *call.options, call.x_type, out_type, 0 if ws is None else ws.data_ptr(),
-                                             0 if ws is None else ws.numel(), _raw_stream(torch, device.index)),
-               "fno_group_norm_backward")
+    ws, ws_ptr, ws_size = _group_norm_scratch(torch, x, sizes, options, 1)
+    _enqueue(torch, device, "fno_group_norm_backward", x.data_ptr(), *params, stats_ptr, grad_out.data_ptr(), gx_ptr,
+             gw_ptr, gb_ptr, *sizes, *options, out_type, ws_ptr, ws_size)
     return gx, gw, gb
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _tensor_table(torch, tensors, name):
-    """Host arrays (addresses, element counts, types) of a list of tensors, and their device.  Attribute by
-    attribute over the whole list: a model has hundreds of gradients, and this is most of a call's host time."""
+    """Host arrays (addresses, element counts, types) of a list of tensors, and their device.  One attribute of
+    all tensors at a time, by map: a model has hundreds of gradients, and this is most of a call's host time."""
     tensors = list(tensors)
     if not tensors:
         return tensors, array.array("Q"), array.array("q"), array.array("i"), \
             torch.device("cuda", torch.cuda.current_device())
-    if not all([isinstance(t, torch.Tensor) for t in tensors]):
-        raise TypeError(f"{name} must be torch tensors")
-    index = tensors[0].get_device()
-    if index < 0 or not all([t.get_device() == index for t in tensors]):
-        raise ValueError(f"{name} must live on one GPU device")
-    codes = _element_types()
+    tensor = torch.Tensor
     try:
-        types = array.array("i", [codes[t.dtype] for t in tensors])
+        devices = set(map(tensor.get_device, tensors))
+    except TypeError:
+        raise TypeError(f"{name} must be torch tensors") from None
+    if len(devices) > 1 or min(devices) < 0:
+        raise ValueError(f"{name} must live on one GPU device")
+    try:
+        types = array.array("i", map(_element_types().__getitem__, map(_dtype_of, tensors)))
     except KeyError as e:
         raise TypeError(f"{name} must be float32, bfloat16, float16 or complex64, got {e.args[0]}") from None
-    if not all([t.is_contiguous() for t in tensors]):
+    if not all(map(tensor.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    if 3 in types and any(t.is_conj() for t, k in zip(tensors, types) if k == 3):
+    if 3 in types and any([t.is_conj() for t, k in zip(tensors, types) if k == 3]):
         raise ValueError(f"{name} must not be lazily conjugated (call resolve_conj())")
-    return (tensors, array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]),
+    return (tensors, array.array("Q", map(tensor.data_ptr, tensors)), array.array("q", map(tensor.numel, tensors)),
             types, tensors[0].device)
 
 
@@ -747,11 +772,9 @@ def fno_grad_norm(grads, out=None):
     torch = _torch()
     grads, ptrs, numels, types, device = _tensor_table(torch, grads, "grads")
     out = _norm_scalar(torch, out, device, "out")
-    with _on_device(out):
-        ws = _grad_workspace(torch, len(grads), device)
-        _check(lib().fno_grad_norm(ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], len(grads),
-                                   out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(torch, device.index)),
-               "fno_grad_norm")
+    ws = _grad_workspace(torch, len(grads), device)
+    _enqueue(torch, device, "fno_grad_norm", ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0],
+             len(grads), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -772,13 +795,11 @@ def fno_clip_grad_norm(grads, max_norm: float, norm=None, out=None):
             raise ValueError(f"out must be on {device}")
     given = norm is not None
     norm = _norm_scalar(torch, norm, device, "norm")
-    with _on_device(norm):
-        ws = _grad_workspace(torch, len(grads), device)
-        at = norm.data_ptr()
-        _check(lib().fno_clip_grad_norm(ptrs.buffer_info()[0], outs.buffer_info()[0], numels.buffer_info()[0],
-                                        types.buffer_info()[0], len(grads), max_norm, at if given else 0,
-                                        0 if given else at, ws.data_ptr(), ws.numel(),
-                                        _raw_stream(torch, device.index)), "fno_clip_grad_norm")
+    ws = _grad_workspace(torch, len(grads), device)
+    at = norm.data_ptr()
+    _enqueue(torch, device, "fno_clip_grad_norm", ptrs.buffer_info()[0], outs.buffer_info()[0], numels.buffer_info()[0],
+             types.buffer_info()[0], len(grads), max_norm, at if given else 0, 0 if given else at, ws.data_ptr(),
+             ws.numel())
     return norm
 
 
