@@ -749,7 +749,7 @@ def _tensor_table(torch, tensors, name):
         raise TypeError(f"{name} must be float32, bfloat16, float16 or complex64, got {e.args[0]}") from None
     if not all(map(tensor.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    if 3 in types and any([t.is_conj() for t, k in zip(tensors, types) if k == 3]):
+    if 3 in types and any(map(tensor.is_conj, tensors)):
         raise ValueError(f"{name} must not be lazily conjugated (call resolve_conj())")
     return (tensors, array.array("Q", map(tensor.data_ptr, tensors)), array.array("q", map(tensor.numel, tensors)),
             types, tensors[0].device)

@@ -609,21 +609,76 @@ __global__ __launch_bounds__(kOnceThreads, 4) void k_gn_once_last(OnceArgs<TX, T
     f.write(at, rows, [&](int i) { return cur[i]; });
 }
 
+// ---- chunks joined by the kernel that writes the output ------------------------------------
+// With few chunks every workgroup of the output joins those of its own groups
+// (a launch less: 3.5 us of a small call); `part` is null where k_gn_finish
+// has done it.
+struct Join {
+    const float2* part;
+    int chunks, groups;
+    bool last;
+    int64_t per, n;
+    float eps;
+};
+// (mean, 1 / deviation) of groups g0 .. g0 + ng - 1 (numbered over the items),
+// to res[2 i], res[2 i + 1] in LDS; `own` also stores them to stats.
+__device__ __forceinline__ void join_chunks(const Join& f, int64_t g0, int ng, float* res, bool own,
+                                            float* __restrict__ stats) {
+    const int t = threadIdx.x, threads = blockDim.x;
+    int parts = 1;
+    while (parts < 64 && 2 * parts * ng <= threads && parts < f.chunks) parts *= 2;
+    const int part = t & (parts - 1);
+    for (int i = t / parts; i < ng; i += threads / parts) {
+        const int64_t g = g0 + i;
+        const float2* p = f.part + (f.last ? g / f.groups * f.chunks * f.groups + g % f.groups : g * f.chunks);
+        const int step = f.last ? f.groups : 1;
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int k = part; k < f.chunks; k += parts)
+            sum = fmaf((float)min(f.per, f.n - k * f.per), p[(int64_t)k * step].x, sum);
+        const float mean = team_sum(sum, parts) / (float)f.n;
+        sum = 0.0f;
+#pragma unroll 4
+        for (int k = part; k < f.chunks; k += parts) {
+            const float2 q = p[(int64_t)k * step];
+            const float d = q.x - mean;
+            sum += fmaf((float)min(f.per, f.n - k * f.per) * d, d, q.y);
+        }
+        sum = team_sum(sum, parts);
+        if (part == 0) {
+            const float rstd = rsqrtf(sum / (float)f.n + f.eps);
+            res[2 * i] = mean;
+            res[2 * i + 1] = rstd;
+            if (own) {
+                stats[2 * g] = mean;
+                stats[2 * g + 1] = rstd;
+            }
+        }
+    }
+    __syncthreads();
+}
+
 // ---- output, the layout kept ------------------------------------------------------------
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kMaxSlots) void k_gn_apply_last(const TX* __restrict__ x, const float* __restrict__ w,
-                                                             const float* __restrict__ bias,
-                                                             const float* __restrict__ stats, TY* __restrict__ out,
-                                                             LastRows r, int per, int chunks, int64_t blocks) {
+                                                             const float* __restrict__ bias, float* stats,
+                                                             TY* __restrict__ out, LastRows r, Join f, int per,
+                                                             int chunks, int64_t blocks) {
     constexpr int V = kVec<TX>;
+    extern __shared__ float joined[];
     const int64_t id = block_id();
     if (id >= blocks) return;
     const int64_t b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
     const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
+    const int groups = div_by(r.C, r.by_D);
+    const float* st = stats + 2 * b * groups;
+    if (f.part) {
+        join_chunks(f, b * groups, groups, joined, first == 0, stats);
+        st = joined;
+    }
     if (row >= r.q) return;
     const int64_t base = b * r.P * r.C + slot * V;
-    const float* st = stats + 2 * b * (div_by(r.C, r.by_D));
     float m[V], a[V], o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -658,17 +713,25 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_apply_last(const TX* __restric
 
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_apply_first(const TX* __restrict__ x, const float* __restrict__ w,
-                                                               const float* __restrict__ bias,
-                                                               const float* __restrict__ stats, TY* __restrict__ out,
-                                                               FirstRows r, int C, int D, int64_t blocks) {
+                                                               const float* __restrict__ bias, float* stats,
+                                                               TY* __restrict__ out, FirstRows r, Join f, int C, int D,
+                                                               int64_t blocks) {
     constexpr int V = kVec<TX>;
+    extern __shared__ float joined[];
     const int64_t id = block_id();
     if (id >= blocks) return;
-    const int64_t row = id / r.chunks * (kGnThreads / r.team) + threadIdx.x / r.team;
-    if (row >= r.rows) return;
+    const int teams = kGnThreads / r.team;
+    const int64_t row0 = id / r.chunks * teams, row = row0 + threadIdx.x / r.team;
     const int at = (int)(id % r.chunks) * r.piece, end = min(at + r.piece, r.P);
-    const int c = (int)(row % C);
     const float* st = stats + 2 * (row / D);
+    if (f.part) {
+        // every workgroup that holds a part of a group may store its statistics: the same bits
+        const int64_t g0 = row0 / D, g1 = min(row0 + teams - 1, r.rows - 1) / D;
+        join_chunks(f, g0, (int)(g1 - g0) + 1, joined, at == 0, stats);
+        st = joined + 2 * (row / D - g0);
+    }
+    if (row >= r.rows) return;
+    const int c = (int)(row % C);
     const float m = st[0], a = st[1] * or_one(w, c), o = or_zero(bias, c);
     const int64_t base = row * r.P;
     for (int p = at + (threadIdx.x & (r.team - 1)) * V; p < end; p += r.team * V) {
@@ -686,11 +749,12 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_first(const TX* __restr
 // out's.
 template <int ACT, bool XLAST, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_apply_cross(const TX* __restrict__ x, const float* __restrict__ w,
-                                                               const float* __restrict__ bias,
-                                                               const float* __restrict__ stats, TY* __restrict__ out,
-                                                               Tiles q, int C, int P, int D, int64_t blocks) {
+                                                               const float* __restrict__ bias, float* stats,
+                                                               TY* __restrict__ out, Tiles q, Join f, int C, int P,
+                                                               int D, int64_t blocks) {
     constexpr int V = kVec<TX>, VY = kVec<TY>;
     __shared__ float tile[kTileLds];
+    __shared__ float joined[2 * kMaxTileChannels];
     const int64_t id = block_id();
     if (id >= blocks) return;
     const int64_t b = id / q.tiles_c / q.tiles_p;
@@ -700,6 +764,11 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_cross(const TX* __restr
     const int nc = min(q.tc(), C - c0), np = min(q.tp(), P - p0);
     const float* st = stats + 2 * b * (C / D);
     const int64_t item = b * (int64_t)P * C;
+    if (f.part) {
+        const int g0 = c0 / D;
+        join_chunks(f, b * (C / D) + g0, (c0 + nc - 1) / D - g0 + 1, joined, p0 == 0, stats);
+        st = joined - 2 * g0;
+    }
     if constexpr (XLAST) {
         const int lv = q.log2c - (V == 4 ? 2 : 3);           // log2 of vectors a row
         const int c = (t & ((1 << lv) - 1)) * V, n = max(0, min(V, nc - c));
@@ -809,7 +878,14 @@ struct Plan {
     int per, chunks;              // split: super-rows or values a chunk
     int64_t parts;                // float2 of workspace
     Once once;
+    bool join;                    // split: the output's workgroups join the chunks
 };
+
+// Joining in every workgroup of the output reads `groups` times the chunks' pairs in each: worth it while those are
+// few and the workgroups too.
+bool joins(const GroupNorm& g, int chunks) {
+    return (int64_t)chunks * g.groups <= 1024 && g.B * g.C * g.P <= (int64_t)4096 * 4096;
+}
 
 size_t once_lds(const GroupNorm& g, const Plan& p) {
     const LastRows& r = p.rows;
@@ -835,6 +911,7 @@ Plan plan_forward(const GroupNorm& g) {
         p.how = kSplitFirst;
         split_chunks(g.B * g.groups, n, 4 * kGnThreads * V, 64 * kGnThreads * V, &p.per, &p.chunks);
         p.parts = g.B * g.groups * p.chunks;
+        p.join = joins(g, p.chunks);
         return p;
     }
     if (!last_rows_ok(g.C, V)) {
@@ -870,6 +947,7 @@ Plan plan_forward(const GroupNorm& g) {
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
     split_chunks(g.B, p.rows.ns, 4 * p.rows.q, 64 * p.rows.q, &p.per, &p.chunks);
     p.parts = g.B * p.chunks * g.groups;
+    p.join = joins(g, p.chunks);
     return p;
 }
 
@@ -890,10 +968,11 @@ int gn_forward_kernels(const GroupNorm& g, const char** names) {
         names[1] = "gn_once";
         return 2;
     }
+    const bool two = p.how == kWide || p.join;
     names[0] = p.how == kWide ? "gn_stats_wide" : "gn_stats";
-    names[1] = p.how == kWide ? apply : "gn_finish";
+    names[1] = two ? apply : "gn_finish";
     names[2] = apply;
-    return p.how == kWide ? 2 : 3;
+    return two ? 2 : 3;
 }
 
 hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int kernel, hipStream_t s) {
@@ -907,7 +986,10 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
         constexpr int V = kVec<TX>;
         const TX* x = static_cast<const TX*>(a.x);
         TY* out = static_cast<TY*>(a.out);
-        const float* stats = a.stats;
+        float* stats = a.stats;
+        const bool last = p.how == kSplitLast;
+        const int64_t per = last ? (int64_t)p.per * p.rows.R * D : p.per;
+        const Join join{p.join ? part : nullptr, p.chunks, (int)g.groups, last, per, n, g.eps};
         const size_t lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * (D ? p.rows.cs / D : 0));
         if (kernel == 0 && p.how == kOnceLast)
             return launch_clear((uint64_t*)part, p.parts, s);
@@ -924,9 +1006,7 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
         if (kernel == 0 && p.how == kWide)
             return launch_kernel(k_gn_stats_wide<TX>, grid_of(runs), dim3(kGnThreads), 0, s, x, a.stats, g.C, D, g.P,
                                  runs, g.eps);
-        if (kernel == 1 && p.how != kWide && p.how != kOnceLast) {
-            const bool last = p.how == kSplitLast;
-            const int64_t per = last ? (int64_t)p.per * p.rows.R * D : p.per;
+        if (kernel == 1 && p.how != kWide && p.how != kOnceLast && !p.join) {
             return launch_kernel(k_gn_finish, grid_of(runs), dim3(kGnThreads), 0, s, (const float2*)part,
                                  a.stats, runs, (int)g.groups, p.chunks, last, per, n, g.eps);
         }
@@ -956,26 +1036,28 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
                 const int64_t blocks = g.B * q.tiles_c * q.tiles_p;
                 if (g.x_last)
                     return launch_kernel(k_gn_apply_cross<ACT, true, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s,
-                                         x, a.weight, a.bias, stats, out, q, C, P, D, blocks);
+                                         x, a.weight, a.bias, stats, out, q, join, C, P, D, blocks);
                 return launch_kernel(k_gn_apply_cross<ACT, false, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
-                                     a.weight, a.bias, stats, out, q, C, P, D, blocks);
+                                     a.weight, a.bias, stats, out, q, join, C, P, D, blocks);
             }
             if (p.how == kSplitLast) {
                 // eight vectors a thread: 32 KiB of a 16-byte-vector field a workgroup
                 const int per = std::min(8 * p.rows.q, p.rows.ns), chunks = (p.rows.ns + per - 1) / per;
                 const int64_t blocks = g.B * chunks;
-                return launch_kernel(k_gn_apply_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), 0, s, x,
-                                     a.weight, a.bias, stats, out, p.rows, per, chunks, blocks);
+                return launch_kernel(k_gn_apply_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads),
+                                     p.join ? sizeof(float) * 2 * (size_t)g.groups : 0, s, x, a.weight, a.bias, stats,
+                                     out, p.rows, join, per, chunks, blocks);
             }
             if (p.how == kSplitFirst) {
                 const FirstRows r = first_rows(g.B * g.C, g.P, V, 8);
                 const int64_t blocks = first_blocks(r);
-                return launch_kernel(k_gn_apply_first<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
-                                     a.weight, a.bias, stats, out, r, C, D, blocks);
+                return launch_kernel(k_gn_apply_first<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads),
+                                     p.join ? sizeof(float) * 2 * kGnThreads : 0, s, x, a.weight, a.bias, stats, out,
+                                     r, join, C, D, blocks);
             }
             const int64_t blocks = g.B * g.P;
             return launch_kernel(k_gn_apply_wide<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x, a.weight,
-                                 a.bias, stats, out, g.C, D, g.P, blocks);
+                                 a.bias, (const float*)stats, out, g.C, D, g.P, blocks);
         });
     });
 }

@@ -306,6 +306,7 @@ inline Tiles tiles_of(int64_t C, int64_t P) {
     t.tiles_c = (int)((C + t.tc() - 1) / t.tc());
     return t;
 }
+constexpr int kMaxTileChannels = 64;
 constexpr int kTileLds = kTile + 256;     // tc (tp + 1) <= 4096 + 64
 
 __device__ __forceinline__ float or_one(const float* w, int64_t c) { return w ? w[c] : 1.0f; }

@@ -730,10 +730,19 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __res
 }
 
 // ---- joining the partial sums -----------------------------------------------------------
-// First (with gsum) the B G groups' (s1, s2), a wave each; then the C channels'
-// gradients, a workgroup for each or for eight, over items and chunks.  The partial sums come
-// from other XCDs' kernels and are far away (a microsecond), so a lane asks
-// for eight at a time.
+// Partial sums of a backward pass: pair (b, chunk, c) is part[(b chunks +
+// chunk) C + c] (`last`) or part[(b C + c) chunks + chunk].  They come from
+// other XCDs' kernels and are far away (a microsecond), so a lane asks for
+// eight at a time.
+struct Parts {
+    const float2* part;
+    int64_t B;
+    int C, D, chunks;
+    bool last;
+    float inv_n;
+    float *gw, *gb;
+};
+
 template <typename F>
 __device__ __forceinline__ void sum_parts(int64_t n, int first, int step, F&& at, float& s, float& z) {
     for (int64_t k = first; k < n; k += 8 * step) {
@@ -748,58 +757,86 @@ __device__ __forceinline__ void sum_parts(int64_t n, int first, int step, F&& at
     }
 }
 
-__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(const float2* __restrict__ part,
-                                                              const float* __restrict__ w, float2* __restrict__ gsum,
-                                                              float* __restrict__ gw, float* __restrict__ gb, int64_t B,
-                                                              int C, int D, int chunks, bool last, float inv_n,
-                                                              int64_t ngroups) {
-    __shared__ float red[16];
+// s1 and s2 of group `g` (numbered over the items), added by `parts` lanes.
+__device__ __forceinline__ float2 group_sums(const Parts& f, const float* __restrict__ w, int64_t g, int part,
+                                             int parts) {
+    const int groups = f.C / f.D;
+    const int64_t b = g / groups;
+    const int c0 = (int)(g % groups) * f.D;
+    float s = 0.0f, z = 0.0f;
+    sum_parts((int64_t)f.D * f.chunks, part, parts, [&](int64_t k) {
+        const uint32_t e = (uint32_t)k, by = (uint32_t)(f.last ? f.D : f.chunks);
+        const int hi = (int)(e / by), lo = (int)(e - hi * by), d = f.last ? lo : hi, ch = f.last ? hi : lo;
+        const float2 q = f.part[f.last ? (b * f.chunks + ch) * f.C + c0 + d : (b * f.C + c0 + d) * f.chunks + ch];
+        const float wc = or_one(w, c0 + d);
+        return make_float2(wc * q.x, wc * q.y);
+    }, s, z);
+    return make_float2(team_sum(s, parts) * f.inv_n, team_sum(z, parts) * f.inv_n);
+}
+
+// The parameters' gradients, over items and chunks, a workgroup for eight
+// channels (`last`: their pairs share a 64-byte piece of each chunk's row) or
+// for one.  `both` holds a float2 a thread.
+__device__ __forceinline__ void param_sums(const Parts& f, int64_t block, float2* both) {
+    const int t = threadIdx.x, threads = blockDim.x, per = f.last ? 8 : 1;
+    const int64_t c = block * per + t % per;
+    float s = 0.0f, z = 0.0f;
+    if (c < f.C) {
+        if (f.last) {
+            sum_parts(f.B * f.chunks, t / 8, threads / 8, [&](int64_t k) { return f.part[k * f.C + c]; }, s, z);
+        } else {
+            sum_parts(f.B * f.chunks, t, threads,
+                      [&](int64_t k) { return f.part[(k / f.chunks * f.C + c) * f.chunks + k % f.chunks]; }, s, z);
+        }
+    }
+    both[t] = make_float2(s, z);
+    // halves added until a row of `per` is left (a row without a partner stays)
+    for (int rows = threads / per; rows > 1;) {
+        const int keep = (rows + 1) / 2;
+        __syncthreads();
+        if (t < (rows - keep) * per) {
+            both[t].x += both[t + keep * per].x;
+            both[t].y += both[t + keep * per].y;
+        }
+        rows = keep;
+    }
+    if (t < per && c < f.C) {
+        if (f.gb) f.gb[c] = both[t].x;
+        if (f.gw) f.gw[c] = both[t].y;
+    }
+}
+inline int64_t param_blocks(const Parts& f) {
+    return !f.gw && !f.gb ? 0 : f.last ? (f.C + 7) / 8 : f.C;
+}
+
+// First (with gsum) the B G groups' (s1, s2), a wave each; then the parameters.
+__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(Parts f, const float* __restrict__ w,
+                                                              float2* __restrict__ gsum, int64_t ngroups) {
     __shared__ float2 both[kGnThreads];
     const int64_t id = block_id(), gblocks = (ngroups + 3) / 4;
-    float s = 0.0f, z = 0.0f;
     if (id < gblocks) {
         const int64_t i = id * 4 + (threadIdx.x >> 6);
         if (i >= ngroups) return;
-        const int64_t b = i / (C / D);
-        const int c0 = (int)(i % (C / D)) * D;
-        sum_parts((int64_t)D * chunks, threadIdx.x & 63, 64, [&](int64_t k) {
-            const int d = last ? (int)(k % D) : (int)(k / chunks), ch = last ? (int)(k / D) : (int)(k % chunks);
-            const float2 q = part[last ? (b * chunks + ch) * C + c0 + d : (b * C + c0 + d) * chunks + ch];
-            const float wc = or_one(w, c0 + d);
-            return make_float2(wc * q.x, wc * q.y);
-        }, s, z);
-        s = wave_sum(s);
-        z = wave_sum(z);
-        if ((threadIdx.x & 63) == 0) gsum[i] = make_float2(s * inv_n, z * inv_n);
-    } else if (last) {
-        // eight channels a workgroup: their pairs share a 64-byte piece of each chunk's row
-        const int64_t c = (id - gblocks) * 8 + (threadIdx.x & 7);
-        if (c < C)
-            sum_parts(B * chunks, threadIdx.x >> 3, kGnThreads / 8, [&](int64_t k) { return part[k * C + c]; }, s, z);
-        both[threadIdx.x] = make_float2(s, z);
-        __syncthreads();
-        for (int half = kGnThreads / 2; half >= 8; half >>= 1) {
-            if ((int)threadIdx.x < half) {
-                both[threadIdx.x].x += both[threadIdx.x + half].x;
-                both[threadIdx.x].y += both[threadIdx.x + half].y;
-            }
-            __syncthreads();
-        }
-        if (threadIdx.x < 8 && c < C) {
-            if (gb) gb[c] = both[threadIdx.x].x;
-            if (gw) gw[c] = both[threadIdx.x].y;
-        }
-    } else if (id - gblocks < C) {
-        const int64_t c = id - gblocks;
-        sum_parts(B * chunks, threadIdx.x, kGnThreads,
-                  [&](int64_t k) { return part[(k / chunks * C + c) * chunks + k % chunks]; }, s, z);
-        s = block_sum(s, red);
-        z = block_sum(z, red);
-        if (threadIdx.x == 0) {
-            if (gb) gb[c] = s;
-            if (gw) gw[c] = z;
-        }
+        const float2 s = group_sums(f, w, i, threadIdx.x & 63, 64);
+        if ((threadIdx.x & 63) == 0) gsum[i] = s;
+    } else if ((id - gblocks) * (f.last ? 8 : 1) < f.C) {
+        param_sums(f, id - gblocks, both);
     }
+}
+
+// With few chunks there is no k_gn_bwd_finish: the workgroups of grad_x add
+// their own groups' sums (Parts::part not null), and further workgroups behind
+// them the parameters' gradients.
+__device__ __forceinline__ void join_groups(const Parts& f, const float* __restrict__ w, int64_t g0, int ng,
+                                            float2* res) {
+    const int t = threadIdx.x, threads = blockDim.x;
+    int parts = 1;
+    while (parts < 64 && 2 * parts * ng <= threads) parts *= 2;
+    for (int i = t / parts; i < ng; i += threads / parts) {
+        const float2 s = group_sums(f, w, g0 + i, t & (parts - 1), parts);
+        if ((t & (parts - 1)) == 0) res[i] = s;
+    }
+    __syncthreads();
 }
 
 // ---- grad_x --------------------------------------------------------------------------------
@@ -809,17 +846,28 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_apply_last(const TX* __res
                                                                  const float* __restrict__ bias,
                                                                  const float* __restrict__ stats,
                                                                  const float2* __restrict__ gsum, TX* __restrict__ gx,
-                                                                 LastRows r, int per, int chunks, int64_t blocks) {
+                                                                 LastRows r, Parts f, int per, int chunks,
+                                                                 int64_t blocks, int64_t extra) {
     constexpr int V = kVec<TX>;
+    extern __shared__ float2 joined[];
     const int64_t id = block_id();
-    if (id >= blocks) return;
+    if (id >= blocks + extra) return;
+    if (id >= blocks) {
+        param_sums(f, id - blocks, joined);
+        return;
+    }
     const int64_t b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, r.ns);
     const int t = threadIdx.x, row = div_by(t, r.by_cv), slot = t - row * r.cv;
+    const int groups = div_by(r.C, r.by_D);
+    const float2* gs = gsum + b * groups;
+    if (f.part) {
+        join_groups(f, w, b * groups, groups, joined);
+        gs = joined;
+    }
     if (row >= r.q) return;
     const int64_t base = b * r.P * r.C + slot * V;
-    const float* st = stats + 2 * b * (div_by(r.C, r.by_D));
-    const float2* gs = gsum + b * (div_by(r.C, r.by_D));
+    const float* st = stats + 2 * b * groups;
     float m[V], k[V], a[V], o[V], s1[V], s2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -853,17 +901,29 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_first(const TX* __r
                                                                    const float* __restrict__ bias,
                                                                    const float* __restrict__ stats,
                                                                    const float2* __restrict__ gsum,
-                                                                   TX* __restrict__ gx, FirstRows r, int C, int D,
-                                                                   int64_t blocks) {
+                                                                   TX* __restrict__ gx, FirstRows r, Parts f, int C,
+                                                                   int D, int64_t blocks, int64_t extra) {
     constexpr int V = kVec<TX>;
+    __shared__ float2 joined[kGnThreads];
     const int64_t id = block_id();
-    if (id >= blocks) return;
-    const int64_t row = id / r.chunks * (kGnThreads / r.team) + threadIdx.x / r.team;
+    if (id >= blocks + extra) return;
+    if (id >= blocks) {
+        param_sums(f, id - blocks, joined);
+        return;
+    }
+    const int teams = kGnThreads / r.team;
+    const int64_t row0 = id / r.chunks * teams, row = row0 + threadIdx.x / r.team;
+    int64_t g0 = 0;
+    if (f.part) {
+        g0 = row0 / D;
+        join_groups(f, w, g0, (int)(min(row0 + teams - 1, r.rows - 1) / D - g0) + 1, joined);
+        gsum = joined;
+    }
     if (row >= r.rows) return;
     const int at = (int)(id % r.chunks) * r.piece, end = min(at + r.piece, r.P);
     const int c = (int)(row % C);
     const float* st = stats + 2 * (row / D);
-    const float2 gs = gsum[row / D];
+    const float2 gs = gsum[row / D - g0];
     const float m = st[0], k = st[1], a = or_one(w, c), o = or_zero(bias, c);
     const int64_t base = row * r.P;
     for (int p = at + (threadIdx.x & (r.team - 1)) * V; p < end; p += r.team * V) {
@@ -887,12 +947,17 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_cross(const TX* __r
                                                                    const float* __restrict__ bias,
                                                                    const float* __restrict__ stats,
                                                                    const float2* __restrict__ gsum,
-                                                                   TX* __restrict__ gx, Tiles q, int C, int P, int D,
-                                                                   int64_t blocks) {
+                                                                   TX* __restrict__ gx, Tiles q, Parts f, int C, int P,
+                                                                   int D, int64_t blocks, int64_t extra) {
     constexpr int V = kVec<TX>, N = kTile / V / kGnThreads;
     __shared__ float tile[kTileLds];
+    __shared__ float2 joined[kGnThreads];
     const int64_t id = block_id();
-    if (id >= blocks) return;
+    if (id >= blocks + extra) return;
+    if (id >= blocks) {
+        param_sums(f, id - blocks, joined);
+        return;
+    }
     const int64_t b = id / q.tiles_c / q.tiles_p;
     const int r0 = (int)(id % ((int64_t)q.tiles_c * q.tiles_p));
     const int c0 = r0 % q.tiles_c << q.log2c, p0 = r0 / q.tiles_c * q.tp();
@@ -901,6 +966,11 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_cross(const TX* __r
     const int lv = (XLAST ? q.log2c : 12 - q.log2c) - (V == 4 ? 2 : 3);
     const float* st = stats + 2 * b * (C / D);
     const float2* gs = gsum + b * (C / D);
+    if (f.part) {
+        const int g0 = c0 / D;
+        join_groups(f, w, b * (C / D) + g0, (c0 + nc - 1) / D - g0 + 1, joined);
+        gs = joined - g0;
+    }
     const int64_t item = b * (int64_t)P * C;
     load_turned(dy, tile, q, !XLAST, item, c0, p0, nc, np, C, P);
     constexpr int S = XLAST ? V : N;
@@ -970,9 +1040,10 @@ struct Plan {
     int slices, threads, per, chunks;
     size_t lds;
     Once once;
+    bool join;                    // no k_gn_bwd_finish
 };
 
-Plan plan_backward(const GroupNorm& g) {
+Plan plan_kernels(const GroupNorm& g) {
     const int V = vec_of(g);
     const int64_t D = g.C / g.groups, n = D * g.P;
     const int64_t capacity = (int64_t)kFusedThreads * kHeld;      // vectors
@@ -1033,6 +1104,15 @@ Plan plan_backward(const GroupNorm& g) {
     return p;
 }
 
+// Joining in every workgroup of grad_x reads its item's partial sums in each: worth it while those and the
+// workgroups are few.
+Plan plan_backward(const GroupNorm& g) {
+    Plan p = plan_kernels(g);
+    const bool split = p.how == kSplitLast || p.how == kSplitFirst || p.how == kCross;
+    p.join = split && g.C * p.chunks <= 2048 && g.B * g.C * g.P <= (int64_t)4096 * 4096;
+    return p;
+}
+
 bool fused(const Plan& p) { return p.how == kFusedLast || p.how == kFusedFirst; }
 
 // (s1, s2) of each group, or the slots where chunks exchange theirs
@@ -1057,7 +1137,7 @@ int gn_backward_kernels(const GroupNorm& g, bool need_x, bool need_w, const char
         return k;
     }
     names[k++] = fused(p) ? "gn_bwd_fused" : p.how == kCross ? "gn_bwd_sums_cross" : "gn_bwd_sums";
-    if (need_w || !fused(p)) names[k++] = "gn_bwd_finish";
+    if (need_w ? !(p.join && need_x) : !fused(p) && !p.join) names[k++] = "gn_bwd_finish";
     if (need_x && !fused(p)) names[k++] = p.how == kCross ? "gn_bwd_apply_cross" : "gn_bwd_apply";
     return k;
 }
@@ -1070,13 +1150,16 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
     float2* gsum = part + g.B * g.C * p.chunks;
     if (p.how == kOnceLast && kernel == 0)
         return launch_clear(reinterpret_cast<uint64_t*>(gsum), group_pairs(g, p), s);
-    if (kernel == (p.how == kOnceLast ? 2 : 1)) {
-        const bool need_groups = !fused(p) && p.how != kOnceLast && a.grad_x, need_w = a.grad_weight || a.grad_bias;
-        const int64_t ngroups = need_groups ? runs : 0, blocks = (ngroups + 3) / 4 + (!need_w ? 0 : p.last ? (C + 7) / 8 : C);
-        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kGnThreads), 0, s, (const float2*)part,
-                             a.weight, gsum, a.grad_weight, a.grad_bias, g.B, C, D, p.chunks, p.last,
-                             1.0f / ((float)D * (float)P), ngroups);
+    const bool need_w = a.grad_weight || a.grad_bias, join = p.join && a.grad_x;
+    const Parts parts{part, g.B, C, D, p.chunks, p.last, 1.0f / ((float)D * (float)P), a.grad_weight, a.grad_bias};
+    if (!join && kernel == (p.how == kOnceLast ? 2 : 1)) {
+        const bool need_groups = !fused(p) && p.how != kOnceLast && a.grad_x;
+        const int64_t ngroups = need_groups ? runs : 0, blocks = (ngroups + 3) / 4 + param_blocks(parts);
+        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kGnThreads), 0, s, parts, a.weight, gsum, ngroups);
     }
+    Parts joined = parts;             // as the kernels of grad_x get it
+    if (!join) joined.part = nullptr;
+    const int64_t extra = join && need_w ? param_blocks(parts) : 0;
     return with_types(g, [&](auto tx, auto ty) {
         using TX = decltype(tx);
         using TY = decltype(ty);
@@ -1136,14 +1219,16 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
             if (p.how == kSplitLast) {
                 const int per = std::min(8 * p.rows.q, p.rows.ns), chunks = (p.rows.ns + per - 1) / per;
                 const int64_t blocks = g.B * chunks;
-                return launch_kernel(k_gn_bwd_apply_last<ACT, TX, TY>, grid_of(blocks), dim3(p.rows.threads), 0, s, x,
-                                     dy, a.weight, a.bias, stats, gs, gx, p.rows, per, chunks, blocks);
+                const size_t lds = join ? sizeof(float2) * (size_t)std::max<int64_t>(p.rows.threads, g.groups) : 0;
+                return launch_kernel(k_gn_bwd_apply_last<ACT, TX, TY>, grid_of(blocks + extra), dim3(p.rows.threads),
+                                     lds, s, x, dy, a.weight, a.bias, stats, gs, gx, p.rows, joined, per, chunks,
+                                     blocks, extra);
             }
             if (p.how == kSplitFirst) {
                 const FirstRows r = first_rows(g.B * g.C, g.P, kVec<TX>, 8);
                 const int64_t blocks = first_blocks(r);
-                return launch_kernel(k_gn_bwd_apply_first<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x, dy,
-                                     a.weight, a.bias, stats, gs, gx, r, C, D, blocks);
+                return launch_kernel(k_gn_bwd_apply_first<ACT, TX, TY>, grid_of(blocks + extra), dim3(kGnThreads), 0, s,
+                                     x, dy, a.weight, a.bias, stats, gs, gx, r, joined, C, D, blocks, extra);
             }
             if (p.how == kWide) {
                 const int64_t blocks = g.B * g.P;
@@ -1152,10 +1237,11 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
             }
             const int64_t blocks = g.B * p.tiles.tiles_c * p.tiles.tiles_p;
             if (g.x_last)
-                return launch_kernel(k_gn_bwd_apply_cross<ACT, true, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s,
-                                     x, dy, a.weight, a.bias, stats, gs, gx, p.tiles, C, P, D, blocks);
-            return launch_kernel(k_gn_bwd_apply_cross<ACT, false, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
-                                 dy, a.weight, a.bias, stats, gs, gx, p.tiles, C, P, D, blocks);
+                return launch_kernel(k_gn_bwd_apply_cross<ACT, true, TX, TY>, grid_of(blocks + extra), dim3(kGnThreads),
+                                     0, s, x, dy, a.weight, a.bias, stats, gs, gx, p.tiles, joined, C, P, D, blocks,
+                                     extra);
+            return launch_kernel(k_gn_bwd_apply_cross<ACT, false, TX, TY>, grid_of(blocks + extra), dim3(kGnThreads), 0,
+                                 s, x, dy, a.weight, a.bias, stats, gs, gx, p.tiles, joined, C, P, D, blocks, extra);
         });
     });
 }
