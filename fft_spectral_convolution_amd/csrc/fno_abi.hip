@@ -1092,6 +1092,14 @@ size_t type_bytes(int type) { return type == FNO_C64 ? 8 : type == FNO_F32 ? 4 :
 
 bool off_grain(const void* p, size_t grain) { return reinterpret_cast<uintptr_t>(p) % grain != 0; }
 
+// A field of one channel or of one position has one layout: rows of P values,
+// or of C.
+GroupNorm plain_layouts(GroupNorm g) {
+    if (g.C == 1) g.x_last = g.out_last = false;
+    else if (g.P == 1) g.x_last = g.out_last = true;
+    return g;
+}
+
 int check_group_norm(const GroupNorm& g) {
     if (g.B < 1 || g.C < 1 || g.P < 1 || g.groups < 1 || g.C % g.groups != 0) return FNO_ERR_SHAPE;
     // positions and channels of an item are indexed in 32 bits, and no device holds more than 2^40 values
@@ -1528,7 +1536,8 @@ int fno_inverse1d(const void* yh, float* out, int B, int C, int N, int modes, vo
 size_t fno_group_norm_workspace_size(int B, int C, int P, int groups, int x_last, int out_last, int x_type,
                                      int backward) {
     if ((x_last & ~1) || (out_last & ~1) || (backward & ~1)) return 0;
-    const GroupNorm g{B, C, P, groups, 0.0f, FNO_ACT_NONE, x_last != 0, out_last != 0, x_type, x_type};
+    const GroupNorm g =
+        plain_layouts({B, C, P, groups, 0.0f, FNO_ACT_NONE, x_last != 0, out_last != 0, x_type, x_type});
     return check_group_norm(g) == FNO_OK ? group_norm_workspace(g, backward != 0) : 0;
 }
 
@@ -1536,7 +1545,7 @@ int fno_group_norm(const void* x, const float* weight, const float* bias, void* 
                    int groups, float eps, int act, int x_last, int out_last, int x_type, int out_type, void* workspace,
                    size_t ws_bytes, void* stream) {
     if ((x_last & ~1) || (out_last & ~1) || !(eps > 0.0f) || !std::isfinite(eps)) return FNO_ERR_VALUE;
-    const GroupNorm g{B, C, P, groups, eps, act, x_last != 0, out_last != 0, x_type, out_type};
+    const GroupNorm g = plain_layouts({B, C, P, groups, eps, act, x_last != 0, out_last != 0, x_type, out_type});
     const int rc = check_group_norm(g);
     if (rc) return rc;
     const GroupNormArgs a{x, weight, bias, stats, out, nullptr, nullptr, nullptr, workspace};
@@ -1548,7 +1557,7 @@ int fno_group_norm_backward(const void* x, const float* weight, const float* bia
                             int P, int groups, int act, int x_last, int out_last, int x_type, int out_type,
                             void* workspace, size_t ws_bytes, void* stream) {
     if ((x_last & ~1) || (out_last & ~1)) return FNO_ERR_VALUE;
-    const GroupNorm g{B, C, P, groups, 0.0f, act, x_last != 0, out_last != 0, x_type, out_type};
+    const GroupNorm g = plain_layouts({B, C, P, groups, 0.0f, act, x_last != 0, out_last != 0, x_type, out_type});
     const int rc = check_group_norm(g);
     if (rc) return rc;
     const GroupNormArgs a{x, weight, bias, const_cast<float*>(stats), const_cast<void*>(grad_out), grad_x, grad_weight,

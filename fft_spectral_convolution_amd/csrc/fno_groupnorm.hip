@@ -745,85 +745,56 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_first(const TX* __restr
 }
 
 // ---- output in the other layout -----------------------------------------------------------
-// One tile a workgroup: read along x's rows, turned in LDS, written along
-// out's.
 template <int ACT, bool XLAST, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_apply_cross(const TX* __restrict__ x, const float* __restrict__ w,
                                                                const float* __restrict__ bias, float* stats,
                                                                TY* __restrict__ out, Tiles q, Join f, int C, int P,
                                                                int D, int64_t blocks) {
-    constexpr int V = kVec<TX>, VY = kVec<TY>;
+    constexpr int V = kVec<TX>;
     __shared__ float tile[kTileLds];
     __shared__ float joined[2 * kMaxTileChannels];
     const int64_t id = block_id();
     if (id >= blocks) return;
-    const int64_t b = id / q.tiles_c / q.tiles_p;
-    const int r0 = (int)(id % ((int64_t)q.tiles_c * q.tiles_p));
-    const int c0 = r0 % q.tiles_c << q.log2c, p0 = r0 / q.tiles_c * q.tp();
-    const int ld = q.tp() + 1, t = threadIdx.x;
-    const int nc = min(q.tc(), C - c0), np = min(q.tp(), P - p0);
+    const int64_t per_item = (int64_t)q.tiles_c * q.tiles_p, b = id / per_item;
+    const Spot s = spot_of(q, id % per_item, b, C, P);
     const float* st = stats + 2 * b * (C / D);
-    const int64_t item = b * (int64_t)P * C;
     if (f.part) {
-        const int g0 = c0 / D;
-        join_chunks(f, b * (C / D) + g0, (c0 + nc - 1) / D - g0 + 1, joined, p0 == 0, stats);
+        const int g0 = s.c0 / D;
+        join_chunks(f, b * (C / D) + g0, (s.c0 + s.nc - 1) / D - g0 + 1, joined, s.p0 == 0, stats);
         st = joined - 2 * g0;
     }
     if constexpr (XLAST) {
-        const int lv = q.log2c - (V == 4 ? 2 : 3);           // log2 of vectors a row
-        const int c = (t & ((1 << lv) - 1)) * V, n = max(0, min(V, nc - c));
-        float m[V], a[V], o[V];
+        load_last(x, tile, q, s, C);
+        __syncthreads();
+    }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int ch = min(c0 + c + j, C - 1);
-            m[j] = st[2 * (ch / D)];
-            a[j] = st[2 * (ch / D) + 1] * or_one(w, ch);
-            o[j] = or_zero(bias, ch);
-        }
-#pragma unroll
-        for (int i = 0; i < kTile / V / kGnThreads; ++i) {
-            const int p = (i * kGnThreads + t) >> lv;
+    for (int i = 0; i < kTile / V / kGnThreads; ++i) {
+        const Along<V> a(q, s, i);
+        if (a.n) {
+            const int c = s.c0 + a.c;
+            const float m = st[2 * (c / D)], k = st[2 * (c / D) + 1] * or_one(w, c), o = or_zero(bias, c);
+            const int64_t e = s.item + (int64_t)c * P + s.p0 + a.p;
+            float* row = tile + a.c * (q.tp() + 1) + a.p;
             float u[V];
-            load_part<V>(x + item + (int64_t)(p0 + p) * C + c0 + c, p < np ? n : 0, u);
+            if constexpr (XLAST) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) tile[(c + j) * ld + p] = act_value<ACT>(fmaf(u[j] - m[j], a[j], o[j]));
-        }
-    } else {
-        const int lv = 12 - q.log2c - (V == 4 ? 2 : 3);
+                for (int j = 0; j < V; ++j) u[j] = row[j];
+            } else {
+                load_part<V>(x + e, a.n, u);
+            }
 #pragma unroll
-        for (int i = 0; i < kTile / V / kGnThreads; ++i) {
-            const int v = i * kGnThreads + t, c = v >> lv, p = (v & ((1 << lv) - 1)) * V;
-            const int ch = min(c0 + c, C - 1);
-            const float m = st[2 * (ch / D)], a = st[2 * (ch / D) + 1] * or_one(w, ch), o = or_zero(bias, ch);
-            float u[V];
-            load_part<V>(x + item + (int64_t)(c0 + c) * P + p0 + p, c < nc ? max(0, min(V, np - p)) : 0, u);
+            for (int j = 0; j < V; ++j) u[j] = act_value<ACT>(fmaf(u[j] - m, k, o));
+            if constexpr (XLAST) {
+                store_part(out + e, a.n, u);
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) tile[c * ld + p + j] = act_value<ACT>(fmaf(u[j] - m, a, o));
+                for (int j = 0; j < V; ++j) row[j] = u[j];
+            }
         }
     }
-    __syncthreads();
-    if constexpr (XLAST) {
-        const int lv = 12 - q.log2c - (VY == 4 ? 2 : 3);
-#pragma unroll
-        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
-            const int v = i * kGnThreads + t, c = v >> lv, p = (v & ((1 << lv) - 1)) * VY;
-            if (c >= nc || p >= np) continue;
-            float u[VY];
-#pragma unroll
-            for (int j = 0; j < VY; ++j) u[j] = tile[c * ld + p + j];
-            store_part(out + item + (int64_t)(c0 + c) * P + p0 + p, min(VY, np - p), u);
-        }
-    } else {
-        const int lv = q.log2c - (VY == 4 ? 2 : 3);
-#pragma unroll
-        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
-            const int v = i * kGnThreads + t, p = v >> lv, c = (v & ((1 << lv) - 1)) * VY;
-            if (c >= nc || p >= np) continue;
-            float u[VY];
-#pragma unroll
-            for (int j = 0; j < VY; ++j) u[j] = tile[(c + j) * ld + p];
-            store_part(out + item + (int64_t)(p0 + p) * C + c0 + c, min(VY, nc - c), u);
-        }
+    if constexpr (!XLAST) {
+        __syncthreads();
+        store_last(out, tile, q, s, C);
     }
 }
 
@@ -889,7 +860,7 @@ bool joins(const GroupNorm& g, int chunks) {
 
 size_t once_lds(const GroupNorm& g, const Plan& p) {
     const LastRows& r = p.rows;
-    const int turn = g.x_last != g.out_last && g.P > 1 ? std::min(p.once.nv, 4) : 0;
+    const int turn = g.x_last != g.out_last ? std::min(p.once.nv, 4) : 0;
     return sizeof(float) * (size_t)(once_buffer(r.threads, vec_of(g), r.C, turn, r.q * r.R) + r.q + 2 * g.groups);
 }
 
@@ -897,8 +868,8 @@ Plan plan_forward(const GroupNorm& g) {
     const int V = vec_of(g);
     const int64_t D = g.C / g.groups, n = D * g.P;
     const int64_t capacity = (int64_t)kFusedThreads * kHeld * V;
-    const bool same = g.x_last == g.out_last || g.P == 1;
-    const bool last = g.x_last || g.P == 1;       // [B][C][1] is [B][1][C]
+    const bool same = g.x_last == g.out_last;
+    const bool last = g.x_last;
     Plan p{};
     if (!last) {
         if (same && n <= capacity) {
@@ -957,7 +928,7 @@ size_t gn_forward_workspace(const GroupNorm& g) { return sizeof(float2) * (size_
 
 int gn_forward_kernels(const GroupNorm& g, const char** names) {
     const Plan p = plan_forward(g);
-    const bool same = g.x_last == g.out_last || g.P == 1;
+    const bool same = g.x_last == g.out_last;
     const char* apply = same ? "gn_apply" : "gn_apply_cross";
     if (p.how == kFusedLast || p.how == kFusedFirst) {
         names[0] = "gn_fused";
@@ -1022,7 +993,7 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
                     const OnceArgs<TX, TY> args{x,      a.weight, a.bias, out, a.stats, (uint64_t*)part,
                                                 p.rows, p.once,   g.eps,  once_spin()};
                     constexpr int NV = decltype(nv)::value;
-                    const bool turn = g.x_last != g.out_last && g.P > 1;
+                    const bool turn = g.x_last != g.out_last;
                     const auto kernel_of = turn ? k_gn_once_last<ACT, NV, true, TX, TY>
                                                 : k_gn_once_last<ACT, NV, false, TX, TY>;
                     return launch_kernel(kernel_of, dim3((unsigned)p.once.total), dim3(p.rows.threads),
@@ -1031,7 +1002,7 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
             if (p.how == kFusedFirst)
                 return launch_kernel(k_gn_fused_first<ACT, TX, TY>, grid_of(runs), dim3(p.threads), 0, s, x, a.weight,
                                      a.bias, out, a.stats, D, P, (int)g.groups, fast_div(P), runs, g.eps);
-            if (g.x_last != g.out_last && g.P > 1) {
+            if (g.x_last != g.out_last) {
                 const Tiles q = tiles_of(C, P);
                 const int64_t blocks = g.B * q.tiles_c * q.tiles_p;
                 if (g.x_last)

@@ -289,25 +289,110 @@ inline int64_t first_blocks(const FirstRows& r) {
 }
 
 // ---- one layout to the other ----------------------------------------------------
-// Tiles of 4096 values: 2^log2c channels times 4096 / 2^log2c positions,
-// turned in LDS.  The row length is odd, so that both the writes (lanes along
-// channels) and the reads (lanes along positions) fall on different banks.
-constexpr int kTile = 4096;
+// Tiles of 2^log2c channels and tp = 4096 / 2^log2c positions, turned in LDS
+// (a row per channel, of odd length: lanes along channels and lanes along
+// positions both fall on different banks).  The arithmetic is done along the
+// positions, where a vector lies in one channel.  The channels-last side is
+// read and written as runs: with up to 64 channels a tile's positions are one
+// run of memory, whatever C is; of wider fields a tile takes 64 channels.
+constexpr int kTile = 4096, kMaxTileChannels = 64;
+constexpr int kTileLds = kTile + kMaxTileChannels;     // 2^log2c (tp + 1)
 struct Tiles {
-    int log2c;
-    int tiles_p, tiles_c;
+    int log2c, tiles_p, tiles_c;
+    FastDiv by_c;                                      // the run's channels
     __host__ __device__ int tc() const { return 1 << log2c; }
     __host__ __device__ int tp() const { return kTile >> log2c; }
 };
 inline Tiles tiles_of(int64_t C, int64_t P) {
-    Tiles t{4, 0, 0};
-    while (t.log2c < 6 && (1 << t.log2c) < C) ++t.log2c;
+    Tiles t{0, 0, 0, {}};
+    while (t.tc() < kMaxTileChannels && t.tc() < C) ++t.log2c;
     t.tiles_p = (int)((P + t.tp() - 1) / t.tp());
     t.tiles_c = (int)((C + t.tc() - 1) / t.tc());
+    t.by_c = fast_div((int)std::min<int64_t>(C, kMaxTileChannels));
     return t;
 }
-constexpr int kMaxTileChannels = 64;
-constexpr int kTileLds = kTile + 256;     // tc (tp + 1) <= 4096 + 64
+// Where a tile lies: item, channels c0 .. c0 + nc - 1, positions p0 .. p0 + np - 1.
+struct Spot {
+    int64_t item;
+    int c0, p0, nc, np;
+};
+
+// Calls f(element of the channels-last field, place in the tile of each of
+// its V values, how many there are) for a thread's vectors of the tile.
+template <int V, typename F>
+__device__ __forceinline__ void last_side(const Tiles& q, const Spot& s, int C, F&& f) {
+    const int ld = q.tp() + 1;
+    if (q.tiles_c == 1) {
+        const int n = s.np * C;
+#pragma unroll
+        for (int i = 0; i < kTile / V / kGnThreads; ++i) {
+            const int e = (i * kGnThreads + (int)threadIdx.x) * V;
+            if (e < n) {
+                int place[V], p = div_by(e, q.by_c), c = e - p * C;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    place[j] = c * ld + p;
+                    if (++c == C) {
+                        c = 0;
+                        ++p;
+                    }
+                }
+                f(s.item + (int64_t)s.p0 * C + e, place, min(V, n - e));
+            }
+        }
+    } else {
+        constexpr int kPer = kMaxTileChannels / V;         // vectors of a position
+#pragma unroll
+        for (int i = 0; i < kTile / V / kGnThreads; ++i) {
+            const int v = i * kGnThreads + (int)threadIdx.x, p = v / kPer, c = v % kPer * V;
+            if (p < s.np && c < s.nc) {
+                int place[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) place[j] = (c + j) * ld + p;
+                f(s.item + (int64_t)(s.p0 + p) * C + s.c0 + c, place, min(V, s.nc - c));
+            }
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void load_last(const T* x, float* tile, const Tiles& q, const Spot& s, int C) {
+    constexpr int V = kVec<T>;
+    last_side<V>(q, s, C, [&](int64_t e, const int(&place)[V], int n) {
+        float u[V];
+        load_part<V>(x + e, n, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < n) tile[place[j]] = u[j];
+    });
+}
+template <typename T>
+__device__ __forceinline__ void store_last(T* out, const float* tile, const Tiles& q, const Spot& s, int C) {
+    constexpr int V = kVec<T>;
+    last_side<V>(q, s, C, [&](int64_t e, const int(&place)[V], int n) {
+        float u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = j < n ? tile[place[j]] : 0.0f;
+        store_part(out + e, n, u);
+    });
+}
+__device__ __forceinline__ Spot spot_of(const Tiles& q, int64_t tile_id, int64_t b, int C, int P) {
+    const int ct = (int)(tile_id % q.tiles_c), pt = (int)(tile_id / q.tiles_c);
+    Spot s{b * (int64_t)P * C, ct << q.log2c, pt * q.tp(), 0, 0};
+    s.nc = min(q.tc(), C - s.c0);
+    s.np = min(q.tp(), P - s.p0);
+    return s;
+}
+// A thread's vectors along the positions: i < kTile / V / kGnThreads.
+template <int V>
+struct Along {
+    int c, p, n;          // channel and position in the tile, values (0: none)
+    __device__ __forceinline__ Along(const Tiles& q, const Spot& s, int i) {
+        const int lv = 12 - q.log2c - (V == 4 ? 2 : 3), v = i * kGnThreads + (int)threadIdx.x;
+        c = v >> lv;
+        p = (v & ((1 << lv) - 1)) * V;
+        n = c < s.nc ? max(0, min(V, s.np - p)) : 0;
+    }
+};
 
 __device__ __forceinline__ float or_one(const float* w, int64_t c) { return w ? w[c] : 1.0f; }
 __device__ __forceinline__ float or_zero(const float* b, int64_t c) { return b ? b[c] : 0.0f; }

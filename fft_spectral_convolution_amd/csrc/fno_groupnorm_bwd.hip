@@ -583,37 +583,9 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __re
     if ((threadIdx.x & (r.team - 1)) == 0 && row < r.rows) part[row * r.chunks + piece] = make_float2(sg, sx);
 }
 
-// x and grad_out of different layouts: workgroup (item, channel tile, chunk
-// of `per` position tiles); grad_out is turned in LDS, x read in its own
-// order.  part as that of x's layout.
-template <typename TY>
-__device__ __forceinline__ void load_turned(const TY* dy, float* tile, const Tiles& q, bool dy_last, int64_t item,
-                                            int c0, int p0, int nc, int np, int C, int P) {
-    constexpr int VY = kVec<TY>;
-    const int ld = q.tp() + 1, t = threadIdx.x;
-    if (dy_last) {
-        const int lv = q.log2c - (VY == 4 ? 2 : 3);
-#pragma unroll
-        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
-            const int v = i * kGnThreads + t, p = v >> lv, c = (v & ((1 << lv) - 1)) * VY;
-            float u[VY];
-            load_part<VY>(dy + item + (int64_t)(p0 + p) * C + c0 + c, p < np ? max(0, min(VY, nc - c)) : 0, u);
-#pragma unroll
-            for (int j = 0; j < VY; ++j) tile[(c + j) * ld + p] = u[j];
-        }
-    } else {
-        const int lv = 12 - q.log2c - (VY == 4 ? 2 : 3);
-#pragma unroll
-        for (int i = 0; i < kTile / VY / kGnThreads; ++i) {
-            const int v = i * kGnThreads + t, c = v >> lv, p = (v & ((1 << lv) - 1)) * VY;
-            float u[VY];
-            load_part<VY>(dy + item + (int64_t)(c0 + c) * P + p0 + p, c < nc ? max(0, min(VY, np - p)) : 0, u);
-#pragma unroll
-            for (int j = 0; j < VY; ++j) tile[c * ld + p + j] = u[j];
-        }
-    }
-}
-
+// x and grad_out of different layouts: workgroup (item, chunk of `per`
+// position tiles, channel tile); the channels-last one of the two is turned
+// in LDS.  part as that of x's layout.
 template <int ACT, bool XLAST, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __restrict__ x, const TY* __restrict__ dy,
                                                                   const float* __restrict__ w,
@@ -623,81 +595,72 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
                                                                   int D, int per, int chunks, int64_t blocks) {
     constexpr int V = kVec<TX>, N = kTile / V / kGnThreads;
     __shared__ float tile[kTileLds];
+    __shared__ float2 waves[N * kGnThreads / 64];
     const int64_t id = block_id();
     if (id >= blocks) return;
-    const int64_t b = id / chunks / q.tiles_c;
-    const int chunk = (int)(id / q.tiles_c % chunks), c0 = (int)(id % q.tiles_c) << q.log2c;
+    const int64_t b = id / q.tiles_c / chunks;
+    const int chunk = (int)(id / q.tiles_c % chunks), ct = (int)(id % q.tiles_c);
     const int first = chunk * per, last = min(first + per, q.tiles_p);
-    const int ld = q.tp() + 1, t = threadIdx.x, nc = min(q.tc(), C - c0);
-    const int lv = (XLAST ? q.log2c : 12 - q.log2c) - (V == 4 ? 2 : 3);      // log2 of vectors along x's rows
     const float* st = stats + 2 * b * (C / D);
-    const int64_t item = b * (int64_t)P * C;
-    // sums of a channel for each place of the vector (x channels last), or for
-    // each of the thread's N vectors (x channels first)
-    constexpr int S = XLAST ? V : N;
-    float sg[S] = {}, sx[S] = {}, m[S], k[S], a[S], o[S];
+    float2 sum[N];
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-        const int c = XLAST ? (t & ((1 << lv) - 1)) * V + j : (j * kGnThreads + t) >> lv;
-        const int ch = min(c0 + c, C - 1);
-        m[j] = st[2 * (ch / D)];
-        k[j] = st[2 * (ch / D) + 1];
-        a[j] = or_one(w, ch);
-        o[j] = or_zero(bias, ch);
-    }
+    for (int i = 0; i < N; ++i) sum[i] = make_float2(0.0f, 0.0f);
+    Spot s{};
     for (int pt = first; pt < last; ++pt) {
-        const int p0 = pt * q.tp(), np = min(q.tp(), P - p0);
+        s = spot_of(q, (int64_t)pt * q.tiles_c + ct, b, C, P);
         __syncthreads();
-        load_turned(dy, tile, q, !XLAST, item, c0, p0, nc, np, C, P);
+        if constexpr (XLAST) load_last(x, tile, q, s, C);
+        else load_last(dy, tile, q, s, C);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int v = i * kGnThreads + t;
-            const int along = (v & ((1 << lv) - 1)) * V, across = v >> lv;
-            const int n = XLAST ? (across < np ? max(0, min(V, nc - along)) : 0)
-                                : (across < nc ? max(0, min(V, np - along)) : 0);
-            const int64_t e = XLAST ? item + (int64_t)(p0 + across) * C + c0 + along
-                                    : item + (int64_t)(c0 + across) * P + p0 + along;
-            float u[V];
-            load_part<V>(x + e, n, u);
+            const Along<V> a(q, s, i);
+            if (a.n) {
+                const int c = s.c0 + a.c;
+                const float m = st[2 * (c / D)], k = st[2 * (c / D) + 1], wc = or_one(w, c), bc = or_zero(bias, c);
+                const int64_t e = s.item + (int64_t)c * P + s.p0 + a.p;
+                const float* row = tile + a.c * (q.tp() + 1) + a.p;
+                float u[V];
+                if constexpr (XLAST) load_part<V>(dy + e, a.n, u);
+                else load_part<V>(x + e, a.n, u);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int h = XLAST ? j : i;
-                const float d = XLAST ? tile[(along + j) * ld + across] : tile[across * ld + along + j];
-                const float xh = (u[j] - m[h]) * k[h];
-                const float g = slope_times<ACT>(d, xh, a[h], o[h]);
-                if (j < n) {
-                    sg[h] += g;
-                    sx[h] = fmaf(g, xh, sx[h]);
+                for (int j = 0; j < V; ++j) {
+                    const float xh = ((XLAST ? row[j] : u[j]) - m) * k;
+                    const float g = slope_times<ACT>(XLAST ? u[j] : row[j], xh, wc, bc);
+                    if (j < a.n) {
+                        sum[i].x += g;
+                        sum[i].y = fmaf(g, xh, sum[i].y);
+                    }
                 }
             }
         }
     }
-    if constexpr (XLAST) {
-        // threads 2^lv apart hold the same channels
-        __syncthreads();
-        for (int pass = 0; pass < 2; ++pass) {
+    // lanes of a row (a whole wave, or a part of one), then the waves of a row
+    const int lv = 12 - q.log2c - (V == 4 ? 2 : 3), lanes = min(64, 1 << lv), t = threadIdx.x;
+    const auto put = [&](int c, float2 v) {
+        const int64_t ch = s.c0 + c;
+        part[XLAST ? (b * chunks + chunk) * C + ch : (b * C + ch) * chunks + chunk] = v;
+    };
 #pragma unroll
-            for (int j = 0; j < V; ++j) tile[(pass * kGnThreads + t) * V + j] = pass ? sx[j] : sg[j];
+    for (int i = 0; i < N; ++i) {
+        const float2 v = make_float2(team_sum(sum[i].x, lanes), team_sum(sum[i].y, lanes));
+        const int c = (i * kGnThreads + t) >> lv;
+        if (lv < 6) {
+            if ((t & (lanes - 1)) == 0 && c < s.nc) put(c, v);
+        } else if ((t & 63) == 0) {
+            waves[(i * kGnThreads + t) >> 6] = v;
         }
-        __syncthreads();
-        const int c = t, rows = kGnThreads >> lv, width = V << lv;
-        if (c < nc) {
-            float s = 0.0f, z = 0.0f;
-            for (int i = 0; i < rows; ++i) {
-                s += tile[i * width + c];
-                z += tile[kGnThreads * V + i * width + c];
-            }
-            part[(b * chunks + chunk) * C + c0 + c] = make_float2(s, z);
+    }
+    if (lv < 6) return;
+    __syncthreads();
+    if (t < s.nc) {
+        const int per_row = 1 << (lv - 6);
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < per_row; ++k) {
+            v.x += waves[t * per_row + k].x;
+            v.y += waves[t * per_row + k].y;
         }
-    } else {
-        const int lanes = min(64, 1 << lv);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float s = team_sum(sg[i], lanes), z = team_sum(sx[i], lanes);
-            const int c = (i * kGnThreads + t) >> lv;
-            if ((t & (lanes - 1)) == 0 && c < nc) part[(b * C + c0 + c) * chunks + chunk] = make_float2(s, z);
-        }
+        put(t, v);
     }
 }
 
@@ -949,7 +912,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_cross(const TX* __r
                                                                    const float2* __restrict__ gsum,
                                                                    TX* __restrict__ gx, Tiles q, Parts f, int C, int P,
                                                                    int D, int64_t blocks, int64_t extra) {
-    constexpr int V = kVec<TX>, N = kTile / V / kGnThreads;
+    constexpr int V = kVec<TX>;
     __shared__ float tile[kTileLds];
     __shared__ float2 joined[kGnThreads];
     const int64_t id = block_id();
@@ -958,54 +921,44 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_apply_cross(const TX* __r
         param_sums(f, id - blocks, joined);
         return;
     }
-    const int64_t b = id / q.tiles_c / q.tiles_p;
-    const int r0 = (int)(id % ((int64_t)q.tiles_c * q.tiles_p));
-    const int c0 = r0 % q.tiles_c << q.log2c, p0 = r0 / q.tiles_c * q.tp();
-    const int ld = q.tp() + 1, t = threadIdx.x;
-    const int nc = min(q.tc(), C - c0), np = min(q.tp(), P - p0);
-    const int lv = (XLAST ? q.log2c : 12 - q.log2c) - (V == 4 ? 2 : 3);
+    const int64_t per_item = (int64_t)q.tiles_c * q.tiles_p, b = id / per_item;
+    const Spot s = spot_of(q, id % per_item, b, C, P);
     const float* st = stats + 2 * b * (C / D);
     const float2* gs = gsum + b * (C / D);
     if (f.part) {
-        const int g0 = c0 / D;
-        join_groups(f, w, b * (C / D) + g0, (c0 + nc - 1) / D - g0 + 1, joined);
+        const int g0 = s.c0 / D;
+        join_groups(f, w, b * (C / D) + g0, (s.c0 + s.nc - 1) / D - g0 + 1, joined);
         gs = joined - g0;
     }
-    const int64_t item = b * (int64_t)P * C;
-    load_turned(dy, tile, q, !XLAST, item, c0, p0, nc, np, C, P);
-    constexpr int S = XLAST ? V : N;
-    float m[S], k[S], a[S], o[S], s1[S], s2[S];
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-        const int c = XLAST ? (t & ((1 << lv) - 1)) * V + j : (j * kGnThreads + t) >> lv;
-        const int ch = min(c0 + c, C - 1), g = ch / D;
-        m[j] = st[2 * g];
-        k[j] = st[2 * g + 1];
-        a[j] = or_one(w, ch);
-        o[j] = or_zero(bias, ch);
-        s1[j] = gs[g].x;
-        s2[j] = gs[g].y;
-    }
+    if constexpr (XLAST) load_last(x, tile, q, s, C);
+    else load_last(dy, tile, q, s, C);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int v = i * kGnThreads + t;
-        const int along = (v & ((1 << lv) - 1)) * V, across = v >> lv;
-        const int n = XLAST ? (across < np ? max(0, min(V, nc - along)) : 0)
-                            : (across < nc ? max(0, min(V, np - along)) : 0);
-        const int64_t e = XLAST ? item + (int64_t)(p0 + across) * C + c0 + along
-                                : item + (int64_t)(c0 + across) * P + p0 + along;
-        float u[V];
-        load_part<V>(x + e, n, u);
+    for (int i = 0; i < kTile / V / kGnThreads; ++i) {
+        const Along<V> a(q, s, i);
+        if (a.n) {
+            const int c = s.c0 + a.c, g0 = c / D;
+            const float m = st[2 * g0], k = st[2 * g0 + 1], wc = or_one(w, c), bc = or_zero(bias, c);
+            const float2 sums = gs[g0];
+            const int64_t e = s.item + (int64_t)c * P + s.p0 + a.p;
+            float* row = tile + a.c * (q.tp() + 1) + a.p;
+            float u[V];
+            if constexpr (XLAST) load_part<V>(dy + e, a.n, u);
+            else load_part<V>(x + e, a.n, u);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int h = XLAST ? j : i;
-            const float d = XLAST ? tile[(along + j) * ld + across] : tile[across * ld + along + j];
-            const float xh = (u[j] - m[h]) * k[h];
-            const float g = slope_times<ACT>(d, xh, a[h], o[h]);
-            u[j] = k[h] * (fmaf(g, a[h], -s1[h]) - xh * s2[h]);
+            for (int j = 0; j < V; ++j) {
+                const float xh = ((XLAST ? row[j] : u[j]) - m) * k;
+                const float g = slope_times<ACT>(XLAST ? u[j] : row[j], xh, wc, bc);
+                const float v = k * (fmaf(g, wc, -sums.x) - xh * sums.y);
+                if constexpr (XLAST) row[j] = v;
+                else u[j] = v;
+            }
+            if constexpr (!XLAST) store_part(gx + e, a.n, u);
         }
-        store_part(gx + e, n, u);
+    }
+    if constexpr (XLAST) {
+        __syncthreads();
+        store_last(gx, tile, q, s, C);
     }
 }
 
@@ -1049,8 +1002,8 @@ Plan plan_kernels(const GroupNorm& g) {
     const int64_t capacity = (int64_t)kFusedThreads * kHeld;      // vectors
     Plan p{};
     p.chunks = 1;
-    const bool same = g.x_last == g.out_last || g.P == 1;
-    p.last = g.x_last || g.P == 1;
+    const bool same = g.x_last == g.out_last;
+    p.last = g.x_last;
     if (!same) {
         p.how = kCross;
         p.tiles = tiles_of(g.C, g.P);
