@@ -52,54 +52,59 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
 }
 
 // ---- activations ---------------------------------------------------------------
-// gelu(z) = z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2 by the fit of epi_erfc
-// with the device's reciprocal (1 ulp) in place of a division: 21 vector
-// instructions against 30, which counts where a 16-bit field is read and
-// written at the memory's rate.  Slopes:
-//   gelu'(z) = Phi(z) + z phi(z),  silu'(z) = s (1 + z (1 - s)), s = sigmoid(z).
-// sigmoid(z) = 1 / (1 + e^-z): e^-z overflows to infinity for z < -88, where
-// the quotient is 0, its limit.
-__device__ __forceinline__ float phi_cdf(float z) {
-    const float a = 0.707106781186547524f * fabsf(z);
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.5f, a, 1.0f));
-    float p = 0.17087277f;
-    p = fmaf(p, t, -0.82215223f);
-    p = fmaf(p, t, 1.48851587f);
-    p = fmaf(p, t, -1.13520398f);
-    p = fmaf(p, t, 0.27886807f);
-    p = fmaf(p, t, -0.18628806f);
-    p = fmaf(p, t, 0.09678418f);
-    p = fmaf(p, t, 0.37409196f);
-    p = fmaf(p, t, 1.00002368f);
-    p = fmaf(p, t, -1.26551223f);
-    const float r = 0.5f * t * __expf(fmaf(-a, a, p));    // Phi(-|z|)
-    return z >= 0.0f ? 1.0f - r : r;
-}
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// The vector instructions per value count: a 16-bit field is read and written
+// at the memory's rate in about 40 of them.
+//
+// gelu(z) = z Phi(z) = max(z, 0) - |z| Phi(-|z|), with
+//   Phi(-|z|) = erfc(a) / 2 = t exp(-a^2 + P(t)) / 2,  a = |z| / sqrt 2, t = 1 / (1 + a / 2),
+// P the fit of epi_erfc (Numerical Recipes, "erfcc").  The exponential is a
+// power of two: P's coefficients carry log2 e, the constant one also the
+// factor 1/2.  18 instructions (a division and Phi itself: 30).  The device's
+// reciprocal and power of two are good to 1 ulp.
+constexpr float kLog2e = 1.44269504088896341f;
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == kActGelu) return z * phi_cdf(z);
-    if constexpr (ACT == kActSilu) return z * sigmoid(z);
+    if constexpr (ACT == kActGelu) {
+        constexpr double L = 1.44269504088896341;
+        const float t = __builtin_amdgcn_rcpf(fmaf(0.353553390593273762f, fabsf(z), 1.0f));
+        float p = (float)(0.17087277 * L);
+        p = fmaf(p, t, (float)(-0.82215223 * L));
+        p = fmaf(p, t, (float)(1.48851587 * L));
+        p = fmaf(p, t, (float)(-1.13520398 * L));
+        p = fmaf(p, t, (float)(0.27886807 * L));
+        p = fmaf(p, t, (float)(-0.18628806 * L));
+        p = fmaf(p, t, (float)(0.09678418 * L));
+        p = fmaf(p, t, (float)(0.37409196 * L));
+        p = fmaf(p, t, (float)(1.00002368 * L));
+        p = fmaf(p, t, (float)(-1.26551223 * L - 1.0));
+        const float r = t * __builtin_amdgcn_exp2f(fmaf(-0.5f * kLog2e * z, z, p));
+        // (the bound keeps infinity times 0 out of gelu(infinity))
+        return fmaf(-fminf(fabsf(z), 3e38f), r, fmaxf(z, 0.0f));
+    }
+    // z / (1 + e^-z): e^-z overflows to infinity for z < -88, where the quotient is 0, its limit
+    if constexpr (ACT == kActSilu) return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
     return z;
 }
+// gelu'(z) = Phi(z) + z phi(z),  silu'(z) = s (1 + z (1 - s)), s = 1 / (1 + e^-z).
 // Phi here by Abramowitz and Stegun 7.1.26 (absolute error of erf below
-// 1.5e-7, all a slope near 1 needs), which shares its exponential with phi.
+// 1.5e-7, all a slope near 1 needs; the coefficients halved), which shares its
+// exponential with phi.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == kActGelu) {
-        const float e = __expf(-0.5f * z * z);
+        const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
         const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.707106781186547524f, fabsf(z), 1.0f));
-        float p = 1.061405429f;
-        p = fmaf(p, t, -1.453152027f);
-        p = fmaf(p, t, 1.421413741f);
-        p = fmaf(p, t, -0.284496736f);
-        p = fmaf(p, t, 0.254829592f);
-        const float r = 0.5f * p * t * e;
+        float p = 0.5f * 1.061405429f;
+        p = fmaf(p, t, 0.5f * -1.453152027f);
+        p = fmaf(p, t, 0.5f * 1.421413741f);
+        p = fmaf(p, t, 0.5f * -0.284496736f);
+        p = fmaf(p, t, 0.5f * 0.254829592f);
+        const float r = p * t * e;
         return fmaf(z * 0.398942280401432678f, e, z >= 0.0f ? 1.0f - r : r);
     }
     if constexpr (ACT == kActSilu) {
-        const float s = sigmoid(z);
+        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     return 1.0f;
@@ -169,10 +174,14 @@ __device__ __forceinline__ T block_sum(T v, T* red) {
 
 // Quotient by a small divisor without a division: exact for n d < 2^32.
 struct FastDiv {
-    uint32_t d, m;
+    uint32_t d, m, one;       // one: all bits where d is 1
 };
-inline FastDiv fast_div(int d) { return FastDiv{(uint32_t)d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
-__device__ __forceinline__ int div_by(int n, const FastDiv& f) { return f.m ? (int)__umulhi((uint32_t)n, f.m) : n; }
+inline FastDiv fast_div(int d) {
+    return d == 1 ? FastDiv{1, 0, ~0u} : FastDiv{(uint32_t)d, (uint32_t)((1ull << 32) / d + 1), 0};
+}
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) {
+    return (int)(__umulhi((uint32_t)n, f.m) + ((uint32_t)n & f.one));
+}
 __device__ __forceinline__ int mod_by(int n, const FastDiv& f) { return n - div_by(n, f) * (int)f.d; }
 
 }  // namespace fno

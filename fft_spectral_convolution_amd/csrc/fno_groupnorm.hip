@@ -378,7 +378,19 @@ struct OnceLast {
     int* missing;
     int t, row, slot, groups, chunk;
     int64_t item, step;
+    float w[V], b[V];
 
+    // The constants of the thread's channels.  Four each are asked for long before `write` uses them; eight would cost
+    // registers that hold the field (they spill: 60 us instead of 48 for the 128 x 128 field in 16 bits).
+    static constexpr bool kEarly = V <= 4;
+    __device__ __forceinline__ void constants() {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = mod_by(slot * V + j, r.by_cs);
+            w[j] = or_one(a.w, c);
+            b[j] = or_zero(a.bias, c);
+        }
+    }
     __device__ __forceinline__ OnceLast(const OnceArgs<TX, TY>& args, float* lds, int* flag)
         : a(args), r(args.r), buf(lds), missing(flag) {
         t = threadIdx.x;
@@ -474,19 +486,24 @@ struct OnceLast {
             const int lost = gather_pairs(pairs() + g * chunks, chunks, part, parts, looks, v);
             if (lost < chunks) atomicMin(missing, lost);
             const float n = (float)r.P * (float)r.D;
+            const float whole = values_of(0), rest = values_of(chunks - 1);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kLooks; ++i) {
+                if (i * parts >= chunks) break;
                 const int k = part + i * parts;
-                if (k < chunks) sum = fmaf(values_of(k), unpack_pair(v[i]).x, sum);
+                const float m = k + 1 < chunks ? whole : rest;
+                if (k < chunks) sum = fmaf(m, unpack_pair(v[i]).x, sum);
             }
             const float mu = team_sum(sum, parts) / n;
             sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kLooks; ++i) {
+                if (i * parts >= chunks) break;
                 const int k = part + i * parts;
                 const float2 q = unpack_pair(v[i]);
-                if (k < chunks) sum += fmaf(values_of(k) * (q.x - mu), q.x - mu, q.y);
+                const float m = k + 1 < chunks ? whole : rest;
+                if (k < chunks) sum += fmaf(m * (q.x - mu), q.x - mu, q.y);
             }
             sum = team_sum(sum, parts);
             if (part == 0) {
@@ -499,19 +516,19 @@ struct OnceLast {
     }
     // The output of this workgroup's chunk from its vectors: get(i) is vector i < rows.
     template <typename F>
-    __device__ __forceinline__ void write(int64_t at, int rows, F&& get) const {
+    __device__ __forceinline__ void write(int64_t at, int rows, F&& get) {
+        if constexpr (!kEarly) constants();
         if (chunk == 0)
             for (int i = t; i < groups; i += blockDim.x) {
                 a.stats[2 * (item * groups + i)] = mean[i];
                 a.stats[2 * (item * groups + i) + 1] = sq[i];
             }
-        float m[V], k[V], c[V];
+        float m[V], k[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int ch = mod_by(slot * V + j, r.by_cs), gr = div_by(ch, r.by_D);
-            m[j] = mean[gr];
-            k[j] = sq[gr] * or_one(a.w, ch);
-            c[j] = or_zero(a.bias, ch);
+            const int g = div_by(mod_by(slot * V + j, r.by_cs), r.by_D);
+            m[j] = mean[g];
+            k[j] = sq[g] * w[j];
         }
         if constexpr (!TURN) {
             TY* y = a.out + item * r.P * r.C + at;
@@ -521,7 +538,7 @@ struct OnceLast {
                     const Vec h = get(i);
                     float u[V];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) u[j] = act_value<ACT>(fmaf((float)h[j] - m[j], k[j], c[j]));
+                    for (int j = 0; j < V; ++j) u[j] = act_value<ACT>(fmaf((float)h[j] - m[j], k[j], b[j]));
                     store_vec<V>(y + i * step, u);
                 }
         } else {
@@ -545,11 +562,11 @@ struct OnceLast {
                         const Vec h = get(i0 + i);
 #pragma unroll
                         for (int j = 0; j < V; ++j)
-                            buf[place[j] + i * r.q * r.R] = act_value<ACT>(fmaf((float)h[j] - m[j], k[j], c[j]));
+                            buf[place[j] + i * r.q * r.R] = act_value<ACT>(fmaf((float)h[j] - m[j], k[j], b[j]));
                     }
                 __syncthreads();
                 const int runs = (np + VY - 1) / VY;                 // vectors of a channel
-                const FastDiv by_runs{(uint32_t)runs, runs == 1 ? 0u : 0xffffffffu / (uint32_t)runs + 1u};
+                const FastDiv by_runs{(uint32_t)runs, runs == 1 ? 0u : 0xffffffffu / (uint32_t)runs + 1u, runs == 1 ? ~0u : 0u};
 #pragma unroll 4
                 for (int e = t; e < r.C * runs; e += blockDim.x) {
                     const int ch = div_by(e, by_runs), p = (e - ch * runs) * VY;
@@ -569,7 +586,8 @@ struct OnceLast {
 template <int ACT, int NV, bool TURN, typename TX, typename TY>
 __device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float* lds, int* flag, int lost) {
     typedef OnceLast<ACT, NV, TURN, TX, TY> F;
-    const F f(args, lds, flag);
+    F f(args, lds, flag);
+    if constexpr (F::kEarly) f.constants();
     do {
         const TX* p = f.x_item() + f.at_of(lost);
         const int n = f.rows_of(lost);
@@ -589,13 +607,14 @@ __global__ __launch_bounds__(kOnceThreads, 4) void k_gn_once_last(OnceArgs<TX, T
     typedef OnceLast<ACT, NV, TURN, TX, TY> F;
     extern __shared__ float lds[];
     __shared__ int missing;
-    const F f(args, lds, &missing);
+    F f(args, lds, &missing);
     typename F::Vec cur[NV];
     const int rows = f.rows_of(f.chunk);
     const int64_t at = rows ? f.at_of(f.chunk) : 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         cur[i] = *reinterpret_cast<const typename F::Vec*>(f.x_item() + at + max(0, min(i, rows - 1)) * f.step);
+    if constexpr (F::kEarly) f.constants();
     f.put(f.chunk, rows, [&](auto&& take) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -907,7 +926,7 @@ Plan plan_forward(const GroupNorm& g) {
         }
     }
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
-    if (once_plan(g, p.rows, 16, &p.once)) {
+    if (once_plan(g, p.rows, 16, 1024, &p.once)) {
         if (once_lds(g, p) <= kLdsMax) {
             p.how = kOnceLast;
             p.parts = p.once.total * g.groups;

@@ -137,7 +137,7 @@ __device__ __forceinline__ void last_sums(const float (&val)[V], float* buf, flo
         for (int j = 0; j < V; ++j) buf[t * V + j] = val[j];
     }
     __syncthreads();
-    const FastDiv by_width = width == 1 ? FastDiv{1, 0} : r.by_D;
+    const FastDiv by_width = width == 1 ? FastDiv{1, 0, ~0u} : r.by_D;
     const int count = width == 1 ? r.cs : div_by(r.cs, r.by_D), entries = r.q * r.R * width;
     int parts = 1;
     while (parts < 64 && 2 * parts * count <= (int)blockDim.x) parts *= 2;
@@ -210,7 +210,7 @@ __device__ __forceinline__ int gather_pairs(const uint64_t* slots, int n, int pa
             }
         }
         if (missing == n) break;
-        __builtin_amdgcn_s_sleep(4);
+        __builtin_amdgcn_s_sleep(1);
     }
     return missing;
 }
@@ -222,17 +222,16 @@ struct Once {
     int64_t total;
 };
 
-// Whether a one-pass kernel serves the field, and how.  An item must fit the
-// workgroups that run at once, and its pairs the looks of a workgroup.
-inline bool once_plan(const GroupNorm& g, const LastRows& r, int vectors, Once* o) {
-    constexpr int kRunning = 1024;        // workgroups: four a CU
+// Whether a one-pass kernel serves the field, and how.  An item must fit half
+// the workgroups that run at once, and its pairs the looks of a workgroup.
+inline bool once_plan(const GroupNorm& g, const LastRows& r, int vectors, int running, Once* o) {
     if (r.threads > kOnceThreads || r.P % r.R) return false;
     // vectors a thread: as many as `vectors`, fewer where that would leave CUs without work
     const auto chunks_of = [&](int nv) { return (r.ns + (int64_t)r.q * nv - 1) / ((int64_t)r.q * nv); };
     o->nv = vectors;
-    while (o->nv > 2 && g.B * chunks_of(o->nv) < kRunning / 2) o->nv /= 2;
+    while (o->nv > 2 && g.B * chunks_of(o->nv) < 512) o->nv /= 2;
     const int64_t chunks = chunks_of(o->nv);
-    if (chunks > kRunning / 2 || g.B * chunks >= 1 << 22) return false;
+    if (chunks > running / 2 || g.B * chunks >= 1 << 22) return false;
     o->chunks = (int)chunks;
     o->parts = 1;
     while (o->parts < 64 && 2 * o->parts * g.groups <= r.threads) o->parts *= 2;

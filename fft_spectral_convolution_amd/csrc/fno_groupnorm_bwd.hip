@@ -260,7 +260,7 @@ struct OnceLast {
     int* missing;
     int t, row, slot, groups, chunk;
     int64_t item, step;
-    float m[V], k[V], b[V];
+    float m[V], k[V], b[V], wc[V];
 
     __device__ __forceinline__ OnceLast(const OnceArgs<TX, TY>& args, float* lds, int* flag)
         : a(args), r(args.r), buf(lds), missing(flag) {
@@ -274,7 +274,10 @@ struct OnceLast {
         item = blockIdx.x / a.o.chunks;
         chunk = (int)(blockIdx.x - item * a.o.chunks);
         step = (int64_t)r.q * r.stride();
-        for (int c = t; c < r.C; c += blockDim.x) w[c] = or_one(a.w, c);
+    }
+    // The constants of the thread's channels.  Asked for before the field: loads come back in order, and the first
+    // vectors are worked on while the last are on their way.
+    __device__ __forceinline__ void constants() {
         const float* st = a.stats + 2 * item * groups;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -282,8 +285,8 @@ struct OnceLast {
             m[j] = st[2 * g];
             k[j] = st[2 * g + 1];
             b[j] = or_zero(a.bias, c);
+            wc[j] = or_one(a.w, c);
         }
-        __syncthreads();
     }
     __device__ __forceinline__ int channel(int j) const { return mod_by(slot * V + j, r.by_cs); }
     __device__ __forceinline__ int per() const { return r.q * NV; }
@@ -304,7 +307,7 @@ struct OnceLast {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float xh = ((float)x[j] - m[j]) * k[j];
-                const float g = slope_times<ACT>((float)y[j], xh, w[channel(j)], b[j]);
+                const float g = slope_times<ACT>((float)y[j], xh, wc[j], b[j]);
                 sg[j] += g;
                 sx[j] = fmaf(g, xh, sx[j]);
                 if constexpr (kKeep) y[j] = g;
@@ -313,6 +316,10 @@ struct OnceLast {
         float* gs = buf;
         float* xs = buf + r.threads * V;
         __syncthreads();
+        if (row == 0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[channel(j)] = wc[j];
+        }
         if (row < r.q) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -365,12 +372,14 @@ struct OnceLast {
             if (lost < chunks) atomicMin(missing, lost);
             float s = 0.0f, z = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kLooks; ++i)
+            for (int i = 0; i < kLooks; ++i) {
+                if (i * parts >= chunks) break;
                 if (part + i * parts < chunks) {
                     const float2 q = unpack_pair(v[i]);
                     s += q.x;
                     z += q.y;
                 }
+            }
             s = team_sum(s, parts);
             z = team_sum(z, parts);
             if (part == 0) {
@@ -397,9 +406,9 @@ struct OnceLast {
             float u[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float xh = ((float)x[j] - m[j]) * k[j], wc = w[channel(j)];
-                const float g = KEPT ? (float)y[j] : slope_times<ACT>((float)y[j], xh, wc, b[j]);
-                u[j] = k[j] * (fmaf(g, wc, -p[j]) - xh * q[j]);
+                const float xh = ((float)x[j] - m[j]) * k[j];
+                const float g = KEPT ? (float)y[j] : slope_times<ACT>((float)y[j], xh, wc[j], b[j]);
+                u[j] = k[j] * (fmaf(g, wc[j], -p[j]) - xh * q[j]);
             }
             store_vec<V>(out + i * step, u);
         });
@@ -409,7 +418,8 @@ struct OnceLast {
 template <int ACT, int NV, typename TX, typename TY>
 __device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float* lds, int* flag, int lost) {
     typedef OnceLast<ACT, NV, TX, TY> F;
-    const F f(args, lds, flag);
+    F f(args, lds, flag);
+    f.constants();
     const auto pair_at = [&](int64_t at, int i, auto&& use) {
         const int64_t e = f.base() + at + i * f.step;
         const typename F::VecX x = *reinterpret_cast<const typename F::VecX*>(args.x + e);
@@ -433,12 +443,17 @@ __device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float
     });
 }
 
+// Two waves a SIMD, with 16 vectors of each field in 256 registers: 95 us for
+// the 128 x 128 field (32 x 64 channels, float32) where four waves of 8
+// vectors took 111 and of 4 vectors 165 (what a workgroup costs whatever it
+// holds shows; not waiting for the others changed none of them).
 template <int ACT, int NV, typename TX, typename TY>
-__global__ __launch_bounds__(kOnceThreads, 4) void k_gn_bwd_once_last(OnceArgs<TX, TY> args) {
+__global__ __launch_bounds__(kOnceThreads, 2) void k_gn_bwd_once_last(OnceArgs<TX, TY> args) {
     typedef OnceLast<ACT, NV, TX, TY> F;
     extern __shared__ float lds[];
     __shared__ int missing;
-    const F f(args, lds, &missing);
+    F f(args, lds, &missing);
+    f.constants();
     typename F::VecX x[NV];
     typename F::VecY y[NV];
     const int rows = f.rows_of(f.chunk);
@@ -1046,7 +1061,7 @@ Plan plan_kernels(const GroupNorm& g) {
     }
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
     p.lds = sizeof(float) * (size_t)(2 * p.rows.threads * V + g.C + 2 * g.groups);
-    if (p.lds <= kLdsMax && once_plan(g, p.rows, V == 4 || g.out_type != kTypeF32 ? 8 : 4, &p.once)) {
+    if (p.lds <= kLdsMax && once_plan(g, p.rows, V == 4 || g.out_type != kTypeF32 ? 16 : 8, 512, &p.once)) {
         p.how = kOnceLast;
         p.chunks = p.once.chunks;
         return p;
@@ -1134,7 +1149,7 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
             }
             if (p.how == kOnceLast)
                 return with_vectors(p.once.nv, [&](auto nv) {
-                    constexpr int NV = std::min(decltype(nv)::value, 8);
+                    constexpr int NV = decltype(nv)::value;
                     const OnceArgs<TX, TY> args{x,  dy,
                                                 a.weight, a.bias,
                                                 stats, gx,
