@@ -14,7 +14,12 @@
 namespace fno {
 namespace {
 
-constexpr int kHeld = 8;              // vectors a thread keeps in the one-pass kernels
+// Vectors a thread keeps in the one-workgroup kernels: 32 values.  (Of a
+// 16-bit field twice as many would fit, but a vector of eight has eight
+// channels' constants beside it, which then spill.)
+template <typename TX>
+constexpr int kHeld = 32 / kVec<TX>;
+constexpr int64_t kFusedValues = 1024 * 32;
 constexpr int kFusedThreads = 1024;
 
 // ---- one pass, channels last -----------------------------------------------------
@@ -25,7 +30,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
                                                                 const float* __restrict__ bias,
                                                                 TY* __restrict__ out, float* __restrict__ stats,
                                                                 LastRows r, int slices, int64_t blocks, float eps) {
-    constexpr int V = kVec<TX>;
+    constexpr int V = kVec<TX>, kHold = kHeld<TX>;
     extern __shared__ float lds[];
     const int64_t id = block_id();
     if (id >= blocks) return;
@@ -40,15 +45,15 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
     const int64_t base = b * r.P * r.C + c0 + slot * V;
     const float n_group = (float)r.P * (float)r.D, inv_n = 1.0f / n_group;
 
-    Raw<TX, V> held[kHeld];
+    Raw<TX, V> held[kHold];
     float sum[V] = {};
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int s = row + i * r.q;
         held[i].load(x + base + (int64_t)s * r.stride(), on ? last_valid<V>(r, s, slot) : 0);
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
+    for (int i = 0; i < kHold; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] += held[i][j];
     float m[V], a[V], o[V];
@@ -65,7 +70,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
         sum[j] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int n = on ? last_valid<V>(r, row + i * r.q, slot) : 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -84,7 +89,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
     for (int j = 0; j < V; ++j)
         a[j] *= rsqrtf(fmaf(rstd[div_by(mod_by(slot * V + j, r.by_cs), r.by_D)], inv_n, eps));
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int s = row + i * r.q, n = last_valid<V>(r, s, slot);
         if (n == 0) break;
         float y[V];
@@ -103,7 +108,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_first(const TX* __re
                                                                  TY* __restrict__ out, float* __restrict__ stats,
                                                                  int D, int P, int groups, FastDiv by_p, int64_t blocks,
                                                                  float eps) {
-    constexpr int V = kVec<TX>;
+    constexpr int V = kVec<TX>, kHold = kHeld<TX>;
     __shared__ float red[16];
     const int64_t id = block_id();
     if (id >= blocks) return;
@@ -112,21 +117,21 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_first(const TX* __re
     const int64_t base = id * n;
     const float inv_n = 1.0f / (float)n;
 
-    Raw<TX, V> held[kHeld];
+    Raw<TX, V> held[kHold];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int e = i * step + t * V;
         held[i].load(x + base + e, max(0, min(V, n - e)));
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
+    for (int i = 0; i < kHold; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) sum += held[i][j];
     const float mean = block_sum(sum, red) / (float)n;
     sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int left = n - (i * step + t * V);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -141,7 +146,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_first(const TX* __re
     }
     const bool whole = P % V == 0;        // a vector lies in one channel
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int e = i * step + t * V, left = n - e;
         if (left <= 0) break;
         float y[V];
@@ -886,16 +891,16 @@ size_t once_lds(const GroupNorm& g, const Plan& p) {
 Plan plan_forward(const GroupNorm& g) {
     const int V = vec_of(g);
     const int64_t D = g.C / g.groups, n = D * g.P;
-    const int64_t capacity = (int64_t)kFusedThreads * kHeld * V;
+    const int held = 32 / V;
     const bool same = g.x_last == g.out_last;
     const bool last = g.x_last;
     Plan p{};
     if (!last) {
-        if (same && n <= capacity) {
+        if (same && n <= kFusedValues) {
             p.how = kFusedFirst;
             const int64_t vectors = (n + V - 1) / V;
             p.threads = 64;
-            while (p.threads < kFusedThreads && p.threads * kHeld < vectors) p.threads *= 2;
+            while (p.threads < kFusedThreads && p.threads * held < vectors) p.threads *= 2;
             return p;
         }
         p.how = kSplitFirst;
@@ -914,11 +919,11 @@ Plan plan_forward(const GroupNorm& g) {
         while (cs < g.C && (g.C % cs != 0 || cs % V != 0 || cs * 16 / V < 64)) cs += D;
         const LastRows r = last_rows(g.C, cs, D, g.P, V, kGnThreads);
         const int64_t vectors = (int64_t)r.ns * r.cv;
-        if (vectors <= (int64_t)kFusedThreads * kHeld) {
+        if (vectors <= kFusedValues / V) {
             int threads = 64;
-            while (threads < kFusedThreads && (threads < r.cv || (int64_t)(threads / r.cv) * kHeld < r.ns)) threads *= 2;
+            while (threads < kFusedThreads && (threads < r.cv || (int64_t)(threads / r.cv) * held < r.ns)) threads *= 2;
             p.rows = last_rows(g.C, cs, D, g.P, V, threads);
-            if ((int64_t)p.rows.q * kHeld >= p.rows.ns && p.rows.threads <= kFusedThreads) {
+            if ((int64_t)p.rows.q * held >= p.rows.ns && p.rows.threads <= kFusedThreads) {
                 p.how = kFusedLast;
                 p.slices = (int)(g.C / cs);
                 return p;

@@ -15,7 +15,12 @@
 namespace fno {
 namespace {
 
-constexpr int kHeld = 4;              // vectors of x and of grad_out a thread keeps
+// Vectors of x and of grad_out a thread keeps: 16 values of each.  (Of 16-bit
+// fields twice as many would fit, but a vector of eight has eight channels'
+// constants beside it, which then spill: 36 us for one 32 x 1024 item.)
+template <typename TX>
+constexpr int kHeld = 16 / kVec<TX>;
+constexpr int64_t kFusedValues = 1024 * 16;
 constexpr int kFusedThreads = 1024;
 
 template <int ACT>
@@ -53,7 +58,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
     const TX* __restrict__ x, const TY* __restrict__ dy, const float* __restrict__ w, const float* __restrict__ bias,
     const float* __restrict__ stats, TX* __restrict__ gx, float2* __restrict__ part, LastRows r, int slices,
     int64_t blocks) {
-    constexpr int V = kVec<TX>;
+    constexpr int V = kVec<TX>, kHold = kHeld<TX>;
     extern __shared__ float lds[];
     const int64_t id = block_id();
     if (id >= blocks) return;
@@ -69,10 +74,10 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
     const int64_t base = b * r.P * r.C + c0 + slot * V;
     const float* st = stats + 2 * (b * (div_by(r.C, r.by_D)) + div_by(c0, r.by_D));
 
-    Raw<TX, V> hx[kHeld];
-    Raw<TY, V> hy[kHeld];
+    Raw<TX, V> hx[kHold];
+    Raw<TY, V> hy[kHold];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int s = row + i * r.q, n = on ? last_valid<V>(r, s, slot) : 0;
         const int64_t e = base + (int64_t)s * r.stride();
         hx[i].load(x + e, n);
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
     // that xh is 0 however large the mean
     float sg[V] = {}, sx[V] = {};
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int n = on ? last_valid<V>(r, row + i * r.q, slot) : 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -117,7 +122,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
         s2[j] = res[groups + g] * inv_n;
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int s = row + i * r.q, n = last_valid<V>(r, s, slot);
         if (n == 0) break;
         float u[V];
@@ -140,7 +145,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
     const TX* __restrict__ x, const TY* __restrict__ dy, const float* __restrict__ w, const float* __restrict__ bias,
     const float* __restrict__ stats, TX* __restrict__ gx, float2* __restrict__ part, int D, int P, int groups,
     FastDiv by_p, int64_t blocks) {
-    constexpr int V = kVec<TX>;
+    constexpr int V = kVec<TX>, kHold = kHeld<TX>;
     extern __shared__ float lds[];
     const int64_t id = block_id();
     if (id >= blocks) return;
@@ -155,16 +160,16 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
     const int64_t base = id * n;
     const float mean = stats[2 * id], rstd = stats[2 * id + 1];
 
-    Raw<TX, V> hx[kHeld];
-    Raw<TY, V> hy[kHeld];
+    Raw<TX, V> hx[kHold];
+    Raw<TY, V> hy[kHold];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int e = i * step + t * V, m = max(0, min(V, n - e));
         hx[i].load(x + base + e, m);
         hy[i].load(dy + base + e, m);
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int e = i * step + t * V;
         if (e >= n) break;
         const int d = div_by(e, by_p), cut = (d + 1) * P - e;      // places of the vector in channel d
@@ -212,7 +217,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
     group_means(cg, cx, w, c0, D, 1, res);
     const float inv_n = 1.0f / (float)n, s1 = res[0] * inv_n, s2 = res[1] * inv_n;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < kHold; ++i) {
         const int e = i * step + t * V;
         if (e >= n) break;
         const int d = div_by(e, by_p), cut = (d + 1) * P - e;
@@ -788,12 +793,16 @@ inline int64_t param_blocks(const Parts& f) {
 }
 
 // First (with gsum) the B G groups' (s1, s2), a wave each; then the parameters.
-__global__ __launch_bounds__(kGnThreads) void k_gn_bwd_finish(Parts f, const float* __restrict__ w,
-                                                              float2* __restrict__ gsum, int64_t ngroups) {
-    __shared__ float2 both[kGnThreads];
-    const int64_t id = block_id(), gblocks = (ngroups + 3) / 4;
+// Large workgroups: all a parameter's pairs are then asked for in one or two
+// goes (2048 chunks of 64 channels: 8.1 us with 256 threads, 5.1 with 1024).
+constexpr int kFinishThreads = 1024;
+__global__ __launch_bounds__(kFinishThreads) void k_gn_bwd_finish(Parts f, const float* __restrict__ w,
+                                                                  float2* __restrict__ gsum, int64_t ngroups) {
+    constexpr int kWaves = kFinishThreads / 64;
+    __shared__ float2 both[kFinishThreads];
+    const int64_t id = block_id(), gblocks = (ngroups + kWaves - 1) / kWaves;
     if (id < gblocks) {
-        const int64_t i = id * 4 + (threadIdx.x >> 6);
+        const int64_t i = id * kWaves + (threadIdx.x >> 6);
         if (i >= ngroups) return;
         const float2 s = group_sums(f, w, i, threadIdx.x & 63, 64);
         if ((threadIdx.x & 63) == 0) gsum[i] = s;
@@ -1014,7 +1023,8 @@ struct Plan {
 Plan plan_kernels(const GroupNorm& g) {
     const int V = vec_of(g);
     const int64_t D = g.C / g.groups, n = D * g.P;
-    const int64_t capacity = (int64_t)kFusedThreads * kHeld;      // vectors
+    const int held = 16 / V;
+    const int64_t capacity = kFusedValues / V;                    // vectors
     Plan p{};
     p.chunks = 1;
     const bool same = g.x_last == g.out_last;
@@ -1031,7 +1041,7 @@ Plan plan_kernels(const GroupNorm& g) {
         if (g.P >= V && vectors <= capacity && p.lds <= kLdsMax) {
             p.how = kFusedFirst;
             p.threads = 64;
-            while (p.threads < kFusedThreads && p.threads * kHeld < vectors) p.threads *= 2;
+            while (p.threads < kFusedThreads && p.threads * held < vectors) p.threads *= 2;
             return p;
         }
         p.how = kSplitFirst;
@@ -1050,10 +1060,10 @@ Plan plan_kernels(const GroupNorm& g) {
     const LastRows r = last_rows(g.C, cs, D, g.P, V, kGnThreads);
     if ((int64_t)r.ns * r.cv <= capacity) {
         int threads = 64;
-        while (threads < kFusedThreads && (threads < r.cv || (int64_t)(threads / r.cv) * kHeld < r.ns)) threads *= 2;
+        while (threads < kFusedThreads && (threads < r.cv || (int64_t)(threads / r.cv) * held < r.ns)) threads *= 2;
         p.rows = last_rows(g.C, cs, D, g.P, V, threads);
         p.lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * cs + 2 * (cs / D));
-        if ((int64_t)p.rows.q * kHeld >= p.rows.ns && p.rows.threads <= kFusedThreads && p.lds <= kLdsMax) {
+        if ((int64_t)p.rows.q * held >= p.rows.ns && p.rows.threads <= kFusedThreads && p.lds <= kLdsMax) {
             p.how = kFusedLast;
             p.slices = (int)(g.C / cs);
             return p;
@@ -1122,8 +1132,9 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
     const Parts parts{part, g.B, C, D, p.chunks, p.last, 1.0f / ((float)D * (float)P), a.grad_weight, a.grad_bias};
     if (!join && kernel == (p.how == kOnceLast ? 2 : 1)) {
         const bool need_groups = !fused(p) && p.how != kOnceLast && a.grad_x;
-        const int64_t ngroups = need_groups ? runs : 0, blocks = (ngroups + 3) / 4 + param_blocks(parts);
-        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kGnThreads), 0, s, parts, a.weight, gsum, ngroups);
+        const int64_t ngroups = need_groups ? runs : 0, waves = kFinishThreads / 64;
+        const int64_t blocks = (ngroups + waves - 1) / waves + param_blocks(parts);
+        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kFinishThreads), 0, s, parts, a.weight, gsum, ngroups);
     }
     Parts joined = parts;             // as the kernels of grad_x get it
     if (!join) joined.part = nullptr;
