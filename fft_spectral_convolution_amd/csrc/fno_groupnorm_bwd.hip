@@ -28,6 +28,19 @@ __device__ __forceinline__ float slope_times(float dy, float xh, float w, float 
     return dy * act_slope<ACT>(fmaf(xh, w, b));
 }
 
+// A sum with the rounding of each addition carried along (Knuth's two-sum):
+// a parameter's gradient is a sum of values of either sign over a whole batch,
+// often thousands of times smaller than their magnitudes' sum.
+struct Compensated {
+    float s, c;
+    __device__ __forceinline__ void add(float v) {
+        const float t = s + v, z = t - s;
+        c += (s - (t - z)) + (v - z);
+        s = t;
+    }
+    __device__ __forceinline__ float total() const { return s + c; }
+};
+
 // s1, s2 (not yet divided by n) of `groups` groups of D channels from the
 // channels' sums; res[g] and res[groups + g].
 __device__ __forceinline__ void group_means(const float* cg, const float* cx, const float* w, int64_t c0, int D,
@@ -517,7 +530,16 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_sums_last(const TX* __rest
         a[j] = or_one(w, c);
         o[j] = or_zero(bias, c);
     }
-    float sg[V] = {}, sx[V] = {};
+    // sums of 16 rows at a time, then of those: shorter chains of additions
+    float sg[V] = {}, sx[V] = {}, tg[V] = {}, tx[V] = {};
+    auto fold = [&] {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            tg[j] += sg[j];
+            tx[j] += sx[j];
+            sg[j] = sx[j] = 0.0f;
+        }
+    };
     auto take = [&](const float (&u)[V], const float (&v)[V], int n) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -532,8 +554,10 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_sums_last(const TX* __rest
     if (row < r.q) {
         int s = first + row;
         const int full = min(last, r.P / r.R);
+        int pairs = 0;
         for (; s + r.q < full; s += 2 * r.q) {
             float u[2][V], v[2][V];
+            if ((++pairs & 7) == 0) fold();
             const int64_t e = base + (int64_t)s * r.stride(), f = e + (int64_t)r.q * r.stride();
             load_vec<V>(x + e, u[0]);
             load_vec<V>(dy + e, v[0]);
@@ -551,8 +575,9 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_sums_last(const TX* __rest
             take(u, v, n);
         }
     }
-    last_sums(sg, buf, cg, r, 1);
-    last_sums(sx, buf, cx, r, 1);
+    fold();
+    last_sums(tg, buf, cg, r, 1);
+    last_sums(tx, buf, cx, r, 1);
     for (int c = t; c < r.C; c += blockDim.x) part[id * r.C + c] = make_float2(cg[c], cx[c]);
 }
 
@@ -570,7 +595,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __re
     if (id >= blocks) return;
     const int64_t row = id / r.chunks * (kGnThreads / r.team) + threadIdx.x / r.team;
     const int piece = (int)(id % r.chunks);
-    float sg = 0.0f, sx = 0.0f;
+    Compensated cg{}, cx{};
     if (row < r.rows) {
         const int at = piece * r.piece, end = min(at + r.piece, r.P);
         const int c = (int)(row % C);
@@ -582,6 +607,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __re
             const int n = min(V, end - p);
             load_part<V>(x + base + p, n, u);
             load_part<V>(dy + base + p, n, v);
+            float sg = 0.0f, sx = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float xh = (u[j] - m) * k;
@@ -591,8 +617,11 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __re
                     sx = fmaf(g, xh, sx);
                 }
             }
+            cg.add(sg);
+            cx.add(sx);
         }
     }
+    float sg = cg.total(), sx = cx.total();
     if (r.team == kGnThreads) {
         sg = block_sum(sg, red);
         sx = block_sum(sx, red);
@@ -622,9 +651,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
     const int chunk = (int)(id / q.tiles_c % chunks), ct = (int)(id % q.tiles_c);
     const int first = chunk * per, last = min(first + per, q.tiles_p);
     const float* st = stats + 2 * b * (C / D);
-    float2 sum[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum[i] = make_float2(0.0f, 0.0f);
+    Compensated cg[N] = {}, cx[N] = {};
     Spot s{};
     for (int pt = first; pt < last; ++pt) {
         s = spot_of(q, (int64_t)pt * q.tiles_c + ct, b, C, P);
@@ -643,15 +670,18 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
                 float u[V];
                 if constexpr (XLAST) load_part<V>(dy + e, a.n, u);
                 else load_part<V>(x + e, a.n, u);
+                float sg = 0.0f, sx = 0.0f;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float xh = ((XLAST ? row[j] : u[j]) - m) * k;
                     const float g = slope_times<ACT>(XLAST ? u[j] : row[j], xh, wc, bc);
                     if (j < a.n) {
-                        sum[i].x += g;
-                        sum[i].y = fmaf(g, xh, sum[i].y);
+                        sg += g;
+                        sx = fmaf(g, xh, sx);
                     }
                 }
+                cg[i].add(sg);
+                cx[i].add(sx);
             }
         }
     }
@@ -663,7 +693,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
     };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float2 v = make_float2(team_sum(sum[i].x, lanes), team_sum(sum[i].y, lanes));
+        const float2 v = make_float2(team_sum(cg[i].total(), lanes), team_sum(cx[i].total(), lanes));
         const int c = (i * kGnThreads + t) >> lv;
         if (lv < 6) {
             if ((t & (lanes - 1)) == 0 && c < s.nc) put(c, v);
@@ -700,15 +730,15 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __res
     for (int c = threadIdx.x; c < C; c += kGnThreads) {
         const float* st = stats + 2 * (b * (C / D) + c / D);
         const float m = st[0], k = st[1], a = or_one(w, c), o = or_zero(bias, c);
-        float sg = 0.0f, sx = 0.0f;
+        Compensated sg{}, sx{};
         for (int p = first; p < last; ++p) {
             const int64_t e = (b * P + p) * C + c;
             const float xh = ((float)x[e] - m) * k;
             const float g = slope_times<ACT>((float)dy[e], xh, a, o);
-            sg += g;
-            sx = fmaf(g, xh, sx);
+            sg.add(g);
+            sx.add(g * xh);
         }
-        part[id * C + c] = make_float2(sg, sx);
+        part[id * C + c] = make_float2(sg.total(), sx.total());
     }
 }
 
@@ -716,7 +746,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __res
 // Partial sums of a backward pass: pair (b, chunk, c) is part[(b chunks +
 // chunk) C + c] (`last`) or part[(b C + c) chunks + chunk].  They come from
 // other XCDs' kernels and are far away (a microsecond), so a lane asks for
-// eight at a time.
+// eight at a time, and adds them in double.
 struct Parts {
     const float2* part;
     int64_t B;
@@ -727,7 +757,7 @@ struct Parts {
 };
 
 template <typename F>
-__device__ __forceinline__ void sum_parts(int64_t n, int first, int step, F&& at, float& s, float& z) {
+__device__ __forceinline__ void sum_parts(int64_t n, int first, int step, F&& at, double& s, double& z) {
     for (int64_t k = first; k < n; k += 8 * step) {
         float2 q[8];
 #pragma unroll
@@ -746,7 +776,7 @@ __device__ __forceinline__ float2 group_sums(const Parts& f, const float* __rest
     const int groups = f.C / f.D;
     const int64_t b = g / groups;
     const int c0 = (int)(g % groups) * f.D;
-    float s = 0.0f, z = 0.0f;
+    double s = 0.0, z = 0.0;
     sum_parts((int64_t)f.D * f.chunks, part, parts, [&](int64_t k) {
         const uint32_t e = (uint32_t)k, by = (uint32_t)(f.last ? f.D : f.chunks);
         const int hi = (int)(e / by), lo = (int)(e - hi * by), d = f.last ? lo : hi, ch = f.last ? hi : lo;
@@ -754,7 +784,7 @@ __device__ __forceinline__ float2 group_sums(const Parts& f, const float* __rest
         const float wc = or_one(w, c0 + d);
         return make_float2(wc * q.x, wc * q.y);
     }, s, z);
-    return make_float2(team_sum(s, parts) * f.inv_n, team_sum(z, parts) * f.inv_n);
+    return make_float2(team_sum((float)s, parts) * f.inv_n, team_sum((float)z, parts) * f.inv_n);
 }
 
 // The parameters' gradients, over items and chunks, a workgroup for eight
@@ -763,7 +793,7 @@ __device__ __forceinline__ float2 group_sums(const Parts& f, const float* __rest
 __device__ __forceinline__ void param_sums(const Parts& f, int64_t block, float2* both) {
     const int t = threadIdx.x, threads = blockDim.x, per = f.last ? 8 : 1;
     const int64_t c = block * per + t % per;
-    float s = 0.0f, z = 0.0f;
+    double s = 0.0, z = 0.0;
     if (c < f.C) {
         if (f.last) {
             sum_parts(f.B * f.chunks, t / 8, threads / 8, [&](int64_t k) { return f.part[k * f.C + c]; }, s, z);
@@ -772,7 +802,7 @@ __device__ __forceinline__ void param_sums(const Parts& f, int64_t block, float2
                       [&](int64_t k) { return f.part[(k / f.chunks * f.C + c) * f.chunks + k % f.chunks]; }, s, z);
         }
     }
-    both[t] = make_float2(s, z);
+    both[t] = make_float2((float)s, (float)z);
     // halves added until a row of `per` is left (a row without a partner stays)
     for (int rows = threads / per; rows > 1;) {
         const int keep = (rows + 1) / 2;
