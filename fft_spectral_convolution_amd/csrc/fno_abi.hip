@@ -14,6 +14,7 @@
 #include <cstring>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "../../include/fno.h"
@@ -1149,7 +1150,7 @@ int check_grads(const void* const* grads, const long long* numels, const int* ty
     if (count && (!grads || !numels || !types)) return FNO_ERR_NULL;
     for (int i = 0; i < count; ++i) {
         if (types[i] < FNO_F32 || types[i] > FNO_C64) return FNO_ERR_VALUE;
-        if (numels[i] < 0 || numels[i] > (1LL << 40)) return FNO_ERR_SHAPE;
+        if (numels[i] < 0 || numels[i] > (1LL << 35)) return FNO_ERR_SHAPE;      // chunks are counted in 32 bits
         if (numels[i] && !grads[i]) return FNO_ERR_NULL;
         if (numels[i] && off_grain(grads[i], types[i] == FNO_C64 ? 4 : type_bytes(types[i]))) return FNO_ERR_ALIGN;
     }
@@ -1585,9 +1586,13 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
     if (rc) return rc;
     if (!given_norm && !norm) return FNO_ERR_NULL;
     if (!(max_norm >= 0.0f)) return FNO_ERR_VALUE;
-    if (grads_overlap(grads, outs, numels, types, count,
-                      {{norm, 4}, {given_norm == norm ? nullptr : given_norm, 4}, {workspace, ws_bytes}}))
-        return FNO_ERR_ALIAS;
+    try {
+        if (grads_overlap(grads, outs, numels, types, count,
+                          {{norm, 4}, {given_norm == norm ? nullptr : given_norm, 4}, {workspace, ws_bytes}}))
+            return FNO_ERR_ALIAS;
+    } catch (const std::bad_alloc&) {
+        return FNO_ERR_NOMEM;
+    }
     return grad_norm_common(grads, outs, numels, types, count, max_norm, given_norm, norm, workspace, ws_bytes, stream);
 }
 

@@ -1081,7 +1081,10 @@ Plan plan_kernels(const GroupNorm& g) {
     }
     if (!last_rows_ok(g.C, V)) {
         p.how = kWide;
-        split_chunks(g.B, g.P, 1, 256, &p.per, &p.chunks);
+        // the partial sums of an item are C times the chunks: few chunks where the channels fill the chip
+        const int64_t most = std::max<int64_t>(1, (int64_t(1) << 22) / g.C);
+        split_chunks(g.B, g.P, std::max<int64_t>(1, (g.P + most - 1) / most), std::max<int64_t>(256, g.P / most + 1),
+                     &p.per, &p.chunks);
         return p;
     }
     // the narrowest slice of whole groups that is a run of 64 bytes or more, or the whole rows

@@ -381,7 +381,7 @@ int fno_group_norm_backward(const void* x, const float* weight, const float* bia
  *   norm = sqrt(sum over all values of |g|^2)
  *   outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6))
  *
- * grads, outs (device pointers), numels (elements, 0 allowed) and types
+ * grads, outs (device pointers), numels (elements, 0 to 2^35) and types
  * (enum fno_type) are host arrays, read before the call returns; they may
  * mix types.  Squares are summed in float64.  norm is one float32 in device
  * memory: nothing is copied to the host or waited for.

@@ -37,7 +37,8 @@ def back(lib, x=X, w=W, b=B, stats=S, dy=O, gx=G, gw=GW, gb=GB, dims=(2, 8, 10, 
 @pytest.mark.parametrize("call", [norm, back])
 def test_group_norm_sizes_and_options(lib, call):
     for dims in ((0, 8, 10, 4), (2, 0, 10, 4), (2, 8, 0, 4), (2, 8, 10, 0), (2, 8, 10, 3), (2, 8, 10, 16),
-                 (-1, 8, 10, 4), (2, 8, -10, 4), (65536, 65536, 1, 1), (1 << 20, 1 << 10, 1 << 20, 1)):
+                 (-1, 8, 10, 4), (2, 8, -10, 4), (65536, 65536, 1, 1), (1 << 20, 1 << 10, 1 << 20, 1),
+                 (1, (1 << 24) + 1, 1, 1), (1, 1, (1 << 30) + 1, 1)):
         assert call(lib, dims=dims) == SHAPE, dims
         assert lib.fno_group_norm_workspace_size(*dims, 1, 1, 0, 0) == 0
     assert call(lib, act=3) == VALUE and call(lib, act=-1) == VALUE
@@ -100,7 +101,7 @@ def total(lib, entries, n=O, ws=WS, ws_bytes=BIG, count=None):
 @pytest.mark.parametrize("call", [total, clip])
 def test_grad_norm_refusals(lib, call):
     assert call(lib, [(X, 10, 0)], count=-1) == SHAPE
-    assert call(lib, [(X, -1, 0)]) == SHAPE
+    assert call(lib, [(X, -1, 0)]) == SHAPE and call(lib, [(X, (1 << 35) + 1, 0)]) == SHAPE
     assert call(lib, [(X, 10, 4)]) == VALUE and call(lib, [(X, 10, -1)]) == VALUE
     assert call(lib, [(None, 10, 0)]) == NULL
     assert call(lib, [(X + 2, 10, 0)]) == ALIGN and call(lib, [(X + 1, 10, 1)]) == ALIGN
