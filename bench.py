@@ -111,6 +111,12 @@ def kernel_bytes(name: str, cfg, backward: bool = False) -> int:
         # sum of the batch splits' partial weight gradients (when the batch
         # is split): counted as its one compulsory write
         "wgrad_reduce": wb,
+        # norm and clipping of the weight gradient: read once, scaled into
+        # another tensor, the chunks' sums joined (a table holds 1024)
+        "grad_sumsq": wb,
+        "grad_scale": 2 * wb,
+        "grad_small": 2 * wb,
+        "grad_finish": 8 * 1024,
     }
     return table[name.split(":")[0]]
 
