@@ -226,16 +226,17 @@ struct Once {
 // the workgroups that run at once, and its pairs the looks of a workgroup.
 inline bool once_plan(const GroupNorm& g, const LastRows& r, int vectors, int running, Once* o) {
     if (r.threads > kOnceThreads || r.P % r.R) return false;
+    o->parts = 1;
+    while (o->parts < 64 && 2 * o->parts * g.groups <= r.threads) o->parts *= 2;
+    if (o->parts * g.groups > r.threads) return false;
+    const int64_t most = std::min(running / 2, o->parts * kLooks);
     // vectors a thread: as many as `vectors`, fewer where that would leave CUs without work
     const auto chunks_of = [&](int nv) { return (r.ns + (int64_t)r.q * nv - 1) / ((int64_t)r.q * nv); };
     o->nv = vectors;
-    while (o->nv > 2 && g.B * chunks_of(o->nv) < 512) o->nv /= 2;
+    while (o->nv > 2 && g.B * chunks_of(o->nv) < 512 && chunks_of(o->nv / 2) <= most) o->nv /= 2;
     const int64_t chunks = chunks_of(o->nv);
-    if (chunks > running / 2 || g.B * chunks >= 1 << 22) return false;
+    if (chunks > most || g.B * chunks >= 1 << 22) return false;
     o->chunks = (int)chunks;
-    o->parts = 1;
-    while (o->parts < 64 && 2 * o->parts * g.groups <= r.threads) o->parts *= 2;
-    if (o->parts * g.groups > r.threads || (int64_t)o->parts * kLooks < chunks) return false;
     o->total = g.B * chunks;
     return true;
 }

@@ -541,3 +541,93 @@ def test_between_spectral_layers(last):
     coef = min(1.0, 1.0 / (total.item() + 1e-6))
     for got, g in zip(grads, raw):
         assert torch.allclose(got, g * coef, rtol=4 * U, atol=0)
+
+
+@pytest.mark.parametrize("last", [True, False])
+def test_thousands_of_chunks(last):
+    """One item of 3 10^8 values: its statistics come from more chunks than a
+    workgroup joins at a time.  (Chains as in test_offsets_past_32_bits.)"""
+    c, p = 2, 150_000_001
+    x = torch.empty(shape_of(1, c, (p,), last), dtype=BF16, device=DEV)
+    x.normal_(3.0, 1.0, generator=torch.Generator(device=DEV).manual_seed(190))
+    out, stats = fno.fno_group_norm(x, 1, act="silu", channels_last=last)
+    xd = x.double()
+    mean, var = xd.mean(), xd.var(unbiased=False)
+    assert abs(stats[0, 0, 0].item() - mean.item()) <= 2 ** 13 * U * mean.item()
+    assert abs(stats[0, 0, 1].item() - (var + 1e-5).rsqrt().item()) <= 2 ** 13 * U
+    z = (xd - mean) * (var + 1e-5).rsqrt()
+    del xd
+    want = z * torch.sigmoid(z)
+    err = (out.double() - want).abs_()
+    assert (err <= 2 ** -8 * want.abs() + 2 ** 14 * U * (1 + z.abs())).all()
+    del z, want, err
+    dy = torch.ones_like(out)
+    gx, _, _ = fno.fno_group_norm_backward(x, stats, dy, 1, channels_last=last)
+    # without an activation a constant gradient is taken back out by the mean: only roundings stay
+    assert gx.float().abs().max().item() <= 2 ** 14 * U
+
+
+SCHEDULES = {
+    # (b, c, grid, groups, dtype, last, out_last): kernels of the forward and of the backward call
+    (2, 4, (32, 32), 2, F32, True, True): (["gn_fused"], ["gn_bwd_fused", "gn_bwd_finish"]),
+    (2, 4, (32, 32), 2, F32, False, False): (["gn_fused"], ["gn_bwd_fused", "gn_bwd_finish"]),
+    (4, 32, (64, 64), 4, F32, True, True): (["gn_clear", "gn_once"], ["gn_clear", "gn_bwd_once", "gn_bwd_finish"]),
+    (4, 32, (64, 64), 4, F32, True, False): (["gn_clear", "gn_once"],
+                                             ["gn_bwd_sums_cross", "gn_bwd_apply_cross"]),
+    (1, 6, (30, 30), 2, F32, True, False): (["gn_clear", "gn_once"], ["gn_bwd_sums_cross", "gn_bwd_apply_cross"]),
+    (1, 6, (30, 30), 2, F32, False, True): (["gn_stats", "gn_apply_cross"],
+                                            ["gn_bwd_sums_cross", "gn_bwd_apply_cross"]),
+    (3, 30, (61, 47), 5, F16, True, True): (["gn_stats", "gn_apply"], ["gn_bwd_sums", "gn_bwd_apply"]),
+    # the fewest chunks that give every CU work, and no more than a workgroup has looks for
+    (1, 64, (256, 256), 8, F32, True, True): (["gn_clear", "gn_once"], ["gn_clear", "gn_bwd_once", "gn_bwd_finish"]),
+    (1, 64, (512, 512), 64, F32, True, True): (["gn_stats", "gn_finish", "gn_apply"],
+                                               ["gn_bwd_sums", "gn_bwd_finish", "gn_bwd_apply"]),
+    (2, 16, (300, 300), 2, F32, False, False): (["gn_stats", "gn_apply"], ["gn_bwd_sums", "gn_bwd_apply"]),
+    (2, 64, (512, 512), 2, F32, False, False): (["gn_stats", "gn_finish", "gn_apply"],
+                                                ["gn_bwd_sums", "gn_bwd_finish", "gn_bwd_apply"]),
+    (2, 64, (512, 512), 2, F32, False, True): (["gn_stats", "gn_finish", "gn_apply_cross"],
+                                               ["gn_bwd_sums_cross", "gn_bwd_finish", "gn_bwd_apply_cross"]),
+    (1, 2049, (8,), 3, F32, True, True): (["gn_stats_wide", "gn_apply"], ["gn_bwd_sums", "gn_bwd_finish", "gn_bwd_apply"]),
+    (1, 2049, (8,), 3, F32, True, False): (["gn_stats_wide", "gn_apply_cross"],
+                                           ["gn_bwd_sums_cross", "gn_bwd_finish", "gn_bwd_apply_cross"]),
+}
+
+
+@pytest.mark.parametrize("key", SCHEDULES, ids=str)
+def test_schedules(key):
+    """Which kernels a call runs, and that each schedule is right."""
+    b, c, grid, groups, dtype, last, out_last = key
+    x = field(shape_of(b, c, grid, last), dtype, 200)
+    w, bias = params(c, 200)
+    opts = dict(weight=w, bias=bias, act="gelu", channels_last=last, out_channels_last=out_last)
+    out, stats = fno.fno_group_norm(x, groups, **opts)
+    forward = fno.fno_last_kernels()
+    fno.fno_group_norm_backward(x, stats, out, groups, **opts)
+    assert (forward, fno.fno_last_kernels()) == SCHEDULES[key]
+    check(b, c, grid, groups, "gelu", dtype, None, last, out_last, seed=201)
+
+
+def test_host_threads_at_once():
+    import threading
+    x = field((4, 64, 64, 32), F32, 210)
+    want, stats = fno.fno_group_norm(x, 8, act="gelu", channels_last=True)
+    grads = [field((1000, 7), F32, 211), field((33,), BF16, 212)]
+    norm = fno.fno_grad_norm(grads)
+    results, errors = [], []
+
+    def work():
+        try:
+            for _ in range(20):
+                out, _ = fno.fno_group_norm(x, 8, act="gelu", channels_last=True)
+                results.append((out, fno.fno_grad_norm(grads)))
+        except Exception as e:          # noqa: BLE001 (shown below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and len(results) == 80
+    assert all(torch.equal(o, want) and torch.equal(n, norm) for o, n in results)
