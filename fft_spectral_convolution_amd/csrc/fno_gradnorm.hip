@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 16384;
-constexpr int kPartBlocks = 1024;     // partial sums a launch leaves
+constexpr int kPartBlocks = 2048;     // partial sums a launch leaves
 
 __device__ __forceinline__ int64_t chunk_elems(int type) {
     return kChunkBytes / (type == kTypeBf16 || type == kTypeF16 ? 2 : 4);
@@ -46,13 +46,23 @@ __device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t n
     constexpr int V = 16 / sizeof(T);
     double s = 0.0;
     const int64_t nv = n / V;
-    for (int64_t i = t; i < nv; i += threads) {
+    int64_t i = t;
+    for (; i + 3 * threads < nv; i += 4 * threads) {          // four loads in flight: 16 KiB a workgroup
+        float v[4][V];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load_vec<V>(p + (i + k * threads) * V, v[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s = fma((double)v[k][j], (double)v[k][j], s);
+    }
+    for (; i < nv; i += threads) {
         float v[V];
         load_vec<V>(p + i * V, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) s = fma((double)v[j], (double)v[j], s);
     }
-    for (int64_t i = nv * V + t; i < n; i += threads) s = fma((double)(float)p[i], (double)(float)p[i], s);
+    for (i = nv * V + t; i < n; i += threads) s = fma((double)(float)p[i], (double)(float)p[i], s);
     return s;
 }
 

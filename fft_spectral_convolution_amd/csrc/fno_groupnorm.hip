@@ -823,28 +823,33 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_cross(const TX* __restr
 }
 
 // ---- channels last, too wide for a workgroup ------------------------------------------------
-// Workgroup (item, group), reading P short runs of D values: right for any C.
+// Workgroup (item, chunk of `per` positions, group), reading runs of D values,
+// twice (the second time from the caches); part[(b chunks + chunk) G + g].
 template <typename TX>
-__global__ __launch_bounds__(kGnThreads) void k_gn_stats_wide(const TX* __restrict__ x, float* __restrict__ stats,
-                                                              int64_t C, int D, int64_t P, int64_t blocks, float eps) {
-    __shared__ float red[16];
+__global__ __launch_bounds__(kGnThreads) void k_gn_stats_wide(const TX* __restrict__ x, float2* __restrict__ part,
+                                                              int64_t C, int D, FastDiv by_D, int64_t P, int per,
+                                                              int chunks, int64_t blocks) {
+    __shared__ double red[16];
     const int64_t id = block_id();
     if (id >= blocks) return;
-    const int64_t G = C / D, b = id / G, n = P * D;
-    const TX* p = x + b * P * C + id % G * D;
-    float sum = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += kGnThreads) sum += (float)p[i / D * C + i % D];
-    const float mean = block_sum(sum, red) / (float)n;
-    float sq = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += kGnThreads) {
-        const float d = (float)p[i / D * C + i % D] - mean;
-        sq = fmaf(d, d, sq);
+    const int64_t G = C / D, row = id / G, first = row % chunks * per;
+    const TX* p = x + (row / chunks * P + first) * C + id % G * D;
+    const int n = (int)min((int64_t)per, P - first) * D;
+    const auto at = [&](int i) {
+        // per D <= 65536 where per > 1: the division is exact
+        const int r = per == 1 ? 0 : div_by(i, by_D);
+        return (float)p[r * C + (i - r * D)];
+    };
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < n; i += kGnThreads) sum += at(i);
+    const float mean = (float)(block_sum(sum, red) / n);
+    double sq = 0.0;
+    for (int i = threadIdx.x; i < n; i += kGnThreads) {
+        const float d = at(i) - mean;
+        sq += d * d;
     }
     sq = block_sum(sq, red);
-    if (threadIdx.x == 0) {
-        stats[2 * id] = mean;
-        stats[2 * id + 1] = rsqrtf(sq / (float)n + eps);
-    }
+    if (threadIdx.x == 0) part[id] = make_float2(mean, (float)sq);
 }
 
 // Workgroup (row): C values of one position.
@@ -911,6 +916,9 @@ Plan plan_forward(const GroupNorm& g) {
     }
     if (!last_rows_ok(g.C, V)) {
         p.how = kWide;
+        split_chunks(g.B * g.groups, g.P, std::max<int64_t>(1, 4096 / D), std::max<int64_t>(1, 65536 / D), &p.per,
+                     &p.chunks);
+        p.parts = g.B * p.chunks * g.groups;
         return p;
     }
     if (same) {
@@ -963,7 +971,7 @@ int gn_forward_kernels(const GroupNorm& g, const char** names) {
         names[1] = "gn_once";
         return 2;
     }
-    const bool two = p.how == kWide || p.join;
+    const bool two = p.join;
     names[0] = p.how == kWide ? "gn_stats_wide" : "gn_stats";
     names[1] = two ? apply : "gn_finish";
     names[2] = apply;
@@ -982,8 +990,8 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
         const TX* x = static_cast<const TX*>(a.x);
         TY* out = static_cast<TY*>(a.out);
         float* stats = a.stats;
-        const bool last = p.how == kSplitLast;
-        const int64_t per = last ? (int64_t)p.per * p.rows.R * D : p.per;
+        const bool last = p.how == kSplitLast || p.how == kWide;
+        const int64_t per = last ? (int64_t)p.per * (p.how == kWide ? 1 : p.rows.R) * D : p.per;
         const Join join{p.join ? part : nullptr, p.chunks, (int)g.groups, last, per, n, g.eps};
         const size_t lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * (D ? p.rows.cs / D : 0));
         if (kernel == 0 && p.how == kOnceLast)
@@ -998,10 +1006,12 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
             return launch_kernel(k_gn_stats_first<TX>, grid_of(blocks), dim3(kGnThreads), 0, s, x, part, n, p.per,
                                  p.chunks, blocks);
         }
-        if (kernel == 0 && p.how == kWide)
-            return launch_kernel(k_gn_stats_wide<TX>, grid_of(runs), dim3(kGnThreads), 0, s, x, a.stats, g.C, D, g.P,
-                                 runs, g.eps);
-        if (kernel == 1 && p.how != kWide && p.how != kOnceLast && !p.join) {
+        if (kernel == 0 && p.how == kWide) {
+            const int64_t blocks = runs * p.chunks;
+            return launch_kernel(k_gn_stats_wide<TX>, grid_of(blocks), dim3(kGnThreads), 0, s, x, part, g.C, D,
+                                 fast_div(D), g.P, p.per, p.chunks, blocks);
+        }
+        if (kernel == 1 && p.how != kOnceLast && !p.join) {
             return launch_kernel(k_gn_finish, grid_of(runs), dim3(kGnThreads), 0, s, (const float2*)part,
                                  a.stats, runs, (int)g.groups, p.chunks, last, per, n, g.eps);
         }

@@ -714,8 +714,9 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
     }
 }
 
-// Channels last, any width: workgroup (item, chunk of positions), threads along
-// the channels; part[(b chunks + chunk) C + c].
+// Channels last, any width: workgroup (item, chunk of positions, kWideC
+// channels), threads along the channels; part[(b chunks + chunk) C + c].
+constexpr int kWideC = 4 * kGnThreads;
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __restrict__ x, const TY* __restrict__ dy,
                                                                  const float* __restrict__ w,
@@ -723,11 +724,11 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __res
                                                                  const float* __restrict__ stats,
                                                                  float2* __restrict__ part, int C, int P, int D,
                                                                  int per, int chunks, int64_t blocks) {
-    const int64_t id = block_id();
-    if (id >= blocks) return;
-    const int64_t b = id / chunks;
+    if (block_id() >= blocks) return;
+    const int pieces = (C + kWideC - 1) / kWideC, c0 = (int)(block_id() % pieces) * kWideC;
+    const int64_t id = block_id() / pieces, b = id / chunks;
     const int first = (int)(id % chunks) * per, last = min(first + per, P);
-    for (int c = threadIdx.x; c < C; c += kGnThreads) {
+    for (int c = c0 + threadIdx.x; c < min(C, c0 + kWideC); c += kGnThreads) {
         const float* st = stats + 2 * (b * (C / D) + c / D);
         const float m = st[0], k = st[1], a = or_one(w, c), o = or_zero(bias, c);
         Compensated sg{}, sx{};
@@ -770,7 +771,8 @@ __device__ __forceinline__ void sum_parts(int64_t n, int first, int step, F&& at
     }
 }
 
-// s1 and s2 of group `g` (numbered over the items), added by `parts` lanes.
+// s1 and s2 of group `g` (numbered over the items), added by `parts` threads:
+// what those of one wave have, if it is more than a wave.
 __device__ __forceinline__ float2 group_sums(const Parts& f, const float* __restrict__ w, int64_t g, int part,
                                              int parts) {
     const int groups = f.C / f.D;
@@ -784,6 +786,7 @@ __device__ __forceinline__ float2 group_sums(const Parts& f, const float* __rest
         const float wc = or_one(w, c0 + d);
         return make_float2(wc * q.x, wc * q.y);
     }, s, z);
+    parts = min(parts, 64);
     return make_float2(team_sum((float)s, parts) * f.inv_n, team_sum((float)z, parts) * f.inv_n);
 }
 
@@ -822,24 +825,40 @@ inline int64_t param_blocks(const Parts& f) {
     return !f.gw && !f.gb ? 0 : f.last ? (f.C + 7) / 8 : f.C;
 }
 
-// First (with gsum) the B G groups' (s1, s2), a wave each; then the parameters.
+// First (with gsum) the B G groups' (s1, s2); then the parameters.  A group has
+// a wave, or a workgroup (`waves` > 1) where its pairs are more than a wave asks
+// for in one go: 4096 pairs a group 31 us with a wave, 6.3 with a workgroup;
+// 65536 pairs 3.7 ms (of 16 x as many chunks) and 32 us.  Latency of memory
+// far away bounds both.
 // Large workgroups: all a parameter's pairs are then asked for in one or two
 // goes (2048 chunks of 64 channels: 8.1 us with 256 threads, 5.1 with 1024).
 constexpr int kFinishThreads = 1024;
 __global__ __launch_bounds__(kFinishThreads) void k_gn_bwd_finish(Parts f, const float* __restrict__ w,
-                                                                  float2* __restrict__ gsum, int64_t ngroups) {
+                                                                  float2* __restrict__ gsum, int64_t ngroups,
+                                                                  int waves) {
     constexpr int kWaves = kFinishThreads / 64;
     __shared__ float2 both[kFinishThreads];
-    const int64_t id = block_id(), gblocks = (ngroups + kWaves - 1) / kWaves;
-    if (id < gblocks) {
-        const int64_t i = id * kWaves + (threadIdx.x >> 6);
+    const int64_t id = block_id(), gblocks = waves == 1 ? (ngroups + kWaves - 1) / kWaves : ngroups;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (id >= gblocks) {
+        if ((id - gblocks) * (f.last ? 8 : 1) < f.C) param_sums(f, id - gblocks, both);
+    } else if (waves == 1) {
+        const int64_t i = id * kWaves + wave;
         if (i >= ngroups) return;
-        const float2 s = group_sums(f, w, i, threadIdx.x & 63, 64);
-        if ((threadIdx.x & 63) == 0) gsum[i] = s;
-    } else if ((id - gblocks) * (f.last ? 8 : 1) < f.C) {
-        param_sums(f, id - gblocks, both);
+        const float2 s = group_sums(f, w, i, lane, 64);
+        if (lane == 0) gsum[i] = s;
+    } else {
+        const float2 s = group_sums(f, w, id, threadIdx.x, kFinishThreads);
+        if (lane == 0) both[wave] = s;
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            const float2 v = lane < kWaves ? both[lane] : make_float2(0.0f, 0.0f);
+            const float2 all = make_float2(team_sum(v.x, 64), team_sum(v.y, 64));
+            if (lane == 0) gsum[id] = all;
+        }
     }
 }
+inline int finish_waves(const Parts& f) { return (int64_t)f.D * f.chunks <= 8 * 64 ? 1 : kFinishThreads / 64; }
 
 // With few chunks there is no k_gn_bwd_finish: the workgroups of grad_x add
 // their own groups' sums (Parts::part not null), and further workgroups behind
@@ -1081,10 +1100,11 @@ Plan plan_kernels(const GroupNorm& g) {
     }
     if (!last_rows_ok(g.C, V)) {
         p.how = kWide;
-        // the partial sums of an item are C times the chunks: few chunks where the channels fill the chip
+        // the partial sums of an item are C times the chunks: 16 positions a chunk or more, so that they stay a
+        // small part of what is read, and few chunks where the channels fill the chip
         const int64_t most = std::max<int64_t>(1, (int64_t(1) << 22) / g.C);
-        split_chunks(g.B, g.P, std::max<int64_t>(1, (g.P + most - 1) / most), std::max<int64_t>(256, g.P / most + 1),
-                     &p.per, &p.chunks);
+        split_chunks(g.B * ((g.C + kWideC - 1) / kWideC), g.P, std::max<int64_t>(16, (g.P + most - 1) / most),
+                     std::max<int64_t>(256, g.P / most + 1), &p.per, &p.chunks);
         return p;
     }
     // the narrowest slice of whole groups that is a run of 64 bytes or more, or the whole rows
@@ -1165,9 +1185,11 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
     const Parts parts{part, g.B, C, D, p.chunks, p.last, 1.0f / ((float)D * (float)P), a.grad_weight, a.grad_bias};
     if (!join && kernel == (p.how == kOnceLast ? 2 : 1)) {
         const bool need_groups = !fused(p) && p.how != kOnceLast && a.grad_x;
-        const int64_t ngroups = need_groups ? runs : 0, waves = kFinishThreads / 64;
-        const int64_t blocks = (ngroups + waves - 1) / waves + param_blocks(parts);
-        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kFinishThreads), 0, s, parts, a.weight, gsum, ngroups);
+        const int64_t ngroups = need_groups ? runs : 0, all = kFinishThreads / 64;
+        const int waves = finish_waves(parts);
+        const int64_t blocks = (waves == 1 ? (ngroups + all - 1) / all : ngroups) + param_blocks(parts);
+        return launch_kernel(k_gn_bwd_finish, grid_of(blocks), dim3(kFinishThreads), 0, s, parts, a.weight, gsum,
+                             ngroups, waves);
     }
     Parts joined = parts;             // as the kernels of grad_x get it
     if (!join) joined.part = nullptr;
@@ -1215,7 +1237,7 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
                                          dy, a.weight, a.bias, stats, part, p.frows, C, D, blocks);
                 }
                 if (p.how == kWide) {
-                    const int64_t blocks = g.B * p.chunks;
+                    const int64_t blocks = g.B * p.chunks * ((C + kWideC - 1) / kWideC);
                     return launch_kernel(k_gn_bwd_sums_wide<ACT, TX, TY>, grid_of(blocks), dim3(kGnThreads), 0, s, x,
                                          dy, a.weight, a.bias, stats, part, C, P, D, p.per, p.chunks, blocks);
                 }

@@ -587,8 +587,9 @@ SCHEDULES = {
                                                 ["gn_bwd_sums", "gn_bwd_finish", "gn_bwd_apply"]),
     (2, 64, (512, 512), 2, F32, False, True): (["gn_stats", "gn_finish", "gn_apply_cross"],
                                                ["gn_bwd_sums_cross", "gn_bwd_finish", "gn_bwd_apply_cross"]),
-    (1, 2049, (8,), 3, F32, True, True): (["gn_stats_wide", "gn_apply"], ["gn_bwd_sums", "gn_bwd_finish", "gn_bwd_apply"]),
-    (1, 2049, (8,), 3, F32, True, False): (["gn_stats_wide", "gn_apply_cross"],
+    (1, 2049, (8,), 3, F32, True, True): (["gn_stats_wide", "gn_finish", "gn_apply"],
+                                          ["gn_bwd_sums", "gn_bwd_finish", "gn_bwd_apply"]),
+    (1, 2049, (8,), 3, F32, True, False): (["gn_stats_wide", "gn_finish", "gn_apply_cross"],
                                            ["gn_bwd_sums_cross", "gn_bwd_finish", "gn_bwd_apply_cross"]),
 }
 
@@ -631,3 +632,29 @@ def test_host_threads_at_once():
     torch.cuda.synchronize()
     assert not errors and len(results) == 80
     assert all(torch.equal(o, want) and torch.equal(n, norm) for o, n in results)
+
+
+@pytest.mark.parametrize("b,c,grid,groups", [
+    (2, 4100, (701,), 41),         # several chunks of positions, the last one short
+    (3, 2050, (1031,), 2050),      # a group a channel
+    (1, 70000, (9,), 1),           # a group of more than 65536 channels
+    (2, 131072 + 2, (3,), 2),
+    (1, 2051, (5000,), 7),
+])
+@pytest.mark.parametrize("dtype", [F32, F16])
+def test_wide_channels_in_chunks(b, c, grid, groups, dtype):
+    check(b, c, grid, groups, "silu", dtype, None, True, True, seed=220)
+
+
+def test_wide_channels_of_one_value():
+    """A chunk's mean is its values' own, so a constant group has no deviation."""
+    x = torch.full((2, 300, 4100), 1234.5678, device="cuda")
+    out, stats = fno.fno_group_norm(x, 41, channels_last=True)
+    assert torch.equal(out, torch.zeros_like(out))
+    assert torch.equal(stats[..., 0], torch.full_like(stats[..., 0], 1234.5678))
+
+
+def test_groups_of_many_pairs():
+    """Groups whose partial sums a workgroup joins, and those a wave does."""
+    for c, grid, groups in ((64, (512, 512), 1), (16, (512, 2048), 4), (64, (512, 512), 64)):
+        check(1, c, grid, groups, "gelu", F32, None, True, True, seed=230)
