@@ -9,6 +9,8 @@ cannot be loaded, every call raises; there is no fallback.
     import fft_spectral_convolution_amd as fno
     out = fno.fno_spectral_conv2d(x, w, mx, my)      # x [B,Cin,H,W] f32, w [2,mx,my,Cin,Cout] c64
     out = fno.fno_spectral_conv1d(x, w, modes)       # x [B,Cin,N]   f32, w [modes,Cin,Cout]   c64
+    y, stats = fno.fno_group_norm(out, 8, act="gelu")  # and its backward; see its docstring for layouts
+    norm = fno.fno_clip_grad_norm(grads, 1.0)        # in place
 """
 from __future__ import annotations
 

@@ -126,8 +126,7 @@ struct Raw {
 // and over `width` neighbouring channels: res[c / width].  width is D for
 // group sums, 1 for channel sums.  buf holds threads * V floats.  Lanes
 // `parts` at a time share a result, in an order that depends on the sizes
-// alone.  buf may be reused after the next barrier,
-// res is complete on return.
+// alone.  buf may be reused after the next barrier, res is complete on return.
 template <int V>
 __device__ __forceinline__ void last_sums(const float (&val)[V], float* buf, float* res, const LastRows& r, int width) {
     const int t = threadIdx.x, active = r.cv * r.q;
