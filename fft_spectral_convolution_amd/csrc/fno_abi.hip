@@ -1537,9 +1537,15 @@ int fno_inverse1d(const void* yh, float* out, int B, int C, int N, int modes, vo
 size_t fno_group_norm_workspace_size(int B, int C, int P, int groups, int x_last, int out_last, int x_type,
                                      int backward) {
     if ((x_last & ~1) || (out_last & ~1) || (backward & ~1)) return 0;
-    const GroupNorm g =
-        plain_layouts({B, C, P, groups, 0.0f, FNO_ACT_NONE, x_last != 0, out_last != 0, x_type, x_type});
-    return check_group_norm(g) == FNO_OK ? group_norm_workspace(g, backward != 0) : 0;
+    // out's type is not an argument and the backward schedule depends on it: what the more demanding of the two
+    // types that x's allows (its own, float32) needs
+    size_t need = 0;
+    for (const int out_type : {x_type, (int)FNO_F32}) {
+        const GroupNorm g =
+            plain_layouts({B, C, P, groups, 0.0f, FNO_ACT_NONE, x_last != 0, out_last != 0, x_type, out_type});
+        if (check_group_norm(g) == FNO_OK) need = std::max(need, group_norm_workspace(g, backward != 0));
+    }
+    return need;
 }
 
 int fno_group_norm(const void* x, const float* weight, const float* bias, void* out, float* stats, int B, int C, int P,

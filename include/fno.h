@@ -347,7 +347,8 @@ int fno_linear_conv1d(const float* x, const void* wspec, float* out, int B, int 
  * makes its group NaN, no other.
  *
  * Scratch is the caller's: `workspace`, 256-byte aligned, at least
- * fno_group_norm_workspace_size bytes (backward: 1 for the backward call; 0
+ * fno_group_norm_workspace_size bytes (backward: 1 for the backward call; enough
+ * for either out_type that x_type allows; 0
  * where none is needed, NULL will do then, and for invalid arguments), free
  * again when the call's kernels have run.  Nothing is allocated, so the calls can be
  * captured into graphs at any time; graphs that may run at the same time

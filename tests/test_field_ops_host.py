@@ -145,3 +145,40 @@ def test_binding_refuses_before_the_device():
         fno.fno_grad_norm([1.0])
     with pytest.raises(TypeError):
         fno.fno_group_norm([1.0], 1)
+
+
+# Fields far apart, and a workspace that is off its alignment by 16 bytes: a call that finds it large enough is refused
+# for that (ALIGN), one that needs more for its size (WORKSPACE), and none is launched.
+FAR = [k << 44 for k in range(1, 9)]
+OFF = (9 << 44) + 16
+
+
+def _queried_size_serves(lib, dims, x_last, out_last, x_type):
+    for backward in (0, 1):
+        need = lib.fno_group_norm_workspace_size(*dims, x_last, out_last, x_type, backward)
+        for out_type in sorted({x_type, 0}):
+            opts = dict(dims=dims, x_last=x_last, out_last=out_last, x_type=x_type, out_type=out_type, ws=OFF,
+                        ws_bytes=need)
+            rc = back(lib, *FAR, **opts) if backward else norm(lib, *FAR[:5], **opts)
+            assert rc == ALIGN, (backward, out_type, need)
+
+
+@pytest.mark.parametrize("x_type", [0, 1, 2])
+@pytest.mark.parametrize("x_last,out_last", [(1, 1), (0, 0), (1, 0), (0, 1)])
+@pytest.mark.parametrize("dims", [
+    (32, 64, 16384, 8), (16, 64, 16384, 8), (8, 64, 16384, 8), (64, 64, 4096, 8), (1, 145, 16632, 1),
+    (2, 4, 1024, 2), (3, 30, 2867, 5), (2, 16, 1 << 22, 4), (4, 8192, 1024, 8), (256, 64, 4096, 16), (1, 1, 1, 1),
+])
+def test_queried_workspace_serves_every_type(lib, dims, x_last, out_last, x_type):
+    _queried_size_serves(lib, dims, x_last, out_last, x_type)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_queried_workspace_serves_random_fields(lib, seed):
+    import random
+    rng = random.Random(seed)
+    for _ in range(500):
+        c = int(2 ** rng.uniform(0, 13))
+        groups = rng.choice([g for g in range(1, c + 1) if c % g == 0])
+        dims = (int(2 ** rng.uniform(0, 8)), c, int(2 ** rng.uniform(0, 20)), groups)
+        _queried_size_serves(lib, dims, rng.randint(0, 1), rng.randint(0, 1), rng.randint(0, 2))

@@ -658,3 +658,15 @@ def test_groups_of_many_pairs():
     """Groups whose partial sums a workgroup joins, and those a wave does."""
     for c, grid, groups in ((64, (512, 512), 1), (16, (512, 2048), 4), (64, (512, 512), 64)):
         check(1, c, grid, groups, "gelu", F32, None, True, True, seed=230)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("b,c,grid,groups", [
+    (32, 64, (128, 128), 8),
+    (64, 64, (64, 64), 8),
+    (1, 145, (132, 126), 1),       # rows of odd length, eight at a time
+    (13, 600, (2161,), 3),
+])
+def test_16_bit_fields_with_float32_grad_out(b, c, grid, groups, dtype):
+    """Larger fields that stay in 16 bits on one side only, in one layout."""
+    check(b, c, grid, groups, "gelu", dtype, F32, True, True, seed=240)
