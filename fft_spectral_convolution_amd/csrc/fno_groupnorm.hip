@@ -363,6 +363,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_finish(const float2* __restri
 // Workgroup (item, chunk of q NV super-rows).  Vectors are whole (P is a
 // multiple of R); rows past the end of an item are read as the thread's last
 // one and left out.
+constexpr int kOnceVectors = 16;      // of a thread, at most
 template <typename TX, typename TY>
 struct OnceArgs {
     const TX* x;
@@ -958,7 +959,7 @@ Plan plan_forward(const GroupNorm& g) {
         }
     }
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
-    if (once_plan(g, p.rows, 16, 1024, &p.once)) {
+    if (once_plan(g, p.rows, kOnceVectors, 1024, &p.once)) {
         if (once_lds(g, p) <= kLdsMax) {
             p.how = kOnceLast;
             p.parts = p.once.total * g.groups;
@@ -1042,7 +1043,7 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
                                      a.weight, a.bias, out, a.stats, p.rows, p.slices, blocks, g.eps);
             }
             if (p.how == kOnceLast)
-                return with_vectors(p.once.nv, [&](auto nv) {
+                return with_vectors<kOnceVectors>(p.once.nv, [&](auto nv) {
                     const OnceArgs<TX, TY> args{x,      a.weight, a.bias, out, a.stats, (uint64_t*)part,
                                                 p.rows, p.once,   g.eps,  once_spin()};
                     constexpr int NV = decltype(nv)::value;

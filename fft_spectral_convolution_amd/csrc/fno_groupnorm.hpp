@@ -247,13 +247,14 @@ __host__ __device__ inline int once_buffer(int threads, int V, int C, int turn, 
     return pairs > turned ? pairs : turned;
 }
 
-template <typename F>
+// MOST: the vectors that once_plan was given
+template <int MOST, typename F>
 hipError_t with_vectors(int nv, F&& f) {
     switch (nv) {
-        case 16: return f(std::integral_constant<int, 16>{});
-        case 8: return f(std::integral_constant<int, 8>{});
-        case 4: return f(std::integral_constant<int, 4>{});
-        default: return f(std::integral_constant<int, 2>{});
+        case MOST: return f(std::integral_constant<int, MOST>{});
+        case MOST / 2: return f(std::integral_constant<int, MOST / 2>{});
+        case 2: return f(std::integral_constant<int, 2>{});
+        default: return f(std::integral_constant<int, 4>{});     // MOST is 8 or 16
     }
 }
 

@@ -256,6 +256,12 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
 // Workgroup (item, chunk of q NV super-rows), as k_gn_once_last: x and
 // grad_out stay in registers while the chunks' (s1, s2) are exchanged.  Each
 // chunk's channel sums go to part[(item chunks + chunk) C + c].
+//
+// Vectors a thread holds of each field, at most: 16, and half as many where a
+// 16-bit x meets a float32 grad_out, whose vectors of eight are 32 bytes (16 of
+// each spill 24 to 28 registers).
+template <typename TX, typename TY>
+constexpr int kOnceVectors = kVec<TX> == kVec<TY> ? 16 : 8;
 template <typename TX, typename TY>
 struct OnceArgs {
     const TX* x;
@@ -1135,7 +1141,8 @@ Plan plan_kernels(const GroupNorm& g) {
     }
     p.rows = last_rows(g.C, g.C, D, g.P, V, kGnThreads);
     p.lds = sizeof(float) * (size_t)(2 * p.rows.threads * V + g.C + 2 * g.groups);
-    if (p.lds <= kLdsMax && once_plan(g, p.rows, V == 4 || g.out_type != kTypeF32 ? 16 : 8, 512, &p.once)) {
+    const int vectors = g.out_type == g.x_type ? kOnceVectors<float, float> : kOnceVectors<bf16, float>;
+    if (p.lds <= kLdsMax && once_plan(g, p.rows, vectors, 512, &p.once)) {
         p.how = kOnceLast;
         p.chunks = p.once.chunks;
         return p;
@@ -1225,7 +1232,7 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
                                      a.weight, a.bias, stats, gx, mine, D, P, (int)g.groups, fast_div(P), runs);
             }
             if (p.how == kOnceLast)
-                return with_vectors(p.once.nv, [&](auto nv) {
+                return with_vectors<kOnceVectors<TX, TY>>(p.once.nv, [&](auto nv) {
                     constexpr int NV = decltype(nv)::value;
                     const OnceArgs<TX, TY> args{x,  dy,
                                                 a.weight, a.bias,
