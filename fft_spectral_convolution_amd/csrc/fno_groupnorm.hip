@@ -649,21 +649,25 @@ __global__ __launch_bounds__(kOnceThreads, 4) void k_gn_once_last(OnceArgs<TX, T
 // ---- chunks joined by the kernel that writes the output ------------------------------------
 // With few chunks every workgroup of the output joins those of its own groups
 // (a launch less: 3.5 us of a small call); `part` is null where k_gn_finish
-// has done it.
+// has done it.  `most` groups at most are a workgroup's: the lanes that share a
+// group, and so the order of its sum, follow from that and the chunks and not
+// from how many groups a workgroup has, so that all those that hold a part of a
+// group see the same bits.
 struct Join {
     const float2* part;
-    int chunks, groups;
+    int chunks, groups, most;
     bool last;
     int64_t per, n;
     float eps;
 };
 // (mean, 1 / deviation) of groups g0 .. g0 + ng - 1 (numbered over the items),
-// to res[2 i], res[2 i + 1] in LDS; `own` also stores them to stats.
-__device__ __forceinline__ void join_chunks(const Join& f, int64_t g0, int ng, float* res, bool own,
+// to res[2 i], res[2 i + 1] in LDS; those from i = `own` on also to stats (one
+// workgroup for each group).
+__device__ __forceinline__ void join_chunks(const Join& f, int64_t g0, int ng, float* res, int own,
                                             float* __restrict__ stats) {
     const int t = threadIdx.x, threads = blockDim.x;
     int parts = 1;
-    while (parts < 64 && 2 * parts * ng <= threads && parts < f.chunks) parts *= 2;
+    while (parts < 64 && 2 * parts * f.most <= threads && parts < f.chunks) parts *= 2;
     const int part = t & (parts - 1);
     for (int i = t / parts; i < ng; i += threads / parts) {
         const int64_t g = g0 + i;
@@ -686,7 +690,7 @@ __device__ __forceinline__ void join_chunks(const Join& f, int64_t g0, int ng, f
             const float rstd = rsqrtf(sum / (float)f.n + f.eps);
             res[2 * i] = mean;
             res[2 * i + 1] = rstd;
-            if (own) {
+            if (i >= own) {
                 stats[2 * g] = mean;
                 stats[2 * g + 1] = rstd;
             }
@@ -713,7 +717,7 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_apply_last(const TX* __restric
     const int groups = div_by(r.C, r.by_D);
     const float* st = stats + 2 * b * groups;
     if (f.part) {
-        join_chunks(f, b * groups, groups, joined, first == 0, stats);
+        join_chunks(f, b * groups, groups, joined, first == 0 ? 0 : groups, stats);
         st = joined;
     }
     if (row >= r.q) return;
@@ -764,9 +768,10 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_first(const TX* __restr
     const int at = (int)(id % r.chunks) * r.piece, end = min(at + r.piece, r.P);
     const float* st = stats + 2 * (row / D);
     if (f.part) {
-        // every workgroup that holds a part of a group may store its statistics: the same bits
+        // the workgroup with the first row of a group, and the first piece of it, stores its statistics
         const int64_t g0 = row0 / D, g1 = min(row0 + teams - 1, r.rows - 1) / D;
-        join_chunks(f, g0, (int)(g1 - g0) + 1, joined, at == 0, stats);
+        const int ng = (int)(g1 - g0) + 1;
+        join_chunks(f, g0, ng, joined, at ? ng : row0 % D ? 1 : 0, stats);
         st = joined + 2 * (row / D - g0);
     }
     if (row >= r.rows) return;
@@ -801,8 +806,9 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_apply_cross(const TX* __restr
     const Spot s = spot_of(q, id % per_item, b, C, P);
     const float* st = stats + 2 * b * (C / D);
     if (f.part) {
-        const int g0 = s.c0 / D;
-        join_chunks(f, b * (C / D) + g0, (s.c0 + s.nc - 1) / D - g0 + 1, joined, s.p0 == 0, stats);
+        // the tile with the first channel of a group, and the first positions, stores its statistics
+        const int g0 = s.c0 / D, ng = (s.c0 + s.nc - 1) / D - g0 + 1;
+        join_chunks(f, b * (C / D) + g0, ng, joined, s.p0 ? ng : s.c0 % D ? 1 : 0, stats);
         st = joined - 2 * g0;
     }
     if constexpr (XLAST) {
@@ -905,6 +911,17 @@ struct Plan {
 // few and the workgroups too.
 bool joins(const GroupNorm& g, int chunks) {
     return (int64_t)chunks * g.groups <= 1024 && g.B * g.C * g.P <= (int64_t)4096 * 4096;
+}
+
+// Groups that a workgroup of the output has a part of, at most.
+int join_most(const GroupNorm& g) {
+    const int64_t D = g.C / g.groups;
+    if (g.x_last == g.out_last)
+        // channels first: 256 threads' rows are fewer values than a group that does not fit a workgroup
+        return g.x_last ? (int)g.groups : 2;
+    // a tile of 64 channels; where borders of groups are none of tiles, it can begin and end within one
+    if (g.C <= kMaxTileChannels) return (int)g.groups;
+    return kMaxTileChannels % D == 0 ? (int)(kMaxTileChannels / D) : (int)((kMaxTileChannels - 2) / D + 2);
 }
 
 size_t once_lds(const GroupNorm& g, const Plan& p) {
@@ -1012,7 +1029,7 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
         float* stats = a.stats;
         const bool last = p.how == kSplitLast || p.how == kWide;
         const int64_t per = last ? (int64_t)p.per * (p.how == kWide ? 1 : p.rows.R) * D : p.per;
-        const Join join{p.join ? part : nullptr, p.chunks, (int)g.groups, last, per, n, g.eps};
+        const Join join{p.join ? part : nullptr, p.chunks, (int)g.groups, join_most(g), last, per, n, g.eps};
         const size_t lds = sizeof(float) * (size_t)(p.rows.threads * V + 2 * (D ? p.rows.cs / D : 0));
         if (kernel == 0 && p.how == kOnceLast)
             return launch_clear((uint64_t*)part, p.parts, s);

@@ -670,3 +670,27 @@ def test_groups_of_many_pairs():
 def test_16_bit_fields_with_float32_grad_out(b, c, grid, groups, dtype):
     """Larger fields that stay in 16 bits on one side only, in one layout."""
     check(b, c, grid, groups, "gelu", dtype, F32, True, True, seed=240)
+
+
+@pytest.mark.parametrize("b,c,grid,groups,last", [
+    (4, 133, (128, 128), 19, False),       # group 18 lies in two tiles of 64 channels, group 9 too
+    (2, 130, (16384,), 10, False),
+    (1, 192, (16384,), 2, False),          # of 96 channels
+    (2, 66, (128, 129), 33, False),
+    (3, 150, (2001,), 6, True),            # 2001 positions: two passes
+])
+@pytest.mark.parametrize("seed", range(4))
+def test_groups_in_two_tiles(b, c, grid, groups, last, seed):
+    """A group whose output several workgroups write, each joining the chunks itself, has one set of statistics: every
+    output is, to the bit, what the stored ones make of its value."""
+    x = field(shape_of(b, c, grid, last), F32, 250 + seed)
+    opts = dict(channels_last=last, out_channels_last=not last)
+    out, stats = fno.fno_group_norm(x, groups, **opts)
+    assert fno.fno_last_kernels() == ["gn_stats", "gn_apply_cross"]
+    mean, rstd = (s.repeat_interleave(c // groups, 1).view(b, c, 1) for s in stats.unbind(2))
+    flat = x.view(b, -1, c).transpose(1, 2) if last else x.view(b, c, -1)
+    want = (flat - mean) * rstd
+    got = out.view(b, c, -1) if last else out.view(b, -1, c).transpose(1, 2)
+    assert torch.equal(got, want)
+    again, st = fno.fno_group_norm(x, groups, **opts)
+    assert torch.equal(again, out) and torch.equal(st, stats)
