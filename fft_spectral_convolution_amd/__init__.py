@@ -111,6 +111,7 @@ _SIGNATURES = {
     "fno_group_norm_workspace_size": (_S, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "fno_group_norm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _I, _I, _I, _P, _S, _P]),
     "fno_group_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _S, _P]),
+    "fno_set_exchange_looks": (_I, [_I]),
     "fno_grad_norm_workspace_size": (_S, [_I]),
     "fno_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _S, _P]),
     "fno_clip_grad_norm": (_I, [_P, _P, _P, _P, _I, _F, _P, _P, _P, _S, _P]),
@@ -643,12 +644,27 @@ def _group_norm_args(torch, x, groups, weight, bias, act, channels_last, out_cha
             out_shape, (b, max(groups, 0), 2))
 
 
+_MOST_LOOKS = 4096          # of include/fno.h, and the library's own choice
+_looks = _MOST_LOOKS
+
+
+def _follow_looks():
+    """FNO_GN_SPIN, as it stands at the call, sets the looks of fno_set_exchange_looks."""
+    global _looks
+    want = min(max(int(os.environ["FNO_GN_SPIN"]), 0), _MOST_LOOKS) if "FNO_GN_SPIN" in os.environ else _MOST_LOOKS
+    if want != _looks:
+        _check(lib().fno_set_exchange_looks(want), "fno_set_exchange_looks")
+        _looks = want
+
+
 def _group_norm_scratch(torch, x, sizes, options, backward):
     """Scratch of one call alone (so calls on other streams and captured graphs share none): a tensor or None, its
     address and size."""
     size = _group_norm_workspace_size(*sizes, *options[1:], backward)
     if not size:
         return None, 0, 0
+    if options[1]:          # channels last: the items may be spread over workgroups
+        _follow_looks()
     ws = x.new_empty(size, dtype=torch.uint8)
     return ws, ws.data_ptr(), size
 

@@ -1572,6 +1572,12 @@ int fno_group_norm_backward(const void* x, const float* weight, const float* bia
     return group_norm_common(g, a, true, ws_bytes, stream);
 }
 
+int fno_set_exchange_looks(int looks) {
+    if (looks < 0 || looks > kExchangeLooks) return FNO_ERR_VALUE;
+    set_exchange_looks(looks);
+    return FNO_OK;
+}
+
 size_t fno_grad_norm_workspace_size(int count) { return count < 0 ? 0 : grad_norm_workspace(count); }
 
 int fno_grad_norm(const void* const* grads, const long long* numels, const int* types, int count, float* norm,

@@ -1062,7 +1062,7 @@ hipError_t gn_forward_launch(const GroupNorm& g, const GroupNormArgs& a, int ker
             if (p.how == kOnceLast)
                 return with_vectors<kOnceVectors>(p.once.nv, [&](auto nv) {
                     const OnceArgs<TX, TY> args{x,      a.weight, a.bias, out, a.stats, (uint64_t*)part,
-                                                p.rows, p.once,   g.eps,  once_spin()};
+                                                p.rows, p.once,   g.eps,  once_looks.load()};
                     constexpr int NV = decltype(nv)::value;
                     const bool turn = g.x_last != g.out_last;
                     const auto kernel_of = turn ? k_gn_once_last<ACT, NV, true, TX, TY>

@@ -3,7 +3,7 @@
 #pragma once
 
 #include <algorithm>
-#include <cstdlib>
+#include <atomic>
 
 #include "fno_fields.hpp"
 
@@ -258,13 +258,9 @@ hipError_t with_vectors(int nv, F&& f) {
     }
 }
 
-// Looks for another workgroup's sums before a workgroup forms them itself:
-// some milliseconds.  FNO_GN_SPIN sets another count (0: at once), which is how
-// that path is tested.
-inline int once_spin() {
-    const char* v = std::getenv("FNO_GN_SPIN");
-    return v ? std::max(0, std::atoi(v)) : 4096;
-}
+// Looks for another workgroup's sums before a workgroup forms them itself: at
+// most some milliseconds.  fno_set_exchange_looks sets another count.
+inline std::atomic<int> once_looks{kExchangeLooks};
 
 // ---- channels first ------------------------------------------------------------
 // Rows (b, c) of P positions.  A team of `team` threads (a power of two, at

@@ -1239,7 +1239,7 @@ hipError_t gn_backward_launch(const GroupNorm& g, const GroupNormArgs& a, int ke
                                                 stats, gx,
                                                 a.grad_weight || a.grad_bias ? part : nullptr,
                                                 reinterpret_cast<uint64_t*>(gsum),
-                                                p.rows, p.once, once_spin()};
+                                                p.rows, p.once, once_looks.load()};
                     return launch_kernel(k_gn_bwd_once_last<ACT, NV, TX, TY>, dim3((unsigned)p.once.total),
                                          dim3(p.rows.threads), p.lds, s, args);
                 });
@@ -1309,6 +1309,8 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_clear(uint64_t* slots, int64_
 hipError_t launch_clear(uint64_t* slots, int64_t n, hipStream_t s) {
     return launch_kernel(k_gn_clear, grid_of((n + kGnThreads - 1) / kGnThreads), dim3(kGnThreads), 0, s, slots, n);
 }
+
+void set_exchange_looks(int looks) { once_looks.store(looks); }
 
 // ---- both directions ---------------------------------------------------------------------------
 int group_norm_kernels(const GroupNorm& g, const GroupNormArgs& a, bool backward, const char** names) {

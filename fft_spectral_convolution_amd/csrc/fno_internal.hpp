@@ -314,6 +314,8 @@ struct GroupNormArgs {
 // A call is a list of kernels, launched one after the other.
 int group_norm_kernels(const GroupNorm& g, const GroupNormArgs& a, bool backward, const char** names);
 size_t group_norm_workspace(const GroupNorm& g, bool backward);
+constexpr int kExchangeLooks = 4096;
+void set_exchange_looks(int looks);                     // 0 to kExchangeLooks
 hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s);
 
 // ---- gradient norm and clipping (fno_gradnorm.hip) ----------------------------

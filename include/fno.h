@@ -377,6 +377,15 @@ int fno_group_norm_backward(const void* x, const float* weight, const float* bia
                             int x_type, int out_type, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Large channels-last items are spread over workgroups that read the field
+ * once and exchange their sums.  A workgroup that does not see another's after
+ * so many looks (0 to 4096, which is where it stands at first, a few
+ * milliseconds) forms them itself, from the field: the same bits, later.  For
+ * the process, from the next call on.
+ */
+int fno_set_exchange_looks(int looks);
+
+/*
  * Global norm of `count` gradients, and clipping by it:
  *
  *   norm = sqrt(sum over all values of |g|^2)

@@ -182,3 +182,25 @@ def test_queried_workspace_serves_random_fields(lib, seed):
         groups = rng.choice([g for g in range(1, c + 1) if c % g == 0])
         dims = (int(2 ** rng.uniform(0, 8)), c, int(2 ** rng.uniform(0, 20)), groups)
         _queried_size_serves(lib, dims, rng.randint(0, 1), rng.randint(0, 1), rng.randint(0, 2))
+
+
+def test_looks_are_bounded(lib, monkeypatch):
+    """The wait for another workgroup's sums ends, whatever is asked for."""
+    for looks in (-1, 4097, 2 ** 31 - 1, -2 ** 31):
+        assert lib.fno_set_exchange_looks(looks) == VALUE
+    asked = []
+    monkeypatch.setattr(fno, "lib", lambda: type("L", (), {"fno_set_exchange_looks": lambda self, n: asked.append(n)
+                                                           or lib.fno_set_exchange_looks(n)})())
+    for value, want in (("0", [0]), ("0", []), ("-5", []), ("17", [17]), ("2147483647", [4096]), ("99999999999", []),
+                        ("1", [1]), (None, [4096])):
+        asked.clear()
+        if value is None:
+            monkeypatch.delenv("FNO_GN_SPIN")
+        else:
+            monkeypatch.setenv("FNO_GN_SPIN", value)
+        fno._follow_looks()
+        assert asked == want, value
+    # nothing in the library follows the environment, which other threads may be changing
+    src = os.path.join(os.path.dirname(fno.__file__), "csrc")
+    for name in os.listdir(src):
+        assert "getenv" not in open(os.path.join(src, name)).read(), name
