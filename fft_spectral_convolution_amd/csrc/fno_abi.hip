@@ -1585,6 +1585,12 @@ int fno_grad_norm(const void* const* grads, const long long* numels, const int* 
     const int rc = check_grads(grads, numels, types, count);
     if (rc) return rc;
     if (!norm) return FNO_ERR_NULL;
+    // the gradients are only read and may overlap each other
+    const Span n{norm, sizeof(float)}, ws{workspace, ws_bytes};
+    if (any_overlap({n, ws}, {})) return FNO_ERR_ALIAS;
+    for (int i = 0; i < count; ++i)
+        if (numels[i] && any_overlap({n, ws}, {{grads[i], (size_t)numels[i] * type_bytes(types[i])}}))
+            return FNO_ERR_ALIAS;
     return grad_norm_common(grads, nullptr, numels, types, count, 0.0f, nullptr, norm, workspace, ws_bytes, stream);
 }
 

@@ -396,6 +396,9 @@ int fno_set_exchange_looks(int looks);
  * mix types.  Squares are summed in float64.  norm is one float32 in device
  * memory: nothing is copied to the host or waited for.
  *
+ * fno_grad_norm: neither norm nor workspace may overlap a gradient or each
+ * other (FNO_ERR_ALIAS); the same gradient given twice counts twice.
+ *
  * fno_clip_grad_norm: outs[i] == grads[i] clips in place; otherwise nothing
  * written may overlap anything else, the same tensor given twice included
  * (FNO_ERR_ALIAS).  In place and with norm + 1e-6 <= max_norm nothing is

@@ -204,3 +204,16 @@ def test_looks_are_bounded(lib, monkeypatch):
     src = os.path.join(os.path.dirname(fno.__file__), "csrc")
     for name in os.listdir(src):
         assert "getenv" not in open(os.path.join(src, name)).read(), name
+
+
+def test_norm_written_over_a_gradient(lib):
+    """fno_grad_norm writes its norm and workspace and nothing else."""
+    grads = [(X, 100, 0), (G, 100, 3), (B, 0, 0)]
+    for n in (X, X + 396, G + 796):
+        assert total(lib, grads, n=n) == ALIAS, hex(n)
+    assert total(lib, grads, ws=X - 256) == ALIAS and total(lib, grads, ws=G + 512) == ALIAS
+    assert total(lib, grads, n=WS + 1024) == ALIAS
+    # next to them, on an empty one, and a gradient twice: taken (and then refused for the workspace's alignment)
+    for n in (X - 4, X + 400, G + 800, B):
+        assert total(lib, grads, n=n, ws=WS + 8) == ALIGN, hex(n)
+    assert total(lib, [(X, 100, 0), (X, 100, 0), (X + 4, 9, 0)], ws=WS + 8) == ALIGN

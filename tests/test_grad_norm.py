@@ -249,3 +249,15 @@ def test_captured_and_replayed(name):
         for (_, _, outs, norm), (o, n) in zip(runs, wants):
             assert torch.equal(norm, n)
             assert all(torch.equal(a, b) for a, b in zip(outs, o))
+
+
+def test_norm_over_a_gradient_is_refused():
+    g = torch.full((), 3.0, device=DEV)
+    packed = torch.ones(8, device=DEV)
+    for grads, out in (([g], g), ([packed], packed[5]), ([packed[:3], packed[3:]], packed[7])):
+        with pytest.raises(fno.FnoError) as e:
+            fno.fno_grad_norm(grads, out=out)
+        assert e.value.status == -4
+    assert fno.fno_grad_norm([packed[:5]], out=packed[5]) is not None
+    torch.cuda.synchronize()
+    assert g.item() == 3.0 and (packed[:5] == 1).all() and abs(packed[5].item() - 5 ** 0.5) < 4 * U
