@@ -1161,13 +1161,13 @@ int check_grads(const void* const* grads, const long long* numels, const int* ty
 // writes, but for a tensor clipped in place: sorted by address, each span
 // must end before the next that either side writes.
 bool grads_overlap(const void* const* grads, void* const* outs, const long long* numels, const int* types, int count,
-                   std::initializer_list<Span> others) {
+                   std::initializer_list<Span> written, const Span& given) {
     struct Piece {
         uintptr_t at, end;
         bool written;
     };
     std::vector<Piece> v;
-    v.reserve(2 * (size_t)count + others.size());
+    v.reserve(2 * (size_t)count + written.size() + 1);
     auto add = [&](const void* p, size_t bytes, bool written) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p);
         if (p && bytes) v.push_back({a, a + bytes, written});
@@ -1177,7 +1177,8 @@ bool grads_overlap(const void* const* grads, void* const* outs, const long long*
         if (outs[i] != grads[i]) add(grads[i], bytes, false);
         add(outs[i], bytes, true);
     }
-    for (const Span& o : others) add(o.p, o.bytes, true);
+    for (const Span& o : written) add(o.p, o.bytes, true);
+    add(given.p, given.bytes, false);
     std::sort(v.begin(), v.end(), [](const Piece& a, const Piece& b) { return a.at < b.at; });
     uintptr_t read_end = 0, write_end = 0;   // ends of what lies before, by kind
     for (const Piece& p : v) {
@@ -1605,8 +1606,8 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
     if (!given_norm && !norm) return FNO_ERR_NULL;
     if (!(max_norm >= 0.0f)) return FNO_ERR_VALUE;
     try {
-        if (grads_overlap(grads, outs, numels, types, count,
-                          {{norm, 4}, {given_norm == norm ? nullptr : given_norm, 4}, {workspace, ws_bytes}}))
+        if (grads_overlap(grads, outs, numels, types, count, {{norm, 4}, {workspace, ws_bytes}},
+                          {given_norm == norm ? nullptr : given_norm, 4}))
             return FNO_ERR_ALIAS;
     } catch (const std::bad_alloc&) {
         return FNO_ERR_NOMEM;

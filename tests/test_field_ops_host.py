@@ -217,3 +217,14 @@ def test_norm_written_over_a_gradient(lib):
     for n in (X - 4, X + 400, G + 800, B):
         assert total(lib, grads, n=n, ws=WS + 8) == ALIGN, hex(n)
     assert total(lib, [(X, 100, 0), (X, 100, 0), (X + 4, 9, 0)], ws=WS + 8) == ALIGN
+
+
+def test_given_norm_is_only_read(lib):
+    """It may be one of the gradients that are only read, not of those written, nor in the workspace."""
+    two, apart = [(X, 100, 0), (G, 100, 0)], [GW, GW + 400]
+    assert clip(lib, two, outs=apart, given=X + 40, ws=WS + 8) == ALIGN           # taken up to the workspace's alignment
+    assert clip(lib, two, outs=apart, given=O, ws=WS + 8) == ALIGN                # norm itself
+    assert clip(lib, two, outs=[X, GW], given=X + 40) == ALIAS
+    assert clip(lib, two, outs=apart, given=GW + 796) == ALIAS
+    assert clip(lib, two, outs=apart, given=WS + 512) == ALIAS
+    assert clip(lib, two, outs=apart, given=O + 2) == ALIAS

@@ -261,3 +261,10 @@ def test_norm_over_a_gradient_is_refused():
     assert fno.fno_grad_norm([packed[:5]], out=packed[5]) is not None
     torch.cuda.synchronize()
     assert g.item() == 3.0 and (packed[:5] == 1).all() and abs(packed[5].item() - 5 ** 0.5) < 4 * U
+
+
+def test_given_norm_among_the_gradients():
+    g = torch.tensor([3.0, 4.0], device=DEV)
+    out = torch.empty_like(g)
+    assert fno.fno_clip_grad_norm([g], 1.5, norm=g[0], out=[out]).item() == 3.0
+    check_scaled([out], [g], 1.5 / (3.0 + 1e-6))
