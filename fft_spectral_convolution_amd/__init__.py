@@ -636,6 +636,8 @@ def _group_norm_args(torch, x, groups, weight, bias, act, channels_last, out_cha
     if b > 0x7fffffff or c > 0x7fffffff or p > 0x7fffffff:
         raise ValueError(f"x is too large: shape {tuple(shape)}")
     groups = int(groups)
+    if not -0x80000000 <= groups <= 0x7fffffff:       # ctypes would pass its low 32 bits
+        raise ValueError(f"groups is too large: {groups}")
     device = x.device
     params = (_f32_ptr(torch, weight, (c,), device, "weight"), _f32_ptr(torch, bias, (c,), device, "bias"))
     out_shape = shape if bool(channels_last) == bool(out_channels_last) else \

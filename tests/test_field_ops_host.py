@@ -228,3 +228,12 @@ def test_given_norm_is_only_read(lib):
     assert clip(lib, two, outs=apart, given=GW + 796) == ALIAS
     assert clip(lib, two, outs=apart, given=WS + 512) == ALIAS
     assert clip(lib, two, outs=apart, given=O + 2) == ALIAS
+
+
+@pytest.mark.parametrize("groups", [2 ** 32 + 2, -2 ** 32 + 2, 2 ** 31, 2 ** 63])
+def test_groups_beyond_32_bits(groups, monkeypatch):
+    """Refused by the binding: the call would see the low 32 bits, here a divisor of the channels."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(fno, "_field_type", lambda *a: 0)         # a CPU tensor stands for the field
+    with pytest.raises(ValueError):
+        fno._group_norm_args(torch, torch.zeros(1, 8, 4), groups, None, None, "none", False, None)
