@@ -67,7 +67,7 @@ std::vector<std::unique_ptr<DeviceState>> g_devices;
 
 // Optional per-kernel timing (fno_set_timing_events): kernel k of a call
 // launches with events[2k], events[2k + 1] as its start and stop events.
-constexpr int kMaxKernels = 16;
+constexpr int kMaxKernels = 256;      // counted and named: clipping launches two for every 128 tensors
 struct Recorder {
     void** events = nullptr;
     int n_events = 0;

@@ -426,7 +426,8 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
  * Kernels whose pair lies beyond n_events-1 launch without events.  Pass NULL
  * to stop.  Returns FNO_OK.  fno_last_kernel_count / fno_last_kernel_name
  * report, for the calling thread's last successful call, how many kernels it
- * launched and their names (static storage; "" for an index out of range).
+ * launched (counted up to 256) and their names (static storage; "" for an
+ * index out of range).
  */
 int fno_set_timing_events(void** events, int n_events);
 int fno_last_kernel_count(void);

@@ -268,3 +268,15 @@ def test_given_norm_among_the_gradients():
     out = torch.empty_like(g)
     assert fno.fno_clip_grad_norm([g], 1.5, norm=g[0], out=[out]).item() == 3.0
     check_scaled([out], [g], 1.5 / (3.0 + 1e-6))
+
+
+@pytest.mark.parametrize("count", [129, 1000, 3000])
+def test_every_kernel_of_a_long_list_is_counted(count):
+    tables = (count + 127) // 128
+    grads = make([((100,), F32)] * count, 12)
+    norm = norm_of(grads)
+    raw = [g.clone() for g in grads]
+    got = fno.fno_clip_grad_norm(grads, 0.5)
+    assert fno.fno_last_kernels() == ["grad_sumsq"] * tables + ["grad_finish"] + ["grad_scale"] * tables
+    assert abs(got.item() - norm) <= 2 * U * norm
+    check_scaled(grads, raw, 0.5 / (norm + 1e-6))
