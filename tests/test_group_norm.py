@@ -694,3 +694,87 @@ def test_groups_in_two_tiles(b, c, grid, groups, last, seed):
     assert torch.equal(got, want)
     again, st = fno.fno_group_norm(x, groups, **opts)
     assert torch.equal(again, out) and torch.equal(st, stats)
+
+
+# every schedule of the backward pass, with remainders of vectors, rows, tiles and chunks
+SUMS = [
+    (2, 4, (32, 32), 2), (5, 33, (7, 9), 11), (300, 4, (3,), 2), (2, 511, (9,), 7), (3, 30, (61, 47), 5),
+    (4, 32, (64, 64), 4), (70, 32, (64, 64), 8), (32, 64, (128, 128), 8), (256, 64, (4096,), 16),
+    (1, 3, (100003,), 1), (8, 128, (16384,), 32), (1, 64, (512, 512), 64), (2, 16, (1031, 1033), 4),
+    (4, 133, (128, 127), 19), (1, 2049, (8,), 3), (2, 4100, (701,), 41), (1, 2051, (5000,), 7),
+]
+
+
+@pytest.mark.parametrize("last,out_last", LAYOUTS)
+@pytest.mark.parametrize("dtype,out_dtype", [(F32, F32), (BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("b,c,grid,groups", SUMS)
+def test_parameter_gradients_of_whole_numbers(b, c, grid, groups, dtype, out_dtype, last, out_last):
+    """With whole numbers x (mean 0 and deviation 1 prescribed) and grad_out the sums are whole numbers below 2^24 and
+    exact in float32 in any order.  All are positive: no position can be lost or counted twice."""
+    g = torch.Generator(device=DEV).manual_seed(260)
+    x = torch.randint(1, 3, shape_of(b, c, grid, last), generator=g, device=DEV).to(dtype)
+    dy = torch.randint(1, 4, shape_of(b, c, grid, out_last), generator=g, device=DEV).to(out_dtype)
+    w, bias = params(c, 261)
+    stats = torch.tensor([0.0, 1.0], device=DEV).expand(b, groups, 2).contiguous()
+    xg, yg = to_groups(x, groups, last), to_groups(dy, groups, out_last)
+    want_b, want_w = yg.sum((0, 3)).flatten(), (xg * yg).sum((0, 3)).flatten()
+    assert want_w.max().item() < 2 ** 24
+    for need_x in (True, False):
+        _, gw, gb = fno.fno_group_norm_backward(x, stats, dy, groups, weight=w, bias=bias, channels_last=last,
+                                                out_channels_last=out_last, need_x=need_x)
+        assert torch.equal(gb.double(), want_b) and torch.equal(gw.double(), want_w), need_x
+
+
+@pytest.mark.parametrize("last,out_last", LAYOUTS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("b,c,grid,groups", SUMS)
+def test_statistics_of_the_ends(b, c, grid, groups, dtype, last, out_last):
+    """Ones at an item's first and last 61 positions and zeros between: with a share k of ones the mean is k and the
+    variance k (1 - k).  One of the at most 122 positions lost or counted twice changes both by a hundredth.  A
+    thread's sums of these whole numbers are exact; the joins of threads and chunks, fewer than 64 additions in a row,
+    leave 64 u."""
+    p = 1
+    for v in grid:
+        p *= v
+    at = torch.arange(p, device=DEV)
+    line = ((at < 61) | (at >= p - 61)).to(dtype)
+    x = (line.view(1, p, 1).expand(b, p, c) if last else line.view(1, 1, p).expand(b, c, p)).contiguous()
+    x = x.view(shape_of(b, c, grid, last))
+    _, stats = fno.fno_group_norm(x, groups, eps=1e-5, channels_last=last, out_channels_last=out_last)
+    k = line.sum().item() / p
+    mean = torch.full((b, groups), k, dtype=torch.float64, device=DEV)
+    rstd = torch.full_like(mean, (k * (1 - k) + 1e-5) ** -0.5)
+    close(stats[..., 0], mean, 64 * U * mean, "mean")
+    # the squares about a mean that is itself off by 64 u of at most 1, where all values are ones
+    close(stats[..., 1], rstd, rstd * 64 * U + rstd ** 3 * (64 * U) ** 2, "rstd")
+
+
+@pytest.mark.parametrize("last,out_last", LAYOUTS)
+def test_parameter_gradients_of_many_values(last, out_last):
+    """26 million values of either sign a channel.  A value's rounding errors are random; one of an addition has a
+    deviation of 0.45 u times the sum it leaves.  n values in chains of L, whose sums are added pairwise over l levels,
+    then carry 0.45 u (L / 2 + l)^1/2 n^1/2 rms: 2.5 u n^1/2 rms for chains of 16 and, together, 20 levels.  Over 64
+    channels the root mean square is within a third of that; 4 is allowed (chains of hundreds give more)."""
+    b, c, p, groups = 25, 64, 1 << 20, 8
+    x = torch.empty(shape_of(b, c, (p,), last), device=DEV)
+    dy = torch.empty(shape_of(b, c, (p,), out_last), device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(270)
+    x.normal_(generator=g)
+    dy.normal_(generator=g)
+    stats = torch.tensor([0.0, 1.0], device=DEV).expand(b, groups, 2).contiguous()
+    w, bias = params(c, 271)
+    _, gw, gb = fno.fno_group_norm_backward(x, stats, dy, groups, weight=w, bias=bias, channels_last=last,
+                                            out_channels_last=out_last, need_x=False)
+    want_w, want_b, sq_w, sq_b = (torch.zeros(c, dtype=torch.float64, device=DEV) for _ in range(4))
+    for i in range(b):
+        xi = x[i].double() if last else x[i].double().t()
+        yi = dy[i].double() if out_last else dy[i].double().t()
+        want_b += yi.sum(0)
+        sq_b += yi.square().sum(0)
+        xi = xi * yi
+        want_w += xi.sum(0)
+        sq_w += xi.square_().sum(0)
+    for got, want, sq, what in ((gw, want_w, sq_w, "grad_weight"), (gb, want_b, sq_b, "grad_bias")):
+        rms = ((got.double() - want).square() / sq).mean().sqrt().item() / U
+        print(f"  {what}: root mean square error {rms:.2f} u n^1/2 rms", flush=True)
+        assert rms <= 4.0, what
