@@ -112,11 +112,12 @@ def kernel_bytes(name: str, cfg, backward: bool = False) -> int:
         # is split): counted as its one compulsory write
         "wgrad_reduce": wb,
         # norm and clipping of the weight gradient: read once, scaled into
-        # another tensor, the chunks' sums joined (a table holds 1024)
+        # another tensor; a float64 sum of each 16 KiB chunk, or of the 2048
+        # workgroups that take more chunks in turn, joined
         "grad_sumsq": wb,
         "grad_scale": 2 * wb,
         "grad_small": 2 * wb,
-        "grad_finish": 8 * 1024,
+        "grad_finish": 8 * min(-(-wb // 16384), 2048),
     }
     return table[name.split(":")[0]]
 

@@ -46,3 +46,17 @@ def test_every_recorded_kernel_has_bench_byte_figures():
         for cfg in (CONFIGS["c1"], CONFIGS["c4"]):
             assert bench.kernel_bytes(name, cfg) > 0, name
             bench.compulsory_share(name, cfg)
+
+
+def test_joined_sums_of_the_gradient_norm():
+    # a launch leaves a float64 for each chunk of 16 KiB, 2048 at most; the
+    # constants are those of the kernel's source
+    import re
+    sys.path.insert(0, ROOT)
+    import bench
+    from fft_spectral_convolution_amd.inputs import CONFIGS
+    src = open(os.path.join(ROOT, "fft_spectral_convolution_amd", "csrc", "fno_gradnorm.hip")).read()
+    chunk, most = (int(re.search(r"constexpr int %s = (\d+);" % n, src).group(1)) for n in ("kChunkBytes", "kPartBlocks"))
+    for cfg in CONFIGS.values():
+        parts = min((bench.kernel_bytes("grad_sumsq", cfg) + chunk - 1) // chunk, most)
+        assert bench.kernel_bytes("grad_finish", cfg) == 8 * parts
