@@ -180,7 +180,8 @@ struct Running {
         q = fmaf(d, d, q);
     }
     __device__ __forceinline__ float mean(float n) const { return pivot + s / n; }
-    __device__ __forceinline__ float squares(float n) const { return fmaxf(q - s * (s / n), 0.0f); }
+    // (one rounding: where q has passed float32's range, it stays infinite instead of infinity less infinity)
+    __device__ __forceinline__ float squares(float n) const { return fmaxf(fmaf(-s, s / n, q), 0.0f); }
 };
 
 // The first of two reads, bound by memory: 537 MB in 95 us (5.6 TB/s).

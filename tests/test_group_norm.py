@@ -778,3 +778,30 @@ def test_parameter_gradients_of_many_values(last, out_last):
         rms = ((got.double() - want).square() / sq).mean().sqrt().item() / U
         print(f"  {what}: root mean square error {rms:.2f} u n^1/2 rms", flush=True)
         assert rms <= 4.0, what
+
+
+@pytest.mark.parametrize("key", [*SUMS, (1, 64, (256, 256), 8), (2, 64, (512, 512), 2)], ids=str)
+@pytest.mark.parametrize("last,out_last", LAYOUTS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_squares_beyond_float32(key, last, out_last, dtype):
+    """Finite values whose squares are not: the deviation is infinite, out = act(bias), and the gradient is zero."""
+    b, c, grid, groups = key
+    p = 1
+    for v in grid:
+        p *= v
+    w, bias = params(c, 281)
+    opts = dict(weight=w, bias=bias, channels_last=last, out_channels_last=out_last)
+    want = to_groups(bias.to(dtype).view(1, c, 1), groups, False).expand(b, -1, -1, p)
+    # one magnitude, the sign alternating at every so many positions: each thread's values have the same mean
+    for period in (1, 2, 4, 16, 64, 256, 1024):
+        line = 1e21 * (1 - 2 * (torch.arange(p, device=DEV) // period % 2))
+        line = (line.view(1, p, 1).expand(b, p, c) if last else line.view(1, 1, p).expand(b, c, p)).contiguous()
+        x = line.to(dtype).view(shape_of(b, c, grid, last))
+        out, stats = fno.fno_group_norm(x, groups, **opts)
+        assert torch.isfinite(stats[..., 0]).all()
+        if period >= p:
+            continue              # no deviation at all
+        assert (stats[..., 1] == 0).all(), period
+        assert torch.equal(to_groups(out, groups, out_last), want.double()), period
+        gx, _, _ = fno.fno_group_norm_backward(x, stats, torch.ones_like(out), groups, **opts)
+        assert (gx == 0).all()
