@@ -103,7 +103,7 @@ __device__ __forceinline__ float clip_coef(double norm, float max_norm) {
     return c > 1.0 ? 1.0f : (float)c;
 }
 
-// One block: the norm from the partial sums (or as given), and the factor.  4.7
+// One block: the norm from the partial sums (or as given), and the factor.  4.7 to 5.0
 // us, a launch and the latency of the sums: workgroups that leave them to the
 // last of them would need a counter that someone clears.
 __global__ __launch_bounds__(kThreads) void k_grad_finish(const double* __restrict__ part, int nparts,
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void k_grad_finish(const double* __restri
 }
 
 // At most kGradSmallChunks chunks: everything in one workgroup, a wave a chunk.
-// The second read comes from the caches.  11 tensors of 17 KB: 8.2 us, latency.
+// The second read comes from the caches.  11 tensors of 17 KB: 7 to 8 us, latency.
 __global__ __launch_bounds__(1024) void k_grad_small(GradTable t, uint32_t nchunks, float max_norm, bool scale,
                                                      float* __restrict__ norm) {
     __shared__ double red[16];

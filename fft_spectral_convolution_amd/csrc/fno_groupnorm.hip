@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_last(const TX* __res
 
 // ---- one pass, channels first ------------------------------------------------------
 // Workgroup (item, group): D rows of P values, one run of memory, read once.
-// 1024 groups of 32768 values, float32: 58 us, 4.6 TB/s where a copy has 5.1.
+// 1024 groups of 32768 values, float32: 58 to 60 us, 4.5 to 4.6 TB/s where a copy has 5.1.
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kFusedThreads) void k_gn_fused_first(const TX* __restrict__ x,
                                                                  const float* __restrict__ w,
@@ -594,8 +594,9 @@ struct OnceLast {
 };
 
 // Where others' sums stayed out: their chunks from memory, in the same order,
-// then this workgroup's own again.  A call that does not return to the
-// kernel's registers, which are thus not sized for it.
+// then this workgroup's own again.  A call, so that the kernel's own registers
+// are not allotted around it; its frame costs every lane 200 to 290 bytes of
+// scratch, touched only here.
 template <int ACT, int NV, bool TURN, typename TX, typename TY>
 __device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float* lds, int* flag, int lost) {
     typedef OnceLast<ACT, NV, TURN, TX, TY> F;
@@ -618,8 +619,8 @@ __device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float
 // Four waves a SIMD, each with 16 vectors a thread in its registers: 65 us for
 // the 128 x 128 field (32 x 64 channels, float32) where 8 vectors took 83; 62
 // with the channels' constants asked for before the join; the kernel alone now
-// takes 58 (268 MB, 4.6 TB/s), and 46 from bfloat16 to a channels-first float32
-// field (4.4 TB/s).  Memory bounds it, and that a workgroup loads, joins and
+// takes 58 (268 MB, 4.6 TB/s), with 4 to 6 of its 128 registers spilled, and 46 to
+// 47 from bfloat16 to a channels-first float32 field (4.3 TB/s).  Memory bounds it, and that a workgroup loads, joins and
 // stores in turn.
 template <int ACT, int NV, bool TURN, typename TX, typename TY>
 __global__ __launch_bounds__(kOnceThreads, 4) void k_gn_once_last(OnceArgs<TX, TY> args) {

@@ -156,7 +156,7 @@ __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_last(
 // Every vector leaves its sums of g and g xh in LDS, for its first channel
 // and, where the row length is no multiple of V, for the next one (a row is
 // at least a vector long); the vectors of each channel are then added in order.
-// 4096 groups of 16384 values, float32: 150 us for 805 MB (5.4 TB/s): memory.
+// 4096 groups of 16384 values, float32: 149 to 151 us for 805 MB (5.3 to 5.4 TB/s): memory.
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kFusedThreads) void k_gn_bwd_fused_first(
     const TX* __restrict__ x, const TY* __restrict__ dy, const float* __restrict__ w, const float* __restrict__ bias,
@@ -475,7 +475,8 @@ __device__ __attribute__((noinline)) void once_late(OnceArgs<TX, TY> args, float
 // the 128 x 128 field (32 x 64 channels, float32) where four waves of 8
 // vectors took 111 and of 4 vectors 165 (what a workgroup costs whatever it
 // holds shows; not waiting for the others changed none of them).  The kernel
-// alone now takes 86 us (403 MB, 4.7 TB/s).
+// alone now takes 86 us (403 MB, 4.7 TB/s); with 8 vectors of a bfloat16 field and
+// a float32 grad_out 64 us (268 MB, 4.2 TB/s).
 template <int ACT, int NV, typename TX, typename TY>
 __global__ __launch_bounds__(kOnceThreads, 2) void k_gn_bwd_once_last(OnceArgs<TX, TY> args) {
     typedef OnceLast<ACT, NV, TX, TY> F;
@@ -594,7 +595,7 @@ __global__ __launch_bounds__(kMaxSlots) void k_gn_bwd_sums_last(const TX* __rest
 }
 
 // Channels first: a team takes a row or a piece of it; part[row chunks + piece].
-// 1.07 GB in 186 us (5.8 TB/s): memory.
+// 1.07 GB in 182 to 186 us (5.8 to 5.9 TB/s): memory.
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __restrict__ x, const TY* __restrict__ dy,
                                                                   const float* __restrict__ w,
@@ -647,7 +648,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_first(const TX* __re
 
 // x and grad_out of different layouts: workgroup (item, chunk of `per`
 // position tiles, channel tile); the channels-last one of the two is turned
-// in LDS.  part as that of x's layout.  268 MB in 57 us (4.7 TB/s) for 32 x 64
+// in LDS.  part as that of x's layout.  268 MB in 57 to 60 us (4.4 to 4.7 TB/s) for 32 x 64
 // x 128 x 128: memory, and the tiles' barriers.
 template <int ACT, bool XLAST, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __restrict__ x, const TY* __restrict__ dy,
@@ -730,7 +731,7 @@ __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_cross(const TX* __re
 
 // Channels last, any width: workgroup (item, chunk of positions, kWideC
 // channels), threads along the channels; part[(b chunks + chunk) C + c].
-// 268 MB in 66 us (4 x 8192 channels x 1024, float32): scalar loads.
+// 268 MB in 65 us (4 x 8192 channels x 1024, float32): scalar loads.
 constexpr int kWideC = 4 * kGnThreads;
 template <int ACT, typename TX, typename TY>
 __global__ __launch_bounds__(kGnThreads) void k_gn_bwd_sums_wide(const TX* __restrict__ x, const TY* __restrict__ dy,

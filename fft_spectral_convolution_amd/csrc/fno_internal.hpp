@@ -319,7 +319,7 @@ void set_exchange_looks(int looks);                     // 0 to kExchangeLooks
 hipError_t launch_group_norm(const GroupNorm& g, const GroupNormArgs& a, bool backward, int kernel, hipStream_t s);
 
 // ---- gradient norm and clipping (fno_gradnorm.hip) ----------------------------
-// Tensors of one launch, passed by value (3.7 KiB of the 4 KiB of kernel
+// Tensors of one launch, passed by value (3.6 KiB of the 4 KiB of kernel
 // arguments).  n counts floats (two a complex value); first is a tensor's
 // first chunk (grad_table_chunks fills it and returns the chunk count).
 constexpr int kGradTable = 128;

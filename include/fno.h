@@ -344,7 +344,8 @@ int fno_linear_conv1d(const float* x, const void* wspec, float* out, int B, int 
  * eps must be positive and finite, C a multiple of groups, 1 <= B,
  * 1 <= C <= 2^24, 1 <= P <= 2^30, B C < 2^31, B C P <= 2^40.  Fields need the alignment of their elements only.  Nothing
  * written may overlap anything else (FNO_ERR_ALIAS).  A NaN or infinity
- * makes its group NaN, no other.
+ * makes its group NaN, no other; squares of deviations whose sum is beyond
+ * float32 count as an infinite deviation (rstd 0), sums beyond it as a NaN.
  *
  * Scratch is the caller's: `workspace`, 256-byte aligned, at least
  * fno_group_norm_workspace_size bytes (backward: 1 for the backward call; enough
