@@ -53,6 +53,9 @@ __all__ = [
     "fno_group_norm_backward",
     "fno_grad_norm",
     "fno_clip_grad_norm",
+    "fno_adamw",
+    "fno_adamw_states",
+    "fno_adamw_moments",
     "fno_workspace_size_2d",
     "fno_workspace_size_1d",
     "fno_forward2d",
@@ -75,6 +78,20 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _S = ctypes.c_size_t
 _F = ctypes.c_float
+
+
+
+class _AdamwTensors(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("params", "out_params", "grads", "exp_avgs", "out_exp_avgs", "exp_avg_sqs",
+                                  "out_exp_avg_sqs", "copies", "numels", "param_types", "grad_types", "state_bits",
+                                  "copy_types")]
+
+
+class _AdamwOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_longlong), ("lr_device", _P), ("step_device", _P), ("norm", _P),
+        ("max_norm", ctypes.c_double), ("seed", ctypes.c_ulonglong)]
+
 
 # name -> (restype, argtypes); mirrors include/fno.h
 _SIGNATURES = {
@@ -115,6 +132,9 @@ _SIGNATURES = {
     "fno_grad_norm_workspace_size": (_S, [_I]),
     "fno_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _S, _P]),
     "fno_clip_grad_norm": (_I, [_P, _P, _P, _P, _I, _F, _P, _P, _P, _S, _P]),
+    "fno_adamw_moment_size": (_S, [ctypes.c_longlong, _I]),
+    "fno_adamw": (_I, [_P, _I, _P, _P]),
+    "fno_adamw_moments": (_I, [_P, _P, _P, _P, _P, _I, _P]),
     "fno_set_timing_events": (_I, [ctypes.POINTER(ctypes.c_void_p), _I]),
     "fno_last_kernel_count": (_I, []),
     "fno_last_kernel_name": (ctypes.c_char_p, [_I]),
@@ -821,6 +841,171 @@ def fno_clip_grad_norm(grads, max_norm: float, norm=None, out=None):
              types.buffer_info()[0], len(grads), max_norm, at if given else 0, 0 if given else at, ws.data_ptr(),
              ws.numel())
     return norm
+
+
+def _same_shapes(tensors, like, name, what):
+    if len(tensors) != len(like) or not all([a.shape == b.shape for a, b in zip(tensors, like)]):
+        raise ValueError(f"{name} must hold a tensor of each {what} shape")
+
+
+def _moment_floats(numels, types):
+    return array.array("q", [2 * n if t == 3 else n for n, t in zip(numels, types)]) if 3 in types else numels
+
+
+def _moment_bytes(n):
+    blocks = -(-n // 128)
+    return -(-129 * blocks // 16) * 16
+
+
+def _moment_table(torch, moments, name, device, floats=None):
+    """Addresses and bits of a list of moments: float32 (or complex64, two values each) or the bytes of 8-bit ones."""
+    moments = list(moments)
+    tensor = torch.Tensor
+    try:
+        devices = set(map(tensor.get_device, moments))
+    except TypeError:
+        raise TypeError(f"{name} must be torch tensors") from None
+    if moments and devices != {device.index}:
+        raise ValueError(f"{name} must be on {device}")
+    wide = {torch.float32: 1, torch.complex64: 2}
+    dtypes = list(map(_dtype_of, moments))
+    if not set(dtypes) <= {torch.uint8, *wide}:
+        raise TypeError(f"{name} must be float32 or the uint8 tensors of fno_adamw_states")
+    if not all(map(tensor.is_contiguous, moments)):
+        raise ValueError(f"{name} must be contiguous")
+    if floats is not None:
+        sizes = list(map(tensor.numel, moments))
+        if len(sizes) != len(floats) or not all([
+                s == _moment_bytes(n) if d not in wide else wide[d] * s == n
+                for s, n, d in zip(sizes, floats, dtypes)]):
+            raise ValueError(f"{name} must hold a moment of each parameter's size")
+    bits = array.array("i", [8 if d not in wide else 32 for d in dtypes])
+    return moments, array.array("Q", map(tensor.data_ptr, moments)), bits
+
+
+def _address(column):
+    return column.buffer_info()[0]
+
+
+def fno_adamw_states(params, bits: int = 32):
+    """Zero moments (exp_avgs, exp_avg_sqs) for fno_adamw: float32 tensors of each parameter's shape (a complex
+    one's with two values at the end) for 32 bits, uint8 tensors of packed codes for 8."""
+    torch = _torch()
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits!r}")
+    params, _, numels, types, device = _tensor_table(torch, params, "params")
+    floats = _moment_floats(numels, types)
+
+    def one(p, n):
+        if bits == 8:
+            return torch.zeros(_moment_bytes(n), dtype=torch.uint8, device=device)
+        return torch.zeros((*p.shape, 2) if p.is_complex() else p.shape, dtype=torch.float32, device=device)
+
+    return [one(p, n) for p, n in zip(params, floats)], [one(p, n) for p, n in zip(params, floats)]
+
+
+def fno_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+              weight_decay: float = 1e-2, norm=None, max_norm=None, copies=None, seed: int = 0, out=None) -> None:
+    """One AdamW step (decoupled weight decay) over lists of tensors, in one kernel for every 48 of them.
+
+    params are float32, bfloat16, float16 or complex64, mixed; grads have their shapes, of any of the
+    real types (complex64 where the parameter is).  exp_avgs, exp_avg_sqs are what fno_adamw_states
+    returned: float32, or uint8 moments of 8 bits, rounded up or down by chance drawn from `seed`, `step`
+    and the value's place; a parameter's two are of the same kind.  step counts from 1; step and lr may be
+    device scalars (int64, float32), so that a captured graph takes another at each replay.  With norm (a
+    device scalar, of fno_grad_norm) and max_norm the gradients are clipped on the way, as
+    fno_clip_grad_norm would.  copies may hold a bfloat16 or float16 tensor beside each parameter (or
+    None) that receives its new values.  In place, or into out = (params, exp_avgs, exp_avg_sqs)."""
+    torch = _torch()
+    params, p_ptrs, numels, types, device = _tensor_table(torch, params, "params")
+    grads, g_ptrs, _, g_types, g_device = _tensor_table(torch, grads, "grads")
+    _same_shapes(grads, params, "grads", "parameter's")
+    if g_device != device:
+        raise ValueError(f"grads must be on {device}")
+    if [t == 3 for t in g_types] != [t == 3 for t in types]:
+        raise TypeError("grads must be complex where the parameters are")
+    floats = _moment_floats(numels, types)
+    exp_avgs, m_ptrs, bits = _moment_table(torch, exp_avgs, "exp_avgs", device, floats)
+    exp_avg_sqs, v_ptrs, v_bits = _moment_table(torch, exp_avg_sqs, "exp_avg_sqs", device, floats)
+    if v_bits != bits:
+        raise TypeError("a parameter's exp_avg and exp_avg_sq must be of the same kind")
+    po, mo, vo = p_ptrs, m_ptrs, v_ptrs
+    if out is not None:
+        out_params, out_avgs, out_sqs = out
+        out_params, po, _, o_types, o_device = _tensor_table(torch, out_params, "out")
+        _same_shapes(out_params, params, "out", "parameter's")
+        if o_types != types or o_device != device:
+            raise TypeError(f"out must have the parameters' types, on {device}")
+        out_avgs, mo, o_bits = _moment_table(torch, out_avgs, "out", device, floats)
+        out_sqs, vo, s_bits = _moment_table(torch, out_sqs, "out", device, floats)
+        if o_bits != bits or s_bits != bits:
+            raise TypeError("out must have the moments' kinds")
+    c_ptrs = c_types = None
+    if copies is not None:
+        copies = list(copies)
+        held = [c for c in copies if c is not None]
+        _, _, _, kinds, c_device = _tensor_table(torch, held, "copies")
+        if len(copies) != len(params) or any([c is not None and c.shape != p.shape for c, p in zip(copies, params)]):
+            raise ValueError("copies must hold None or a tensor of each parameter's shape")
+        if held and c_device != device:
+            raise ValueError(f"copies must be on {device}")
+        if not set(kinds) <= {1, 2}:
+            raise TypeError("copies must be bfloat16 or float16")
+        kinds = iter(kinds)
+        c_types = array.array("i", [0 if c is None else next(kinds) for c in copies])
+        c_ptrs = array.array("Q", [0 if c is None else c.data_ptr() for c in copies])
+        if any([t == 3 and c is not None for t, c in zip(types, copies)]):
+            raise TypeError("a complex parameter has no 16-bit copy")
+    if (norm is None) != (max_norm is None):
+        raise ValueError("give norm and max_norm, or neither")
+    options = _AdamwOptions(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
+                            norm=_f32_ptr(torch, norm, (), device, "norm"),
+                            max_norm=0.0 if max_norm is None else max_norm, seed=seed & 0xffffffffffffffff)
+    if isinstance(lr, torch.Tensor):
+        options.lr_device = _f32_ptr(torch, lr, (), device, "lr")
+    else:
+        options.lr = lr
+    if isinstance(step, torch.Tensor):
+        if step.dtype != torch.int64 or step.shape != () or step.device != device:
+            raise TypeError(f"step must be a number or an int64 scalar on {device}")
+        options.step_device = step.data_ptr()
+    else:
+        step = operator.index(step)
+        if not 1 <= step <= 0x7fffffffffffffff:
+            raise ValueError(f"step counts from 1, got {step}")
+        options.step = step
+    columns = _AdamwTensors(*map(_address, (p_ptrs, po, g_ptrs, m_ptrs, mo, v_ptrs, vo)),
+                            _address(c_ptrs) if c_ptrs else None, *map(_address, (numels, types, g_types, bits)),
+                            _address(c_types) if c_types else None)
+    _enqueue(torch, device, "fno_adamw", ctypes.addressof(columns), len(params), ctypes.addressof(options))
+
+
+def fno_adamw_moments(exp_avgs, exp_avg_sqs, numels=None, out=None):
+    """The float32 values of 8-bit moments: lists (exp_avgs, exp_avg_sqs) of vectors of numels[i] values (two
+    for each complex one of the parameter), or written into the float32 tensors of out = (exp_avgs, exp_avg_sqs)."""
+    torch = _torch()
+    exp_avgs = list(exp_avgs)
+    if not exp_avgs:
+        return ([], []) if out is None else out
+    if not isinstance(exp_avgs[0], torch.Tensor) or not exp_avgs[0].is_cuda:
+        raise ValueError("exp_avgs must be tensors on a GPU device")
+    device = exp_avgs[0].device
+    if (numels is None) == (out is None):
+        raise ValueError("give numels or out")
+    if out is None:
+        numels = list(numels)
+        out = tuple([torch.empty(n, dtype=torch.float32, device=device) for n in numels] for _ in range(2))
+    out_avgs, mo, _, types, o_device = _tensor_table(torch, out[0], "out")
+    out_sqs, vo, floats, s_types, s_device = _tensor_table(torch, out[1], "out")
+    _same_shapes(out_sqs, out_avgs, "out", "first moment's")
+    if set(types) | set(s_types) != {0} or o_device != device or s_device != device:
+        raise TypeError(f"out must be float32 tensors on {device}")
+    exp_avgs, m_ptrs, bits = _moment_table(torch, exp_avgs, "exp_avgs", device, floats)
+    exp_avg_sqs, v_ptrs, v_bits = _moment_table(torch, exp_avg_sqs, "exp_avg_sqs", device, floats)
+    if set(bits) | set(v_bits) != {8}:
+        raise TypeError("moments must be the uint8 tensors of fno_adamw_states")
+    _enqueue(torch, device, "fno_adamw_moments", *map(_address, (m_ptrs, v_ptrs, mo, vo, floats)), len(floats))
+    return out
 
 
 def fno_forward2d(x, mx: int, my: int, xh=None):

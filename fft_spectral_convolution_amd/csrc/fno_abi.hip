@@ -1242,6 +1242,132 @@ int grad_norm_common(const void* const* grads, void* const* outs, const long lon
     return rec_end(hs, run());
 }
 
+// Pieces of memory that a call over many tensors reads or writes, a column (a
+// tensor list) after the other.  Nothing written may overlap anything else:
+// sorted by address, each piece must end before the next that either side
+// writes.  Columns often come sorted (slices of packed buffers), so each is
+// sorted only where it is not, and then they are merged.
+class Pieces {
+public:
+    void add(const void* p, size_t bytes, bool written) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (p && bytes) v_.push_back({a, a + bytes, written});
+    }
+    void end_column() {
+        auto by_address = [](const Piece& a, const Piece& b) { return a.at < b.at; };
+        if (!std::is_sorted(v_.begin() + start_, v_.end(), by_address))
+            std::sort(v_.begin() + start_, v_.end(), by_address);
+        std::inplace_merge(v_.begin(), v_.begin() + start_, v_.end(), by_address);
+        start_ = (long)v_.size();
+    }
+    bool overlap() const {
+        uintptr_t read_end = 0, write_end = 0;   // ends of what lies before, by kind
+        for (const Piece& p : v_) {
+            if (p.at < write_end || (p.written && p.at < read_end)) return true;
+            (p.written ? write_end : read_end) = std::max(p.written ? write_end : read_end, p.end);
+        }
+        return false;
+    }
+
+private:
+    struct Piece {
+        uintptr_t at, end;
+        bool written;
+    };
+    std::vector<Piece> v_;
+    long start_ = 0;
+};
+
+bool finite_from_zero(double v) { return v >= 0.0 && v <= 1.7976931348623157e308; }
+
+// Bytes of a moment of `bits` bits.
+size_t moment_bytes(long long numel, int type, int bits) {
+    const int64_t n = numel * (type == FNO_C64 ? 2 : 1);
+    return (size_t)(bits == 8 ? adam_moment_bytes(n) : 4 * n);
+}
+
+int check_adamw(const fno_adamw_tensors* t, int count, const fno_adamw_options* o) {
+    if (!o || (count && !t)) return FNO_ERR_NULL;
+    if (count < 0) return FNO_ERR_SHAPE;
+    if (!(o->beta1 >= 0.0 && o->beta1 < 1.0 && o->beta2 >= 0.0 && o->beta2 < 1.0)) return FNO_ERR_VALUE;
+    if (!finite_from_zero(o->eps) || !finite_from_zero(o->weight_decay)) return FNO_ERR_VALUE;
+    if (!o->lr_device && !finite_from_zero(o->lr)) return FNO_ERR_VALUE;
+    if (!o->step_device && o->step < 1) return FNO_ERR_VALUE;
+    if (o->norm && !(o->max_norm >= 0.0)) return FNO_ERR_VALUE;
+    if (off_grain(o->lr_device, 4) || off_grain(o->step_device, 8) || off_grain(o->norm, 4)) return FNO_ERR_ALIGN;
+    if (!count) return FNO_OK;
+    if (!t->params || !t->out_params || !t->grads || !t->exp_avgs || !t->out_exp_avgs || !t->exp_avg_sqs ||
+        !t->out_exp_avg_sqs || !t->numels || !t->param_types || !t->grad_types || !t->state_bits ||
+        (t->copies && !t->copy_types))
+        return FNO_ERR_NULL;
+    for (int i = 0; i < count; ++i) {
+        const int pt = t->param_types[i], gt = t->grad_types[i], bits = t->state_bits[i];
+        if (pt < FNO_F32 || pt > FNO_C64 || gt < FNO_F32 || gt > FNO_C64) return FNO_ERR_VALUE;
+        if ((pt == FNO_C64) != (gt == FNO_C64) || (bits != 32 && bits != 8)) return FNO_ERR_VALUE;
+        const long long n = t->numels[i];
+        if (n < 0 || n > (1LL << 35)) return FNO_ERR_SHAPE;           // chunks are counted in 32 bits
+        const void* copy = t->copies ? t->copies[i] : nullptr;
+        if (copy && (pt == FNO_C64 || (t->copy_types[i] != FNO_BF16 && t->copy_types[i] != FNO_F16)))
+            return FNO_ERR_VALUE;
+        if (!n) continue;
+        const size_t pg = pt == FNO_C64 ? 4 : type_bytes(pt), gg = gt == FNO_C64 ? 4 : type_bytes(gt);
+        const size_t mg = bits == 8 ? 16 : 4;
+        const void* must[] = {t->params[i],   t->out_params[i],   t->grads[i],          t->exp_avgs[i],
+                              t->out_exp_avgs[i], t->exp_avg_sqs[i], t->out_exp_avg_sqs[i]};
+        const size_t grain[] = {pg, pg, gg, mg, mg, mg, mg};
+        for (int k = 0; k < 7; ++k) {
+            if (!must[k]) return FNO_ERR_NULL;
+            if (off_grain(must[k], grain[k])) return FNO_ERR_ALIGN;
+        }
+        if (off_grain(copy, 2)) return FNO_ERR_ALIGN;
+    }
+    return FNO_OK;
+}
+
+bool adamw_overlap(const fno_adamw_tensors& t, int count, const fno_adamw_options& o) {
+    Pieces all;
+    auto column = [&](const void* const* in, void* const* out, auto&& bytes) {
+        for (int i = 0; in && i < count; ++i)
+            if (!out || in[i] != out[i]) all.add(in[i], bytes(i), false);
+        all.end_column();
+        for (int i = 0; out && i < count; ++i) all.add(out[i], bytes(i), true);
+        all.end_column();
+    };
+    auto moment = [&](int i) { return moment_bytes(t.numels[i], t.param_types[i], t.state_bits[i]); };
+    column(t.params, t.out_params, [&](int i) { return (size_t)t.numels[i] * type_bytes(t.param_types[i]); });
+    column(t.grads, nullptr, [&](int i) { return (size_t)t.numels[i] * type_bytes(t.grad_types[i]); });
+    column(t.exp_avgs, t.out_exp_avgs, moment);
+    column(t.exp_avg_sqs, t.out_exp_avg_sqs, moment);
+    column(nullptr, t.copies, [&](int i) { return (size_t)t.numels[i] * 2; });
+    all.add(o.norm, 4, false);
+    all.end_column();
+    all.add(o.lr_device, 4, false);
+    all.end_column();
+    all.add(o.step_device, 8, false);
+    all.end_column();
+    return all.overlap();
+}
+
+// Launch a kernel for every kAdamTable tensors; fill(table, k, i) writes entry k for tensor i.
+template <typename Fill, typename Launch>
+int adam_tables(int count, const char* name, hipStream_t hs, Fill&& fill, Launch&& launch) {
+    rec_begin();
+    auto run = [&]() -> int {
+        for (int at = 0; at < count; at += kAdamTable) {
+            AdamTable t{};
+            const int m = std::min(count - at, kAdamTable);
+            for (int k = 0; k < m; ++k) fill(t, k, at + k);
+            const uint32_t chunks = adam_table_chunks(t, m);
+            if (!chunks) continue;
+            rec_kernel(name, hs);
+            const hipError_t e = launch(t, chunks, at);
+            if (e != hipSuccess) return hip_fail(e);
+        }
+        return FNO_OK;
+    };
+    return rec_end(hs, run());
+}
+
 }  // namespace
 
 LaunchEvents take_launch_events() {
@@ -1613,6 +1739,98 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
         return FNO_ERR_NOMEM;
     }
     return grad_norm_common(grads, outs, numels, types, count, max_norm, given_norm, norm, workspace, ws_bytes, stream);
+}
+
+size_t fno_adamw_moment_size(long long numel, int param_type) {
+    if (numel < 0 || numel > (1LL << 35) || param_type < FNO_F32 || param_type > FNO_C64) return 0;
+    return moment_bytes(numel, param_type, 8);
+}
+
+int fno_adamw(const struct fno_adamw_tensors* tensors, int count, const struct fno_adamw_options* options,
+              void* stream) {
+    const int rc = check_adamw(tensors, count, options);
+    if (rc) return rc;
+    const fno_adamw_options& o = *options;
+    try {
+        if (count && adamw_overlap(*tensors, count, o)) return FNO_ERR_ALIAS;
+    } catch (const std::bad_alloc&) {
+        return FNO_ERR_NOMEM;
+    }
+    AdamOptions a{};
+    a.lr = o.lr;
+    a.weight_decay = o.weight_decay;
+    a.b1 = o.beta1;
+    a.b2 = o.beta2;
+    a.log_b1 = std::log(o.beta1);
+    a.log_b2 = std::log(o.beta2);
+    a.c1 = -std::expm1((double)o.step * a.log_b1);
+    a.c2 = -std::expm1((double)o.step * a.log_b2);
+    a.eps = o.eps;
+    a.lr_dev = o.lr_device;
+    a.step_dev = o.step_device;
+    a.norm = o.norm;
+    a.max_norm = (float)o.max_norm;
+    a.seed = o.seed;
+    a.step = o.step;
+    const fno_adamw_tensors& t = tensors ? *tensors : fno_adamw_tensors{};
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    auto fill = [&](AdamTable& q, int k, int i) {
+        q.p[k] = t.params[i];
+        q.po[k] = t.out_params[i];
+        q.g[k] = t.grads[i];
+        q.m[k] = t.exp_avgs[i];
+        q.mo[k] = t.out_exp_avgs[i];
+        q.v[k] = t.exp_avg_sqs[i];
+        q.vo[k] = t.out_exp_avg_sqs[i];
+        q.copy[k] = t.copies ? t.copies[i] : nullptr;
+        q.n[k] = t.numels[i] * (t.param_types[i] == FNO_C64 ? 2 : 1);
+        q.ptype[k] = (uint8_t)t.param_types[i];
+        q.gtype[k] = (uint8_t)t.grad_types[i];
+        q.bits[k] = (uint8_t)t.state_bits[i];
+        q.ctype[k] = q.copy[k] ? (uint8_t)t.copy_types[i] : 0;
+    };
+    return adam_tables(count, "adamw", hs, fill, [&](const AdamTable& q, uint32_t chunks, int at) {
+        a.number = at;
+        return launch_adamw(q, chunks, a, hs);
+    });
+}
+
+int fno_adamw_moments(const void* const* exp_avgs, const void* const* exp_avg_sqs, float* const* out_exp_avgs,
+                      float* const* out_exp_avg_sqs, const long long* numels, int count, void* stream) {
+    if (count < 0) return FNO_ERR_SHAPE;
+    if (count && (!exp_avgs || !exp_avg_sqs || !out_exp_avgs || !out_exp_avg_sqs || !numels)) return FNO_ERR_NULL;
+    for (int i = 0; i < count; ++i) {
+        if (numels[i] < 0 || numels[i] > (1LL << 36)) return FNO_ERR_SHAPE;
+        if (!numels[i]) continue;
+        if (!exp_avgs[i] || !exp_avg_sqs[i] || !out_exp_avgs[i] || !out_exp_avg_sqs[i]) return FNO_ERR_NULL;
+        if (off_grain(exp_avgs[i], 16) || off_grain(exp_avg_sqs[i], 16) || off_grain(out_exp_avgs[i], 4) ||
+            off_grain(out_exp_avg_sqs[i], 4))
+            return FNO_ERR_ALIGN;
+    }
+    try {
+        Pieces all;
+        for (const void* const* in : {exp_avgs, exp_avg_sqs}) {
+            for (int i = 0; i < count; ++i) all.add(in[i], moment_bytes(numels[i], FNO_F32, 8), false);
+            all.end_column();
+        }
+        for (float* const* out : {out_exp_avgs, out_exp_avg_sqs}) {
+            for (int i = 0; i < count; ++i) all.add(out[i], (size_t)numels[i] * 4, true);
+            all.end_column();
+        }
+        if (all.overlap()) return FNO_ERR_ALIAS;
+    } catch (const std::bad_alloc&) {
+        return FNO_ERR_NOMEM;
+    }
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    auto fill = [&](AdamTable& q, int k, int i) {
+        q.m[k] = exp_avgs[i];
+        q.v[k] = exp_avg_sqs[i];
+        q.mo[k] = out_exp_avgs[i];
+        q.vo[k] = out_exp_avg_sqs[i];
+        q.n[k] = numels[i];
+    };
+    return adam_tables(count, "adamw_moments", hs, fill,
+                       [&](const AdamTable& q, uint32_t chunks, int) { return launch_adamw_moments(q, chunks, hs); });
 }
 
 }  // extern "C"

@@ -343,4 +343,32 @@ hipError_t launch_grad_finish(const double* part, int nparts, const float* given
                               float* coef, hipStream_t s);
 hipError_t launch_grad_scale(const GradTable& t, uint32_t nchunks, const float* coef, hipStream_t s);
 
+// ---- AdamW (fno_adamw.hip) ------------------------------------------------------
+// Tensors of one launch, passed by value.  n counts floats (two a complex
+// value); bits is 32 or 8; first is a tensor's first chunk
+// (adam_table_chunks fills it and returns the chunk count).
+constexpr int kAdamTable = 48;
+struct AdamTable {
+    const void *p[kAdamTable], *g[kAdamTable], *m[kAdamTable], *v[kAdamTable];
+    void *po[kAdamTable], *mo[kAdamTable], *vo[kAdamTable], *copy[kAdamTable];
+    int64_t n[kAdamTable];
+    uint32_t first[kAdamTable];
+    uint8_t ptype[kAdamTable], gtype[kAdamTable], bits[kAdamTable], ctype[kAdamTable];
+};
+struct AdamOptions {
+    double lr, weight_decay, b1, b2, c1, c2, log_b1, log_b2, eps;   // c = 1 - b^t
+    const float* lr_dev;            // stand for lr and the step where not null
+    const long long* step_dev;
+    const float* norm;              // null: no clipping
+    float max_norm;
+    int number;                     // of the table's first tensor
+    uint64_t seed;
+    int64_t step;
+};
+static_assert(sizeof(AdamTable) + sizeof(AdamOptions) + 8 <= 4096, "kernel arguments");
+int64_t adam_moment_bytes(int64_t n);                    // of an 8-bit moment of n floats
+uint32_t adam_table_chunks(AdamTable& t, int count);
+hipError_t launch_adamw(const AdamTable& t, uint32_t nchunks, const AdamOptions& o, hipStream_t s);
+hipError_t launch_adamw_moments(const AdamTable& t, uint32_t nchunks, hipStream_t s);
+
 }  // namespace fno

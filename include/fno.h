@@ -419,6 +419,86 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
                        float* norm, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * One AdamW step over `count` tensors at once: the optimizer behind
+ * fno_grad_norm.  For every value (two a complex one),
+ *
+ *   g' = g min(1, max_norm / (norm + 1e-6))          (norm NULL: g' = g)
+ *   m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2
+ *   p' = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) m' / (sqrt(v' / (1 - beta2^step)) + eps)
+ *
+ * params are float32, bfloat16, float16 or complex64; grads any of the first
+ * three types (complex64 where the parameter is).  out_* may be the tensors
+ * themselves (in place) or others; nothing written may overlap anything else,
+ * the same tensor given twice included (FNO_ERR_ALIAS).  Arithmetic is float32
+ * (8-bit moments: float64 up to the code); a 16-bit parameter is rounded once.
+ * copies (NULL for none; entries may be NULL) receive p' rounded to bfloat16
+ * or float16, the weights that fno_channel_linear reads beside float32
+ * parameters; complex parameters have none.
+ *
+ * Moments (exp_avgs, exp_avg_sqs) of state_bits 32 are float32, of the
+ * parameter's layout.  Those of 8 are fno_adamw_moment_size(numel, type)
+ * bytes, 16-byte aligned: the codes, one a value in whole blocks of 128, then a
+ * byte for each block.  With E the block's byte less 127, a code c of 0 is 0,
+ * else, with u = c & 127 for exp_avgs (bit 7 is the sign; u = 127 a NaN) and
+ * u = c for exp_avg_sqs (255 a NaN),
+ *
+ *   (1 + (u & 7) / 8) 2^((u >> 3) - T + E),   T = 14 for exp_avgs, 30 for exp_avg_sqs
+ *
+ * Zero bytes are zero moments.  2^E is the largest finite value's power of two
+ * (E at least -126, for exp_avg_sqs -96).  With f the 20 leading fraction bits of
+ * the new moment, the 17 lower of them are dropped and the code is one higher
+ * where they and 2 r + 1 reach 2^17; r is the lower half (exp_avg_sqs: upper)
+ * of 32 bits h(i ^ h(k + floor(i / 2^32))), i the value's number in its tensor,
+ * k = h(h(h(h(seed) + floor(seed / 2^32)) + step) + tensor), tensor its place in the list,
+ * all modulo 2^32, and
+ * h(x): x = (x ^ x >> 16) 0x6A09E667; x = (x ^ x >> 15) 0xBB67AE85; x ^ x >> 16.
+ * Codes below the range are 0, for exp_avg_sqs 1 (0 only for 0); values that
+ * would pass float32 take its highest code.
+ *
+ * lr_device and step_device (device memory, NULL for none) stand for lr and
+ * step, so that a captured graph can take another at each replay; step >= 1,
+ * the first step's number, also in memory.  0 <= lr, eps, weight_decay, all
+ * finite, 0 <= beta < 1, max_norm >= 0 (FNO_ERR_VALUE).  No workspace.  The
+ * arrays are read before the call returns.
+ */
+struct fno_adamw_tensors {
+    const void* const* params;
+    void* const* out_params;
+    const void* const* grads;
+    const void* const* exp_avgs;
+    void* const* out_exp_avgs;
+    const void* const* exp_avg_sqs;
+    void* const* out_exp_avg_sqs;
+    void* const* copies;
+    const long long* numels;      /* elements, 0 to 2^35 */
+    const int* param_types;       /* enum fno_type */
+    const int* grad_types;
+    const int* state_bits;        /* 32 or 8 */
+    const int* copy_types;        /* FNO_BF16 or FNO_F16, read where copies are */
+};
+struct fno_adamw_options {
+    double lr, beta1, beta2, eps, weight_decay;
+    long long step;
+    const float* lr_device;
+    const long long* step_device;
+    const float* norm;            /* device, float32 */
+    double max_norm;
+    unsigned long long seed;
+};
+size_t fno_adamw_moment_size(long long numel, int param_type);
+int fno_adamw(const struct fno_adamw_tensors* tensors, int count,
+              const struct fno_adamw_options* options, void* stream);
+
+/*
+ * The float32 values that 8-bit moments stand for, numels[i] floats each (two
+ * a complex value of the parameter).
+ */
+int fno_adamw_moments(const void* const* exp_avgs, const void* const* exp_avg_sqs,
+                      float* const* out_exp_avgs, float* const* out_exp_avg_sqs,
+                      const long long* numels, int count, void* stream);
+
+/*
  * Per-kernel timing for benchmarks and profilers.  While `events` is non-NULL,
  * every convolution or stage call made on the calling thread launches its
  * k-th kernel with events[2k] and events[2k+1] (hipEvent_t, created by the
