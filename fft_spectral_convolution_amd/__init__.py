@@ -53,6 +53,8 @@ __all__ = [
     "fno_group_norm_backward",
     "fno_grad_norm",
     "fno_clip_grad_norm",
+    "fno_channel_linear",
+    "fno_channel_linear_backward",
     "fno_adamw",
     "fno_adamw_states",
     "fno_adamw_moments",
@@ -132,6 +134,9 @@ _SIGNATURES = {
     "fno_grad_norm_workspace_size": (_S, [_I]),
     "fno_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _S, _P]),
     "fno_clip_grad_norm": (_I, [_P, _P, _P, _P, _I, _F, _P, _P, _P, _S, _P]),
+    "fno_channel_linear": (_I, [_P] * 5 + [_I] * 10 + [_P]),
+    "fno_channel_linear_workspace_size": (_S, [_I] * 9),
+    "fno_channel_linear_backward": (_I, [_P] * 9 + [_I] * 10 + [_P, _S, _P]),
     "fno_adamw_moment_size": (_S, [ctypes.c_longlong, _I]),
     "fno_adamw": (_I, [_P, _I, _P, _P]),
     "fno_adamw_moments": (_I, [_P, _P, _P, _P, _P, _I, _P]),
@@ -841,6 +846,126 @@ def fno_clip_grad_norm(grads, max_norm: float, norm=None, out=None):
              types.buffer_info()[0], len(grads), max_norm, at if given else 0, 0 if given else at, ws.data_ptr(),
              ws.numel())
     return norm
+
+
+def _channel_args(torch, x, weight, bias, branch, branch_after, act, channels_last, out_channels_last):
+    """Checked arguments of both directions: (weight, bias, branch) addresses, (B, Cin, Cout, P), (act, branch_after,
+    x_last, out_last, x_type), out's shape."""
+    x_type = _field_type(torch, x, "x")
+    shape, device = x.shape, x.device
+    if len(shape) < 2:
+        raise ValueError(f"x must have a batch and a channel axis, got shape {tuple(shape)}")
+    code = _ACTIVATIONS.get(act, -1)
+    if code < 0:
+        raise ValueError(f"act must be one of {', '.join(_ACTIVATIONS)}, got {act!r}")
+    if out_channels_last is None:
+        out_channels_last = channels_last
+    b = shape[0]
+    if channels_last:
+        c, grid = shape[-1], shape[1:-1]
+    else:
+        c, grid = shape[1], shape[2:]
+    p = math.prod(grid)
+    if _field_type(torch, weight, "weight", device) != x_type:
+        raise TypeError(f"weight must be {x.dtype} as x, got {weight.dtype}")
+    if len(weight.shape) != 2 or weight.shape[1] != c:
+        raise ValueError(f"weight must have shape (Cout, {c}), got {tuple(weight.shape)}")
+    cout = weight.shape[0]
+    if b > 0x7fffffff or c > 0x7fffffff or p > 0x7fffffff or cout > 0x7fffffff:
+        raise ValueError(f"x is too large: shape {tuple(shape)}")
+    out_shape = (b, *grid, cout) if out_channels_last else (b, cout, *grid)
+    branch_ptr = 0
+    if branch is not None:
+        _field_type(torch, branch, "branch", device)
+        if branch.shape != out_shape:
+            raise ValueError(f"branch has shape {tuple(branch.shape)}, expected {out_shape}")
+        branch_ptr = branch.data_ptr()
+    return ((weight.data_ptr(), _f32_ptr(torch, bias, (cout,), device, "bias"), branch_ptr), (b, c, cout, p),
+            (code, 1 if branch_after else 0, 1 if channels_last else 0, 1 if out_channels_last else 0, x_type), out_shape)
+
+
+def fno_channel_linear(x, weight, bias=None, branch=None, branch_after: bool = False, act: str = "none",
+                       channels_last: bool = False, out_channels_last=None, out_dtype=None, out=None):
+    """act(W x + bias + branch) at every position of a field, or act(W x + bias) + branch with branch_after.
+
+    x is [B, Cin, *grid], or [B, *grid, Cin] with channels_last, of float32, bfloat16 or float16;
+    weight [Cout, Cin] has x's type, bias [Cout] is float32.  out has x's layout unless out_channels_last
+    says otherwise, and x's type or float32 (out_dtype, or that of `out`); branch has out's shape and
+    type.  act is "none", "gelu" (the exact erf form) or "silu"."""
+    torch = _torch()
+    ptrs, sizes, options, out_shape = _channel_args(torch, x, weight, bias, branch, branch_after, act, channels_last,
+                                                    out_channels_last)
+    if out is None:
+        out = x.new_empty(out_shape, dtype=out_dtype)
+        out_type = options[4] if out_dtype is None else _field_type(torch, out, "out")
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        out_type = _field_type(torch, out, "out", x.device)
+        if out.shape != out_shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {out_shape}")
+    if branch is not None and branch.dtype != out.dtype:
+        raise TypeError(f"branch must be {out.dtype} as out, got {branch.dtype}")
+    _enqueue(torch, x.device, "fno_channel_linear", x.data_ptr(), *ptrs, out.data_ptr(), *sizes, *options, out_type)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _channel_workspace_size(*key):
+    return int(lib().fno_channel_linear_workspace_size(*key))
+
+
+def fno_channel_linear_backward(x, weight, grad_out, bias=None, branch=None, branch_after: bool = False,
+                                act: str = "none", channels_last: bool = False, out_channels_last=None,
+                                need_x: bool = True, need_w: bool = True, need_branch: bool = True, grad_x=None,
+                                grad_weight=None, grad_bias=None, grad_branch=None):
+    """Gradients (grad_x, grad_weight, grad_bias, grad_branch) through fno_channel_linear, given its x, weight, bias,
+    branch and options, and grad_out of its output's layout and type.  Those of weight and bias are float32 whatever
+    x's type.  need_x, need_w (weight and bias) and need_branch choose; what is not asked for, or belongs to
+    an argument that is None, is returned as None.  The gradient of a branch behind the activation, or without
+    one, is grad_out itself."""
+    torch = _torch()
+    ptrs, sizes, options, out_shape = _channel_args(torch, x, weight, bias, branch, branch_after, act, channels_last,
+                                                    out_channels_last)
+    device = x.device
+    out_type = _field_type(torch, grad_out, "grad_out", device)
+    if grad_out.shape != out_shape:
+        raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, expected {out_shape}")
+    if branch is not None and branch.dtype != grad_out.dtype:
+        raise TypeError(f"branch must be {grad_out.dtype} as grad_out, got {branch.dtype}")
+    gx = gw = gb = gr = None
+    gx_ptr = gr_ptr = 0
+    if need_x:
+        gx = torch.empty_like(x) if grad_x is None else grad_x
+        if grad_x is not None and (_field_type(torch, gx, "grad_x", device) != options[4] or gx.shape != x.shape):
+            raise ValueError(f"grad_x must match {tuple(x.shape)} {x.dtype}")
+        gx_ptr = gx.data_ptr()
+    if need_w:
+        gw = x.new_empty(weight.shape, dtype=torch.float32) if grad_weight is None else grad_weight
+        if bias is not None:
+            gb = torch.empty_like(bias) if grad_bias is None else grad_bias
+    if need_branch and branch is not None:
+        if branch_after or act == "none":
+            if grad_branch is not None:
+                raise ValueError("the gradient of this branch is grad_out itself")
+            gr = grad_out
+        else:
+            gr = torch.empty_like(grad_out) if grad_branch is None else grad_branch
+            if grad_branch is not None and (_field_type(torch, gr, "grad_branch", device) != out_type
+                                            or gr.shape != out_shape):
+                raise ValueError(f"grad_branch must match {out_shape} {grad_out.dtype}")
+            gr_ptr = gr.data_ptr()
+    if not (gx_ptr or need_w or gr_ptr):
+        if gr is None:
+            raise ValueError("ask for at least one gradient")
+        return None, None, None, gr
+    gw_ptr = _f32_ptr(torch, gw, weight.shape, device, "grad_weight")
+    gb_ptr = _f32_ptr(torch, gb, (weight.shape[0],), device, "grad_bias")
+    size = _channel_workspace_size(*sizes, options[0], *options[2:], out_type)
+    ws = x.new_empty(size, dtype=torch.uint8)
+    _enqueue(torch, device, "fno_channel_linear_backward", x.data_ptr(), *ptrs, grad_out.data_ptr(), gx_ptr, gw_ptr,
+             gb_ptr, gr_ptr, *sizes, *options, out_type, ws.data_ptr(), size)
+    return gx, gw, gb, gr
 
 
 def _same_shapes(tensors, like, name, what):

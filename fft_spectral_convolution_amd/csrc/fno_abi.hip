@@ -1242,6 +1242,60 @@ int grad_norm_common(const void* const* grads, void* const* outs, const long lon
     return rec_end(hs, run());
 }
 
+int check_channels(const ChannelProduct& c) {
+    if (c.B < 1 || c.P < 1 || c.Cin < 1 || c.Cout < 1 || c.Cin > 1 << 16 || c.Cout > 1 << 16) return FNO_ERR_SHAPE;
+    // rows of 32 channels are indexed in 31 bits of bytes
+    if (c.P > (c.x_last && c.out_last ? 1 << 30 : 1 << 24)) return FNO_ERR_SHAPE;
+    if (c.B * c.P > (INT64_C(1) << 40) / std::max(c.Cin, c.Cout)) return FNO_ERR_SHAPE;
+    if (c.act < FNO_ACT_NONE || c.act > FNO_ACT_SILU) return FNO_ERR_VALUE;
+    if (c.x_type < FNO_F32 || c.x_type > FNO_F16) return FNO_ERR_VALUE;
+    if (c.out_type != c.x_type && c.out_type != FNO_F32) return FNO_ERR_VALUE;
+    return FNO_OK;
+}
+
+// The product of a call's arguments; an error where an option is none.
+int channel_product(ChannelProduct& c, int B, int Cin, int Cout, int P, int act, int branch_after, int x_last,
+                    int out_last, int x_type, int out_type) {
+    for (int flag : {branch_after, x_last, out_last})
+        if (flag != 0 && flag != 1) return FNO_ERR_VALUE;
+    c = ChannelProduct{B, P, Cin, Cout, act, branch_after != 0, x_last != 0, out_last != 0, x_type, out_type};
+    return check_channels(c);
+}
+
+int channels_common(const ChannelProduct& c, const ChannelArgs& a, bool backward, size_t ws_bytes, void* stream) {
+    const size_t xg = type_bytes(c.x_type), og = type_bytes(c.out_type);
+    const size_t xb = (size_t)(c.B * c.P) * c.Cin * xg, ob = (size_t)(c.B * c.P) * c.Cout * og;
+    const size_t wn = (size_t)c.Cin * c.Cout, bb = (size_t)c.Cout * 4;
+    if (!a.x || !a.w || !a.out) return FNO_ERR_NULL;
+    if (backward && !a.grad_x && !a.grad_w && !a.grad_b && !a.grad_branch) return FNO_ERR_NULL;
+    if (a.grad_branch && (c.branch_after || c.act == FNO_ACT_NONE)) return FNO_ERR_VALUE;
+    if (off_grain(a.x, xg) || off_grain(a.w, xg) || off_grain(a.bias, 4) || off_grain(a.branch, og) ||
+        off_grain(a.out, og) || off_grain(a.grad_x, xg) || off_grain(a.grad_w, 4) || off_grain(a.grad_b, 4) ||
+        off_grain(a.grad_branch, og))
+        return FNO_ERR_ALIGN;
+    const Span x{a.x, xb}, w{a.w, wn * xg}, b{a.bias, bb}, r{a.branch, ob}, o{a.out, ob}, ws{a.ws, ws_bytes};
+    if (backward ? any_overlap({{a.grad_x, xb}, {a.grad_w, wn * 4}, {a.grad_b, bb}, {a.grad_branch, ob}, ws},
+                               {x, w, b, r, o})
+                 : any_overlap({o}, {x, w, b, r}))
+        return FNO_ERR_ALIAS;
+    const size_t need = channel_workspace(c, backward);
+    if (need && (!a.ws || ws_bytes < need)) return FNO_ERR_WORKSPACE;
+    if (off_grain(a.ws, 256)) return FNO_ERR_ALIGN;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    auto run = [&]() -> int {
+        const char* names[4] = {};
+        const int count = channel_kernels(c, a, backward, names);
+        for (int k = 0; k < count; ++k) {
+            rec_kernel(names[k], hs);
+            const hipError_t e = launch_channels(c, a, backward, k, hs);
+            if (e != hipSuccess) return hip_fail(e);
+        }
+        return FNO_OK;
+    };
+    rec_begin();
+    return rec_end(hs, run());
+}
+
 // Pieces of memory that a call over many tensors reads or writes, a column (a
 // tensor list) after the other.  Nothing written may overlap anything else:
 // sorted by address, each piece must end before the next that either side
@@ -1739,6 +1793,36 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
         return FNO_ERR_NOMEM;
     }
     return grad_norm_common(grads, outs, numels, types, count, max_norm, given_norm, norm, workspace, ws_bytes, stream);
+}
+
+int fno_channel_linear(const void* x, const void* weight, const float* bias, const void* branch, void* out, int B,
+                       int Cin, int Cout, int P, int act, int branch_after, int x_last, int out_last, int x_type,
+                       int out_type, void* stream) {
+    ChannelProduct c;
+    const int rc = channel_product(c, B, Cin, Cout, P, act, branch_after, x_last, out_last, x_type, out_type);
+    if (rc) return rc;
+    const ChannelArgs a{x, weight, bias, branch, out, nullptr, nullptr, nullptr, nullptr, nullptr};
+    return channels_common(c, a, false, 0, stream);
+}
+
+size_t fno_channel_linear_workspace_size(int B, int Cin, int Cout, int P, int act, int x_last, int out_last, int x_type,
+                                         int out_type) {
+    ChannelProduct c;
+    if (channel_product(c, B, Cin, Cout, P, act, 0, x_last, out_last, x_type, out_type) != FNO_OK) return 0;
+    return channel_workspace(c, true);
+}
+
+int fno_channel_linear_backward(const void* x, const void* weight, const float* bias, const void* branch,
+                                const void* grad_out, void* grad_x, float* grad_weight, float* grad_bias,
+                                void* grad_branch, int B, int Cin, int Cout, int P, int act, int branch_after,
+                                int x_last, int out_last, int x_type, int out_type, void* workspace, size_t ws_bytes,
+                                void* stream) {
+    ChannelProduct c;
+    const int rc = channel_product(c, B, Cin, Cout, P, act, branch_after, x_last, out_last, x_type, out_type);
+    if (rc) return rc;
+    const ChannelArgs a{x,      weight,      bias,        branch,    const_cast<void*>(grad_out),
+                        grad_x, grad_branch, grad_weight, grad_bias, workspace};
+    return channels_common(c, a, true, ws_bytes, stream);
 }
 
 size_t fno_adamw_moment_size(long long numel, int param_type) {

@@ -1,0 +1,350 @@
+// Device-side pieces of the channel products (fno_channels.hip,
+// fno_channels_bwd.hip): operands of the matrix instructions, the splitting of
+// float32 into them, and the tiles of fields they are loaded from.
+//
+// All products run on v_mfma_f32_32x32x16_{bf16,f16}.  A lane l holds, of
+// either operand, row (column) l % 32 and 8 neighbouring k from 8 (l / 32) on;
+// of the result, column l % 32 and the rows 8 (r / 4) + 4 (l / 32) + r % 4 for
+// r < 16.  The order of k and of rows is ours to choose as long as both
+// operands agree: channels are dealt to the result's rows such that a lane's 16
+// values are 16 neighbouring channels (row_channel), so that fields of either
+// layout are read and written from registers as they lie.
+//
+// float32 values take three bfloat16 parts, each the rounding of what the ones
+// before it leave: 8 bits of fraction each, 24 together.  Of the nine products
+// of parts the six largest are formed; what the other three would add is below
+// 2^-26 of the product.  The 16-bit instructions do 16 times the float32 one's
+// work in the same time, so six of them still take 3/8 of it.  A part of an
+// infinity, or of a value above bfloat16's largest (3.39e38), is an infinity and
+// the rest then a NaN: such inputs give a NaN where float32 sums might give an infinity.
+#pragma once
+
+#include "fno_fields.hpp"
+
+namespace fno {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// Channel of a 32-channel tile that row m of the result stands for.
+__host__ __device__ __forceinline__ constexpr int row_channel(int m) { return 16 * ((m >> 2) & 1) + 4 * (m >> 3) + (m & 3); }
+
+// An operand of type T: parts of type E.
+template <typename T>
+struct Operand;
+template <>
+struct Operand<float> {
+    typedef __bf16 E;
+    typedef bf16x8 V;
+    static constexpr int parts = 3;
+};
+template <>
+struct Operand<bf16> {
+    typedef __bf16 E;
+    typedef bf16x8 V;
+    static constexpr int parts = 1;
+};
+template <>
+struct Operand<f16> {
+    typedef _Float16 E;
+    typedef f16x8 V;
+    static constexpr int parts = 1;
+};
+
+template <typename V, int N>
+struct Frag {
+    V part[N];
+};
+
+// Parts of eight values.
+template <typename V, int N>
+__device__ __forceinline__ Frag<V, N> split(const float (&v)[8]) {
+    Frag<V, N> f;
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            f.part[k][i] = r[i];
+            if (k + 1 < N) r[i] -= (float)f.part[k][i];
+        }
+    }
+    return f;
+}
+
+// c += a b over the products of parts that matter, the smallest first.
+template <typename V, int NA, int NB>
+__device__ __forceinline__ f32x16 mfma_parts(const Frag<V, NA>& a, const Frag<V, NB>& b, f32x16 c) {
+    constexpr int most = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int s = most; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) c = mfma(a.part[i], b.part[s - i], c);
+    return c;
+}
+
+// A run of positions of one item that a wave works on: 32 NT of them, of
+// which lane n % 32's j-th is p0 + pn n + pj j.
+struct Tile {
+    int64_t item;        // of which item (0 where all positions are one run)
+    int64_t p0;
+    int pn, pj;
+    bool full;           // no position is behind the item's end
+};
+
+template <typename F>
+__device__ __forceinline__ void with_field_type(int type, F&& f) {
+    if (type == kTypeBf16) {
+        f(bf16{});
+    } else if (type == kTypeF16) {
+        f(f16{});
+    } else {
+        f(0.0f);
+    }
+}
+
+// Addresses are a base that all lanes share and 32-bit byte offsets.  Where
+// something lies outside the field (a ragged tile), values are moved one by one
+// through a buffer resource that ends with the field, places outside it at
+// offset kOutside: such loads return zero and such stores are dropped, without a branch.
+constexpr uint32_t kOutside = 0x80000000u;
+
+template <typename T>
+__device__ __forceinline__ T buffer_load(__amdgpu_buffer_rsrc_t rs, uint32_t at) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)at, 0, 0));
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(rs, (int)at, 0, 0));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t rs, uint32_t at, T v) {
+    if constexpr (sizeof(T) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rs, (int)at, 0, 0);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rs, (int)at, 0, 0);
+    }
+}
+template <typename T>
+__device__ __forceinline__ T* from(T* base, uint32_t bytes) {
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(base) + bytes);
+}
+template <typename T>
+__device__ __forceinline__ const T* from(const T* base, uint32_t bytes) {
+    return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
+}
+
+// The places of half of a 32-channel part of a result tile in a field (halves keep few
+// registers busy at a time): z[j][r], r < 8, is channel c0 + 16 (lane / 32) + 8 half + r at
+// the lane's position j.
+template <typename T, bool LAST, int NT>
+struct Places {
+    int64_t start;           // elements from the field's start to the part's, the same in all lanes
+    uint32_t left;           // bytes from there to the field's (channels first: the item's) end, or enough; 0 behind it
+    uint32_t at, step;       // of r = 0 and position 0; between positions (LAST) or channels; bytes
+    int channels;            // of this half of the part that exist
+    int positions;           // of the tile that exist
+    int first, pj;           // the lane's first position in the tile, and from one to the next
+    bool whole;              // nothing is outside
+
+    __device__ __forceinline__ Places(const Tile& t, int C, int64_t P, int c0, int half) {
+        const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+        start = t.item * P * C + (LAST ? t.p0 * C + c0 : c0 * P + t.p0);
+        const int64_t more = ((LAST ? (P - t.p0) * C - c0 : (C - c0) * P - t.p0)) * (int64_t)sizeof(T);
+        left = (uint32_t)max((int64_t)0, min(more, (int64_t)kOutside));
+        first = n * t.pn;
+        pj = t.pj;
+        at = (LAST ? (uint32_t)(first * C + 16 * h + 8 * half) : (uint32_t)((16 * h + 8 * half) * P + first)) * (uint32_t)sizeof(T);
+        step = (uint32_t)(LAST ? pj * C : P) * (uint32_t)sizeof(T);
+        channels = C - c0 - 16 * h - 8 * half;
+        positions = (int)min(P - t.p0, (int64_t)32 * NT);
+        whole = t.full && c0 + 32 <= C;
+    }
+    __device__ __forceinline__ uint32_t place(int j, int r) const {
+        const bool in = LAST ? r < channels : first + j * pj < positions;
+        const uint32_t o = at + (LAST ? j * step + r * (uint32_t)sizeof(T) : r * step + j * (uint32_t)sizeof(T));
+        return in ? o : kOutside;
+    }
+
+    __device__ __forceinline__ void load(const void* field, float (&z)[NT][8]) const {
+        const T* f = static_cast<const T*>(field) + start;
+        if (whole) {
+            if constexpr (LAST) {
+                constexpr int V = 16 / sizeof(T);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int k = 0; k < 8; k += V) {
+                        float v[V];
+                        load_vec<V>(from(f, at + j * step) + k, v);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) z[j][k + i] = v[i];
+                    }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    float v[NT];
+                    load_vec<NT>(from(f, at + r * step), v);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) z[j][r] = v[j];
+                }
+            }
+        } else {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) z[j][r] = (float)buffer_load<T>(rs, place(j, r));
+        }
+    }
+    __device__ __forceinline__ void store(void* field, const float (&z)[NT][8]) const {
+        T* f = static_cast<T*>(field) + start;
+        if (whole) {
+            if constexpr (LAST) {
+                constexpr int V = 16 / sizeof(T);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int k = 0; k < 8; k += V) {
+                        float v[V];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[i] = z[j][k + i];
+                        store_vec<V>(from(f, at + j * step) + k, v);
+                    }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    float v[NT];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) v[j] = z[j][r];
+                    store_vec<NT>(from(f, at + r * step), v);
+                }
+            }
+        } else {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) buffer_store<T>(rs, place(j, r), (T)z[j][r]);
+        }
+    }
+};
+
+// ---- input tiles ------------------------------------------------------------------
+// 16 channels from k0 on of a tile's positions, as they are loaded: channels
+// first, NT positions of each of the lane's 8 channels; channels last, 8
+// channels of each of its NT positions.  Places outside the field are zero.
+template <typename T, bool LAST, int NT>
+struct Raw {
+    T v[LAST ? NT : 8][LAST ? 8 : NT] __attribute__((aligned(16)));
+};
+
+template <typename T, bool LAST, int NT>
+__device__ __forceinline__ void load_raw(Raw<T, LAST, NT>& raw, const void* field, const Tile& t, int C, int64_t P,
+                                         int64_t items, int k0) {
+    const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+    const T* x = static_cast<const T*>(field) + (t.item * P * C + (LAST ? t.p0 * C + k0 : k0 * P + t.p0));
+    const int more = C - k0 - 8 * h;          // channels that exist from the lane's first on
+    constexpr uint32_t S = sizeof(T);
+    if constexpr (LAST) {
+        typedef typename VecOf<T, 8>::type V8;
+        const uint32_t at = (uint32_t)(n * t.pn * C + 8 * h) * S, step = (uint32_t)(t.pj * C) * S;
+        // a row's tail may be read into the next rows, but not behind the field
+        if (t.full && (k0 + 16 <= C || t.item + 1 < items || t.p0 + 32 * NT + 16 <= P)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                *reinterpret_cast<V8*>(raw.v[j]) = *reinterpret_cast<const V8*>(from(x, at + j * step));
+            if (k0 + 16 > C) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) raw.v[j][i] = i < more ? raw.v[j][i] : (T)0.0f;
+            }
+        } else {
+            const int64_t bytes = ((P - t.p0) * C - k0) * (int64_t)S;
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(x, (uint32_t)min(bytes, (int64_t)kOutside));
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    raw.v[j][i] = buffer_load<T>(rs, i < more ? at + j * step + i * S : kOutside);
+        }
+    } else {
+        typedef typename VecOf<T, NT>::type VN;
+        const uint32_t step = (uint32_t)P * S, at = 8 * h * step + (uint32_t)(n * t.pn) * S;
+        if (t.full && k0 + 16 <= C) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<VN*>(raw.v[i]) = *reinterpret_cast<const VN*>(from(x, at + i * step));
+        } else if (t.full) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {      // channels that do not exist: channel k0, zeroed
+                *reinterpret_cast<VN*>(raw.v[i]) =
+                    *reinterpret_cast<const VN*>(from(x, i < more ? at + i * step : (uint32_t)(n * t.pn) * S));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) raw.v[i][j] = i < more ? raw.v[i][j] : (T)0.0f;
+            }
+        } else {
+            const int64_t bytes = ((C - k0) * P - t.p0) * (int64_t)S;
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(x, (uint32_t)min(bytes, (int64_t)kOutside));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    raw.v[i][j] = buffer_load<T>(rs, n * t.pn + j < P - t.p0 ? at + i * step + j * S : kOutside);
+        }
+    }
+}
+
+// The operand of position j.
+template <typename T, bool LAST, int NT>
+__device__ __forceinline__ Frag<typename Operand<T>::V, Operand<T>::parts> operand(const Raw<T, LAST, NT>& raw, int j) {
+    typedef typename Operand<T>::V V;
+    if constexpr (Operand<T>::parts == 1) {
+        Frag<V, 1> f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f.part[0][i] = LAST ? raw.v[j][i] : raw.v[i][j];
+        return f;
+    } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = LAST ? raw.v[j][i] : raw.v[i][j];
+        return split<V, Operand<T>::parts>(v);
+    }
+}
+
+// ---- the product's kernel (fno_channels_kernel.hpp) ---------------------------------
+struct ProductArgs {
+    const void *x, *w;
+    const float* bias;
+    const void* branch;      // of out's type and layout, null for none
+    void* out;
+    const void* grad;        // slope mode: grad_out, of out's type and layout
+    float* g;                // slope mode: grad_out act'(z), in out's layout
+    int64_t B, P;            // items and positions, as tiles see them
+    int Cin, Cout;
+    int act;
+    bool branch_after, merged, slope, transposed;
+    int w_type;
+    int tiles_item;          // tiles of an item
+    int64_t tiles;
+    int cout_tiles;          // workgroups over the output channels
+    int chunk, nks;          // steps of 16 input channels: in LDS at a time, in all
+};
+// By type of x; out is of out_type (x's or float32; any for float32).
+hipError_t launch_product_f32(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
+hipError_t launch_product_bf16(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
+hipError_t launch_product_f16(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
+
+}  // namespace fno

@@ -1,0 +1,202 @@
+// Channel product of a field with its epilogue:
+//   z[b,o,p] = sum_i W[o,i] x[b,i,p] + bias[o],  out = act(z + branch) or act(z) + branch.
+//
+// A wave takes 32 NT positions and 32 MT output channels: x goes from memory
+// to registers as the operand it is (fno_channels.hpp), the weight stays in LDS
+// as parts in the order of the operands, and the result leaves from registers.
+//
+// Included by one source file for each type of x, so that they build side by side.
+#pragma once
+
+#include <algorithm>
+
+#include "fno_channels.hpp"
+
+namespace fno {
+namespace {
+
+constexpr int kProductThreads = 512;
+
+__device__ __forceinline__ float weight_at(const ProductArgs& a, int o, int i) {
+    if (o >= a.Cout || i >= a.Cin) return 0.0f;
+    const int64_t at = a.transposed ? (int64_t)i * a.Cout + o : (int64_t)o * a.Cin + i;
+    float v = 0.0f;
+    with_field_type(a.w_type, [&](auto e) { v = (float)static_cast<const decltype(e)*>(a.w)[at]; });
+    return v;
+}
+
+template <int ACT, int NT>
+__device__ __forceinline__ void activate(float (&z)[NT][8], bool slope) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) z[j][r] = slope ? act_slope<ACT>(z[j][r]) : act_value<ACT>(z[j][r]);
+}
+
+template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
+__global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) {
+    typedef typename Operand<T>::V V;
+    constexpr int parts = Operand<T>::parts;
+    extern __shared__ __align__(16) unsigned char lds[];
+    V* wfrag = reinterpret_cast<V*>(lds);                     // [part][mt][chunk][64]
+    float* bias = reinterpret_cast<float*>(wfrag + parts * MT * a.chunk * 64);
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ct = blockIdx.x % a.cout_tiles, c0 = ct * 32 * MT;
+    const int64_t group = blockIdx.x / a.cout_tiles, groups = gridDim.x / a.cout_tiles;
+
+    auto stage = [&](int first) {
+        const int steps = min(a.chunk, a.nks - first);
+        for (int q = threadIdx.x; q < MT * steps * 64; q += blockDim.x) {
+            const int l = q & 63, mt = (q >> 6) / steps, ks = (q >> 6) % steps;
+            const int o = c0 + 32 * mt + row_channel(l & 31), k = 16 * (first + ks) + 8 * (l >> 5);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = weight_at(a, o, k + i);
+            const Frag<V, parts> f = split<V, parts>(v);
+#pragma unroll
+            for (int p = 0; p < parts; ++p) wfrag[((p * MT + mt) * a.chunk + ks) * 64 + l] = f.part[p];
+        }
+    };
+    auto tile_at = [&](int64_t t) {
+        Tile q;
+        q.item = a.merged ? 0 : t / a.tiles_item;
+        q.p0 = (a.merged ? t : t % a.tiles_item) * (32 * NT);
+        q.pn = a.merged ? 1 : NT;
+        q.pj = a.merged ? 32 : 1;
+        q.full = q.p0 + 32 * NT <= a.P;
+        return q;
+    };
+    for (int i = threadIdx.x; i < 32 * MT; i += blockDim.x)
+        bias[i] = a.bias && c0 + i < a.Cout ? a.bias[c0 + i] : 0.0f;
+    const bool once = a.chunk >= a.nks;
+    if (once) stage(0);
+    __syncthreads();
+
+    const int64_t stride = groups * waves;
+    // every wave of a workgroup makes the same number of rounds (the barriers of staged weights)
+    const int64_t rounds = (a.tiles + stride - 1) / stride;
+    Raw<T, LAST, NT> raw;
+    int64_t t = group * waves + wave;
+    Tile tile = tile_at(min(t, a.tiles - 1));
+    if (t < a.tiles) load_raw(raw, a.x, tile, a.Cin, a.P, a.B, 0);
+    for (int64_t round = 0; round < rounds; ++round, t += stride) {
+        const bool live = t < a.tiles;
+        const Tile next = tile_at(min(t + stride, a.tiles - 1));
+        f32x16 acc[MT][NT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[mt][j][r] = 0.0f;
+        for (int first = 0; first < a.nks; first += a.chunk) {
+            if (!once) {
+                __syncthreads();
+                stage(first);
+                __syncthreads();
+            }
+            if (!live) continue;
+            const int steps = min(a.chunk, a.nks - first);
+            for (int ks = 0; ks < steps; ++ks) {
+                Frag<V, parts> b[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) b[j] = operand(raw, j);
+                if (first + ks + 1 < a.nks) {
+                    load_raw(raw, a.x, tile, a.Cin, a.P, a.B, 16 * (first + ks + 1));
+                } else if (t + stride < a.tiles) {
+                    load_raw(raw, a.x, next, a.Cin, a.P, a.B, 0);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    Frag<V, parts> w;
+#pragma unroll
+                    for (int p = 0; p < parts; ++p) w.part[p] = wfrag[((p * MT + mt) * a.chunk + ks) * 64 + lane];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[mt][j] = mfma_parts(w, b[j], acc[mt][j]);
+                }
+            }
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int q = 0; q < 2 * MT; ++q) {
+            const int mt = q >> 1, half = q & 1;
+            if (c0 + 32 * mt >= a.Cout) break;
+            const Places<TO, OUT_LAST, NT> at(tile, a.Cout, a.P, c0 + 32 * mt, half);
+            float z[NT][8], u[NT][8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float v = bias[32 * mt + 16 * h + 8 * half + r];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) z[j][r] = acc[mt][j][8 * half + r] + v;
+            }
+            if (a.branch) {
+                at.load(a.branch, u);
+                if (!a.branch_after) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) z[j][r] += u[j][r];
+                }
+            }
+            if (a.act == kActGelu) activate<kActGelu>(z, a.slope);
+            else if (a.act == kActSilu) activate<kActSilu>(z, a.slope);
+            if (a.slope) {
+                at.load(a.grad, u);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) z[j][r] *= u[j][r];
+                Places<float, OUT_LAST, NT>(tile, a.Cout, a.P, c0 + 32 * mt, half).store(a.g, z);
+            } else if (a.branch && a.branch_after) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) z[j][r] += u[j][r];
+            }
+            if (a.out) at.store(a.out, z);
+        }
+        tile = next;
+    }
+}
+
+template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
+hipError_t launch_tiles(ProductArgs a, hipStream_t s) {
+    a.tiles_item = (int)((a.P + 32 * NT - 1) / (32 * NT));
+    a.tiles = a.B * a.tiles_item;
+    a.cout_tiles = (a.Cout + 32 * MT - 1) / (32 * MT);
+    a.nks = (a.Cin + 15) / 16;
+    constexpr int step = Operand<T>::parts * MT * 1024;           // bytes of weights for 16 input channels
+    // 72 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
+    const bool wide = (int64_t)a.nks * step > 72 * 1024;
+    a.chunk = std::min(a.nks, (wide ? 144 : 72) * 1024 / step);
+    const int waves = wide ? 8 : 4;
+    const int64_t groups = std::max<int64_t>(
+        1, std::min<int64_t>((a.tiles + waves - 1) / waves, 512 * 4 / waves / std::min(a.cout_tiles, 8)));
+    const size_t lds = (size_t)a.chunk * step + 32 * MT * sizeof(float);
+    return launch_kernel(k_channels<T, TO, LAST, OUT_LAST, MT, NT>, dim3((unsigned)(groups * a.cout_tiles)),
+                         dim3(64 * waves), lds, s, a);
+}
+
+template <typename T, typename TO, bool LAST, bool OUT_LAST>
+hipError_t launch_couts(const ProductArgs& a, hipStream_t s) {
+    if (a.Cout <= 32) return launch_tiles<T, TO, LAST, OUT_LAST, 1, 2>(a, s);
+    if (a.Cout <= 64) return launch_tiles<T, TO, LAST, OUT_LAST, 2, 2>(a, s);
+    return launch_tiles<T, TO, LAST, OUT_LAST, 4, 2>(a, s);
+}
+
+// all channels last: one run of positions
+template <typename T, typename TO>
+hipError_t launch_layouts(ProductArgs a, bool last, bool out_last, hipStream_t s) {
+    a.merged = last && out_last;
+    if (a.merged) {
+        a.P *= a.B;
+        a.B = 1;
+        return launch_couts<T, TO, true, true>(a, s);
+    }
+    if (last) return launch_couts<T, TO, true, false>(a, s);
+    return out_last ? launch_couts<T, TO, false, true>(a, s) : launch_couts<T, TO, false, false>(a, s);
+}
+
+}  // namespace
+}  // namespace fno

@@ -371,4 +371,28 @@ uint32_t adam_table_chunks(AdamTable& t, int count);
 hipError_t launch_adamw(const AdamTable& t, uint32_t nchunks, const AdamOptions& o, hipStream_t s);
 hipError_t launch_adamw_moments(const AdamTable& t, uint32_t nchunks, hipStream_t s);
 
+// ---- channel product (fno_channels.hip) ---------------------------------------------
+// x of B items, P positions and Cin channels, out of Cout channels, each
+// channels last [B][P][C] or channels first [B][C][P]; weight [Cout][Cin] of x's type.
+struct ChannelProduct {
+    int64_t B, P;
+    int Cin, Cout;
+    int act;
+    bool branch_after, x_last, out_last;
+    int x_type, out_type;
+};
+struct ChannelArgs {
+    const void *x, *w;
+    const float* bias;            // null: zeros
+    const void* branch;           // null: none
+    void* out;                    // backward: grad_out
+    void *grad_x, *grad_branch;   // backward only, null where not asked for
+    float *grad_w, *grad_b;
+    void* ws;
+};
+size_t channel_workspace(const ChannelProduct& c, bool backward);
+// A call is a list of kernels, launched one after the other.
+int channel_kernels(const ChannelProduct& c, const ChannelArgs& a, bool backward, const char** names);
+hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool backward, int kernel, hipStream_t s);
+
 }  // namespace fno

@@ -419,6 +419,54 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
                        float* norm, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Channel product of a field: the pointwise branch of a layer, channel MLPs,
+ * lifting from and projection to the data.  At every position p of an item b
+ *
+ *   z[o] = sum_i weight[o][i] x[i] + bias[o]
+ *   branch_after = 0:  out = act(z + branch)       (branch as in fno_spectral_conv2d_gelu)
+ *   branch_after = 1:  out = act(z) + branch
+ *
+ * x has Cin, out Cout channels at P positions of B items, each channels last
+ * [B][P][C] (x_last / out_last 1) or channels first [B][C][P] (0).  x_type is
+ * FNO_F32, FNO_BF16 or FNO_F16, weight [Cout][Cin] of the same type; out_type
+ * the same or FNO_F32, branch (NULL for none) of out's type and layout; bias
+ * float32 [Cout] (NULL for zeros).  Sums are float32, float32 products as good
+ * as float32's own, a 16-bit output is rounded once.  An infinity, a NaN or a
+ * float32 value beyond bfloat16's largest finite one (3.39e38) in x makes the
+ * outputs of its position, in the weight those of its channel, infinite or NaN;
+ * no others.
+ *
+ * 1 <= B, P; 1 <= Cin, Cout <= 2^16; P <= 2^24 unless x and out are channels
+ * last, then P <= 2^30; B P <= 2^40 / max(Cin, Cout).  Fields need the alignment of their elements only.  out
+ * must not overlap anything else (FNO_ERR_ALIAS).  No workspace, nothing is allocated.
+ */
+int fno_channel_linear(const void* x, const void* weight, const float* bias, const void* branch, void* out,
+                       int B, int Cin, int Cout, int P, int act, int branch_after, int x_last, int out_last,
+                       int x_type, int out_type, void* stream);
+
+/*
+ * Backward pass of fno_channel_linear: with grad_out = dL/dout (out's layout and
+ * type) and g = grad_out act'(z), or act'(z + branch) for branch_after = 0 (z is
+ * formed again from x),
+ *
+ *   grad_x = weight^T g (x's layout and type),  grad_weight[o][i] = sum_{b,p} g[o] x[i],
+ *   grad_bias[o] = sum_{b,p} g[o] (float32, whatever x's type),  grad_branch = g (out's)
+ *
+ * Each may be NULL, not all; they are overwritten.  grad_branch is for
+ * branch_after = 0 and an activation alone: otherwise it is grad_out itself
+ * (FNO_ERR_VALUE).  branch is not read with branch_after = 1.  Sums run in a
+ * fixed order: equal inputs give equal bits.  `workspace`: as for fno_group_norm,
+ * fno_channel_linear_workspace_size bytes.
+ */
+size_t fno_channel_linear_workspace_size(int B, int Cin, int Cout, int P, int act, int x_last, int out_last,
+                                         int x_type, int out_type);
+int fno_channel_linear_backward(const void* x, const void* weight, const float* bias, const void* branch,
+                                const void* grad_out, void* grad_x, float* grad_weight, float* grad_bias,
+                                void* grad_branch, int B, int Cin, int Cout, int P, int act, int branch_after,
+                                int x_last, int out_last, int x_type, int out_type, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/*
  * One AdamW step over `count` tensors at once: the optimizer behind
  * fno_grad_norm.  For every value (two a complex one),
  *
