@@ -145,98 +145,131 @@ __device__ __forceinline__ const T* from(const T* base, uint32_t bytes) {
     return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
 }
 
-// The places of half of a 32-channel part of a result tile in a field (halves keep few
-// registers busy at a time): z[j][r], r < 8, is channel c0 + 16 (lane / 32) + 8 half + r at
-// the lane's position j.
+// 16 of a lane's values of a 32-channel part of a result tile, as one of NT
+// chunks (few registers are busy at a time), and their places in a field.
+// Channels last: chunk j holds position j, z[r] channel c0 + 16 (lane / 32) + r.
+// Channels first: chunk q holds 16 / NT channels, z[NT i + j] is channel
+// c0 + 16 (lane / 32) + 16 / NT q + i at position j.
+template <bool LAST, int NT>
+__device__ __forceinline__ constexpr int chunk_pos(int q, int i) { return LAST ? q : i % NT; }
+template <bool LAST, int NT>
+__device__ __forceinline__ constexpr int chunk_row(int q, int i) { return LAST ? i : 16 / NT * q + i / NT; }
+
+// Bytes of LDS that a wave turns channels-last results in: 32 positions of 32
+// channels, rows 16 bytes longer than that, so that those of neighbouring lanes start on other banks.
+constexpr int kTurnBytes = 32 * (32 * 4 + 16);
+
 template <typename T, bool LAST, int NT>
 struct Places {
     int64_t start;           // elements from the field's start to the part's, the same in all lanes
     uint32_t left;           // bytes from there to the field's (channels first: the item's) end, or enough; 0 behind it
-    uint32_t at, step;       // of r = 0 and position 0; between positions (LAST) or channels; bytes
-    int channels;            // of this half of the part that exist
+    uint32_t at, step;       // of the part's first channel and the lane's position 0; between positions (LAST) or channels; bytes
+    int channels;            // of the lane's half of the part that exist
+    int part;                // of the part that exist
     int positions;           // of the tile that exist
-    int first, pj;           // the lane's first position in the tile, and from one to the next
-    bool whole;              // nothing is outside
+    int C;
+    int first, pn, pj;       // the lane's first position in the tile; from a lane to the next, from one of its positions to the next
+    bool full;               // all positions exist
+    bool readable;           // channels last: rows may be read to the part's end
 
-    __device__ __forceinline__ Places(const Tile& t, int C, int64_t P, int c0, int half) {
+    __device__ __forceinline__ Places(const Tile& t, int C_, int64_t P, int64_t items, int c0) {
         const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+        C = C_;
         start = t.item * P * C + (LAST ? t.p0 * C + c0 : c0 * P + t.p0);
         const int64_t more = ((LAST ? (P - t.p0) * C - c0 : (C - c0) * P - t.p0)) * (int64_t)sizeof(T);
         left = (uint32_t)max((int64_t)0, min(more, (int64_t)kOutside));
-        first = n * t.pn;
+        pn = t.pn;
         pj = t.pj;
-        at = (LAST ? (uint32_t)(first * C + 16 * h + 8 * half) : (uint32_t)((16 * h + 8 * half) * P + first)) * (uint32_t)sizeof(T);
+        first = n * pn;
+        at = (LAST ? (uint32_t)(first * C + 16 * h) : (uint32_t)(16 * h * P + first)) * (uint32_t)sizeof(T);
         step = (uint32_t)(LAST ? pj * C : P) * (uint32_t)sizeof(T);
-        channels = C - c0 - 16 * h - 8 * half;
+        part = C - c0;
+        channels = part - 16 * h;
         positions = (int)min(P - t.p0, (int64_t)32 * NT);
-        whole = t.full && c0 + 32 <= C;
+        full = t.full;
+        readable = full && (c0 + 32 <= C || t.item + 1 < items || t.p0 + 32 * NT + 32 <= P);
     }
-    __device__ __forceinline__ uint32_t place(int j, int r) const {
-        const bool in = LAST ? r < channels : first + j * pj < positions;
-        const uint32_t o = at + (LAST ? j * step + r * (uint32_t)sizeof(T) : r * step + j * (uint32_t)sizeof(T));
-        return in ? o : kOutside;
+    __device__ __forceinline__ uint32_t place(int q, int i) const {
+        const int j = chunk_pos<LAST, NT>(q, i), r = chunk_row<LAST, NT>(q, i);
+        const bool in = r < channels && first + j * pj < positions;
+        return in ? at + (LAST ? j * step + r * (uint32_t)sizeof(T) : r * step + j * (uint32_t)sizeof(T)) : kOutside;
     }
 
-    __device__ __forceinline__ void load(const void* field, float (&z)[NT][8]) const {
+    // (values of channels that do not exist may be anything)
+    __device__ __forceinline__ void load(const void* field, int q, float (&z)[16]) const {
         const T* f = static_cast<const T*>(field) + start;
-        if (whole) {
+        if (LAST ? readable : full) {
             if constexpr (LAST) {
                 constexpr int V = 16 / sizeof(T);
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int k = 0; k < 16; k += V) {
+                    float v[V];
+                    load_vec<V>(from(f, at + q * step) + k, v);
 #pragma unroll
-                    for (int k = 0; k < 8; k += V) {
-                        float v[V];
-                        load_vec<V>(from(f, at + j * step) + k, v);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) z[j][k + i] = v[i];
-                    }
+                    for (int i = 0; i < V; ++i) z[k + i] = v[i];
+                }
             } else {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int i = 0; i < 16; i += NT) {
+                    const int r = chunk_row<LAST, NT>(q, i);
                     float v[NT];
-                    load_vec<NT>(from(f, at + r * step), v);
+                    load_vec<NT>(from(f, r < channels ? at + r * step : (uint32_t)first * (uint32_t)sizeof(T)), v);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) z[j][r] = v[j];
+                    for (int j = 0; j < NT; ++j) z[i + j] = v[j];
                 }
             }
         } else {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int r = 0; r < 8; ++r) z[j][r] = (float)buffer_load<T>(rs, place(j, r));
+            for (int i = 0; i < 16; ++i) z[i] = (float)buffer_load<T>(rs, place(q, i));
         }
     }
-    __device__ __forceinline__ void store(void* field, const float (&z)[NT][8]) const {
+
+    // Channels last, lanes hold 16 channels of a position: the part is turned in `turn` (this wave's), so
+    // that neighbouring lanes write neighbouring 16 bytes of a row.
+    __device__ __forceinline__ void store(void* field, int q, const float (&z)[16], unsigned char* turn) const {
         T* f = static_cast<T*>(field) + start;
-        if (whole) {
-            if constexpr (LAST) {
-                constexpr int V = 16 / sizeof(T);
+        if constexpr (LAST) {
+            const int lane = threadIdx.x & 63;
+            constexpr int V = 16 / sizeof(T), row = 32 * sizeof(T) + 16, lanes = 32 / V;
+            typedef T VT __attribute__((ext_vector_type(V)));
+            VT* mine = reinterpret_cast<VT*>(turn + (lane & 31) * row + (lane >> 5) * 16 * sizeof(T));
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+            for (int k = 0; k < 16 / V; ++k) {
+                VT v;
 #pragma unroll
-                    for (int k = 0; k < 8; k += V) {
-                        float v[V];
+                for (int i = 0; i < V; ++i) v[i] = (T)z[k * V + i];
+                mine[k] = v;
+            }
+            __builtin_amdgcn_wave_barrier();
+            const int c = lane % lanes * V;
 #pragma unroll
-                        for (int i = 0; i < V; ++i) v[i] = z[j][k + i];
-                        store_vec<V>(from(f, at + j * step) + k, v);
-                    }
-            } else {
+            for (int k = 0; k < 32; k += 64 / lanes) {
+                const int n = k + lane / lanes, p = n * pn + q * pj;
+                const VT v = *reinterpret_cast<const VT*>(turn + n * row + c * sizeof(T));
+                T* o = f + (uint32_t)(p * C + c);
+                if (p < positions && c + V <= part) {
+                    *reinterpret_cast<typename VecOf<T, V>::type*>(o) = v;
+                } else if (p < positions) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    float v[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) v[j] = z[j][r];
-                    store_vec<NT>(from(f, at + r * step), v);
+                    for (int i = 0; i < V; ++i)
+                        if (c + i < part) o[i] = v[i];
                 }
+            }
+            __builtin_amdgcn_wave_barrier();
+        } else if (full) {
+#pragma unroll
+            for (int i = 0; i < 16; i += NT) {
+                const int r = chunk_row<LAST, NT>(q, i);
+                float v[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) v[j] = z[i + j];
+                if (r < channels) store_vec<NT>(from(f, at + r * step), v);
             }
         } else {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int r = 0; r < 8; ++r) buffer_store<T>(rs, place(j, r), (T)z[j][r]);
+            for (int i = 0; i < 16; ++i) buffer_store<T>(rs, place(q, i), (T)z[i]);
         }
     }
 };

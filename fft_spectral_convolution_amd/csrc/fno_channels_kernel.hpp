@@ -25,12 +25,10 @@ __device__ __forceinline__ float weight_at(const ProductArgs& a, int o, int i) {
     return v;
 }
 
-template <int ACT, int NT>
-__device__ __forceinline__ void activate(float (&z)[NT][8], bool slope) {
+template <int ACT>
+__device__ __forceinline__ void activate(float (&z)[16], bool slope) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < 8; ++r) z[j][r] = slope ? act_slope<ACT>(z[j][r]) : act_value<ACT>(z[j][r]);
+    for (int i = 0; i < 16; ++i) z[i] = slope ? act_slope<ACT>(z[i]) : act_value<ACT>(z[i]);
 }
 
 template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
@@ -41,6 +39,7 @@ __global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) 
     V* wfrag = reinterpret_cast<V*>(lds);                     // [part][mt][chunk][64]
     float* bias = reinterpret_cast<float*>(wfrag + parts * MT * a.chunk * 64);
     const int lane = threadIdx.x & 63, h = lane >> 5;
+    unsigned char* const turn = reinterpret_cast<unsigned char*>(bias + 32 * MT) + (threadIdx.x >> 6) * kTurnBytes;
     const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ct = blockIdx.x % a.cout_tiles, c0 = ct * 32 * MT;
     const int64_t group = blockIdx.x / a.cout_tiles, groups = gridDim.x / a.cout_tiles;
@@ -119,42 +118,35 @@ __global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) 
         }
         if (!live) continue;
 #pragma unroll
-        for (int q = 0; q < 2 * MT; ++q) {
-            const int mt = q >> 1, half = q & 1;
+        for (int mt = 0; mt < MT; ++mt) {
             if (c0 + 32 * mt >= a.Cout) break;
-            const Places<TO, OUT_LAST, NT> at(tile, a.Cout, a.P, c0 + 32 * mt, half);
-            float z[NT][8], u[NT][8];
+            const Places<TO, OUT_LAST, NT> at(tile, a.Cout, a.P, a.B, c0 + 32 * mt);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float v = bias[32 * mt + 16 * h + 8 * half + r];
+            for (int q = 0; q < NT; ++q) {
+                float z[16], u[16];
+                if (a.branch) at.load(a.branch, q, u);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) z[j][r] = acc[mt][j][8 * half + r] + v;
-            }
-            if (a.branch) {
-                at.load(a.branch, u);
-                if (!a.branch_after) {
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) z[j][r] += u[j][r];
+                for (int i = 0; i < 16; ++i) {
+                    const int j = chunk_pos<OUT_LAST, NT>(q, i), r = chunk_row<OUT_LAST, NT>(q, i);
+                    z[i] = acc[mt][j][r] + bias[32 * mt + 16 * h + r];
                 }
+                if (a.branch && !a.branch_after) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] += u[i];
+                }
+                if (a.act == kActGelu) activate<kActGelu>(z, a.slope);
+                else if (a.act == kActSilu) activate<kActSilu>(z, a.slope);
+                if (a.slope) {
+                    at.load(a.grad, q, u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] *= u[i];
+                    Places<float, OUT_LAST, NT>(tile, a.Cout, a.P, a.B, c0 + 32 * mt).store(a.g, q, z, turn);
+                } else if (a.branch && a.branch_after) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] += u[i];
+                }
+                if (a.out) at.store(a.out, q, z, turn);
             }
-            if (a.act == kActGelu) activate<kActGelu>(z, a.slope);
-            else if (a.act == kActSilu) activate<kActSilu>(z, a.slope);
-            if (a.slope) {
-                at.load(a.grad, u);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) z[j][r] *= u[j][r];
-                Places<float, OUT_LAST, NT>(tile, a.Cout, a.P, c0 + 32 * mt, half).store(a.g, z);
-            } else if (a.branch && a.branch_after) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) z[j][r] += u[j][r];
-            }
-            if (a.out) at.store(a.out, z);
         }
         tile = next;
     }
@@ -167,13 +159,13 @@ hipError_t launch_tiles(ProductArgs a, hipStream_t s) {
     a.cout_tiles = (a.Cout + 32 * MT - 1) / (32 * MT);
     a.nks = (a.Cin + 15) / 16;
     constexpr int step = Operand<T>::parts * MT * 1024;           // bytes of weights for 16 input channels
-    // 72 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
-    const bool wide = (int64_t)a.nks * step > 72 * 1024;
-    a.chunk = std::min(a.nks, (wide ? 144 : 72) * 1024 / step);
+    // 60 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
+    const bool wide = (int64_t)a.nks * step > 60 * 1024;
+    a.chunk = std::min(a.nks, (wide ? 120 : 60) * 1024 / step);
     const int waves = wide ? 8 : 4;
     const int64_t groups = std::max<int64_t>(
         1, std::min<int64_t>((a.tiles + waves - 1) / waves, 512 * 4 / waves / std::min(a.cout_tiles, 8)));
-    const size_t lds = (size_t)a.chunk * step + 32 * MT * sizeof(float);
+    const size_t lds = (size_t)a.chunk * step + 32 * MT * sizeof(float) + (OUT_LAST ? waves * kTurnBytes : 0);
     return launch_kernel(k_channels<T, TO, LAST, OUT_LAST, MT, NT>, dim3((unsigned)(groups * a.cout_tiles)),
                          dim3(64 * waves), lds, s, a);
 }
