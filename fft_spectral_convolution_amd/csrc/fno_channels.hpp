@@ -94,6 +94,41 @@ __device__ __forceinline__ f32x16 mfma_parts(const Frag<V, NA>& a, const Frag<V,
     return c;
 }
 
+// ---- activations ----------------------------------------------------------------------
+// As act_value, in fewer instructions, which the products of 16-bit fields with
+// many output channels are bound by: gelu(z) = max(z, 0) - |z| Phi(-|z|), and
+// log2 Phi(-a) is a smooth function that a polynomial (least squares, weighted to a
+// level error of Phi^1/2 times it, on [0, 6]; falling up to 12, where Phi is 2^-97 or less) gives without a division.  Degree 8: gelu
+// within 8e-8, 2e-7 |z| for small z; degree 6, for results rounded to 16 bits: 2.2e-7, 4e-7 |z|.
+template <int ACT, bool FINE>
+__device__ __forceinline__ float product_act(float z) {
+    if constexpr (ACT == kActGelu) {
+        const float a = fminf(fabsf(z), 12.0f);
+        float q;
+        if constexpr (FINE) {
+            q = -8.72182852e-07f;
+            q = fmaf(q, a, 1.44495389e-05f);
+            q = fmaf(q, a, -6.05394889e-05f);
+            q = fmaf(q, a, -0.000458409078f);
+            q = fmaf(q, a, 0.00750667136f);
+            q = fmaf(q, a, -0.0528182127f);
+            q = fmaf(q, a, -0.459096968f);
+            q = fmaf(q, a, -1.15111935f);
+            q = fmaf(q, a, -0.999999702f);
+        } else {
+            q = 3.2875083e-05f;
+            q = fmaf(q, a, -0.000760217314f);
+            q = fmaf(q, a, 0.00802443828f);
+            q = fmaf(q, a, -0.0532797612f);
+            q = fmaf(q, a, -0.458904028f);
+            q = fmaf(q, a, -1.15114868f);
+            q = fmaf(q, a, -0.999998987f);
+        }
+        return fmaf(-a, __builtin_amdgcn_exp2f(q), z < 0.0f ? 0.0f : z);       // (a NaN stays one)
+    }
+    return act_value<ACT>(z);
+}
+
 // A run of positions of one item that a wave works on: 32 NT of them, of
 // which lane n % 32's j-th is p0 + pn n + pj j.
 struct Tile {
@@ -135,6 +170,12 @@ __device__ __forceinline__ void buffer_store(__amdgpu_buffer_rsrc_t rs, uint32_t
     } else {
         __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rs, (int)at, 0, 0);
     }
+}
+// Offsets that are the same for every tile are formed again where they are
+// used: dozens of them kept from tile to tile would take the registers of the products.
+__device__ __forceinline__ void per_tile(uint32_t& lane_offset, uint32_t& step) {
+    step = __builtin_amdgcn_readfirstlane(step);
+    asm volatile("" : "+v"(lane_offset), "+s"(step));
 }
 template <typename T>
 __device__ __forceinline__ T* from(T* base, uint32_t bytes) {
@@ -183,6 +224,7 @@ struct Places {
         first = n * pn;
         at = (LAST ? (uint32_t)(first * C + 16 * h) : (uint32_t)(16 * h * P + first)) * (uint32_t)sizeof(T);
         step = (uint32_t)(LAST ? pj * C : P) * (uint32_t)sizeof(T);
+        per_tile(at, step);
         part = C - c0;
         channels = part - 16 * h;
         positions = (int)min(P - t.p0, (int64_t)32 * NT);
@@ -292,7 +334,8 @@ __device__ __forceinline__ void load_raw(Raw<T, LAST, NT>& raw, const void* fiel
     constexpr uint32_t S = sizeof(T);
     if constexpr (LAST) {
         typedef typename VecOf<T, 8>::type V8;
-        const uint32_t at = (uint32_t)(n * t.pn * C + 8 * h) * S, step = (uint32_t)(t.pj * C) * S;
+        uint32_t at = (uint32_t)(n * t.pn * C + 8 * h) * S, step = (uint32_t)(t.pj * C) * S;
+        per_tile(at, step);
         // a row's tail may be read into the next rows, but not behind the field
         if (t.full && (k0 + 16 <= C || t.item + 1 < items || t.p0 + 32 * NT + 16 <= P)) {
 #pragma unroll
@@ -315,7 +358,8 @@ __device__ __forceinline__ void load_raw(Raw<T, LAST, NT>& raw, const void* fiel
         }
     } else {
         typedef typename VecOf<T, NT>::type VN;
-        const uint32_t step = (uint32_t)P * S, at = 8 * h * step + (uint32_t)(n * t.pn) * S;
+        uint32_t step = (uint32_t)P * S, at = 8 * h * step + (uint32_t)(n * t.pn) * S;
+        per_tile(at, step);
         if (t.full && k0 + 16 <= C) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -373,6 +417,7 @@ struct ProductArgs {
     int tiles_item;          // tiles of an item
     int64_t tiles;
     int cout_tiles;          // workgroups over the output channels
+    int groups;              // workgroups over the positions
     int chunk, nks;          // steps of 16 input channels: in LDS at a time, in all
 };
 // By type of x; out is of out_type (x's or float32; any for float32).

@@ -25,24 +25,32 @@ __device__ __forceinline__ float weight_at(const ProductArgs& a, int o, int i) {
     return v;
 }
 
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ void activate(float (&z)[16], bool slope) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = slope ? act_slope<ACT>(z[i]) : act_value<ACT>(z[i]);
+    for (int i = 0; i < 16; ++i) z[i] = slope ? act_slope<ACT>(z[i]) : product_act<ACT, FINE>(z[i]);
 }
 
+// Steps of 16 channels that are loaded before they are used: 64 channels of 16
+// bits, 32 of 32 bits.  Chunks of staged weights are whole numbers of them.
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+
 template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
-__global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) {
+__global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_channels(ProductArgs a) {
     typedef typename Operand<T>::V V;
-    constexpr int parts = Operand<T>::parts;
+    constexpr int parts = Operand<T>::parts, ahead = kAhead<T>;
     extern __shared__ __align__(16) unsigned char lds[];
     V* wfrag = reinterpret_cast<V*>(lds);                     // [part][mt][chunk][64]
     float* bias = reinterpret_cast<float*>(wfrag + parts * MT * a.chunk * 64);
     const int lane = threadIdx.x & 63, h = lane >> 5;
     unsigned char* const turn = reinterpret_cast<unsigned char*>(bias + 32 * MT) + (threadIdx.x >> 6) * kTurnBytes;
     const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ct = blockIdx.x % a.cout_tiles, c0 = ct * 32 * MT;
-    const int64_t group = blockIdx.x / a.cout_tiles, groups = gridDim.x / a.cout_tiles;
+    // Neighbouring workgroups are on different XCDs: those that read the same positions for
+    // other output channels are eight apart, on one XCD, and share its L2.
+    const int lanes8 = a.groups % 8 == 0 ? 8 : 1;
+    const int slot = blockIdx.x / lanes8, c0 = slot % a.cout_tiles * 32 * MT;
+    const int64_t group = (int64_t)(slot / a.cout_tiles) * lanes8 + blockIdx.x % lanes8, groups = a.groups;
 
     auto stage = [&](int first) {
         const int steps = min(a.chunk, a.nks - first);
@@ -75,10 +83,12 @@ __global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) 
     const int64_t stride = groups * waves;
     // every wave of a workgroup makes the same number of rounds (the barriers of staged weights)
     const int64_t rounds = (a.tiles + stride - 1) / stride;
-    Raw<T, LAST, NT> raw;
+    Raw<T, LAST, NT> raw[ahead];
     int64_t t = group * waves + wave;
     Tile tile = tile_at(min(t, a.tiles - 1));
-    if (t < a.tiles) load_raw(raw, a.x, tile, a.Cin, a.P, a.B, 0);
+#pragma unroll
+    for (int k = 0; k < ahead; ++k)
+        if (t < a.tiles && k < a.nks) load_raw(raw[k], a.x, tile, a.Cin, a.P, a.B, 16 * k);
     for (int64_t round = 0; round < rounds; ++round, t += stride) {
         const bool live = t < a.tiles;
         const Tile next = tile_at(min(t + stride, a.tiles - 1));
@@ -88,7 +98,7 @@ __global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) 
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[mt][j][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) acc[mt][j][r] = bias[32 * mt + 16 * h + r];
         for (int first = 0; first < a.nks; first += a.chunk) {
             if (!once) {
                 __syncthreads();
@@ -97,30 +107,37 @@ __global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) 
             }
             if (!live) continue;
             const int steps = min(a.chunk, a.nks - first);
-            for (int ks = 0; ks < steps; ++ks) {
-                Frag<V, parts> b[NT];
+            for (int base = 0; base < steps; base += ahead) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) b[j] = operand(raw, j);
-                if (first + ks + 1 < a.nks) {
-                    load_raw(raw, a.x, tile, a.Cin, a.P, a.B, 16 * (first + ks + 1));
-                } else if (t + stride < a.tiles) {
-                    load_raw(raw, a.x, next, a.Cin, a.P, a.B, 0);
-                }
+                for (int k = 0; k < ahead; ++k) {
+                    const int ks = base + k;
+                    if (ks >= steps) break;
+                    Frag<V, parts> b[NT];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    Frag<V, parts> w;
+                    for (int j = 0; j < NT; ++j) b[j] = operand(raw[k], j);
+                    if (first + ks + ahead < a.nks) {
+                        load_raw(raw[k], a.x, tile, a.Cin, a.P, a.B, 16 * (first + ks + ahead));
+                    } else if (t + stride < a.tiles) {
+                        load_raw(raw[k], a.x, next, a.Cin, a.P, a.B, 16 * k);
+                    }
 #pragma unroll
-                    for (int p = 0; p < parts; ++p) w.part[p] = wfrag[((p * MT + mt) * a.chunk + ks) * 64 + lane];
+                    for (int mt = 0; mt < MT; ++mt) {
+                        Frag<V, parts> w;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[mt][j] = mfma_parts(w, b[j], acc[mt][j]);
+                        for (int p = 0; p < parts; ++p) w.part[p] = wfrag[((p * MT + mt) * a.chunk + ks) * 64 + lane];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) acc[mt][j] = mfma_parts(w, b[j], acc[mt][j]);
+                    }
                 }
             }
         }
         if (!live) continue;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            if (c0 + 32 * mt >= a.Cout) break;
-            const Places<TO, OUT_LAST, NT> at(tile, a.Cout, a.P, a.B, c0 + 32 * mt);
+            int c = c0 + 32 * mt;
+            if (c >= a.Cout) break;
+            asm volatile("" : "+s"(c));          // (formed here, not for all parts before the first)
+            const Places<TO, OUT_LAST, NT> at(tile, a.Cout, a.P, a.B, c);
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 float z[16], u[16];
@@ -128,19 +145,19 @@ __global__ __launch_bounds__(kProductThreads, 2) void k_channels(ProductArgs a) 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int j = chunk_pos<OUT_LAST, NT>(q, i), r = chunk_row<OUT_LAST, NT>(q, i);
-                    z[i] = acc[mt][j][r] + bias[32 * mt + 16 * h + r];
+                    z[i] = acc[mt][j][r];
                 }
                 if (a.branch && !a.branch_after) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) z[i] += u[i];
                 }
-                if (a.act == kActGelu) activate<kActGelu>(z, a.slope);
-                else if (a.act == kActSilu) activate<kActSilu>(z, a.slope);
+                if (a.act == kActGelu) activate<kActGelu, sizeof(TO) == 4>(z, a.slope);
+                else if (a.act == kActSilu) activate<kActSilu, true>(z, a.slope);
                 if (a.slope) {
                     at.load(a.grad, q, u);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) z[i] *= u[i];
-                    Places<float, OUT_LAST, NT>(tile, a.Cout, a.P, a.B, c0 + 32 * mt).store(a.g, q, z, turn);
+                    Places<float, OUT_LAST, NT>(tile, a.Cout, a.P, a.B, c).store(a.g, q, z, turn);
                 } else if (a.branch && a.branch_after) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) z[i] += u[i];
@@ -161,20 +178,24 @@ hipError_t launch_tiles(ProductArgs a, hipStream_t s) {
     constexpr int step = Operand<T>::parts * MT * 1024;           // bytes of weights for 16 input channels
     // 60 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
     const bool wide = (int64_t)a.nks * step > 60 * 1024;
-    a.chunk = std::min(a.nks, (wide ? 120 : 60) * 1024 / step);
+    const int most = (wide ? 120 : 60) * 1024 / step;
+    a.chunk = a.nks <= most ? a.nks : most / kAhead<T> * kAhead<T>;
     const int waves = wide ? 8 : 4;
-    const int64_t groups = std::max<int64_t>(
-        1, std::min<int64_t>((a.tiles + waves - 1) / waves, 512 * 4 / waves / std::min(a.cout_tiles, 8)));
+    // as many waves as the CUs hold; groups of workgroups that read the same positions are dealt out in eights
+    const int64_t most_groups = 256 * (MT * NT <= 2 ? 3 : 2) * 4 / waves / std::min(a.cout_tiles, 8);
+    a.groups = (int)std::max<int64_t>(1, std::min<int64_t>((a.tiles + waves - 1) / waves, most_groups));
+    if (a.groups > 8) a.groups = (a.groups + 7) / 8 * 8;
     const size_t lds = (size_t)a.chunk * step + 32 * MT * sizeof(float) + (OUT_LAST ? waves * kTurnBytes : 0);
-    return launch_kernel(k_channels<T, TO, LAST, OUT_LAST, MT, NT>, dim3((unsigned)(groups * a.cout_tiles)),
+    return launch_kernel(k_channels<T, TO, LAST, OUT_LAST, MT, NT>, dim3((unsigned)(a.groups * a.cout_tiles)),
                          dim3(64 * waves), lds, s, a);
 }
 
 template <typename T, typename TO, bool LAST, bool OUT_LAST>
 hipError_t launch_couts(const ProductArgs& a, hipStream_t s) {
-    if (a.Cout <= 32) return launch_tiles<T, TO, LAST, OUT_LAST, 1, 2>(a, s);
-    if (a.Cout <= 64) return launch_tiles<T, TO, LAST, OUT_LAST, 2, 2>(a, s);
-    return launch_tiles<T, TO, LAST, OUT_LAST, 4, 2>(a, s);
+    constexpr int NT = LAST && OUT_LAST ? 1 : 2;
+    if (a.Cout <= 32) return launch_tiles<T, TO, LAST, OUT_LAST, 1, NT>(a, s);
+    if (a.Cout <= 64) return launch_tiles<T, TO, LAST, OUT_LAST, 2, NT>(a, s);
+    return launch_tiles<T, TO, LAST, OUT_LAST, 4, NT>(a, s);
 }
 
 // all channels last: one run of positions
