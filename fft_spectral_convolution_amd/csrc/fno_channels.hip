@@ -15,7 +15,7 @@ namespace {
 // workgroups by k_weight_sum, both in a fixed order.
 struct GradArgs {
     const void *x, *g;
-    float* part;              // [splits][Cout][Cin], then [splits][Cout] sums of g
+    float* part;              // [splits][Cout Cin + Cout]: sums of g x and of g
     int64_t B, P, steps_item, steps;     // steps of 16 positions
     int Cin, Cout, ct_in, ct_out, splits;
     bool x_last, g_last;
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void k_weight_grad(GradArgs a) {
 #pragma unroll
             for (int v = 0; v < 2; ++v) acc[u][v] = mfma_parts(g[u], x[v], acc[u][v]);
     }
-    float* part = a.part + (int64_t)split_no * a.Cout * a.Cin;
+    float* part = a.part + (int64_t)split_no * (a.Cin + 1) * a.Cout;
     for (int u = 0; u < 2; ++u)
         for (int v = 0; v < 2; ++v)
             for (int r = 0; r < 16; ++r) {
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void k_weight_grad(GradArgs a) {
                     part[(int64_t)o * a.Cin + i] = join[0][lane] + join[1][lane] + join[2][lane] + join[3][lane];
             }
     if (i0 != 0) return;
-    float* sums = a.part + (int64_t)a.splits * a.Cout * a.Cin + (int64_t)split_no * a.Cout;
+    float* sums = part + (int64_t)a.Cin * a.Cout;
     for (int u = 0; u < 2; ++u) {
         __syncthreads();
         join[wave][lane] = sum[u];
@@ -103,19 +103,34 @@ __global__ __launch_bounds__(256) void k_weight_grad(GradArgs a) {
     }
 }
 
-// out[k] = sum over splits of part[split][k], for the weight's and then the bias' gradient.
+// grad_w and, behind it, grad_b: sums over the splits, 64 values a workgroup, each
+// wave a quarter of the splits.
 __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ part, float* __restrict__ grad_w,
                                                     float* __restrict__ grad_b, int64_t weights, int couts, int splits) {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= weights + couts) return;
-    const bool b = k >= weights;
-    float* out = b ? grad_b : grad_w;
-    if (!out) return;
-    const float* p = b ? part + splits * weights + (k - weights) : part + k;
-    const int64_t ld = b ? couts : weights;
+    __shared__ double join[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t k = (int64_t)blockIdx.x * 64 + lane, all = weights + couts;
     double s = 0.0;
-    for (int i = 0; i < splits; ++i) s += (double)p[i * ld];
-    out[b ? k - weights : k] = (float)s;
+    if (k < all) {
+        int i = wave;
+        for (; i + 28 < splits; i += 32) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = part[(i + 4 * u) * all + k];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += (double)v[u];
+        }
+        for (; i < splits; i += 4) s += (double)part[i * all + k];
+    }
+    join[wave][lane] = s;
+    __syncthreads();
+    if (wave || k >= all) return;
+    const float v = (float)((join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]));
+    if (k < weights) {
+        if (grad_w) grad_w[k] = v;
+    } else if (grad_b) {
+        grad_b[k - weights] = v;
+    }
 }
 
 int weight_splits(const ChannelProduct& c) {
@@ -135,12 +150,30 @@ size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 // Whether g = grad_out act'(z) is a field of its own.
 bool keeps_g(const ChannelProduct& c) { return c.act != kActNone; }
 
+bool fits(const ChannelProduct& c) { return backward_fits(c.Cin, c.Cout); }
+
+// Workgroups of the one-kernel backward pass: two a CU, one where 128 channels fill its registers.
+int backward_groups(const ChannelProduct& c) {
+    const int64_t tiles = c.x_last && c.out_last ? (c.B * c.P + 31) / 32 : c.B * ((c.P + 31) / 32);
+    return (int)std::min<int64_t>((tiles + 3) / 4, std::max(c.Cin, c.Cout) <= 64 ? 512 : 256);
+}
+
+hipError_t launch_backward(const BackwardArgs& a, const ChannelProduct& c, hipStream_t s) {
+    if (c.x_type == kTypeF32) return launch_backward_f32(a, c.x_last, c.out_last, s);
+    if (c.x_type == kTypeBf16)
+        return c.out_type == kTypeF32 ? launch_backward_bf16_f32(a, c.x_last, c.out_last, s)
+                                      : launch_backward_bf16(a, c.x_last, c.out_last, s);
+    return c.out_type == kTypeF32 ? launch_backward_f16_f32(a, c.x_last, c.out_last, s)
+                                  : launch_backward_f16(a, c.x_last, c.out_last, s);
+}
+
 }  // namespace
 
 size_t channel_workspace(const ChannelProduct& c, bool backward) {
     if (!backward) return 0;
-    const size_t g = keeps_g(c) ? round_up((size_t)(c.B * c.P * c.Cout) * sizeof(float)) : 0;
-    return g + round_up((size_t)weight_splits(c) * ((size_t)c.Cin + 1) * c.Cout * sizeof(float));
+    const size_t g = keeps_g(c) && !fits(c) ? round_up((size_t)(c.B * c.P * c.Cout) * sizeof(float)) : 0;
+    const int splits = fits(c) ? backward_groups(c) : weight_splits(c);
+    return g + round_up((size_t)splits * ((size_t)c.Cin + 1) * c.Cout * sizeof(float));
 }
 
 int channel_kernels(const ChannelProduct& c, const ChannelArgs& a, bool backward, const char** names) {
@@ -149,12 +182,15 @@ int channel_kernels(const ChannelProduct& c, const ChannelArgs& a, bool backward
         return 1;
     }
     int n = 0;
-    if (keeps_g(c)) names[n++] = "channels_slope";
-    if (a.grad_x) names[n++] = "channels_grad_x";
-    if (a.grad_w || a.grad_b) {
-        names[n++] = "channels_grad_w";
-        names[n++] = "channels_grad_sum";
+    const bool sums = a.grad_w || a.grad_b;
+    if (fits(c)) {
+        names[n++] = "channels_bwd";
+    } else {
+        if (keeps_g(c)) names[n++] = "channels_slope";
+        if (a.grad_x) names[n++] = "channels_grad_x";
+        if (sums) names[n++] = "channels_grad_w";
     }
+    if (sums) names[n++] = "channels_grad_sum";
     return n;
 }
 
@@ -179,10 +215,28 @@ hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool b
         return launch_product(q, c.x_type, c.x_last, c.out_last, c.out_type, s);
     }
     float* g = static_cast<float*>(a.ws);
-    const bool own_g = keeps_g(c);
+    const bool own_g = keeps_g(c) && !fits(c);
     float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
                                            (own_g ? round_up((size_t)(c.B * c.P * c.Cout) * sizeof(float)) : 0));
-    const int splits = weight_splits(c);
+    const int splits = fits(c) ? backward_groups(c) : weight_splits(c);
+    if (names[kernel] == std::string_view("channels_bwd")) {
+        BackwardArgs b{};
+        b.x = a.x;
+        b.w = a.w;
+        b.bias = a.bias;
+        b.branch = c.branch_after ? nullptr : a.branch;
+        b.grad = a.out;
+        b.grad_x = a.grad_x;
+        b.grad_branch = a.grad_branch;
+        b.part = a.grad_w || a.grad_b ? part : nullptr;
+        b.B = c.B;
+        b.P = c.P;
+        b.Cin = c.Cin;
+        b.Cout = c.Cout;
+        b.act = c.act;
+        b.groups = splits;
+        return launch_backward(b, c, s);
+    }
     if (slope) {
         if (c.branch_after) q.branch = nullptr;
         q.slope = true;
@@ -228,7 +282,7 @@ hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool b
         return launch_kernel(k_weight_grad<3>, grid, block, 0, s, w);
     }
     const int64_t weights = (int64_t)c.Cin * c.Cout;
-    return launch_kernel(k_weight_sum, dim3((unsigned)((weights + c.Cout + 255) / 256)), dim3(256), 0, s,
+    return launch_kernel(k_weight_sum, dim3((unsigned)((weights + c.Cout + 63) / 64)), dim3(256), 0, s,
                          static_cast<const float*>(part), a.grad_w, a.grad_b, weights, c.Cout, splits);
 }
 

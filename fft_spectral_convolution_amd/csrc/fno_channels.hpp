@@ -19,6 +19,8 @@
 // the rest then a NaN: such inputs give a NaN where float32 sums might give an infinity.
 #pragma once
 
+#include <algorithm>
+
 #include "fno_fields.hpp"
 
 namespace fno {
@@ -82,16 +84,19 @@ __device__ __forceinline__ Frag<V, N> split(const float (&v)[8]) {
     return f;
 }
 
-// c += a b over the products of parts that matter, the smallest first.
-template <typename V, int NA, int NB>
-__device__ __forceinline__ f32x16 mfma_parts(const Frag<V, NA>& a, const Frag<V, NB>& b, f32x16 c) {
-    constexpr int most = (NA > NB ? NA : NB) - 1;
+// c += a b over the products of parts i and j that matter, i + j <= MOST, the smallest first.
+template <int MOST, typename V, int NA, int NB>
+__device__ __forceinline__ f32x16 mfma_upto(const Frag<V, NA>& a, const Frag<V, NB>& b, f32x16 c) {
 #pragma unroll
-    for (int s = most; s >= 0; --s)
+    for (int s = MOST; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB) c = mfma(a.part[i], b.part[s - i], c);
     return c;
+}
+template <typename V, int NA, int NB>
+__device__ __forceinline__ f32x16 mfma_parts(const Frag<V, NA>& a, const Frag<V, NB>& b, f32x16 c) {
+    return mfma_upto<(NA > NB ? NA : NB) - 1>(a, b, c);
 }
 
 // ---- activations ----------------------------------------------------------------------
@@ -196,6 +201,12 @@ __device__ __forceinline__ constexpr int chunk_pos(int q, int i) { return LAST ?
 template <bool LAST, int NT>
 __device__ __forceinline__ constexpr int chunk_row(int q, int i) { return LAST ? i : 16 / NT * q + i / NT; }
 
+// A chunk's values as they lie in the field.
+template <typename T>
+struct Values {
+    T v[16] __attribute__((aligned(16)));
+};
+
 // Bytes of LDS that a wave turns channels-last results in: 32 positions of 32
 // channels, rows 16 bytes longer than that, so that those of neighbouring lanes start on other banks.
 constexpr int kTurnBytes = 32 * (32 * 4 + 16);
@@ -264,6 +275,36 @@ struct Places {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = (float)buffer_load<T>(rs, place(q, i));
+        }
+    }
+
+    // As load, but as the field holds the values, and zeros for channels that do not exist.
+    __device__ __forceinline__ void fetch(const void* field, int q, Values<T>& z) const {
+        const T* f = static_cast<const T*>(field) + start;
+        if (LAST ? readable : full) {
+            if constexpr (LAST) {
+                typedef typename VecOf<T, 8>::type V8;
+#pragma unroll
+                for (int k = 0; k < 16; k += 8)
+                    *reinterpret_cast<V8*>(z.v + k) = *reinterpret_cast<const V8*>(from(f, at + q * step) + k);
+            } else {
+                typedef typename VecOf<T, NT>::type VN;
+#pragma unroll
+                for (int i = 0; i < 16; i += NT) {
+                    const int r = chunk_row<LAST, NT>(q, i);
+                    *reinterpret_cast<VN*>(z.v + i) = *reinterpret_cast<const VN*>(
+                        from(f, r < channels ? at + r * step : (uint32_t)first * (uint32_t)sizeof(T)));
+                }
+            }
+            if (part < 32) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    z.v[i] = chunk_row<LAST, NT>(q, i) < channels ? z.v[i] : (T)0.0f;
+            }
+        } else {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z.v[i] = buffer_load<T>(rs, place(q, i));
         }
     }
 
@@ -424,5 +465,26 @@ struct ProductArgs {
 hipError_t launch_product_f32(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
 hipError_t launch_product_bf16(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
 hipError_t launch_product_f16(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
+
+// ---- the backward pass in one kernel (fno_channels_bwd.hpp) --------------------------
+struct BackwardArgs {
+    const void *x, *w;
+    const float* bias;
+    const void *branch, *grad;     // branch only where it is inside the activation
+    void *grad_x, *grad_branch;    // null where not asked for
+    float* part;                   // [groups][Cout Cin + Cout]: sums of g x and of g; null where not asked for
+    int64_t B, P;
+    int Cin, Cout, act;
+    bool merged;
+    int tiles_item, groups;
+    int64_t tiles;
+};
+// Up to 64 channels on one side and 128 on the other.
+inline bool backward_fits(int Cin, int Cout) { return std::max(Cin, Cout) <= 128 && std::min(Cin, Cout) <= 64; }
+hipError_t launch_backward_f32(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
+hipError_t launch_backward_bf16(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
+hipError_t launch_backward_bf16_f32(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
+hipError_t launch_backward_f16(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
+hipError_t launch_backward_f16_f32(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
 
 }  // namespace fno

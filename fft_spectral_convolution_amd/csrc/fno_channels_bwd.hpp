@@ -1,0 +1,308 @@
+// Backward pass of a channel product, everything in one pass over x and grad_out:
+//   z = W x + bias (+ branch),  g = grad_out act'(z),
+//   grad_x = W^T g,  grad_W += g x^T,  grad_bias += g.
+//
+// A wave takes 32 positions at a time and all channels.  The result of a product
+// (fno_channels.hpp) has positions in lanes and 16 channels in a lane's
+// registers, which is an operand again: two steps of 8 of them, channel
+// 16 (lane / 32) + 8 s + i in step s.  x is loaded in the same order, so z's operands,
+// g's for W^T g and both transposes share it.  grad_W sums over positions, so its
+// operands have channels in lanes: they are turned by products with the
+// identity, exactly, part by part, without a byte of LDS; the turned
+// positions come in an order that is the same for g and x.  Sums of grad_W stay in
+// registers over all of a wave's tiles; then those of a workgroup's waves are
+// joined in LDS and the workgroups' by k_weight_sum, in a fixed order.
+//
+// g of a 16-bit field is two bfloat16 parts (2^-18 of it is lost, against 2^-9
+// for one), x and W of float16 two each, which hold them exactly.
+//
+// Included by one source file for each pair of types, so that they build side by side.
+#pragma once
+
+#include "fno_channels.hpp"
+
+namespace fno {
+namespace {
+
+// Parts of x and W, of g, and which products of them are formed: for z, for the gradients.
+template <typename T>
+struct Scheme;
+template <>
+struct Scheme<float> {
+    static constexpr int x = 3, g = 3, z_most = 2, most = 2;
+};
+template <>
+struct Scheme<bf16> {
+    static constexpr int x = 1, g = 2, z_most = 0, most = 1;
+};
+template <>
+struct Scheme<f16> {
+    static constexpr int x = 2, g = 2, z_most = 2, most = 1;
+};
+
+// Step s (of two) of the operand of 16 values.
+template <int N, typename T>
+__device__ __forceinline__ Frag<bf16x8, N> step_of(const T* v, int s) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)v[8 * s + i];
+    return split<bf16x8, N>(f);
+}
+
+// A 32 x 32 part of an operand, turned: lanes hold what was its steps' k.
+template <int N>
+__device__ __forceinline__ void turned(const Frag<bf16x8, N> (&a)[2], const bf16x8 (&one)[2], Frag<bf16x8, N> (&out)[2],
+                                       float* sum) {
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        f32x16 d;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) d[r] = 0.0f;
+        d = mfma(a[0].part[p], one[0], d);
+        d = mfma(a[1].part[p], one[1], d);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            out[r >> 3].part[p][r & 7] = d[r];
+            if (sum) *sum += d[r];
+        }
+    }
+}
+
+template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
+__global__ __launch_bounds__(256, MO * MI <= 4 ? 2 : 1) void k_channels_bwd(BackwardArgs a) {
+    typedef Scheme<T> S;
+    typedef Frag<bf16x8, S::x> FX;
+    typedef Frag<bf16x8, S::g> FG;
+    extern __shared__ __align__(16) unsigned char lds[];
+    bf16x8* wz = reinterpret_cast<bf16x8*>(lds);             // [part][mo][mi][step][64]: rows o, steps over i
+    bf16x8* wx = wz + S::x * MO * MI * 128;                  // [part][mi][mo][step][64]: rows i, steps over o
+    float* bias = reinterpret_cast<float*>(wx + S::x * MO * MI * 128);
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    unsigned char* const turn = reinterpret_cast<unsigned char*>(bias + 32 * MO) + (threadIdx.x >> 6) * kTurnBytes;
+
+    const T* w = static_cast<const T*>(a.w);
+    for (int q = threadIdx.x; q < MO * MI * 128; q += 256) {
+        const int l = q & 63, s = (q >> 6) & 1, mi = (q >> 7) % MI, mo = (q >> 7) / MI;
+        const int row = row_channel(l & 31), k = 16 * (l >> 5) + 8 * s;
+        float v[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int o = 32 * mo + row, ci = 32 * mi + k + i;
+            v[i] = o < a.Cout && ci < a.Cin ? (float)w[(int64_t)o * a.Cin + ci] : 0.0f;
+            const int o2 = 32 * mo + k + i, ci2 = 32 * mi + row;
+            u[i] = o2 < a.Cout && ci2 < a.Cin ? (float)w[(int64_t)o2 * a.Cin + ci2] : 0.0f;
+        }
+        const FX f = split<bf16x8, S::x>(v), g = split<bf16x8, S::x>(u);
+#pragma unroll
+        for (int p = 0; p < S::x; ++p) {
+            wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + l] = f.part[p];
+            wx[(((p * MI + mi) * MO + mo) * 2 + s) * 64 + l] = g.part[p];
+        }
+    }
+    for (int i = threadIdx.x; i < 32 * MO; i += 256) bias[i] = a.bias && i < a.Cout ? a.bias[i] : 0.0f;
+    __syncthreads();
+
+    bf16x8 one[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) one[s][i] = (lane & 31) == 16 * h + 8 * s + i ? 1.0f : 0.0f;
+
+    f32x16 dw[MO][MI];
+    float db[MO];
+#pragma unroll
+    for (int mo = 0; mo < MO; ++mo) {
+        db[mo] = 0.0f;
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dw[mo][mi][r] = 0.0f;
+    }
+    auto tile_at = [&](int64_t t) {
+        Tile q;
+        q.item = a.merged ? 0 : t / a.tiles_item;
+        q.p0 = (a.merged ? t : t % a.tiles_item) * 32;
+        q.pn = 1;
+        q.pj = 0;
+        q.full = q.p0 + 32 <= a.P;
+        return q;
+    };
+    auto fetch_x = [&](Values<T> (&raw)[MI], const Tile& t) {
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+            if (32 * mi < a.Cin) {
+                Places<T, LAST, 1>(t, a.Cin, a.P, a.B, 32 * mi).fetch(a.x, 0, raw[mi]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) raw[mi].v[i] = (T)0.0f;
+            }
+        }
+    };
+
+    const int64_t stride = (int64_t)a.groups * 4;
+    int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    Values<T> raw[MI];
+    if (t < a.tiles) fetch_x(raw, tile_at(t));
+    for (; t < a.tiles; t += stride) {
+        const Tile tile = tile_at(t);
+        Values<TG> go[MO];
+#pragma unroll
+        for (int mo = 0; mo < MO; ++mo)
+            if (32 * mo < a.Cout) Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, 32 * mo).fetch(a.grad, 0, go[mo]);
+        FX x[MI][2], xt[MI][2];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) x[mi][s] = step_of<S::x>(raw[mi].v, s);
+        if (t + stride < a.tiles) fetch_x(raw, tile_at(t + stride));
+
+        f32x16 z[MO];
+        if (a.act != kActNone) {
+#pragma unroll
+            for (int mo = 0; mo < MO; ++mo) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) z[mo][r] = bias[32 * mo + 16 * h + r];
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        FX f;
+#pragma unroll
+                        for (int p = 0; p < S::x; ++p) f.part[p] = wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + lane];
+                        z[mo] = mfma_upto<S::z_most>(f, x[mi][s], z[mo]);
+                    }
+            }
+        }
+        if (a.part) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) turned(x[mi], one, xt[mi], nullptr);
+        }
+        f32x16 dx[MI];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dx[mi][r] = 0.0f;
+#pragma unroll
+        for (int mo = 0; mo < MO; ++mo) {
+            int c = 32 * mo;
+            if (c >= a.Cout) break;
+            asm volatile("" : "+s"(c));
+            float g[16];
+            if (a.act != kActNone) {
+                const Places<TG, OUT_LAST, 1> at(tile, a.Cout, a.P, a.B, c);
+                if (a.branch) {
+                    Values<TG> u;
+                    at.fetch(a.branch, 0, u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[mo][i] += (float)u.v[i];
+                }
+                if (a.act == kActGelu) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) g[i] = act_slope<kActGelu>(z[mo][i]) * (float)go[mo].v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) g[i] = act_slope<kActSilu>(z[mo][i]) * (float)go[mo].v[i];
+                }
+                if (a.grad_branch) at.store(a.grad_branch, 0, g, turn);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] = (float)go[mo].v[i];
+            }
+            FG gs[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) gs[s] = step_of<S::g>(g, s);
+            if (a.grad_x) {
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        FX f;
+#pragma unroll
+                        for (int p = 0; p < S::x; ++p) f.part[p] = wx[(((p * MI + mi) * MO + mo) * 2 + s) * 64 + lane];
+                        dx[mi] = mfma_upto<S::most>(f, gs[s], dx[mi]);
+                    }
+            }
+            if (a.part) {
+                FG gt[2];
+                turned(gs, one, gt, &db[mo]);
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) dw[mo][mi] = mfma_upto<S::most>(gt[s], xt[mi][s], dw[mo][mi]);
+            }
+        }
+        if (a.grad_x) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                int c = 32 * mi;
+                if (c >= a.Cin) break;
+                asm volatile("" : "+s"(c));
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = dx[mi][i];
+                Places<T, LAST, 1>(tile, a.Cin, a.P, a.B, c).store(a.grad_x, 0, v, turn);
+            }
+        }
+    }
+
+    if (!a.part) return;
+    // the waves' sums, one after the other (the weights in LDS are no longer needed)
+    float* join = reinterpret_cast<float*>(lds);             // [mo][mi][16][64]
+    float* sums = bias;                                      // [32 MO]
+    for (int k = 0; k < 4; ++k) {
+        __syncthreads();
+        if (wave != k) continue;
+#pragma unroll
+        for (int mo = 0; mo < MO; ++mo) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float* q = join + ((mo * MI + mi) * 16 + r) * 64 + lane;
+                    *q = k ? *q + dw[mo][mi][r] : dw[mo][mi][r];
+                }
+            const float s = swap_add<32>(db[mo]);
+            if (h == 0) sums[32 * mo + lane] = k ? sums[32 * mo + lane] + s : s;
+        }
+    }
+    __syncthreads();
+    float* part = a.part + (int64_t)blockIdx.x * (a.Cin + 1) * a.Cout;
+    for (int q = threadIdx.x; q < MO * MI * 1024; q += 256) {
+        const int l = q & 63, r = (q >> 6) & 15, mi = (q >> 10) % MI, mo = (q >> 10) / MI;
+        const int o = 32 * mo + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), i = 32 * mi + (l & 31);
+        if (o < a.Cout && i < a.Cin) part[(int64_t)o * a.Cin + i] = join[q];
+    }
+    for (int o = threadIdx.x; o < a.Cout; o += 256) part[(int64_t)a.Cin * a.Cout + o] = sums[o];
+}
+
+template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
+hipError_t launch_backward_tiles(BackwardArgs a, hipStream_t s) {
+    const size_t lds = (size_t)2 * Scheme<T>::x * MO * MI * 2048 + 32 * MO * sizeof(float) +
+                       (LAST || OUT_LAST ? 4 * kTurnBytes : 0);
+    return launch_kernel(k_channels_bwd<T, TG, LAST, OUT_LAST, MO, MI>, dim3((unsigned)a.groups), dim3(256), lds, s, a);
+}
+
+template <typename T, typename TG, bool LAST, bool OUT_LAST>
+hipError_t launch_backward_couts(const BackwardArgs& a, hipStream_t s) {
+    if (a.Cin <= 32 && a.Cout <= 32) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 1, 1>(a, s);
+    if (a.Cin <= 64 && a.Cout <= 64) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 2, 2>(a, s);
+    if (a.Cin <= 64) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 4, 2>(a, s);
+    return launch_backward_tiles<T, TG, LAST, OUT_LAST, 2, 4>(a, s);
+}
+
+template <typename T, typename TG>
+hipError_t launch_backward(BackwardArgs a, bool last, bool out_last, hipStream_t s) {
+    a.merged = last && out_last;
+    if (a.merged) {
+        a.P *= a.B;
+        a.B = 1;
+    }
+    a.tiles_item = (int)((a.P + 31) / 32);
+    a.tiles = a.B * a.tiles_item;
+    if (last) return out_last ? launch_backward_couts<T, TG, true, true>(a, s) : launch_backward_couts<T, TG, true, false>(a, s);
+    return out_last ? launch_backward_couts<T, TG, false, true>(a, s) : launch_backward_couts<T, TG, false, false>(a, s);
+}
+
+}  // namespace
+}  // namespace fno

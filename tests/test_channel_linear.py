@@ -121,8 +121,13 @@ class Case:
         n, cout = g.shape
         half = HALF_STEP[self.types[0]]
         want = g @ W
-        # a 16-bit field's g is multiplied in two parts: 2^-17 of it where its parts are bfloat16
-        parts = 2.0 ** -17 if self.types[0] != F32 and self.act != "none" else 0.0
+        # g of a 16-bit field is two bfloat16 parts.  Each is the nearest with 8 bits of fraction to what is left:
+        # |g - hi| <= 2^-9 |g|, |g - hi - lo| <= 2^-9 2^-9 |g| = 2^-18 |g|.  Of float16 factors, two parts as well
+        # (f = f1 + f2, |f2| <= 2^-9 |f|), the product lo f2 is left out: another 2^-18.  A 16-bit
+        # grad_out without an activation in between is held exactly by its two parts (8 or 11 bits).
+        parts = 2.0 ** -17 if self.types[0] != F32 and (self.act != "none" or self.types[1] == F32) else 0.0
+        if self.types == (F16, F16):
+            parts = 2.0 ** -17
         bound = g_bound @ W.abs() + ((cout + 8) * EPS + parts) * (g.abs() @ W.abs())
         bound = bound * 1.01 + half * want.abs() * 1.01 + (2.0 ** -24 if self.types[0] == F16 else 0)
         close(points(gx, self.last), want, bound, "grad_x")
