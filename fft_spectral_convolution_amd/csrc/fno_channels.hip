@@ -152,10 +152,10 @@ bool keeps_g(const ChannelProduct& c) { return c.act != kActNone; }
 
 bool fits(const ChannelProduct& c) { return backward_fits(c.Cin, c.Cout); }
 
-// Workgroups of the one-kernel backward pass: two a CU, one where 128 channels fill its registers.
+// Workgroups of the one-kernel backward pass: one a CU, two where 32 channels leave room for them.
 int backward_groups(const ChannelProduct& c) {
     const int64_t tiles = c.x_last && c.out_last ? (c.B * c.P + 31) / 32 : c.B * ((c.P + 31) / 32);
-    return (int)std::min<int64_t>((tiles + 3) / 4, std::max(c.Cin, c.Cout) <= 64 ? 512 : 256);
+    return (int)std::min<int64_t>((tiles + 3) / 4, std::max(c.Cin, c.Cout) <= 32 ? 512 : 256);
 }
 
 hipError_t launch_backward(const BackwardArgs& a, const ChannelProduct& c, hipStream_t s) {
@@ -224,7 +224,7 @@ hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool b
         b.x = a.x;
         b.w = a.w;
         b.bias = a.bias;
-        b.branch = c.branch_after ? nullptr : a.branch;
+        b.branch = c.branch_after || c.act == kActNone ? nullptr : a.branch;
         b.grad = a.out;
         b.grad_x = a.grad_x;
         b.grad_branch = a.grad_branch;

@@ -69,7 +69,7 @@ __device__ __forceinline__ void turned(const Frag<bf16x8, N> (&a)[2], const bf16
 }
 
 template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
-__global__ __launch_bounds__(256, MO * MI <= 4 ? 2 : 1) void k_channels_bwd(BackwardArgs a) {
+__global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(BackwardArgs a) {
     typedef Scheme<T> S;
     typedef Frag<bf16x8, S::x> FX;
     typedef Frag<bf16x8, S::g> FG;
@@ -140,22 +140,32 @@ __global__ __launch_bounds__(256, MO * MI <= 4 ? 2 : 1) void k_channels_bwd(Back
         }
     };
 
+    // Of each field the next tile's values are on their way from the moment that this tile's are used.
     const int64_t stride = (int64_t)a.groups * 4;
     int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= a.tiles) t = a.tiles;
     Values<T> raw[MI];
-    if (t < a.tiles) fetch_x(raw, tile_at(t));
-    for (; t < a.tiles; t += stride) {
-        const Tile tile = tile_at(t);
-        Values<TG> go[MO];
+    Values<TG> go[MO], br[MO];
+    Tile tile = tile_at(min(t, a.tiles - 1));
+    if (t < a.tiles) {
+        fetch_x(raw, tile);
 #pragma unroll
         for (int mo = 0; mo < MO; ++mo)
-            if (32 * mo < a.Cout) Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, 32 * mo).fetch(a.grad, 0, go[mo]);
+            if (32 * mo < a.Cout) {
+                const Places<TG, OUT_LAST, 1> at(tile, a.Cout, a.P, a.B, 32 * mo);
+                at.fetch(a.grad, 0, go[mo]);
+                if (a.branch) at.fetch(a.branch, 0, br[mo]);
+            }
+    }
+    for (; t < a.tiles; t += stride) {
+        const bool more = t + stride < a.tiles;
+        const Tile next = tile_at(min(t + stride, a.tiles - 1));
         FX x[MI][2], xt[MI][2];
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
             for (int s = 0; s < 2; ++s) x[mi][s] = step_of<S::x>(raw[mi].v, s);
-        if (t + stride < a.tiles) fetch_x(raw, tile_at(t + stride));
+        if (more) fetch_x(raw, next);
 
         f32x16 z[MO];
         if (a.act != kActNone) {
@@ -189,25 +199,27 @@ __global__ __launch_bounds__(256, MO * MI <= 4 ? 2 : 1) void k_channels_bwd(Back
             if (c >= a.Cout) break;
             asm volatile("" : "+s"(c));
             float g[16];
-            if (a.act != kActNone) {
-                const Places<TG, OUT_LAST, 1> at(tile, a.Cout, a.P, a.B, c);
-                if (a.branch) {
-                    Values<TG> u;
-                    at.fetch(a.branch, 0, u);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[mo][i] += (float)u.v[i];
+            for (int i = 0; i < 16; ++i) g[i] = (float)go[mo].v[i];
+            if (a.act != kActNone) {
+                if (a.branch) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[mo][i] += (float)br[mo].v[i];
                 }
                 if (a.act == kActGelu) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) g[i] = act_slope<kActGelu>(z[mo][i]) * (float)go[mo].v[i];
+                    for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActGelu>(z[mo][i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) g[i] = act_slope<kActSilu>(z[mo][i]) * (float)go[mo].v[i];
+                    for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActSilu>(z[mo][i]);
                 }
-                if (a.grad_branch) at.store(a.grad_branch, 0, g, turn);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) g[i] = (float)go[mo].v[i];
+                if (a.grad_branch)
+                    Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, c).store(a.grad_branch, 0, g, turn);
+            }
+            if (more) {
+                const Places<TG, OUT_LAST, 1> at(next, a.Cout, a.P, a.B, c);
+                at.fetch(a.grad, 0, go[mo]);
+                if (a.branch) at.fetch(a.branch, 0, br[mo]);
             }
             FG gs[2];
 #pragma unroll
@@ -244,6 +256,7 @@ __global__ __launch_bounds__(256, MO * MI <= 4 ? 2 : 1) void k_channels_bwd(Back
                 Places<T, LAST, 1>(tile, a.Cin, a.P, a.B, c).store(a.grad_x, 0, v, turn);
             }
         }
+        tile = next;
     }
 
     if (!a.part) return;
