@@ -771,33 +771,64 @@ def fno_group_norm_backward(x, stats, grad_out, groups: int, weight=None, bias=N
     return gx, gw, gb
 
 
-_dtype_of = operator.attrgetter("dtype")
+_lists = None
+
+
+def _reader():
+    """The reader of tensor lists (csrc/fno_lists.cpp)."""
+    global _lists
+    if _lists is None:
+        with _lock:
+            path = os.path.join(_HERE, "_fno_lists.so")
+            if not os.path.exists(path):
+                raise ImportError(f"{path} is missing: build it first (python -m fft_spectral_convolution_amd.build)")
+            handle = ctypes.PyDLL(path)            # holds the interpreter's lock: it looks into Python objects
+            handle.fno_read_tensors.argtypes = [ctypes.py_object, _I, _I, _P, _P, _P, _P, _P]
+            handle.fno_read_tensors.restype = _I
+            handle.fno_read_moments.argtypes = [ctypes.c_longlong, _P, _P, _P, _P, _P]
+            handle.fno_read_moments.restype = ctypes.c_longlong
+            _lists = handle
+    return _lists
+
+
+def _address(column):
+    return column.buffer_info()[0]
+
+
+_FLOATS, _HALVES, _MOMENTS = 0b1111, 0b110, 0b11001       # sets of type codes: bit 4 is uint8
+
+
+def _read_tensors(torch, tensors, name, types=_FLOATS, optional=False):
+    """Host arrays (addresses, element counts, type codes) of a list of tensors, and their device (None for no
+    tensor).  A model has hundreds of tensors: they are read in C++."""
+    tensors = list(tensors)
+    n = len(tensors)
+    ptrs, numels, codes = array.array("Q", bytes(8 * n)), array.array("q", bytes(8 * n)), array.array("i", bytes(4 * n))
+    found = array.array("q", (0, 0))              # the device (the lower 32 bits), the entry that is refused
+    at = _address(found)
+    problem = _reader().fno_read_tensors(tensors, types, optional, _address(ptrs), _address(numels), _address(codes),
+                                         at, at + 8)
+    if problem:
+        t = tensors[found[1]]
+        if problem == 1:
+            raise TypeError(f"{name} must be torch tensors")
+        if problem == 2:
+            raise ValueError(f"{name} must live on one GPU device")
+        if problem == 3:
+            kinds = {_FLOATS: "float32, bfloat16, float16 or complex64", _HALVES: "bfloat16 or float16",
+                     _MOMENTS: "float32 or the uint8 tensors of fno_adamw_states"}[types]
+            raise TypeError(f"{name} must be {kinds}, got {t.dtype}")
+        if problem == 4:
+            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} must not be lazily conjugated or negated (call resolve_conj() and resolve_neg())")
+    index = found[0] & 0xffffffff
+    return tensors, ptrs, numels, codes, None if index == 0xffffffff else torch.device("cuda", index)
 
 
 def _tensor_table(torch, tensors, name):
-    """Host arrays (addresses, element counts, types) of a list of tensors, and their device.  One attribute of
-    all tensors at a time, by map: a model has hundreds of gradients, and this is most of a call's host time."""
-    tensors = list(tensors)
-    if not tensors:
-        return tensors, array.array("Q"), array.array("q"), array.array("i"), \
-            torch.device("cuda", torch.cuda.current_device())
-    tensor = torch.Tensor
-    try:
-        devices = set(map(tensor.get_device, tensors))
-    except TypeError:
-        raise TypeError(f"{name} must be torch tensors") from None
-    if len(devices) > 1 or min(devices) < 0:
-        raise ValueError(f"{name} must live on one GPU device")
-    try:
-        types = array.array("i", map(_element_types().__getitem__, map(_dtype_of, tensors)))
-    except KeyError as e:
-        raise TypeError(f"{name} must be float32, bfloat16, float16 or complex64, got {e.args[0]}") from None
-    if not all(map(tensor.is_contiguous, tensors)):
-        raise ValueError(f"{name} must be contiguous")
-    if 3 in types and any(map(tensor.is_conj, tensors)):
-        raise ValueError(f"{name} must not be lazily conjugated (call resolve_conj())")
-    return (tensors, array.array("Q", map(tensor.data_ptr, tensors)), array.array("q", map(tensor.numel, tensors)),
-            types, tensors[0].device)
+    """_read_tensors of gradients or parameters; without any, the device is the current one."""
+    tensors, ptrs, numels, types, device = _read_tensors(torch, tensors, name)
+    return tensors, ptrs, numels, types, device or torch.device("cuda", torch.cuda.current_device())
 
 
 def _norm_scalar(torch, norm, device, name):
@@ -968,48 +999,22 @@ def fno_channel_linear_backward(x, weight, grad_out, bias=None, branch=None, bra
     return gx, gw, gb, gr
 
 
-def _same_shapes(tensors, like, name, what):
-    if len(tensors) != len(like) or not all([a.shape == b.shape for a, b in zip(tensors, like)]):
-        raise ValueError(f"{name} must hold a tensor of each {what} shape")
-
-
-def _moment_floats(numels, types):
-    return array.array("q", [2 * n if t == 3 else n for n, t in zip(numels, types)]) if 3 in types else numels
-
-
 def _moment_bytes(n):
     blocks = -(-n // 128)
     return -(-129 * blocks // 16) * 16
 
 
-def _moment_table(torch, moments, name, device, floats=None):
-    """Addresses and bits of a list of moments: float32 (or complex64, two values each) or the bytes of 8-bit ones."""
-    moments = list(moments)
-    tensor = torch.Tensor
-    try:
-        devices = set(map(tensor.get_device, moments))
-    except TypeError:
-        raise TypeError(f"{name} must be torch tensors") from None
-    if moments and devices != {device.index}:
+def _moment_table(torch, moments, name, device, numels, types):
+    """Addresses and bits of the moments of parameters: float32 (or complex64, two values each) or the bytes of 8-bit
+    ones."""
+    moments, ptrs, sizes, kinds, on = _read_tensors(torch, moments, name, _MOMENTS)
+    if on is not None and on != device:
         raise ValueError(f"{name} must be on {device}")
-    wide = {torch.float32: 1, torch.complex64: 2}
-    dtypes = list(map(_dtype_of, moments))
-    if not set(dtypes) <= {torch.uint8, *wide}:
-        raise TypeError(f"{name} must be float32 or the uint8 tensors of fno_adamw_states")
-    if not all(map(tensor.is_contiguous, moments)):
-        raise ValueError(f"{name} must be contiguous")
-    if floats is not None:
-        sizes = list(map(tensor.numel, moments))
-        if len(sizes) != len(floats) or not all([
-                s == _moment_bytes(n) if d not in wide else wide[d] * s == n
-                for s, n, d in zip(sizes, floats, dtypes)]):
-            raise ValueError(f"{name} must hold a moment of each parameter's size")
-    bits = array.array("i", [8 if d not in wide else 32 for d in dtypes])
-    return moments, array.array("Q", map(tensor.data_ptr, moments)), bits
-
-
-def _address(column):
-    return column.buffer_info()[0]
+    bits = array.array("i", bytes(4 * len(moments)))
+    if len(moments) != len(numels) or _reader().fno_read_moments(
+            len(moments), _address(numels), _address(types), _address(sizes), _address(kinds), _address(bits)) >= 0:
+        raise ValueError(f"{name} must hold a moment of each parameter's size")
+    return moments, ptrs, bits
 
 
 def fno_adamw_states(params, bits: int = 32):
@@ -1019,21 +1024,20 @@ def fno_adamw_states(params, bits: int = 32):
     if bits not in (8, 32):
         raise ValueError(f"bits must be 8 or 32, got {bits!r}")
     params, _, numels, types, device = _tensor_table(torch, params, "params")
-    floats = _moment_floats(numels, types)
 
-    def one(p, n):
+    def one(p, n, t):
         if bits == 8:
-            return torch.zeros(_moment_bytes(n), dtype=torch.uint8, device=device)
-        return torch.zeros((*p.shape, 2) if p.is_complex() else p.shape, dtype=torch.float32, device=device)
+            return torch.zeros(_moment_bytes(2 * n if t == 3 else n), dtype=torch.uint8, device=device)
+        return torch.zeros((*p.shape, 2) if t == 3 else p.shape, dtype=torch.float32, device=device)
 
-    return [one(p, n) for p, n in zip(params, floats)], [one(p, n) for p, n in zip(params, floats)]
+    return tuple([one(*q) for q in zip(params, numels, types)] for _ in range(2))
 
 
 def fno_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
               weight_decay: float = 1e-2, norm=None, max_norm=None, copies=None, seed: int = 0, out=None) -> None:
     """One AdamW step (decoupled weight decay) over lists of tensors, in one kernel for every 48 of them.
 
-    params are float32, bfloat16, float16 or complex64, mixed; grads have their shapes, of any of the
+    params are float32, bfloat16, float16 or complex64, mixed; grads have their sizes, of any of the
     real types (complex64 where the parameter is).  exp_avgs, exp_avg_sqs are what fno_adamw_states
     returned: float32, or uint8 moments of 8 bits, rounded up or down by chance drawn from `seed`, `step`
     and the value's place; a parameter's two are of the same kind.  step counts from 1; step and lr may be
@@ -1043,43 +1047,37 @@ def fno_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0
     None) that receives its new values.  In place, or into out = (params, exp_avgs, exp_avg_sqs)."""
     torch = _torch()
     params, p_ptrs, numels, types, device = _tensor_table(torch, params, "params")
-    grads, g_ptrs, _, g_types, g_device = _tensor_table(torch, grads, "grads")
-    _same_shapes(grads, params, "grads", "parameter's")
+    grads, g_ptrs, g_numels, g_types, g_device = _tensor_table(torch, grads, "grads")
+    if g_numels != numels:
+        raise ValueError("grads must hold a tensor of each parameter's size")
     if g_device != device:
         raise ValueError(f"grads must be on {device}")
-    if [t == 3 for t in g_types] != [t == 3 for t in types]:
+    if g_types != types and [t == 3 for t in g_types] != [t == 3 for t in types]:
         raise TypeError("grads must be complex where the parameters are")
-    floats = _moment_floats(numels, types)
-    exp_avgs, m_ptrs, bits = _moment_table(torch, exp_avgs, "exp_avgs", device, floats)
-    exp_avg_sqs, v_ptrs, v_bits = _moment_table(torch, exp_avg_sqs, "exp_avg_sqs", device, floats)
+    exp_avgs, m_ptrs, bits = _moment_table(torch, exp_avgs, "exp_avgs", device, numels, types)
+    exp_avg_sqs, v_ptrs, v_bits = _moment_table(torch, exp_avg_sqs, "exp_avg_sqs", device, numels, types)
     if v_bits != bits:
         raise TypeError("a parameter's exp_avg and exp_avg_sq must be of the same kind")
     po, mo, vo = p_ptrs, m_ptrs, v_ptrs
     if out is not None:
         out_params, out_avgs, out_sqs = out
-        out_params, po, _, o_types, o_device = _tensor_table(torch, out_params, "out")
-        _same_shapes(out_params, params, "out", "parameter's")
+        out_params, po, o_numels, o_types, o_device = _tensor_table(torch, out_params, "out")
+        if o_numels != numels:
+            raise ValueError("out must hold a tensor of each parameter's size")
         if o_types != types or o_device != device:
             raise TypeError(f"out must have the parameters' types, on {device}")
-        out_avgs, mo, o_bits = _moment_table(torch, out_avgs, "out", device, floats)
-        out_sqs, vo, s_bits = _moment_table(torch, out_sqs, "out", device, floats)
+        out_avgs, mo, o_bits = _moment_table(torch, out_avgs, "out", device, numels, types)
+        out_sqs, vo, s_bits = _moment_table(torch, out_sqs, "out", device, numels, types)
         if o_bits != bits or s_bits != bits:
             raise TypeError("out must have the moments' kinds")
     c_ptrs = c_types = None
     if copies is not None:
-        copies = list(copies)
-        held = [c for c in copies if c is not None]
-        _, _, _, kinds, c_device = _tensor_table(torch, held, "copies")
-        if len(copies) != len(params) or any([c is not None and c.shape != p.shape for c, p in zip(copies, params)]):
-            raise ValueError("copies must hold None or a tensor of each parameter's shape")
-        if held and c_device != device:
+        copies, c_ptrs, c_numels, c_types, c_device = _read_tensors(torch, copies, "copies", _HALVES, optional=True)
+        if len(copies) != len(params) or any([t >= 0 and c != n for t, c, n in zip(c_types, c_numels, numels)]):
+            raise ValueError("copies must hold None or a tensor of each parameter's size")
+        if c_device is not None and c_device != device:
             raise ValueError(f"copies must be on {device}")
-        if not set(kinds) <= {1, 2}:
-            raise TypeError("copies must be bfloat16 or float16")
-        kinds = iter(kinds)
-        c_types = array.array("i", [0 if c is None else next(kinds) for c in copies])
-        c_ptrs = array.array("Q", [0 if c is None else c.data_ptr() for c in copies])
-        if any([t == 3 and c is not None for t, c in zip(types, copies)]):
+        if 3 in types and any([t == 3 and c >= 0 for t, c in zip(types, c_types)]):
             raise TypeError("a complex parameter has no 16-bit copy")
     if (norm is None) != (max_norm is None):
         raise ValueError("give norm and max_norm, or neither")
@@ -1120,16 +1118,17 @@ def fno_adamw_moments(exp_avgs, exp_avg_sqs, numels=None, out=None):
     if out is None:
         numels = list(numels)
         out = tuple([torch.empty(n, dtype=torch.float32, device=device) for n in numels] for _ in range(2))
-    out_avgs, mo, _, types, o_device = _tensor_table(torch, out[0], "out")
-    out_sqs, vo, floats, s_types, s_device = _tensor_table(torch, out[1], "out")
-    _same_shapes(out_sqs, out_avgs, "out", "first moment's")
+    out_avgs, mo, numels, types, o_device = _tensor_table(torch, out[0], "out")
+    out_sqs, vo, s_numels, s_types, s_device = _tensor_table(torch, out[1], "out")
+    if s_numels != numels:
+        raise ValueError("out must hold vectors of the same size for both moments")
     if set(types) | set(s_types) != {0} or o_device != device or s_device != device:
         raise TypeError(f"out must be float32 tensors on {device}")
-    exp_avgs, m_ptrs, bits = _moment_table(torch, exp_avgs, "exp_avgs", device, floats)
-    exp_avg_sqs, v_ptrs, v_bits = _moment_table(torch, exp_avg_sqs, "exp_avg_sqs", device, floats)
-    if set(bits) | set(v_bits) != {8}:
+    exp_avgs, m_ptrs, bits = _moment_table(torch, exp_avgs, "exp_avgs", device, numels, types)
+    exp_avg_sqs, v_ptrs, v_bits = _moment_table(torch, exp_avg_sqs, "exp_avg_sqs", device, numels, types)
+    if 32 in bits or 32 in v_bits:
         raise TypeError("moments must be the uint8 tensors of fno_adamw_states")
-    _enqueue(torch, device, "fno_adamw_moments", *map(_address, (m_ptrs, v_ptrs, mo, vo, floats)), len(floats))
+    _enqueue(torch, device, "fno_adamw_moments", *map(_address, (m_ptrs, v_ptrs, mo, vo, numels)), len(numels))
     return out
 
 

@@ -13,8 +13,10 @@
 // registers over all of a wave's tiles; then those of a workgroup's waves are
 // joined in LDS and the workgroups' by k_weight_sum, in a fixed order.
 //
-// g of a 16-bit field is two bfloat16 parts (2^-18 of it is lost, against 2^-9
-// for one), x and W of float16 two each, which hold them exactly.
+// g of a 16-bit field is three bfloat16 parts as a float32 one's is: the parameters'
+// gradients are float32 sums, in which two parts would leave 2^-18 of every g.  grad_x,
+// rounded to 16 bits, takes two of them.  x and W of float16 are two parts each,
+// which hold them exactly.
 //
 // Included by one source file for each pair of types, so that they build side by side.
 #pragma once
@@ -24,20 +26,21 @@
 namespace fno {
 namespace {
 
-// Parts of x and W, of g, and which products of them are formed: for z, for the gradients.
+// Parts of x and W (those of g are three), and the products formed, i + j up to these: for z,
+// for grad_x (rounded to x's type), for grad_W.
 template <typename T>
 struct Scheme;
 template <>
 struct Scheme<float> {
-    static constexpr int x = 3, g = 3, z_most = 2, most = 2;
+    static constexpr int x = 3, z = 2, gx = 2, gw = 2;
 };
 template <>
 struct Scheme<bf16> {
-    static constexpr int x = 1, g = 2, z_most = 0, most = 1;
+    static constexpr int x = 1, z = 0, gx = 1, gw = 2;
 };
 template <>
 struct Scheme<f16> {
-    static constexpr int x = 2, g = 2, z_most = 2, most = 1;
+    static constexpr int x = 2, z = 2, gx = 1, gw = 2;
 };
 
 // Step s (of two) of the operand of 16 values.
@@ -72,7 +75,7 @@ template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
 __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(BackwardArgs a) {
     typedef Scheme<T> S;
     typedef Frag<bf16x8, S::x> FX;
-    typedef Frag<bf16x8, S::g> FG;
+    typedef Frag<bf16x8, 3> FG;
     extern __shared__ __align__(16) unsigned char lds[];
     bf16x8* wz = reinterpret_cast<bf16x8*>(lds);             // [part][mo][mi][step][64]: rows o, steps over i
     bf16x8* wx = wz + S::x * MO * MI * 128;                  // [part][mi][mo][step][64]: rows i, steps over o
@@ -180,7 +183,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
                         FX f;
 #pragma unroll
                         for (int p = 0; p < S::x; ++p) f.part[p] = wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + lane];
-                        z[mo] = mfma_upto<S::z_most>(f, x[mi][s], z[mo]);
+                        z[mo] = mfma_upto<S::z>(f, x[mi][s], z[mo]);
                     }
             }
         }
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
             }
             FG gs[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) gs[s] = step_of<S::g>(g, s);
+            for (int s = 0; s < 2; ++s) gs[s] = step_of<3>(g, s);
             if (a.grad_x) {
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi)
@@ -232,7 +235,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
                         FX f;
 #pragma unroll
                         for (int p = 0; p < S::x; ++p) f.part[p] = wx[(((p * MI + mi) * MO + mo) * 2 + s) * 64 + lane];
-                        dx[mi] = mfma_upto<S::most>(f, gs[s], dx[mi]);
+                        dx[mi] = mfma_upto<S::gx>(f, gs[s], dx[mi]);
                     }
             }
             if (a.part) {
@@ -241,7 +244,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) dw[mo][mi] = mfma_upto<S::most>(gt[s], xt[mi][s], dw[mo][mi]);
+                    for (int s = 0; s < 2; ++s) dw[mo][mi] = mfma_upto<S::gw>(gt[s], xt[mi][s], dw[mo][mi]);
             }
         }
         if (a.grad_x) {
