@@ -201,10 +201,19 @@ __device__ __forceinline__ constexpr int chunk_pos(int q, int i) { return LAST ?
 template <bool LAST, int NT>
 __device__ __forceinline__ constexpr int chunk_row(int q, int i) { return LAST ? i : 16 / NT * q + i / NT; }
 
-// A chunk's values as they lie in the field.
+// A chunk's values as they lie in the field.  Those of channels that do not
+// exist are made zero where they are used: earlier would wait for the load.
 template <typename T>
 struct Values {
     T v[16] __attribute__((aligned(16)));
+
+    // NT = 1: of the 16 channels of the lane's half of the part at c0
+    __device__ __forceinline__ void keep(int C, int c0) {
+        if (c0 + 32 <= C) return;
+        const int channels = C - c0 - 16 * (int)((threadIdx.x & 63) >> 5);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = i < channels ? v[i] : (T)0.0f;
+    }
 };
 
 // Bytes of LDS that a wave turns channels-last results in: 32 positions of 32
@@ -278,7 +287,7 @@ struct Places {
         }
     }
 
-    // As load, but as the field holds the values, and zeros for channels that do not exist.
+    // As load, but as the field holds the values.
     __device__ __forceinline__ void fetch(const void* field, int q, Values<T>& z) const {
         const T* f = static_cast<const T*>(field) + start;
         if (LAST ? readable : full) {
@@ -295,11 +304,6 @@ struct Places {
                     *reinterpret_cast<VN*>(z.v + i) = *reinterpret_cast<const VN*>(
                         from(f, r < channels ? at + r * step : (uint32_t)first * (uint32_t)sizeof(T)));
                 }
-            }
-            if (part < 32) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    z.v[i] = chunk_row<LAST, NT>(q, i) < channels ? z.v[i] : (T)0.0f;
             }
         } else {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(f, left);
@@ -360,10 +364,23 @@ struct Places {
 // ---- input tiles ------------------------------------------------------------------
 // 16 channels from k0 on of a tile's positions, as they are loaded: channels
 // first, NT positions of each of the lane's 8 channels; channels last, 8
-// channels of each of its NT positions.  Places outside the field are zero.
+// channels of each of its NT positions.  Channels that do not exist may hold
+// anything until keep() makes them zero, where they are used.
 template <typename T, bool LAST, int NT>
 struct Raw {
     T v[LAST ? NT : 8][LAST ? 8 : NT] __attribute__((aligned(16)));
+
+    __device__ __forceinline__ void keep(int C, int k0) {
+        if (k0 + 16 <= C) return;
+        const int more = C - k0 - 8 * (int)((threadIdx.x & 63) >> 5);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                T& q = v[LAST ? j : i][LAST ? i : j];
+                q = i < more ? q : (T)0.0f;
+            }
+    }
 };
 
 template <typename T, bool LAST, int NT>
@@ -382,12 +399,6 @@ __device__ __forceinline__ void load_raw(Raw<T, LAST, NT>& raw, const void* fiel
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 *reinterpret_cast<V8*>(raw.v[j]) = *reinterpret_cast<const V8*>(from(x, at + j * step));
-            if (k0 + 16 > C) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) raw.v[j][i] = i < more ? raw.v[j][i] : (T)0.0f;
-            }
         } else {
             const int64_t bytes = ((P - t.p0) * C - k0) * (int64_t)S;
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(x, (uint32_t)min(bytes, (int64_t)kOutside));
@@ -407,12 +418,9 @@ __device__ __forceinline__ void load_raw(Raw<T, LAST, NT>& raw, const void* fiel
                 *reinterpret_cast<VN*>(raw.v[i]) = *reinterpret_cast<const VN*>(from(x, at + i * step));
         } else if (t.full) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {      // channels that do not exist: channel k0, zeroed
+            for (int i = 0; i < 8; ++i)        // channels that do not exist: channel k0
                 *reinterpret_cast<VN*>(raw.v[i]) =
                     *reinterpret_cast<const VN*>(from(x, i < more ? at + i * step : (uint32_t)(n * t.pn) * S));
-#pragma unroll
-                for (int j = 0; j < NT; ++j) raw.v[i][j] = i < more ? raw.v[i][j] : (T)0.0f;
-            }
         } else {
             const int64_t bytes = ((C - k0) * P - t.p0) * (int64_t)S;
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(x, (uint32_t)min(bytes, (int64_t)kOutside));

@@ -143,35 +143,145 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
         }
     };
 
-    // Of each field the next tile's values are on their way from the moment that this tile's are used.
-    const int64_t stride = (int64_t)a.groups * 4;
-    int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    if (t >= a.tiles) t = a.tiles;
-    Values<T> raw[MI];
-    Values<TG> go[MO], br[MO];
-    Tile tile = tile_at(min(t, a.tiles - 1));
-    if (t < a.tiles) {
-        fetch_x(raw, tile);
+    if constexpr (MI <= 2) {
+        // Of each field the next tile's values are on their way from the moment that this tile's are used.
+        const int64_t stride = (int64_t)a.groups * 4;
+        int64_t t = (int64_t)blockIdx.x * 4 + wave;
+        if (t >= a.tiles) t = a.tiles;
+        Values<T> raw[MI];
+        Values<TG> go[MO], br[MO];
+        Tile tile = tile_at(min(t, a.tiles - 1));
+        if (t < a.tiles) {
+            fetch_x(raw, tile);
 #pragma unroll
-        for (int mo = 0; mo < MO; ++mo)
-            if (32 * mo < a.Cout) {
-                const Places<TG, OUT_LAST, 1> at(tile, a.Cout, a.P, a.B, 32 * mo);
-                at.fetch(a.grad, 0, go[mo]);
-                if (a.branch) at.fetch(a.branch, 0, br[mo]);
+            for (int mo = 0; mo < MO; ++mo)
+                if (32 * mo < a.Cout) {
+                    const Places<TG, OUT_LAST, 1> at(tile, a.Cout, a.P, a.B, 32 * mo);
+                    at.fetch(a.grad, 0, go[mo]);
+                    if (a.branch) at.fetch(a.branch, 0, br[mo]);
+                }
+        }
+        for (; t < a.tiles; t += stride) {
+            const bool more = t + stride < a.tiles;
+            const Tile next = tile_at(min(t + stride, a.tiles - 1));
+            FX x[MI][2], xt[MI][2];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                raw[mi].keep(a.Cin, 32 * mi);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) x[mi][s] = step_of<S::x>(raw[mi].v, s);
             }
-    }
-    for (; t < a.tiles; t += stride) {
-        const bool more = t + stride < a.tiles;
-        const Tile next = tile_at(min(t + stride, a.tiles - 1));
-        FX x[MI][2], xt[MI][2];
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) x[mi][s] = step_of<S::x>(raw[mi].v, s);
-        if (more) fetch_x(raw, next);
+            if (more) fetch_x(raw, next);
 
-        f32x16 z[MO];
-        if (a.act != kActNone) {
+            f32x16 z[MO];
+            if (a.act != kActNone) {
+#pragma unroll
+                for (int mo = 0; mo < MO; ++mo) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) z[mo][r] = bias[32 * mo + 16 * h + r];
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            FX f;
+#pragma unroll
+                            for (int p = 0; p < S::x; ++p) f.part[p] = wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + lane];
+                            z[mo] = mfma_upto<S::z>(f, x[mi][s], z[mo]);
+                        }
+                }
+            }
+            if (a.part) {
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) turned(x[mi], one, xt[mi], nullptr);
+            }
+            f32x16 dx[MI];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) dx[mi][r] = 0.0f;
+#pragma unroll
+            for (int mo = 0; mo < MO; ++mo) {
+                int c = 32 * mo;
+                if (c >= a.Cout) break;
+                asm volatile("" : "+s"(c));
+                float g[16];
+                go[mo].keep(a.Cout, c);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] = (float)go[mo].v[i];
+                if (a.act != kActNone) {
+                    if (a.branch) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) z[mo][i] += (float)br[mo].v[i];
+                    }
+                    if (a.act == kActGelu) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActGelu>(z[mo][i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActSilu>(z[mo][i]);
+                    }
+                    if (a.grad_branch)
+                        Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, c).store(a.grad_branch, 0, g, turn);
+                }
+                if (more) {
+                    const Places<TG, OUT_LAST, 1> at(next, a.Cout, a.P, a.B, c);
+                    at.fetch(a.grad, 0, go[mo]);
+                    if (a.branch) at.fetch(a.branch, 0, br[mo]);
+                }
+                FG gs[2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) gs[s] = step_of<3>(g, s);
+                if (a.grad_x) {
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            FX f;
+#pragma unroll
+                            for (int p = 0; p < S::x; ++p) f.part[p] = wx[(((p * MI + mi) * MO + mo) * 2 + s) * 64 + lane];
+                            dx[mi] = mfma_upto<S::gx>(f, gs[s], dx[mi]);
+                        }
+                }
+                if (a.part) {
+                    FG gt[2];
+                    turned(gs, one, gt, &db[mo]);
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) dw[mo][mi] = mfma_upto<S::gw>(gt[s], xt[mi][s], dw[mo][mi]);
+                }
+            }
+            if (a.grad_x) {
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    int c = 32 * mi;
+                    if (c >= a.Cin) break;
+                    asm volatile("" : "+s"(c));
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = dx[mi][i];
+                    Places<T, LAST, 1>(tile, a.Cin, a.P, a.B, c).store(a.grad_x, 0, v, turn);
+                }
+            }
+            tile = next;
+        }
+    } else {
+        auto fetch_g = [&](Values<TG>& go, Values<TG>& br, const Tile& t, int c) {
+            if (c >= a.Cout) return;
+            const Places<TG, OUT_LAST, 1> at(t, a.Cout, a.P, a.B, c);
+            at.fetch(a.grad, 0, go);
+            if (a.branch) at.fetch(a.branch, 0, br);
+        };
+        auto parts_of_x = [&](Values<T> (&raw)[MI], FX (&x)[MI][2]) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                raw[mi].keep(a.Cin, 32 * mi);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) x[mi][s] = step_of<S::x>(raw[mi].v, s);
+            }
+        };
+        auto form_z = [&](const FX (&x)[MI][2], f32x16 (&z)[MO]) {
+            if (a.act == kActNone) return;
 #pragma unroll
             for (int mo = 0; mo < MO; ++mo) {
 #pragma unroll
@@ -186,80 +296,112 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
                         z[mo] = mfma_upto<S::z>(f, x[mi][s], z[mo]);
                     }
             }
-        }
-        if (a.part) {
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) turned(x[mi], one, xt[mi], nullptr);
-        }
-        f32x16 dx[MI];
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) dx[mi][r] = 0.0f;
-#pragma unroll
-        for (int mo = 0; mo < MO; ++mo) {
-            int c = 32 * mo;
-            if (c >= a.Cout) break;
-            asm volatile("" : "+s"(c));
+        };
+        // g of the 32 output channels from c on, stored where it is asked for, and its parts
+        auto form_g = [&](const Tile& tile, int c, f32x16& z, Values<TG>& go, const Values<TG>& br, FG (&gs)[2]) {
             float g[16];
+            go.keep(a.Cout, c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = (float)go[mo].v[i];
+            for (int i = 0; i < 16; ++i) g[i] = (float)go.v[i];
             if (a.act != kActNone) {
                 if (a.branch) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[mo][i] += (float)br[mo].v[i];
+                    for (int i = 0; i < 16; ++i) z[i] += (float)br.v[i];
                 }
                 if (a.act == kActGelu) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActGelu>(z[mo][i]);
+                    for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActGelu>(z[i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActSilu>(z[mo][i]);
+                    for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActSilu>(z[i]);
                 }
-                if (a.grad_branch)
-                    Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, c).store(a.grad_branch, 0, g, turn);
+                if (a.grad_branch) Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, c).store(a.grad_branch, 0, g, turn);
             }
-            if (more) {
-                const Places<TG, OUT_LAST, 1> at(next, a.Cout, a.P, a.B, c);
-                at.fetch(a.grad, 0, go[mo]);
-                if (a.branch) at.fetch(a.branch, 0, br[mo]);
-            }
-            FG gs[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) gs[s] = step_of<3>(g, s);
+        };
+        auto add_grad_x = [&](const FG (&gs)[2], int mo, int mi, f32x16& dx) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                FX f;
+#pragma unroll
+                for (int p = 0; p < S::x; ++p) f.part[p] = wx[(((p * MI + mi) * MO + mo) * 2 + s) * 64 + lane];
+                dx = mfma_upto<S::gx>(f, gs[s], dx);
+            }
+        };
+        auto store_grad_x = [&](const Tile& tile, int c, const f32x16& dx) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = dx[i];
+            Places<T, LAST, 1>(tile, a.Cin, a.P, a.B, c).store(a.grad_x, 0, v, turn);
+        };
+
+        const int64_t stride = (int64_t)a.groups * 4;
+        int64_t t = (int64_t)blockIdx.x * 4 + wave;
+        if (t >= a.tiles) t = a.tiles;
+        Values<T> raw[MI];
+        Values<TG> go[MO], br[MO];
+        Tile tile = tile_at(min(t, a.tiles - 1));
+        if (t < a.tiles) {
+            fetch_x(raw, tile);
+            fetch_g(go[0], br[0], tile, 0);
+        }
+        // 128 channels of x: all of g first, then 32 input channels at a time, so that fewer of x's values are
+        // alive together.  On their way are the next tile's x and the next 32 channels' grad_out and branch.
+        for (; t < a.tiles; t += stride) {
+            const bool more = t + stride < a.tiles;
+            const Tile next = tile_at(min(t + stride, a.tiles - 1));
+            FX x[MI][2];
+            f32x16 z[MO];
+            parts_of_x(raw, x);
+            if (more) fetch_x(raw, next);
+            form_z(x, z);
+            // all of g first, then 32 input channels at a time: fewer of x's values are alive together
+            FG gs[MO][2];
+#pragma unroll
+            for (int mo = 0; mo < MO; ++mo) {
+                int c = 32 * mo;
+                asm volatile("" : "+s"(c));
+                if (mo + 1 < MO) fetch_g(go[mo + 1], br[mo + 1], tile, c + 32);
+                form_g(tile, c, z[mo], go[mo], br[mo], gs[mo]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (more) fetch_g(go[0], br[0], next, 0);
             if (a.grad_x) {
 #pragma unroll
-                for (int mi = 0; mi < MI; ++mi)
+                for (int mi = 0; mi < MI; ++mi) {
+                    int c = 32 * mi;
+                    if (c >= a.Cin) break;
+                    asm volatile("" : "+s"(c));
+                    f32x16 dx;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        FX f;
+                    for (int r = 0; r < 16; ++r) dx[r] = 0.0f;
 #pragma unroll
-                        for (int p = 0; p < S::x; ++p) f.part[p] = wx[(((p * MI + mi) * MO + mo) * 2 + s) * 64 + lane];
-                        dx[mi] = mfma_upto<S::gx>(f, gs[s], dx[mi]);
-                    }
+                    for (int mo = 0; mo < MO; ++mo) add_grad_x(gs[mo], mo, mi, dx);
+                    store_grad_x(tile, c, dx);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
             if (a.part) {
-                FG gt[2];
-                turned(gs, one, gt, &db[mo]);
 #pragma unroll
-                for (int mi = 0; mi < MI; ++mi)
+                for (int mo = 0; mo < MO; ++mo) {
+                    FG gt[2];
+                    turned(gs[mo], one, gt, &db[mo]);
+                    gs[mo][0] = gt[0];
+                    gs[mo][1] = gt[1];
+                }
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) dw[mo][mi] = mfma_upto<S::gw>(gt[s], xt[mi][s], dw[mo][mi]);
+                for (int mi = 0; mi < MI; ++mi) {
+                    FX xt[2];
+                    turned(x[mi], one, xt, nullptr);
+#pragma unroll
+                    for (int mo = 0; mo < MO; ++mo)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) dw[mo][mi] = mfma_upto<S::gw>(gs[mo][s], xt[s], dw[mo][mi]);
+                }
             }
+            tile = next;
         }
-        if (a.grad_x) {
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) {
-                int c = 32 * mi;
-                if (c >= a.Cin) break;
-                asm volatile("" : "+s"(c));
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = dx[mi][i];
-                Places<T, LAST, 1>(tile, a.Cin, a.P, a.B, c).store(a.grad_x, 0, v, turn);
-            }
-        }
-        tile = next;
     }
 
     if (!a.part) return;

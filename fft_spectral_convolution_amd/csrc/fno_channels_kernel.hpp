@@ -113,6 +113,7 @@ __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_chann
                     const int ks = base + k;
                     if (ks >= steps) break;
                     Frag<V, parts> b[NT];
+                    raw[k].keep(a.Cin, 16 * (first + ks));
 #pragma unroll
                     for (int j = 0; j < NT; ++j) b[j] = operand(raw[k], j);
                     if (first + ks + ahead < a.nks) {
