@@ -7,102 +7,6 @@
 namespace fno {
 namespace {
 
-// ---- gradient of the weight -----------------------------------------------------------
-// grad_w[o][i] = sum over positions g[o] x[i]: the positions are what the
-// matrix instructions sum over, so lanes hold channels and registers positions.
-// A workgroup takes 64 x 64 channels and a share of the positions, each wave a
-// share of those; the sums of a workgroup are joined in LDS, those of the
-// workgroups by k_weight_sum, both in a fixed order.
-struct GradArgs {
-    const void *x, *g;
-    float* part;              // [splits][Cout Cin + Cout]: sums of g x and of g
-    int64_t B, P, steps_item, steps;     // steps of 16 positions
-    int Cin, Cout, ct_in, ct_out, splits;
-    bool x_last, g_last;
-    int x_type, g_type;
-};
-
-// Eight positions from p on of one channel, zero behind the item's end.
-__device__ __forceinline__ void load_positions(float (&v)[8], const void* f, int type, bool last, int64_t item, int c,
-                                               int C, int64_t p, int64_t P) {
-    with_field_type(type, [&](auto e) {
-        typedef decltype(e) T;
-        const T* base = static_cast<const T*>(f) + item * P * C;
-        if (!last && c < C && p + 8 <= P) {
-            load_vec<8>(base + c * P + p, v);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = c < C && p + i < P;
-            const T q = base[in ? (last ? (p + i) * C + c : c * P + p + i) : 0];
-            v[i] = in ? (float)q : 0.0f;
-        }
-    });
-}
-
-// PX: bfloat16 parts that hold an x of its type exactly (float16: two).
-template <int PX>
-__global__ __launch_bounds__(256) void k_weight_grad(GradArgs a) {
-    __shared__ float join[4][64];
-    const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int q = blockIdx.x;
-    const int split_no = q % a.splits;
-    q /= a.splits;
-    const int i0 = q % a.ct_in * 64, o0 = q / a.ct_in * 64;
-    f32x16 acc[2][2];
-    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[u][v][r] = 0.0f;
-    for (int64_t s = split_no * 4 + wave; s < a.steps; s += a.splits * 4) {
-        const int64_t item = s / a.steps_item, p = s % a.steps_item * 16 + 8 * h;
-        Frag<bf16x8, 3> g[2];
-        Frag<bf16x8, PX> x[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float v[8];
-            load_positions(v, a.g, a.g_type, a.g_last, item, o0 + 32 * u + n, a.Cout, p, a.P);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[u] += v[i];
-            g[u] = split<bf16x8, 3>(v);
-            load_positions(v, a.x, a.x_type, a.x_last, item, i0 + 32 * u + n, a.Cin, p, a.P);
-            x[u] = split<bf16x8, PX>(v);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) acc[u][v] = mfma_parts(g[u], x[v], acc[u][v]);
-    }
-    float* part = a.part + (int64_t)split_no * (a.Cin + 1) * a.Cout;
-    for (int u = 0; u < 2; ++u)
-        for (int v = 0; v < 2; ++v)
-            for (int r = 0; r < 16; ++r) {
-                __syncthreads();
-                join[wave][lane] = u ? (v ? acc[1][1][r] : acc[1][0][r]) : (v ? acc[0][1][r] : acc[0][0][r]);
-                __syncthreads();
-                const int o = o0 + 32 * u + 8 * (r >> 2) + 4 * h + (r & 3), i = i0 + 32 * v + n;
-                if (wave == 0 && o < a.Cout && i < a.Cin)
-                    part[(int64_t)o * a.Cin + i] = join[0][lane] + join[1][lane] + join[2][lane] + join[3][lane];
-            }
-    if (i0 != 0) return;
-    float* sums = part + (int64_t)a.Cin * a.Cout;
-    for (int u = 0; u < 2; ++u) {
-        __syncthreads();
-        join[wave][lane] = sum[u];
-        __syncthreads();
-        const int o = o0 + 32 * u + n;
-        if (wave == 0 && h == 0 && o < a.Cout) {
-            float s = 0.0f;
-            for (int w = 0; w < 4; ++w) s += join[w][n] + join[w][n + 32];
-            sums[o] = s;
-        }
-    }
-}
-
 // grad_w and, behind it, grad_b: sums over the splits, 64 values a workgroup, each
 // wave a quarter of the splits.
 __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ part, float* __restrict__ grad_w,
@@ -133,10 +37,11 @@ __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ pa
     }
 }
 
+// Shares of the positions: enough for one workgroup a CU, each of at least four tiles of 32 a wave.
 int weight_splits(const ChannelProduct& c) {
-    const int64_t steps = c.B * ((c.P + 15) / 16);
-    const int64_t tiles = (int64_t)((c.Cin + 63) / 64) * ((c.Cout + 63) / 64);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(steps / 16, 512 / tiles));
+    const int64_t tiles = c.B * ((c.P + 31) / 32);
+    const int64_t parts = (int64_t)((c.Cin + 63) / 64) * ((c.Cout + 63) / 64);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(tiles / 16, 512 / parts));
 }
 
 hipError_t launch_product(const ProductArgs& a, int x_type, bool last, bool out_last, int out_type, hipStream_t s) {
@@ -150,7 +55,7 @@ size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 // Whether g = grad_out act'(z) is a field of its own.
 bool keeps_g(const ChannelProduct& c) { return c.act != kActNone; }
 
-bool fits(const ChannelProduct& c) { return backward_fits(c.Cin, c.Cout); }
+bool fits(const ChannelProduct& c) { return backward_fits(c.Cin, c.Cout, c.x_type); }
 
 // Workgroups of the one-kernel backward pass: one a CU, two where 32 channels leave room for them.
 int backward_groups(const ChannelProduct& c) {
@@ -259,27 +164,16 @@ hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool b
         return launch_product(q, g_type, c.out_last, c.x_last, c.x_type, s);
     }
     if (names[kernel] == std::string_view("channels_grad_w")) {
-        GradArgs w{};
+        WeightGradArgs w{};
         w.x = a.x;
         w.g = gp;
         w.part = part;
         w.B = c.B;
         w.P = c.P;
-        w.steps_item = (c.P + 15) / 16;
-        w.steps = c.B * w.steps_item;
         w.Cin = c.Cin;
         w.Cout = c.Cout;
-        w.ct_in = (c.Cin + 63) / 64;
-        w.ct_out = (c.Cout + 63) / 64;
         w.splits = splits;
-        w.x_last = c.x_last;
-        w.g_last = c.out_last;
-        w.x_type = c.x_type;
-        w.g_type = g_type;
-        const dim3 grid((unsigned)(splits * w.ct_in * w.ct_out)), block(256);
-        if (c.x_type == kTypeBf16) return launch_kernel(k_weight_grad<1>, grid, block, 0, s, w);
-        if (c.x_type == kTypeF16) return launch_kernel(k_weight_grad<2>, grid, block, 0, s, w);
-        return launch_kernel(k_weight_grad<3>, grid, block, 0, s, w);
+        return launch_channel_weight_grad(w, c.x_type, g_type, c.x_last, c.out_last, s);
     }
     const int64_t weights = (int64_t)c.Cin * c.Cout;
     return launch_kernel(k_weight_sum, dim3((unsigned)((weights + c.Cout + 63) / 64)), dim3(256), 0, s,

@@ -94,10 +94,6 @@ __device__ __forceinline__ f32x16 mfma_upto(const Frag<V, NA>& a, const Frag<V, 
             if (s - i >= 0 && s - i < NB) c = mfma(a.part[i], b.part[s - i], c);
     return c;
 }
-template <typename V, int NA, int NB>
-__device__ __forceinline__ f32x16 mfma_parts(const Frag<V, NA>& a, const Frag<V, NB>& b, f32x16 c) {
-    return mfma_upto<(NA > NB ? NA : NB) - 1>(a, b, c);
-}
 
 // ---- activations ----------------------------------------------------------------------
 // As act_value, in fewer instructions, which the products of 16-bit fields with
@@ -434,8 +430,8 @@ __device__ __forceinline__ void load_raw(Raw<T, LAST, NT>& raw, const void* fiel
 }
 
 // The operand of position j.
-template <typename T, bool LAST, int NT>
-__device__ __forceinline__ Frag<typename Operand<T>::V, Operand<T>::parts> operand(const Raw<T, LAST, NT>& raw, int j) {
+template <int N, typename T, bool LAST, int NT>
+__device__ __forceinline__ Frag<typename Operand<T>::V, N> operand(const Raw<T, LAST, NT>& raw, int j) {
     typedef typename Operand<T>::V V;
     if constexpr (Operand<T>::parts == 1) {
         Frag<V, 1> f;
@@ -446,8 +442,90 @@ __device__ __forceinline__ Frag<typename Operand<T>::V, Operand<T>::parts> opera
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = LAST ? raw.v[j][i] : raw.v[i][j];
-        return split<V, Operand<T>::parts>(v);
+        return split<V, N>(v);
     }
+}
+
+// ---- sums over positions -------------------------------------------------------------
+// Parts of x and W (those of g are three), and the products formed, i + j up to these: for z,
+// for grad_x (rounded to x's type), for grad_W.
+template <typename T>
+struct Scheme;
+template <>
+struct Scheme<float> {
+    static constexpr int x = 3, z = 2, gx = 2, gw = 2;
+};
+template <>
+struct Scheme<bf16> {
+    static constexpr int x = 1, z = 0, gx = 1, gw = 2;
+};
+template <>
+struct Scheme<f16> {
+    static constexpr int x = 2, z = 2, gx = 1, gw = 2;
+};
+
+// Step s (of two) of the operand of 16 values.
+template <int N, typename T>
+__device__ __forceinline__ Frag<bf16x8, N> step_of(const T* v, int s) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)v[8 * s + i];
+    return split<bf16x8, N>(f);
+}
+
+// A 32 x 32 part of an operand, turned: lanes hold what was its steps' k.  Returns the sum of the lane's values.
+template <int N>
+__device__ __forceinline__ float turned(const Frag<bf16x8, N> (&a)[2], const bf16x8 (&one)[2],
+                                        Frag<bf16x8, N> (&out)[2]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        f32x16 d;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) d[r] = 0.0f;
+        d = mfma(a[0].part[p], one[0], d);
+        d = mfma(a[1].part[p], one[1], d);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            out[r >> 3].part[p][r & 7] = d[r];
+            sum += d[r];
+        }
+    }
+    return sum;
+}
+
+// Sums of g x (and of g) that four waves of a workgroup hold, joined one after the
+// other, so in a fixed order: rows o0.., columns i0.. of part [Cout][Cin] and, of the
+// first columns' workgroup, the sums of g behind it.  join holds MO MI 1024 floats, sums 32 MO.
+template <int MO, int MI>
+__device__ __forceinline__ void join_sums(const f32x16 (&dw)[MO][MI], const float (&db)[MO], float* join, float* sums,
+                                          float* part, int o0, int i0, int Cout, int Cin) {
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int k = 0; k < 4; ++k) {
+        __syncthreads();
+        if (wave != k) continue;
+#pragma unroll
+        for (int mo = 0; mo < MO; ++mo) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float* q = join + ((mo * MI + mi) * 16 + r) * 64 + lane;
+                    *q = k ? *q + dw[mo][mi][r] : dw[mo][mi][r];
+                }
+            const float s = swap_add<32>(db[mo]);
+            if (h == 0) sums[32 * mo + lane] = k ? sums[32 * mo + lane] + s : s;
+        }
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < MO * MI * 1024; q += 256) {
+        const int l = q & 63, r = (q >> 6) & 15, mi = (q >> 10) % MI, mo = (q >> 10) / MI;
+        const int o = o0 + 32 * mo + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), i = i0 + 32 * mi + (l & 31);
+        if (o < Cout && i < Cin) part[(int64_t)o * Cin + i] = join[q];
+    }
+    if (i0 == 0)
+        for (int o = threadIdx.x; o < 32 * MO && o0 + o < Cout; o += 256) part[(int64_t)Cin * Cout + o0 + o] = sums[o];
 }
 
 // ---- the product's kernel (fno_channels_kernel.hpp) ---------------------------------
@@ -487,12 +565,27 @@ struct BackwardArgs {
     int tiles_item, groups;
     int64_t tiles;
 };
-// Up to 64 channels on one side and 128 on the other.
-inline bool backward_fits(int Cin, int Cout) { return std::max(Cin, Cout) <= 128 && std::min(Cin, Cout) <= 64; }
+// What a wave's registers hold: up to 64 channels, of 16-bit fields 128 on one side.  (float32, 64 -> 128
+// and 128 -> 64 at 32 x 64 x 64: 238 and 99 us in one kernel, 144 and 117 in four; 78 -> 15, channels last: 129 and 63.)
+inline bool backward_fits(int Cin, int Cout, int x_type) {
+    return std::max(Cin, Cout) <= (x_type == kTypeF32 ? 64 : 128) && std::min(Cin, Cout) <= 64;
+}
 hipError_t launch_backward_f32(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
 hipError_t launch_backward_bf16(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
 hipError_t launch_backward_bf16_f32(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
 hipError_t launch_backward_f16(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
 hipError_t launch_backward_f16_f32(const BackwardArgs& a, bool last, bool out_last, hipStream_t s);
+
+
+// ---- gradient of the weight alone (fno_channels_grad.hip) ------------------------------
+struct WeightGradArgs {
+    const void *x, *g;
+    float* part;                   // [splits][Cout Cin + Cout]: sums of g x and of g
+    int64_t B, P, tiles;
+    int Cin, Cout, tiles_item, splits;
+    bool merged;
+};
+// 64 x 64 channels a workgroup, in `splits` shares of the positions
+hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, bool x_last, bool g_last, hipStream_t s);
 
 }  // namespace fno

@@ -26,51 +26,6 @@
 namespace fno {
 namespace {
 
-// Parts of x and W (those of g are three), and the products formed, i + j up to these: for z,
-// for grad_x (rounded to x's type), for grad_W.
-template <typename T>
-struct Scheme;
-template <>
-struct Scheme<float> {
-    static constexpr int x = 3, z = 2, gx = 2, gw = 2;
-};
-template <>
-struct Scheme<bf16> {
-    static constexpr int x = 1, z = 0, gx = 1, gw = 2;
-};
-template <>
-struct Scheme<f16> {
-    static constexpr int x = 2, z = 2, gx = 1, gw = 2;
-};
-
-// Step s (of two) of the operand of 16 values.
-template <int N, typename T>
-__device__ __forceinline__ Frag<bf16x8, N> step_of(const T* v, int s) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)v[8 * s + i];
-    return split<bf16x8, N>(f);
-}
-
-// A 32 x 32 part of an operand, turned: lanes hold what was its steps' k.
-template <int N>
-__device__ __forceinline__ void turned(const Frag<bf16x8, N> (&a)[2], const bf16x8 (&one)[2], Frag<bf16x8, N> (&out)[2],
-                                       float* sum) {
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-        f32x16 d;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) d[r] = 0.0f;
-        d = mfma(a[0].part[p], one[0], d);
-        d = mfma(a[1].part[p], one[1], d);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            out[r >> 3].part[p][r & 7] = d[r];
-            if (sum) *sum += d[r];
-        }
-    }
-}
-
 template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
 __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(BackwardArgs a) {
     typedef Scheme<T> S;
@@ -173,26 +128,30 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
             }
             if (more) fetch_x(raw, next);
 
-            f32x16 z[MO];
-            if (a.act != kActNone) {
+            // z of all output channels first, so that x is no longer needed but turned; of 128, whose z would
+            // take 64 registers, 32 at a time
+            constexpr bool kEach = MO == 4;
+            f32x16 z[kEach ? 1 : MO];
+            auto form_z = [&](int mo, f32x16& q) {
 #pragma unroll
-                for (int mo = 0; mo < MO; ++mo) {
+                for (int r = 0; r < 16; ++r) q[r] = bias[32 * mo + 16 * h + r];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) z[mo][r] = bias[32 * mo + 16 * h + r];
+                for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-                    for (int mi = 0; mi < MI; ++mi)
+                    for (int s = 0; s < 2; ++s) {
+                        FX f;
 #pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            FX f;
+                        for (int p = 0; p < S::x; ++p) f.part[p] = wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + lane];
+                        q = mfma_upto<S::z>(f, x[mi][s], q);
+                    }
+            };
+            if (!kEach && a.act != kActNone) {
 #pragma unroll
-                            for (int p = 0; p < S::x; ++p) f.part[p] = wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + lane];
-                            z[mo] = mfma_upto<S::z>(f, x[mi][s], z[mo]);
-                        }
-                }
+                for (int mo = 0; mo < MO; ++mo) form_z(mo, z[mo]);
             }
             if (a.part) {
 #pragma unroll
-                for (int mi = 0; mi < MI; ++mi) turned(x[mi], one, xt[mi], nullptr);
+                for (int mi = 0; mi < MI; ++mi) turned(x[mi], one, xt[mi]);
             }
             f32x16 dx[MI];
 #pragma unroll
@@ -209,16 +168,19 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
 #pragma unroll
                 for (int i = 0; i < 16; ++i) g[i] = (float)go[mo].v[i];
                 if (a.act != kActNone) {
+                    f32x16& q = z[kEach ? 0 : mo];
+                    if (kEach) form_z(mo, q);
                     if (a.branch) {
+                        br[mo].keep(a.Cout, c);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) z[mo][i] += (float)br[mo].v[i];
+                        for (int i = 0; i < 16; ++i) q[i] += (float)br[mo].v[i];
                     }
                     if (a.act == kActGelu) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActGelu>(z[mo][i]);
+                        for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActGelu>(q[i]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActSilu>(z[mo][i]);
+                        for (int i = 0; i < 16; ++i) g[i] *= act_slope<kActSilu>(q[i]);
                     }
                     if (a.grad_branch)
                         Places<TG, OUT_LAST, 1>(tile, a.Cout, a.P, a.B, c).store(a.grad_branch, 0, g, turn);
@@ -244,7 +206,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
                 }
                 if (a.part) {
                     FG gt[2];
-                    turned(gs, one, gt, &db[mo]);
+                    db[mo] += turned(gs, one, gt);
 #pragma unroll
                     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
@@ -298,13 +260,14 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
             }
         };
         // g of the 32 output channels from c on, stored where it is asked for, and its parts
-        auto form_g = [&](const Tile& tile, int c, f32x16& z, Values<TG>& go, const Values<TG>& br, FG (&gs)[2]) {
+        auto form_g = [&](const Tile& tile, int c, f32x16& z, Values<TG>& go, Values<TG>& br, FG (&gs)[2]) {
             float g[16];
             go.keep(a.Cout, c);
 #pragma unroll
             for (int i = 0; i < 16; ++i) g[i] = (float)go.v[i];
             if (a.act != kActNone) {
                 if (a.branch) {
+                    br.keep(a.Cout, c);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) z[i] += (float)br.v[i];
                 }
@@ -363,7 +326,12 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
                 int c = 32 * mo;
                 asm volatile("" : "+s"(c));
                 if (mo + 1 < MO) fetch_g(go[mo + 1], br[mo + 1], tile, c + 32);
-                form_g(tile, c, z[mo], go[mo], br[mo], gs[mo]);
+                if (c < a.Cout) {
+                    form_g(tile, c, z[mo], go[mo], br[mo], gs[mo]);
+                } else {
+                    const float none[16] = {};
+                    gs[mo][0] = gs[mo][1] = step_of<3>(none, 0);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
             if (more) fetch_g(go[0], br[0], next, 0);
@@ -386,14 +354,14 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
 #pragma unroll
                 for (int mo = 0; mo < MO; ++mo) {
                     FG gt[2];
-                    turned(gs[mo], one, gt, &db[mo]);
+                    db[mo] += turned(gs[mo], one, gt);
                     gs[mo][0] = gt[0];
                     gs[mo][1] = gt[1];
                 }
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi) {
                     FX xt[2];
-                    turned(x[mi], one, xt, nullptr);
+                    turned(x[mi], one, xt);
 #pragma unroll
                     for (int mo = 0; mo < MO; ++mo)
 #pragma unroll
@@ -405,33 +373,9 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
     }
 
     if (!a.part) return;
-    // the waves' sums, one after the other (the weights in LDS are no longer needed)
-    float* join = reinterpret_cast<float*>(lds);             // [mo][mi][16][64]
-    float* sums = bias;                                      // [32 MO]
-    for (int k = 0; k < 4; ++k) {
-        __syncthreads();
-        if (wave != k) continue;
-#pragma unroll
-        for (int mo = 0; mo < MO; ++mo) {
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float* q = join + ((mo * MI + mi) * 16 + r) * 64 + lane;
-                    *q = k ? *q + dw[mo][mi][r] : dw[mo][mi][r];
-                }
-            const float s = swap_add<32>(db[mo]);
-            if (h == 0) sums[32 * mo + lane] = k ? sums[32 * mo + lane] + s : s;
-        }
-    }
-    __syncthreads();
-    float* part = a.part + (int64_t)blockIdx.x * (a.Cin + 1) * a.Cout;
-    for (int q = threadIdx.x; q < MO * MI * 1024; q += 256) {
-        const int l = q & 63, r = (q >> 6) & 15, mi = (q >> 10) % MI, mo = (q >> 10) / MI;
-        const int o = 32 * mo + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), i = 32 * mi + (l & 31);
-        if (o < a.Cout && i < a.Cin) part[(int64_t)o * a.Cin + i] = join[q];
-    }
-    for (int o = threadIdx.x; o < a.Cout; o += 256) part[(int64_t)a.Cin * a.Cout + o] = sums[o];
+    // (the weights in LDS are no longer needed)
+    join_sums<MO, MI>(dw, db, reinterpret_cast<float*>(lds), bias, a.part + (int64_t)blockIdx.x * (a.Cin + 1) * a.Cout,
+                      0, 0, a.Cout, a.Cin);
 }
 
 template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
@@ -445,8 +389,11 @@ template <typename T, typename TG, bool LAST, bool OUT_LAST>
 hipError_t launch_backward_couts(const BackwardArgs& a, hipStream_t s) {
     if (a.Cin <= 32 && a.Cout <= 32) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 1, 1>(a, s);
     if (a.Cin <= 64 && a.Cout <= 64) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 2, 2>(a, s);
-    if (a.Cin <= 64) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 4, 2>(a, s);
-    return launch_backward_tiles<T, TG, LAST, OUT_LAST, 2, 4>(a, s);
+    if constexpr (sizeof(T) == 2) {
+        if (a.Cin <= 64) return launch_backward_tiles<T, TG, LAST, OUT_LAST, 4, 2>(a, s);
+        return launch_backward_tiles<T, TG, LAST, OUT_LAST, 2, 4>(a, s);
+    }
+    return hipErrorInvalidValue;         // (backward_fits)
 }
 
 template <typename T, typename TG>
@@ -458,8 +405,10 @@ hipError_t launch_backward(BackwardArgs a, bool last, bool out_last, hipStream_t
     }
     a.tiles_item = (int)((a.P + 31) / 32);
     a.tiles = a.B * a.tiles_item;
-    if (last) return out_last ? launch_backward_couts<T, TG, true, true>(a, s) : launch_backward_couts<T, TG, true, false>(a, s);
-    return out_last ? launch_backward_couts<T, TG, false, true>(a, s) : launch_backward_couts<T, TG, false, false>(a, s);
+    if (last && out_last) return launch_backward_couts<T, TG, true, true>(a, s);
+    if (last) return launch_backward_couts<T, TG, true, false>(a, s);
+    if (out_last) return launch_backward_couts<T, TG, false, true>(a, s);
+    return launch_backward_couts<T, TG, false, false>(a, s);
 }
 
 }  // namespace

@@ -1,0 +1,111 @@
+// Gradient of the weight of channel products with more channels than one kernel
+// takes (fno_channels_bwd.hpp): grad_W[o][i] = sum over positions g[o] x[i].
+//
+// A workgroup takes 64 x 64 channels and a share of the positions, its waves 32
+// positions at a time: both operands are turned by products with the identity
+// and stay in registers, as in the one-kernel pass.  A field is read once for every 64
+// channels of the other, mostly from the caches.
+#include "fno_channels.hpp"
+
+namespace fno {
+namespace {
+
+template <typename T, typename TG, bool LAST, bool G_LAST>
+__global__ __launch_bounds__(256) void k_weight_grad(WeightGradArgs a) {
+    typedef Scheme<T> S;
+    __shared__ float join[4096];
+    __shared__ float sums[64];
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // shares of the same positions are neighbours
+    const int parts_in = (a.Cin + 63) / 64, parts = parts_in * ((a.Cout + 63) / 64);
+    const int share = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int i0 = part % parts_in * 64, o0 = part / parts_in * 64;
+
+    bf16x8 one[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) one[s][i] = (lane & 31) == 16 * h + 8 * s + i ? 1.0f : 0.0f;
+    f32x16 dw[2][2];
+    float db[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dw[u][v][r] = 0.0f;
+
+    Values<T> x[2];
+    Values<TG> g[2];
+    auto fetch = [&](int64_t t) {
+        Tile q;
+        q.item = a.merged ? 0 : t / a.tiles_item;
+        q.p0 = (a.merged ? t : t % a.tiles_item) * 32;
+        q.pn = 1;
+        q.pj = 0;
+        q.full = q.p0 + 32 <= a.P;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (i0 + 32 * u < a.Cin) Places<T, LAST, 1>(q, a.Cin, a.P, a.B, i0 + 32 * u).fetch(a.x, 0, x[u]);
+            if (o0 + 32 * u < a.Cout) Places<TG, G_LAST, 1>(q, a.Cout, a.P, a.B, o0 + 32 * u).fetch(a.g, 0, g[u]);
+        }
+    };
+    const int64_t stride = (int64_t)a.splits * 4;
+    int64_t t = (int64_t)share * 4 + wave;
+    if (t < a.tiles) fetch(t);
+    for (; t < a.tiles; t += stride) {
+        Frag<bf16x8, S::x> xs[2][2], xt[2][2];
+        Frag<bf16x8, 3> gs[2][2], gt[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            x[u].keep(a.Cin, i0 + 32 * u);
+            g[u].keep(a.Cout, o0 + 32 * u);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                xs[u][s] = step_of<S::x>(x[u].v, s);
+                gs[u][s] = step_of<3>(g[u].v, s);
+            }
+        }
+        if (t + stride < a.tiles) fetch(t + stride);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            turned(xs[u], one, xt[u]);
+            db[u] += turned(gs[u], one, gt[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) dw[u][v] = mfma_upto<S::gw>(gt[u][s], xt[v][s], dw[u][v]);
+    }
+    join_sums<2, 2>(dw, db, join, sums, a.part + (int64_t)share * (a.Cin + 1) * a.Cout, o0, i0, a.Cout, a.Cin);
+}
+
+template <typename T, typename TG>
+hipError_t launch(const WeightGradArgs& a, bool last, bool g_last, hipStream_t s) {
+    const dim3 grid((unsigned)(a.splits * (int64_t)((a.Cin + 63) / 64) * ((a.Cout + 63) / 64))), block(256);
+    if (last && g_last) return launch_kernel(k_weight_grad<T, TG, true, true>, grid, block, 0, s, a);
+    if (last) return launch_kernel(k_weight_grad<T, TG, true, false>, grid, block, 0, s, a);
+    if (g_last) return launch_kernel(k_weight_grad<T, TG, false, true>, grid, block, 0, s, a);
+    return launch_kernel(k_weight_grad<T, TG, false, false>, grid, block, 0, s, a);
+}
+
+}  // namespace
+
+hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, bool x_last, bool g_last, hipStream_t s) {
+    a.merged = x_last && g_last;
+    if (a.merged) {
+        a.P *= a.B;
+        a.B = 1;
+    }
+    a.tiles_item = (int)((a.P + 31) / 32);
+    a.tiles = a.B * a.tiles_item;
+    if (x_type == kTypeF32) return launch<float, float>(a, x_last, g_last, s);
+    if (x_type == kTypeBf16)
+        return g_type == kTypeF32 ? launch<bf16, float>(a, x_last, g_last, s) : launch<bf16, bf16>(a, x_last, g_last, s);
+    return g_type == kTypeF32 ? launch<f16, float>(a, x_last, g_last, s) : launch<f16, f16>(a, x_last, g_last, s);
+}
+
+}  // namespace fno

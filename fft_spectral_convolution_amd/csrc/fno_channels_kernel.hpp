@@ -31,6 +31,16 @@ __device__ __forceinline__ void activate(float (&z)[16], bool slope) {
     for (int i = 0; i < 16; ++i) z[i] = slope ? act_slope<ACT>(z[i]) : product_act<ACT, FINE>(z[i]);
 }
 
+// Parts of x and of the weight, and the products of them that are formed (i + j up to `most`).  A
+// float32 x with a 16-bit result is the g of a 16-bit field's backward pass: the weight is of the
+// result's type, held exactly by one (bfloat16) or two parts, and two parts of g are within 2^-18 of it.
+template <typename T, typename TO>
+struct Parts {
+    static constexpr bool g = sizeof(T) == 4 && sizeof(TO) == 2, f16g = g && __is_same(TO, f16);
+    static constexpr int x = g ? 2 : Operand<T>::parts, w = f16g ? 2 : g ? 1 : Operand<T>::parts,
+                         most = g ? 1 : Operand<T>::parts - 1;
+};
+
 // Steps of 16 channels that are loaded before they are used: 64 channels of 16
 // bits, 32 of 32 bits.  Chunks of staged weights are whole numbers of them.
 template <typename T>
@@ -38,11 +48,12 @@ constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 
 template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
 __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_channels(ProductArgs a) {
+    typedef Parts<T, TO> Q;
     typedef typename Operand<T>::V V;
-    constexpr int parts = Operand<T>::parts, ahead = kAhead<T>;
+    constexpr int parts = Q::x, wparts = Q::w, ahead = kAhead<T>;
     extern __shared__ __align__(16) unsigned char lds[];
     V* wfrag = reinterpret_cast<V*>(lds);                     // [part][mt][chunk][64]
-    float* bias = reinterpret_cast<float*>(wfrag + parts * MT * a.chunk * 64);
+    float* bias = reinterpret_cast<float*>(wfrag + wparts * MT * a.chunk * 64);
     const int lane = threadIdx.x & 63, h = lane >> 5;
     unsigned char* const turn = reinterpret_cast<unsigned char*>(bias + 32 * MT) + (threadIdx.x >> 6) * kTurnBytes;
     const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -60,9 +71,9 @@ __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_chann
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = weight_at(a, o, k + i);
-            const Frag<V, parts> f = split<V, parts>(v);
+            const Frag<V, wparts> f = split<V, wparts>(v);
 #pragma unroll
-            for (int p = 0; p < parts; ++p) wfrag[((p * MT + mt) * a.chunk + ks) * 64 + l] = f.part[p];
+            for (int p = 0; p < wparts; ++p) wfrag[((p * MT + mt) * a.chunk + ks) * 64 + l] = f.part[p];
         }
     };
     auto tile_at = [&](int64_t t) {
@@ -115,7 +126,7 @@ __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_chann
                     Frag<V, parts> b[NT];
                     raw[k].keep(a.Cin, 16 * (first + ks));
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) b[j] = operand(raw[k], j);
+                    for (int j = 0; j < NT; ++j) b[j] = operand<parts>(raw[k], j);
                     if (first + ks + ahead < a.nks) {
                         load_raw(raw[k], a.x, tile, a.Cin, a.P, a.B, 16 * (first + ks + ahead));
                     } else if (t + stride < a.tiles) {
@@ -123,11 +134,11 @@ __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_chann
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        Frag<V, parts> w;
+                        Frag<V, wparts> w;
 #pragma unroll
-                        for (int p = 0; p < parts; ++p) w.part[p] = wfrag[((p * MT + mt) * a.chunk + ks) * 64 + lane];
+                        for (int p = 0; p < wparts; ++p) w.part[p] = wfrag[((p * MT + mt) * a.chunk + ks) * 64 + lane];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) acc[mt][j] = mfma_parts(w, b[j], acc[mt][j]);
+                        for (int j = 0; j < NT; ++j) acc[mt][j] = mfma_upto<Q::most>(w, b[j], acc[mt][j]);
                     }
                 }
             }
@@ -176,7 +187,7 @@ hipError_t launch_tiles(ProductArgs a, hipStream_t s) {
     a.tiles = a.B * a.tiles_item;
     a.cout_tiles = (a.Cout + 32 * MT - 1) / (32 * MT);
     a.nks = (a.Cin + 15) / 16;
-    constexpr int step = Operand<T>::parts * MT * 1024;           // bytes of weights for 16 input channels
+    constexpr int step = Parts<T, TO>::w * MT * 1024;           // bytes of weights for 16 input channels
     // 60 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
     const bool wide = (int64_t)a.nks * step > 60 * 1024;
     const int most = (wide ? 120 : 60) * 1024 / step;

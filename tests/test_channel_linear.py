@@ -153,7 +153,8 @@ def close(got, want, bound, what):
 
 SIZES = [(1, 1, 1, (1,)), (2, 4, 4, (32, 32)), (3, 3, 64, (7, 9)), (1, 64, 1, (65,)), (2, 17, 33, (5, 13)),
          (1, 30, 50, (127,)), (2, 64, 64, (64,)), (5, 32, 32, (31,)), (1, 65, 100, (3, 43)), (2, 128, 130, (100,)),
-         (7, 200, 40, (2,)), (1, 300, 260, (70,)), (1, 16, 16, (1000,))]
+         (7, 200, 40, (2,)), (1, 300, 260, (70,)), (1, 16, 16, (1000,)),
+         (2, 70, 20, (50,)), (1, 33, 127, (97,)), (3, 129, 66, (400,))]
 
 
 @pytest.mark.parametrize("size", SIZES)
@@ -233,6 +234,31 @@ def test_not_finite_values_stay_at_their_position(types, last, out_last):
     touched[list(bad)] = True
     assert torch.equal(out[~touched], clean[~touched])
     assert bool(torch.isnan(out[17]).all())
+
+
+@pytest.mark.parametrize("size", [(2, 20, 50, (9, 15)), (2, 70, 20, (9, 15)), (2, 40, 100, (9, 15)), (2, 130, 70, (9, 15))])
+@pytest.mark.parametrize("last,out_last", LAYOUTS)
+def test_not_finite_gradients_stay_at_their_position(size, last, out_last):
+    """A NaN of grad_out, of the branch or of x reaches grad_x and grad_branch at its own position alone."""
+    for types in ((F32, F32), (BF16, BF16), (F16, F32)):
+        c = Case(*size, types=types, last=last, out_last=out_last, act="silu", branch="before")
+        clean = c.backward(need_w=False)
+        B, cin, cout, grid = size
+        at = {"grad_out": 17, "branch": 18, "x": 133}
+        for name, p in at.items():
+            is_last = last if name == "x" else out_last
+            t = getattr(c, name)
+            flat = points(t, is_last)
+            flat[p] = float("nan")
+            t2 = flat.reshape(B, *grid, -1)
+            setattr(c, name, (t2 if is_last else t2.movedim(-1, 1)).contiguous().to(t.dtype).to(DEV))
+        got = c.backward(need_w=False)
+        touched = torch.zeros(B * 135, dtype=torch.bool)
+        touched[list(at.values())] = True
+        for k, is_last in ((0, last), (3, out_last)):
+            g, w = points(got[k], is_last), points(clean[k], is_last)
+            assert torch.equal(g[~touched], w[~touched])
+            assert bool(torch.isnan(g[touched]).all())
 
 
 def test_large_and_tiny_values():
