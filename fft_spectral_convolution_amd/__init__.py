@@ -1035,7 +1035,7 @@ def fno_adamw_states(params, bits: int = 32):
 
 def fno_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
               weight_decay: float = 1e-2, norm=None, max_norm=None, copies=None, seed: int = 0, out=None) -> None:
-    """One AdamW step (decoupled weight decay) over lists of tensors, in one kernel for every 48 of them.
+    """One AdamW step (decoupled weight decay) over lists of tensors, in one kernel for every 45 of them.
 
     params are float32, bfloat16, float16 or complex64, mixed; grads have their sizes, of any of the
     real types (complex64 where the parameter is).  exp_avgs, exp_avg_sqs are what fno_adamw_states

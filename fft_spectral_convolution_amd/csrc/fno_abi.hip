@@ -1345,6 +1345,7 @@ int check_adamw(const fno_adamw_tensors* t, int count, const fno_adamw_options* 
     if (count < 0) return FNO_ERR_SHAPE;
     if (!(o->beta1 >= 0.0 && o->beta1 < 1.0 && o->beta2 >= 0.0 && o->beta2 < 1.0)) return FNO_ERR_VALUE;
     if (!finite_from_zero(o->eps) || !finite_from_zero(o->weight_decay)) return FNO_ERR_VALUE;
+    if (o->eps > 3.4e38 || (o->eps != 0.0 && o->eps < 1.1754943508222875e-38)) return FNO_ERR_VALUE;
     if (!o->lr_device && !finite_from_zero(o->lr)) return FNO_ERR_VALUE;
     if (!o->step_device && o->step < 1) return FNO_ERR_VALUE;
     if (o->norm && !(o->max_norm >= 0.0)) return FNO_ERR_VALUE;
@@ -1402,24 +1403,22 @@ bool adamw_overlap(const fno_adamw_tensors& t, int count, const fno_adamw_option
     return all.overlap();
 }
 
-// Launch a kernel for every kAdamTable tensors; fill(table, k, i) writes entry k for tensor i.
-template <typename Fill, typename Launch>
-int adam_tables(int count, const char* name, hipStream_t hs, Fill&& fill, Launch&& launch) {
-    rec_begin();
-    auto run = [&]() -> int {
-        for (int at = 0; at < count; at += kAdamTable) {
-            AdamTable t{};
-            const int m = std::min(count - at, kAdamTable);
-            for (int k = 0; k < m; ++k) fill(t, k, at + k);
-            const uint32_t chunks = adam_table_chunks(t, m);
-            if (!chunks) continue;
-            rec_kernel(name, hs);
-            const hipError_t e = launch(t, chunks, at);
-            if (e != hipSuccess) return hip_fail(e);
-        }
-        return FNO_OK;
-    };
-    return rec_end(hs, run());
+// Launch a kernel for every kAdamTable of the tensors that wanted(i); fill(table, k, i)
+// writes entry k for tensor i.
+template <typename Wanted, typename Fill, typename Launch>
+int adam_tables(int count, const char* name, hipStream_t hs, Wanted&& wanted, Fill&& fill, Launch&& launch) {
+    for (int i = 0; i < count;) {
+        AdamTable t{};
+        int m = 0;
+        for (; i < count && m < kAdamTable; ++i)
+            if (wanted(i)) fill(t, m++, i);
+        const uint32_t chunks = adam_table_chunks(t, m);
+        if (!chunks) continue;
+        rec_kernel(name, hs);
+        const hipError_t e = launch(t, chunks);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    return FNO_OK;
 }
 
 }  // namespace
@@ -1870,13 +1869,18 @@ int fno_adamw(const struct fno_adamw_tensors* tensors, int count, const struct f
         q.n[k] = t.numels[i] * (t.param_types[i] == FNO_C64 ? 2 : 1);
         q.ptype[k] = (uint8_t)t.param_types[i];
         q.gtype[k] = (uint8_t)t.grad_types[i];
-        q.bits[k] = (uint8_t)t.state_bits[i];
+        q.number[k] = i;
         q.ctype[k] = q.copy[k] ? (uint8_t)t.copy_types[i] : 0;
     };
-    return adam_tables(count, "adamw", hs, fill, [&](const AdamTable& q, uint32_t chunks, int at) {
-        a.number = at;
-        return launch_adamw(q, chunks, a, hs);
-    });
+    rec_begin();
+    int rc2 = FNO_OK;
+    for (int bits : {32, 8}) {
+        a.bits = bits;
+        if (rc2 == FNO_OK)
+            rc2 = adam_tables(count, bits == 8 ? "adamw8" : "adamw", hs, [&](int i) { return t.state_bits[i] == bits; },
+                              fill, [&](const AdamTable& q, uint32_t chunks) { return launch_adamw(q, chunks, a, hs); });
+    }
+    return rec_end(hs, rc2);
 }
 
 int fno_adamw_moments(const void* const* exp_avgs, const void* const* exp_avg_sqs, float* const* out_exp_avgs,
@@ -1913,8 +1917,11 @@ int fno_adamw_moments(const void* const* exp_avgs, const void* const* exp_avg_sq
         q.vo[k] = out_exp_avg_sqs[i];
         q.n[k] = numels[i];
     };
-    return adam_tables(count, "adamw_moments", hs, fill,
-                       [&](const AdamTable& q, uint32_t chunks, int) { return launch_adamw_moments(q, chunks, hs); });
+    rec_begin();
+    return rec_end(hs, adam_tables(count, "adamw_moments", hs, [](int) { return true; }, fill,
+                                   [&](const AdamTable& q, uint32_t chunks) {
+                                       return launch_adamw_moments(q, chunks, hs);
+                                   }));
 }
 
 }  // extern "C"

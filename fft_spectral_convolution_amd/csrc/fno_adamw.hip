@@ -21,6 +21,8 @@
 // smaller values, codes are 6 to 12% apart, and v would stay where it is.
 // The random bits are a hash of (seed, step, tensor, number of the value), so
 // equal calls give equal bits.
+#include <type_traits>
+
 #include "fno_fields.hpp"
 
 namespace fno {
@@ -53,6 +55,7 @@ __device__ __forceinline__ void with_type(int type, F&& f) {
 // What one step needs besides the tensors, the same for all of them.
 struct Step {
     float decay, size, inv_c2, eps, coef;      // 1 - lr wd, lr / (1 - b1^t), (1 - b2^t)^-1/2
+    float inv_c2_small;                        // 2^-32 of that
     double b1, b2;
     uint32_t step;
 };
@@ -70,6 +73,7 @@ __device__ Step make_step(const AdamOptions& o) {
     s.decay = (float)(1.0 - lr * o.weight_decay);
     s.size = (float)(lr / c1);
     s.inv_c2 = (float)(1.0 / sqrt(c2));
+    s.inv_c2_small = s.inv_c2 * 0x1p-32f;
     s.eps = (float)o.eps;
     s.coef = 1.0f;
     if (o.norm) {                  // the factor of the clipping call: min(1, max_norm / (norm + 1e-6))
@@ -81,25 +85,13 @@ __device__ Step make_step(const AdamOptions& o) {
     return s;
 }
 
+// The device's root and reciprocal, good to 1 ulp: a few last bits of the update, which is
+// a small part of p.  The root takes subnormal numbers for zero, so small v are scaled.
 __device__ __forceinline__ float new_param(float p, float m, float v, const Step& s) {
-    return fmaf(-s.size * m, 1.0f / fmaf(sqrtf(v), s.inv_c2, s.eps), p * s.decay);
-}
-
-// 16 bits of a copy beside the parameter
-template <int N>
-__device__ __forceinline__ void store_copy(void* copy, int type, int64_t at, const float (&v)[N], int n) {
-    if (!copy) return;
-    with_type(type, [&](auto e) {
-        using T = decltype(e);
-        if constexpr (sizeof(T) == 2) {
-            T* q = static_cast<T*>(copy) + at;
-            if (n == N) {
-                store_vec<N>(q, v);
-            } else {
-                for (int j = 0; j < n; ++j) q[j] = (T)v[j];
-            }
-        }
-    });
+    const bool small = v < 0x1p-96f;
+    const float root = __builtin_amdgcn_sqrtf(v * (small ? 0x1p64f : 1.0f));
+    const float denom = fmaf(root, small ? s.inv_c2_small : s.inv_c2, s.eps);
+    return fmaf(-s.size * m, __builtin_amdgcn_rcpf(denom), p * s.decay);
 }
 
 template <int N, typename T>
@@ -122,6 +114,17 @@ __device__ __forceinline__ void store_some(T* p, const float (&v)[N], int n) {
     }
 }
 
+// 16 bits of a copy beside the parameter
+template <int N>
+__device__ __forceinline__ void store_copy(void* copy, int type, int64_t at, const float (&v)[N], int n) {
+    if (!copy) return;
+    if (type == kTypeBf16) {
+        store_some(static_cast<bf16*>(copy) + at, v, n);
+    } else {
+        store_some(static_cast<f16*>(copy) + at, v, n);
+    }
+}
+
 // ---- moments in 32 bits ---------------------------------------------------------
 template <typename TP, typename TG>
 __device__ __forceinline__ void chunk32(const AdamTable& t, int i, int64_t at, int n, const Step& s) {
@@ -133,13 +136,7 @@ __device__ __forceinline__ void chunk32(const AdamTable& t, int i, int64_t at, i
     float* mo = static_cast<float*>(t.mo[i]) + at;
     float* vo = static_cast<float*>(t.vo[i]) + at;
     const float b1 = (float)s.b1, b2 = (float)s.b2, a1 = (float)(1.0 - s.b1), a2 = (float)(1.0 - s.b2);
-    for (int k = 4 * threadIdx.x; k < n; k += 4 * kThreads) {
-        const int left = min(4, n - k);
-        float pv[4], gv[4], mv[4], vv[4];
-        load_some(p + k, pv, left);
-        load_some(g + k, gv, left);
-        load_some(m + k, mv, left);
-        load_some(v + k, vv, left);
+    auto update = [&](float (&pv)[4], const float (&gv)[4], float (&mv)[4], float (&vv)[4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float q = gv[j] * s.coef;
@@ -147,6 +144,41 @@ __device__ __forceinline__ void chunk32(const AdamTable& t, int i, int64_t at, i
             vv[j] = fmaf(b2, vv[j], a2 * (q * q));
             pv[j] = new_param(pv[j], mv[j], vv[j], s);
         }
+    };
+    constexpr int kStep = 4 * kThreads;
+    if (n == kChunk) {
+        // all of a chunk's loads in flight two vectors of each field at a time
+#pragma unroll
+        for (int c = 0; c < kChunk; c += 2 * kStep) {
+            float pv[2][4], gv[2][4], mv[2][4], vv[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = c + u * kStep + 4 * threadIdx.x;
+                load_vec<4>(p + k, pv[u]);
+                load_vec<4>(g + k, gv[u]);
+                load_vec<4>(m + k, mv[u]);
+                load_vec<4>(v + k, vv[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = c + u * kStep + 4 * threadIdx.x;
+                update(pv[u], gv[u], mv[u], vv[u]);
+                store_vec<4>(po + k, pv[u]);
+                store_vec<4>(mo + k, mv[u]);
+                store_vec<4>(vo + k, vv[u]);
+                store_copy(t.copy[i], t.ctype[i], at + k, pv[u], 4);
+            }
+        }
+        return;
+    }
+    for (int k = 4 * threadIdx.x; k < n; k += kStep) {
+        const int left = min(4, n - k);
+        float pv[4], gv[4], mv[4], vv[4];
+        load_some(p + k, pv, left);
+        load_some(g + k, gv, left);
+        load_some(m + k, mv, left);
+        load_some(v + k, vv, left);
+        update(pv, gv, mv, vv);
         store_some(po + k, pv, left);
         store_some(mo + k, mv, left);
         store_some(vo + k, vv, left);
@@ -181,7 +213,8 @@ __device__ __forceinline__ uint32_t high(double d) { return (uint32_t)(__builtin
 
 // Exponent byte of a block from the largest exponent field of its finite values.
 template <bool SIGNED>
-__device__ __forceinline__ int exp_byte(int field) {
+__device__ __forceinline__ int exp_byte(uint32_t f) {
+    const int field = (int)f;
     return field == 0 ? 0 : max(SIGNED ? kLeastM : kLeastV, min(254, field - 1023 + 127));
 }
 // Code of d: `up` (17 bits) is added to the 17 bits of the high word that the code drops.
@@ -200,18 +233,18 @@ __device__ __forceinline__ uint32_t encode8(double d, int e, uint32_t up) {
 
 // Largest of 16 neighbouring lanes, in each of them.
 template <int CTRL>
-__device__ __forceinline__ int dpp_max(int v) {
-    return max(v, __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false));
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
 }
-__device__ __forceinline__ int row_max(int v) {
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
     v = dpp_max<kDppXor1>(v);
     v = dpp_max<kDppXor2>(v);
     v = dpp_max<kDppHalfMirror>(v);
     return dpp_max<kDppMirror>(v);
 }
-__device__ __forceinline__ int finite_field(double d) {
-    const int f = (high(d) >> 20) & 0x7ff;
-    return f == 0x7ff ? 0 : f;
+__device__ __forceinline__ uint32_t finite_high(double d) {
+    const uint32_t h = high(d) & 0x7fffffffu;
+    return h >= 0x7ff00000u ? 0 : h;
 }
 
 __device__ __forceinline__ void unpack8(const uint8_t* p, uint32_t (&c)[8]) {
@@ -238,9 +271,10 @@ __device__ __forceinline__ void chunk8(const AdamTable& t, int i, int64_t at, in
     uint8_t* mo = static_cast<uint8_t*>(t.mo[i]);
     uint8_t* vo = static_cast<uint8_t*>(t.vo[i]);
     key = mix32(key + (uint32_t)(at >> 32));
-    const int whole = (n + kBlock - 1) / kBlock * kBlock;
-    for (int k = 8 * threadIdx.x; k < whole; k += 8 * kThreads) {
-        const int left = max(0, min(8, n - k));
+    const double a1 = 1.0 - s.b1, a2 = 1.0 - s.b2;
+    auto vectors = [&](int k, auto all) {
+        constexpr bool kAll = decltype(all)::value;          // no place is behind the tensor's end
+        const int left = kAll ? 8 : max(0, min(8, n - k));
         const int64_t block = (at + k) / kBlock;
         float pv[8], gv[8];
         uint32_t mc[8], vc[8];
@@ -250,47 +284,63 @@ __device__ __forceinline__ void chunk8(const AdamTable& t, int i, int64_t at, in
         unpack8(v + at + k, vc);
         const float ms = exp8(m[exps + block]), vs = exp8(v[exps + block]);
         double md[8], vd[8];
-        int me = 0, ve = 0;
+        uint32_t me = 0, ve = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const double q = (double)(gv[j] * s.coef);
-            md[j] = fma(s.b1, (double)decode8<true>(mc[j], ms), (1.0 - s.b1) * q);
-            vd[j] = fma(s.b2, (double)decode8<false>(vc[j], vs), (1.0 - s.b2) * (q * q));
-            if (j >= left) md[j] = vd[j] = 0.0;          // places behind the tensor's end hold zeros
-            me = max(me, finite_field(md[j]));
-            ve = max(ve, finite_field(vd[j]));
+            md[j] = fma(s.b1, (double)decode8<true>(mc[j], ms), a1 * q);
+            vd[j] = fma(s.b2, (double)decode8<false>(vc[j], vs), a2 * (q * q));
+            if (!kAll && j >= left) md[j] = vd[j] = 0.0;     // places behind the end hold zeros
+            me = max(me, high(md[j]) & 0x7fffffffu);
+            ve = max(ve, high(vd[j]) & 0x7fffffffu);
         }
-        me = exp_byte<true>(row_max(me));
-        ve = exp_byte<false>(row_max(ve));
+        // a block with infinities or NaN takes the exponent of its finite values
+        if (max(me, ve) >= 0x7ff00000u) {
+            me = ve = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                me = max(me, finite_high(md[j]));
+                ve = max(ve, finite_high(vd[j]));
+            }
+        }
+        const int mx = exp_byte<true>(row_max(me) >> 20), vx = exp_byte<false>(row_max(ve) >> 20);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t r = mix32((uint32_t)(at + k + j) ^ key);
-            mc[j] = encode8<true>(md[j], me, 2 * (r & 0xffff) + 1);
-            vc[j] = encode8<false>(vd[j], ve, 2 * (r >> 16) + 1);
+            mc[j] = encode8<true>(md[j], mx, 2 * (r & 0xffff) + 1);
+            vc[j] = encode8<false>(vd[j], vx, 2 * (r >> 16) + 1);
             pv[j] = new_param(pv[j], (float)md[j], (float)vd[j], s);
         }
         store_some(po + k, pv, left);
         pack8(mo + at + k, mc);
         pack8(vo + at + k, vc);
         if ((threadIdx.x & 15) == 0) {
-            mo[exps + block] = (uint8_t)me;
-            vo[exps + block] = (uint8_t)ve;
+            mo[exps + block] = (uint8_t)mx;
+            vo[exps + block] = (uint8_t)vx;
         }
         store_copy(t.copy[i], t.ctype[i], at + k, pv, left);
+    };
+    const int whole = (n + kBlock - 1) / kBlock * kBlock;
+    if (n == whole) {
+        for (int k = 8 * threadIdx.x; k < whole; k += 8 * kThreads) vectors(k, std::true_type{});
+    } else {
+        for (int k = 8 * threadIdx.x; k < whole; k += 8 * kThreads) vectors(k, std::false_type{});
     }
 }
 
-__global__ __launch_bounds__(kThreads) void k_adamw(AdamTable t, uint32_t nchunks, AdamOptions o) {
+// A table's moments are all of 32 bits or all of 8.
+template <int BITS>
+__global__ __launch_bounds__(kThreads, BITS == 8 ? 3 : 4) void k_adamw(AdamTable t, uint32_t nchunks, AdamOptions o) {
     const Step s = make_step(o);
     for (uint32_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
         const int i = tensor_of(t, c);
         const int64_t at = (int64_t)(c - t.first[i]) * kChunk;
         const int n = (int)min((int64_t)kChunk, t.n[i] - at);
         uint32_t key = mix32(mix32((uint32_t)o.seed) + (uint32_t)(o.seed >> 32));
-        key = mix32(mix32(key + s.step) + (uint32_t)(o.number + i));
+        key = mix32(mix32(key + s.step) + (uint32_t)t.number[i]);
         with_type(t.ptype[i], [&](auto a) {
             with_type(t.gtype[i], [&](auto b) {
-                if (t.bits[i] == 8) {
+                if constexpr (BITS == 8) {
                     chunk8<decltype(a), decltype(b)>(t, i, at, n, s, key);
                 } else {
                     chunk32<decltype(a), decltype(b)>(t, i, at, n, s);
@@ -347,7 +397,9 @@ uint32_t adam_table_chunks(AdamTable& t, int count) {
 }
 
 hipError_t launch_adamw(const AdamTable& t, uint32_t nchunks, const AdamOptions& o, hipStream_t s) {
-    return launch_kernel(k_adamw, dim3(nchunks < 1u << 22 ? nchunks : 1u << 22), dim3(kThreads), 0, s, t, nchunks, o);
+    const dim3 grid(nchunks < 1u << 22 ? nchunks : 1u << 22), block(kThreads);
+    return o.bits == 8 ? launch_kernel(k_adamw<8>, grid, block, 0, s, t, nchunks, o)
+                       : launch_kernel(k_adamw<32>, grid, block, 0, s, t, nchunks, o);
 }
 hipError_t launch_adamw_moments(const AdamTable& t, uint32_t nchunks, hipStream_t s) {
     return launch_kernel(k_adamw_moments, dim3(nchunks < 1u << 22 ? nchunks : 1u << 22), dim3(kThreads), 0, s, t,

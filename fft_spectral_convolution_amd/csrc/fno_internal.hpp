@@ -344,16 +344,18 @@ hipError_t launch_grad_finish(const double* part, int nparts, const float* given
 hipError_t launch_grad_scale(const GradTable& t, uint32_t nchunks, const float* coef, hipStream_t s);
 
 // ---- AdamW (fno_adamw.hip) ------------------------------------------------------
-// Tensors of one launch, passed by value.  n counts floats (two a complex
-// value); bits is 32 or 8; first is a tensor's first chunk
-// (adam_table_chunks fills it and returns the chunk count).
-constexpr int kAdamTable = 48;
+// Tensors of one launch, passed by value, their moments all of 32 bits or all
+// of 8.  n counts floats (two a complex value); number is a tensor's place in
+// the call's list; first is a tensor's first chunk (adam_table_chunks fills it
+// and returns the chunk count).
+constexpr int kAdamTable = 45;
 struct AdamTable {
     const void *p[kAdamTable], *g[kAdamTable], *m[kAdamTable], *v[kAdamTable];
     void *po[kAdamTable], *mo[kAdamTable], *vo[kAdamTable], *copy[kAdamTable];
     int64_t n[kAdamTable];
     uint32_t first[kAdamTable];
-    uint8_t ptype[kAdamTable], gtype[kAdamTable], bits[kAdamTable], ctype[kAdamTable];
+    int32_t number[kAdamTable];
+    uint8_t ptype[kAdamTable], gtype[kAdamTable], ctype[kAdamTable];
 };
 struct AdamOptions {
     double lr, weight_decay, b1, b2, c1, c2, log_b1, log_b2, eps;   // c = 1 - b^t
@@ -361,7 +363,7 @@ struct AdamOptions {
     const long long* step_dev;
     const float* norm;              // null: no clipping
     float max_norm;
-    int number;                     // of the table's first tensor
+    int bits;                       // of the table's moments
     uint64_t seed;
     int64_t step;
 };

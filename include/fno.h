@@ -507,7 +507,7 @@ int fno_channel_linear_backward(const void* x, const void* weight, const float* 
  * lr_device and step_device (device memory, NULL for none) stand for lr and
  * step, so that a captured graph can take another at each replay; step >= 1,
  * the first step's number, also in memory.  0 <= lr, eps, weight_decay, all
- * finite, 0 <= beta < 1, max_norm >= 0 (FNO_ERR_VALUE).  No workspace.  The
+ * finite, eps 0 or a normal float32, 0 <= beta < 1, max_norm >= 0 (FNO_ERR_VALUE).  No workspace.  The
  * arrays are read before the call returns.
  */
 struct fno_adamw_tensors {
