@@ -83,7 +83,9 @@ def build_lists(verbose: bool = False) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    # those of many template instances first: they take minutes, the others seconds
+    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")),
+                     key=lambda s: (not os.path.basename(s).startswith(("fno_channels_", "fno_groupnorm")), s))
     if not sources:
         raise RuntimeError(f"no HIP sources under {CSRC}")
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
