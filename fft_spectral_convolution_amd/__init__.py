@@ -11,6 +11,8 @@ cannot be loaded, every call raises; there is no fallback.
     out = fno.fno_spectral_conv1d(x, w, modes)       # x [B,Cin,N]   f32, w [modes,Cin,Cout]   c64
     y, stats = fno.fno_group_norm(out, 8, act="gelu")  # and its backward; see its docstring for layouts
     norm = fno.fno_clip_grad_norm(grads, 1.0)        # in place
+    z = fno.fno_channel_linear(x, weight, bias, branch=out, act="gelu")      # act(W x + bias + branch)
+    fno.fno_adamw(params, grads, exp_avgs, exp_avg_sqs, step)                # moments of 32 or 8 bits
 """
 from __future__ import annotations
 
@@ -912,7 +914,8 @@ def _channel_args(torch, x, weight, bias, branch, branch_after, act, channels_la
             raise ValueError(f"branch has shape {tuple(branch.shape)}, expected {out_shape}")
         branch_ptr = branch.data_ptr()
     return ((weight.data_ptr(), _f32_ptr(torch, bias, (cout,), device, "bias"), branch_ptr), (b, c, cout, p),
-            (code, 1 if branch_after else 0, 1 if channels_last else 0, 1 if out_channels_last else 0, x_type), out_shape)
+            (code, 1 if branch_after else 0, 1 if channels_last else 0, 1 if out_channels_last else 0, x_type),
+            out_shape)
 
 
 def fno_channel_linear(x, weight, bias=None, branch=None, branch_after: bool = False, act: str = "none",

@@ -1246,7 +1246,8 @@ int check_channels(const ChannelProduct& c) {
     if (c.B < 1 || c.P < 1 || c.Cin < 1 || c.Cout < 1 || c.Cin > 1 << 16 || c.Cout > 1 << 16) return FNO_ERR_SHAPE;
     // rows of 32 channels are indexed in 31 bits of bytes
     if (c.P > (c.x_last && c.out_last ? 1 << 30 : 1 << 24)) return FNO_ERR_SHAPE;
-    if (c.B * c.P > (INT64_C(1) << 40) / std::max(c.Cin, c.Cout)) return FNO_ERR_SHAPE;
+    // tiles of 32 positions are counted in 31 bits
+    if (c.B * c.P > std::min(INT64_C(1) << 35, (INT64_C(1) << 40) / std::max(c.Cin, c.Cout))) return FNO_ERR_SHAPE;
     if (c.act < FNO_ACT_NONE || c.act > FNO_ACT_SILU) return FNO_ERR_VALUE;
     if (c.x_type < FNO_F32 || c.x_type > FNO_F16) return FNO_ERR_VALUE;
     if (c.out_type != c.x_type && c.out_type != FNO_F32) return FNO_ERR_VALUE;

@@ -10,7 +10,8 @@ namespace {
 // grad_w and, behind it, grad_b: sums over the splits, 64 values a workgroup, each
 // wave a quarter of the splits.
 __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ part, float* __restrict__ grad_w,
-                                                    float* __restrict__ grad_b, int64_t weights, int couts, int splits) {
+                                                    float* __restrict__ grad_b, int64_t weights, int couts,
+                                                    int splits) {
     __shared__ double join[4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t k = (int64_t)blockIdx.x * 64 + lane, all = weights + couts;
@@ -57,7 +58,7 @@ bool keeps_g(const ChannelProduct& c) { return c.act != kActNone; }
 
 bool fits(const ChannelProduct& c) { return backward_fits(c.Cin, c.Cout, c.x_type); }
 
-// Workgroups of the one-kernel backward pass: one a CU, two where 32 channels leave room for them.
+// Workgroups of the one-kernel backward pass: one a CU, two where the registers that 32 channels take leave room.
 int backward_groups(const ChannelProduct& c) {
     const int64_t tiles = c.x_last && c.out_last ? (c.B * c.P + 31) / 32 : c.B * ((c.P + 31) / 32);
     return (int)std::min<int64_t>((tiles + 3) / 4, std::max(c.Cin, c.Cout) <= 32 ? 512 : 256);

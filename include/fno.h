@@ -437,8 +437,10 @@ int fno_clip_grad_norm(const void* const* grads, void* const* outs, const long l
  * no others.
  *
  * 1 <= B, P; 1 <= Cin, Cout <= 2^16; P <= 2^24 unless x and out are channels
- * last, then P <= 2^30; B P <= 2^40 / max(Cin, Cout).  Fields need the alignment of their elements only.  out
- * must not overlap anything else (FNO_ERR_ALIAS).  No workspace, nothing is allocated.
+ * last, then P <= 2^30; B P <= 2^35 and <= 2^40 / max(Cin, Cout).  Fields need the
+ * alignment of their elements only.  out must not overlap anything else
+ * (FNO_ERR_ALIAS).  No workspace, nothing is allocated: the call can be captured
+ * at any time, and calls on several streams share nothing.
  */
 int fno_channel_linear(const void* x, const void* weight, const float* bias, const void* branch, void* out,
                        int B, int Cin, int Cout, int P, int act, int branch_after, int x_last, int out_last,
@@ -506,7 +508,8 @@ int fno_channel_linear_backward(const void* x, const void* weight, const float* 
  *
  * lr_device and step_device (device memory, NULL for none) stand for lr and
  * step, so that a captured graph can take another at each replay; step >= 1,
- * the first step's number, also in memory.  0 <= lr, eps, weight_decay, all
+ * the first step's number, also in memory.  A NaN norm makes all parameters
+ * and moments NaN, as clipping by it does.  0 <= lr, eps, weight_decay, all
  * finite, eps 0 or a normal float32, 0 <= beta < 1, max_norm >= 0 (FNO_ERR_VALUE).  No workspace.  The
  * arrays are read before the call returns.
  */

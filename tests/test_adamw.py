@@ -204,7 +204,8 @@ def test_second_moment_decays_in_8_bits():
     for t in range(steps):
         fno.fno_adamw(p, [small], ms, vs, 2 + t, seed=5)
     v = code_values(vs[0], n, False).view(-1, 128)[:, 1:]
-    want = 0.999 ** steps                                  # 0.67; every step adds at most v^2 / 8 of variance times 0.1% / (1/16)
+    want = 0.999 ** steps                                  # 0.67
+    # a step moves v by 0.1% on average, in jumps of at most an eighth of it: its variance is at most 0.001 / 8
     spread = math.sqrt(steps * 0.001 * 0.125)
     assert abs(v.mean().item() - want) < 6 * spread / math.sqrt(v.numel()) + 1e-3
 
@@ -328,6 +329,33 @@ def test_tiny_and_huge_values_in_8_bits():
     m, v = fno.fno_adamw_moments(ms, vs, numels=[512])
     assert bool(torch.isfinite(m[0]).all()) and bool(torch.isfinite(v[0]).all())
     assert bool((v[0][:384] > 0).all()) and bool((v[0][384:] == 0).all())
+
+
+def test_tensor_beyond_32_bits():
+    """A tensor of more than 2^32 values: its last blocks' codes, whose numbers take more than 32 bits."""
+    n = (1 << 32) + 5000
+    p, g = torch.zeros(n, dtype=BF16, device=DEV), torch.zeros(n, dtype=BF16, device=DEV)
+    tail = 5000 + 128
+    g[-tail:] = torch.randn(tail, generator=torch.Generator().manual_seed(8)).to(BF16).to(DEV)
+    ms, vs = fno.fno_adamw_states([p], 8)
+    fno.fno_adamw([p], [g], ms, vs, 1, seed=77)
+    first = n - tail                                   # a whole number of blocks
+    assert first % 128 == 0
+    wide_g = wide(g[-tail:])
+    k = mix(mix(mix(mix(77)) + 1))
+    i = torch.arange(first, n)
+    r = mix((i & 0xFFFFFFFF) ^ mix(torch.tensor(k) + (i >> 32)))
+    codes = -(-tail // 128) * 128
+    blocks = codes // 128
+    whole = -(-n // 128) * 128
+    for held, w, half, signed in ((ms[0], (1 - 0.9) * wide_g, r & 0xFFFF, True),
+                                  (vs[0], (1 - 0.999) * wide_g * wide_g, r >> 16, False)):
+        want = encode(w, half, signed)
+        assert torch.equal(held[first:first + codes].cpu(), want[:codes])
+        exps = whole + first // 128
+        assert torch.equal(held[exps:exps + blocks].cpu(), want[codes:])
+        assert int(held[:first].max()) == 0
+    assert float(p[:first].abs().max()) == 0 and bool((p[-tail:] != 0).any())
 
 
 def test_refusals():

@@ -111,3 +111,19 @@ def test_moment_sizes(lib):
         assert lib.fno_adamw_moment_size(n, t) == size, (n, t)
         if 0 <= t <= 2 and 0 <= n <= 1 << 35:
             assert fno._moment_bytes(n) == size
+
+
+def test_tensor_lists(lib):
+    """What the reader of tensor lists refuses, by its kind of error (of tensors on the CPU, the device)."""
+    torch = pytest.importorskip("torch")
+    with pytest.raises(TypeError, match="must be torch tensors"):
+        fno._read_tensors(torch, [3], "grads")
+    with pytest.raises(TypeError, match="must be torch tensors"):
+        fno._read_tensors(torch, [None], "grads")
+    with pytest.raises(ValueError, match="one GPU device"):
+        fno._read_tensors(torch, (torch.zeros(3),), "grads")
+    assert fno._read_tensors(torch, [None, None], "copies", fno._HALVES, optional=True)[3].tolist() == [-1, -1]
+    assert fno._read_tensors(torch, iter([]), "grads")[4] is None
+    for call in (fno.fno_grad_norm, fno.fno_adamw_states):
+        with pytest.raises(ValueError):
+            call([torch.zeros(3)])

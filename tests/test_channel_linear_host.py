@@ -35,7 +35,7 @@ def backward(lib, x=X, w=W, b=B, branch=R, out=O, gx=GX, gw=GW, gb=GB, gr=GR, di
 def test_sizes_and_options(lib, call):
     for dims in ((0, 8, 12, 10), (2, 0, 12, 10), (2, 8, 0, 10), (2, 8, 12, 0), (-1, 8, 12, 10), (2, 8, 12, -5),
                  (2, (1 << 16) + 1, 12, 10), (2, 8, (1 << 16) + 1, 10), (2, 8, 12, (1 << 30) + 1),
-                 (1 << 20, 1, 2, 1 << 20)):
+                 (1 << 20, 1, 2, 1 << 20), (1 << 12, 1, 1, (1 << 23) + 1)):
         assert call(lib, dims=dims) == SHAPE, dims
         assert lib.fno_channel_linear_workspace_size(*dims, 1, 1, 1, 0, 0) == 0
     for last in ((0, 0), (0, 1), (1, 0)):

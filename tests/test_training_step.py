@@ -116,8 +116,8 @@ def test_training_step(bits):
         fno.fno_adamw(list(p.values()), grads, ms, vs, step, lr=0.01, norm=norm, max_norm=0.1, copies=copies, seed=4)
         factor = min(1.0, 0.1 / (float(norm) + 1e-6))
         for i, k in enumerate(names):
-            flat = [torch.view_as_real(q).reshape(-1) if q.is_complex() else q.reshape(-1) for q in (old[k], g[k], p[k])]
-            q, gr, new = [f.cpu().double() for f in flat]
+            q, gr, new = [(torch.view_as_real(t) if t.is_complex() else t).reshape(-1).cpu().double()
+                          for t in (old[k], g[k], p[k])]
             if bits == 8:
                 n = len(q)
                 m0, v0 = (f[0].cpu().double() for f in fno.fno_adamw_moments(
