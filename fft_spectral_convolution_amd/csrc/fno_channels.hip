@@ -38,11 +38,11 @@ __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ pa
     }
 }
 
-// Shares of the positions: enough for one workgroup a CU, each of at least four tiles of 32 a wave.
+// Shares of the positions: up to two workgroups a CU, each of a tile of 32 a wave or more.
 int weight_splits(const ChannelProduct& c) {
     const int64_t tiles = c.B * ((c.P + 31) / 32);
     const int64_t parts = (int64_t)((c.Cin + 63) / 64) * ((c.Cout + 63) / 64);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(tiles / 16, 512 / parts));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(tiles / 4, 512 / parts));
 }
 
 hipError_t launch_product(const ProductArgs& a, int x_type, bool last, bool out_last, int out_type, hipStream_t s) {

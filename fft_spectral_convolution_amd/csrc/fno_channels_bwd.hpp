@@ -29,7 +29,7 @@ namespace fno {
 namespace {
 
 // 64 -> 64 float32 channels first with a branch and GELU, 524288 positions: 178 to 190 us, 671 MB at 3.5 to 3.8
-// TB/s; 64 -> 128 bfloat16 channels last 161 us, 269 MB at 1.7 TB/s; 30 -> 50 float16, 8601 positions, 19
+// TB/s; 64 -> 128 bfloat16 channels last 161 us, 269 MB at 1.7 TB/s; 30 -> 50 float16, 8601 positions, 18
 // us, two launches.  One wave a SIMD (the sums, a tile's operands and the next tile's
 // fields take up to 512 registers) leaves latencies in the open: of the first case's 30 000 cycles a tile
 // and SIMD, matrix instructions take 5400, vector instructions about 11 000.  Two waves with the
@@ -51,13 +51,19 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
     for (int q = threadIdx.x; q < MO * MI * 128; q += 256) {
         const int l = q & 63, s = (q >> 6) & 1, mi = (q >> 7) % MI, mo = (q >> 7) / MI;
         const int row = row_channel(l & 31), k = 16 * (l >> 5) + 8 * s;
+        // (all loads at once, those outside the weight from its start: a branch for each would wait for each)
+        T p[8], r[8];
         float v[8], u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int o = 32 * mo + row, ci = 32 * mi + k + i;
-            v[i] = o < a.Cout && ci < a.Cin ? (float)w[(int64_t)o * a.Cin + ci] : 0.0f;
-            const int o2 = 32 * mo + k + i, ci2 = 32 * mi + row;
-            u[i] = o2 < a.Cout && ci2 < a.Cin ? (float)w[(int64_t)o2 * a.Cin + ci2] : 0.0f;
+            const int o = 32 * mo + row, ci = 32 * mi + k + i, o2 = 32 * mo + k + i, ci2 = 32 * mi + row;
+            p[i] = w[o < a.Cout && ci < a.Cin ? o * a.Cin + ci : 0];
+            r[i] = w[o2 < a.Cout && ci2 < a.Cin ? o2 * a.Cin + ci2 : 0];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 32 * mo + row < a.Cout && 32 * mi + k + i < a.Cin ? (float)p[i] : 0.0f;
+            u[i] = 32 * mo + k + i < a.Cout && 32 * mi + row < a.Cin ? (float)r[i] : 0.0f;
         }
         const FX f = split<bf16x8, S::x>(v), g = split<bf16x8, S::x>(u);
 #pragma unroll

@@ -17,12 +17,20 @@ namespace {
 
 constexpr int kProductThreads = 512;
 
-__device__ __forceinline__ float weight_at(const ProductArgs& a, int o, int i) {
-    if (o >= a.Cout || i >= a.Cin) return 0.0f;
-    const int64_t at = a.transposed ? (int64_t)i * a.Cout + o : (int64_t)o * a.Cin + i;
-    float v = 0.0f;
-    with_field_type(a.w_type, [&](auto e) { v = (float)static_cast<const decltype(e)*>(a.w)[at]; });
-    return v;
+// Eight weights of output channel o from input channel i on, zero where there are none.  (All loads
+// at once, those outside the weight from its start: a branch for each would wait for each.)
+__device__ __forceinline__ void weights_at(const ProductArgs& a, int o, int i, float (&v)[8]) {
+    with_field_type(a.w_type, [&](auto e) {
+        typedef decltype(e) W;
+        const W* w = static_cast<const W*>(a.w);
+        const int64_t at = a.transposed ? (int64_t)i * a.Cout + o : (int64_t)o * a.Cin + i;
+        const int step = a.transposed ? a.Cout : 1;
+        W q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = w[o < a.Cout && i + k < a.Cin ? at + (int64_t)k * step : 0];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = o < a.Cout && i + k < a.Cin ? (float)q[k] : 0.0f;
+    });
 }
 
 template <int ACT, bool FINE>
@@ -49,9 +57,9 @@ constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 // What bounds it: 64 -> 64 float32 channels first with a branch and GELU, 524288 positions,
 // 81 to 89 us, 403 MB at 4.5 to 5.0 TB/s, memory (the float32 matrix instructions alone would take 27 us at
 // their peak, the six part products 10); 3 -> 64 from channels last 27 us, 140 MB at 5.1
-// TB/s.  64 -> 256 bfloat16 with GELU 158 to 164 us, 335 MB at 2.1 TB/s: the
+// TB/s.  64 -> 256 bfloat16 with GELU 157 to 164 us, 335 MB at 2.1 TB/s: the
 // vector instructions, about 20 a value of the output with the activation, the rounding
-// and the turning; 256 -> 256 with SiLU and a residual, 65536 positions, 48 us.
+// and the turning; 256 -> 256 with SiLU and a residual, 65536 positions, 45 to 48 us.
 // Two waves a SIMD with 64 or 32 channels of x on the way measured faster than three or four without
 // (64 -> 256: 164 against 208 and 268 us; 64 -> 64: 81 against 98 and 132).
 template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
@@ -77,8 +85,7 @@ __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_chann
             const int l = q & 63, mt = (q >> 6) / steps, ks = (q >> 6) % steps;
             const int o = c0 + 32 * mt + row_channel(l & 31), k = 16 * (first + ks) + 8 * (l >> 5);
             float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = weight_at(a, o, k + i);
+            weights_at(a, o, k, v);
             const Frag<V, wparts> f = split<V, wparts>(v);
 #pragma unroll
             for (int p = 0; p < wparts; ++p) wfrag[((p * MT + mt) * a.chunk + ks) * 64 + l] = f.part[p];
