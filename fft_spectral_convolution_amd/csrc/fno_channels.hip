@@ -7,35 +7,45 @@
 namespace fno {
 namespace {
 
-// grad_w and, behind it, grad_b: sums over the splits, 64 values a workgroup, each
+// grad_w and, behind it, grad_b: sums over the splits, 64 values a workgroup at a time, each
 // wave a quarter of the splits.
 __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ part, float* __restrict__ grad_w,
                                                     float* __restrict__ grad_b, int64_t weights, int couts,
                                                     int splits) {
     __shared__ double join[4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t k = (int64_t)blockIdx.x * 64 + lane, all = weights + couts;
-    double s = 0.0;
-    if (k < all) {
-        int i = wave;
-        for (; i + 28 < splits; i += 32) {
-            float v[8];
+    const int64_t all = weights + couts;
+    for (int64_t first = (int64_t)blockIdx.x * 64; first < all; first += (int64_t)gridDim.x * 64) {
+        const int64_t k = first + lane;
+        double s = 0.0;
+        if (k < all) {
+            int i = wave;
+            for (; i + 28 < splits; i += 32) {
+                float v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = part[(i + 4 * u) * all + k];
+                for (int u = 0; u < 8; ++u) v[u] = part[(i + 4 * u) * all + k];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s += (double)v[u];
+                for (int u = 0; u < 8; ++u) s += (double)v[u];
+            }
+            for (; i < splits; i += 4) s += (double)part[i * all + k];
         }
-        for (; i < splits; i += 4) s += (double)part[i * all + k];
+        join[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && k < all) {
+            const float v = (float)((join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]));
+            if (k < weights) {
+                if (grad_w) grad_w[k] = v;
+            } else if (grad_b) {
+                grad_b[k - weights] = v;
+            }
+        }
+        __syncthreads();
     }
-    join[wave][lane] = s;
-    __syncthreads();
-    if (wave || k >= all) return;
-    const float v = (float)((join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]));
-    if (k < weights) {
-        if (grad_w) grad_w[k] = v;
-    } else if (grad_b) {
-        grad_b[k - weights] = v;
-    }
+}
+
+// Workgroups of it: a grid's threads are counted in 32 bits, the weights are up to 2^32.
+unsigned sum_groups(const ChannelProduct& c) {
+    return (unsigned)std::min<int64_t>(((int64_t)c.Cin * c.Cout + c.Cout + 63) / 64, 1 << 20);
 }
 
 // Shares of the positions: up to two workgroups a CU, each of a tile of 32 a wave or more.
@@ -177,7 +187,7 @@ hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool b
         return launch_channel_weight_grad(w, c.x_type, g_type, c.x_last, c.out_last, s);
     }
     const int64_t weights = (int64_t)c.Cin * c.Cout;
-    return launch_kernel(k_weight_sum, dim3((unsigned)((weights + c.Cout + 63) / 64)), dim3(256), 0, s,
+    return launch_kernel(k_weight_sum, dim3(sum_groups(c)), dim3(256), 0, s,
                          static_cast<const float*>(part), a.grad_w, a.grad_b, weights, c.Cout, splits);
 }
 

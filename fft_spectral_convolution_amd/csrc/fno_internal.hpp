@@ -42,6 +42,10 @@ LaunchEvents take_launch_events();
 // and end timestamps (no marker packets between dependent kernels).
 template <typename K, typename... Args>
 hipError_t launch_kernel(K kernel, dim3 grid, dim3 block, size_t lds, hipStream_t s, Args... args) {
+    // threads are counted in 32 bits along an axis: a larger grid would run, but only what its low bits say
+    if ((std::uint64_t)grid.x * block.x >> 32 || (std::uint64_t)grid.y * block.y >> 32 ||
+        (std::uint64_t)grid.z * block.z >> 32)
+        return hipErrorInvalidConfiguration;
     const LaunchEvents ev = take_launch_events();
     hipExtLaunchKernelGGL(kernel, grid, block, (std::uint32_t)lds, s, ev.start, ev.stop, 0u, args...);
     return hipGetLastError();
