@@ -1,6 +1,5 @@
 // Channel products: which kernels a call runs, and the gradient of the weight.
 #include <algorithm>
-#include <string_view>
 
 #include "fno_channels.hpp"
 
@@ -92,50 +91,99 @@ size_t channel_workspace(const ChannelProduct& c, bool backward) {
     return g + round_up((size_t)splits * ((size_t)c.Cin + 1) * c.Cout * sizeof(float));
 }
 
-int channel_kernels(const ChannelProduct& c, const ChannelArgs& a, bool backward, const char** names) {
+namespace {
+
+// The kernels of a call.
+enum Step { kForward, kSlope, kGradX, kGradW, kOnePass, kSum };
+
+int steps_of(const ChannelProduct& c, const ChannelArgs& a, bool backward, Step* steps) {
     if (!backward) {
-        names[0] = "channels";
+        steps[0] = kForward;
         return 1;
     }
     int n = 0;
     const bool sums = a.grad_w || a.grad_b;
     if (fits(c)) {
-        names[n++] = "channels_bwd";
+        steps[n++] = kOnePass;
     } else {
-        if (keeps_g(c)) names[n++] = "channels_slope";
-        if (a.grad_x) names[n++] = "channels_grad_x";
-        if (sums) names[n++] = "channels_grad_w";
+        if (keeps_g(c)) steps[n++] = kSlope;
+        if (a.grad_x) steps[n++] = kGradX;
+        if (sums) steps[n++] = kGradW;
     }
-    if (sums) names[n++] = "channels_grad_sum";
+    if (sums) steps[n++] = kSum;
+    return n;
+}
+
+// Types of what a product reads and writes, and its channels: of the step kForward, kSlope or kGradX.
+struct Sides {
+    int x_type, out_type;
+    bool last, out_last;
+};
+Sides sides_of(const ChannelProduct& c, Step step) {
+    if (step == kGradX) return {keeps_g(c) ? kTypeF32 : c.out_type, c.x_type, c.out_last, c.x_last};
+    return {c.x_type, c.out_type, c.x_last, c.out_last};
+}
+ProductArgs product_of(const ChannelProduct& c, Step step) {
+    ProductArgs q{};
+    q.B = c.B;
+    q.P = c.P;
+    q.Cin = step == kGradX ? c.Cout : c.Cin;
+    q.Cout = step == kGradX ? c.Cin : c.Cout;
+    q.w_type = c.x_type;
+    return q;
+}
+
+// A kernel's name, with the form it takes: output channels a wave, and whether the weight
+// takes a workgroup of eight waves (wide) or does not fit LDS at all (staged).
+#define FNO_FORMS(name) \
+    {name "_32", name "_32_wide", name "_32_staged", name "_64", name "_64_wide", name "_64_staged", \
+     name "_128", name "_128_wide", name "_128_staged"}
+const char* name_of(const ChannelProduct& c, Step step) {
+    static const char* const forms[3][9] = {FNO_FORMS("channels"), FNO_FORMS("channels_slope"),
+                                            FNO_FORMS("channels_grad_x")};
+    switch (step) {
+        case kGradW: return "channels_grad_w";
+        case kOnePass: return "channels_bwd";
+        case kSum: return "channels_grad_sum";
+        default: break;
+    }
+    const Sides t = sides_of(c, step);
+    const ProductPlan p = plan_product(product_of(c, step), t.x_type, t.out_type, t.last && t.out_last);
+    return forms[step][(p.mt == 4 ? 6 : p.mt == 2 ? 3 : 0) + (p.chunk < p.nks ? 2 : p.waves == 8 ? 1 : 0)];
+}
+#undef FNO_FORMS
+
+}  // namespace
+
+int channel_kernels(const ChannelProduct& c, const ChannelArgs& a, bool backward, const char** names) {
+    Step steps[4];
+    const int n = steps_of(c, a, backward, steps);
+    for (int k = 0; k < n; ++k) names[k] = name_of(c, steps[k]);
     return n;
 }
 
 hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool backward, int kernel, hipStream_t s) {
-    const char* names[4] = {};
-    channel_kernels(c, a, backward, names);
-    const bool slope = names[kernel] == std::string_view("channels_slope");
-    ProductArgs q{};
-    q.B = c.B;
-    q.P = c.P;
-    q.Cin = c.Cin;
-    q.Cout = c.Cout;
+    Step steps[4];
+    steps_of(c, a, backward, steps);
+    const Step step = steps[kernel];
+    const Sides t = sides_of(c, step);
+    ProductArgs q = product_of(c, step);
     q.x = a.x;
     q.w = a.w;
-    q.w_type = c.x_type;
     q.bias = a.bias;
     q.branch = a.branch;
     q.branch_after = c.branch_after;
     q.act = c.act;
-    if (!backward) {
+    if (step == kForward) {
         q.out = a.out;
-        return launch_product(q, c.x_type, c.x_last, c.out_last, c.out_type, s);
+        return launch_product(q, t.x_type, t.last, t.out_last, t.out_type, s);
     }
     float* g = static_cast<float*>(a.ws);
     const bool own_g = keeps_g(c) && !fits(c);
     float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
                                            (own_g ? round_up((size_t)(c.B * c.P * c.Cout) * sizeof(float)) : 0));
     const int splits = fits(c) ? backward_groups(c) : weight_splits(c);
-    if (names[kernel] == std::string_view("channels_bwd")) {
+    if (step == kOnePass) {
         BackwardArgs b{};
         b.x = a.x;
         b.w = a.w;
@@ -153,28 +201,26 @@ hipError_t launch_channels(const ChannelProduct& c, const ChannelArgs& a, bool b
         b.groups = splits;
         return launch_backward(b, c, s);
     }
-    if (slope) {
+    if (step == kSlope) {
         if (c.branch_after) q.branch = nullptr;
         q.slope = true;
         q.grad = a.out;
         q.g = g;
         q.out = a.grad_branch;
-        return launch_product(q, c.x_type, c.x_last, c.out_last, c.out_type, s);
+        return launch_product(q, t.x_type, t.last, t.out_last, t.out_type, s);
     }
     const void* gp = own_g ? static_cast<const void*>(g) : a.out;
     const int g_type = own_g ? kTypeF32 : c.out_type;
-    if (names[kernel] == std::string_view("channels_grad_x")) {
+    if (step == kGradX) {
         q.x = gp;
         q.bias = nullptr;
         q.branch = nullptr;
         q.act = kActNone;
         q.transposed = true;
-        q.Cin = c.Cout;
-        q.Cout = c.Cin;
         q.out = a.grad_x;
-        return launch_product(q, g_type, c.out_last, c.x_last, c.x_type, s);
+        return launch_product(q, t.x_type, t.last, t.out_last, t.out_type, s);
     }
-    if (names[kernel] == std::string_view("channels_grad_w")) {
+    if (step == kGradW) {
         WeightGradArgs w{};
         w.x = a.x;
         w.g = gp;

@@ -48,19 +48,19 @@ template <>
 struct Operand<float> {
     typedef __bf16 E;
     typedef bf16x8 V;
-    static constexpr int parts = 3;
+    static constexpr int type = kTypeF32, parts = 3;
 };
 template <>
 struct Operand<bf16> {
     typedef __bf16 E;
     typedef bf16x8 V;
-    static constexpr int parts = 1;
+    static constexpr int type = kTypeBf16, parts = 1;
 };
 template <>
 struct Operand<f16> {
     typedef _Float16 E;
     typedef f16x8 V;
-    static constexpr int parts = 1;
+    static constexpr int type = kTypeF16, parts = 1;
 };
 
 template <typename V, int N>
@@ -550,6 +550,43 @@ struct ProductArgs {
     int groups;              // workgroups over the positions
     int chunk, nks;          // steps of 16 input channels: in LDS at a time, in all
 };
+
+// Parts that a product's weight is held in: it is of x's type, beside a float32 x and a 16-bit result of the result's.
+constexpr int weight_parts(int x_type, int out_type) {
+    return x_type != kTypeF32 || out_type == kTypeBf16 ? 1 : out_type == kTypeF16 ? 2 : 3;
+}
+// Steps of 16 channels that are loaded before they are used: 64 channels of 16
+// bits, 32 of 32 bits.  Chunks of staged weights are whole numbers of them.
+constexpr int steps_ahead(int x_type) { return x_type == kTypeF32 ? 2 : 4; }
+constexpr int positions_a_wave(bool merged) { return merged ? 32 : 64; }
+
+// The form of the kernel that a product takes.
+struct ProductPlan {
+    int mt;          // 32-channel parts of the output a wave: 1, 2 or 4
+    int waves;       // a workgroup: 4 or 8
+    int nks, chunk;  // steps of 16 input channels: in all, in LDS at a time
+};
+inline ProductPlan plan_product(const ProductArgs& a, int x_type, int out_type, bool merged) {
+    const int width = positions_a_wave(merged);
+    const int64_t runs = merged ? 1 : a.B, length = merged ? a.B * a.P : a.P;
+    const int64_t groups = (runs * ((length + width - 1) / width) + 3) / 4;
+    ProductPlan p;
+    // As many output channels a wave as there are, up to 128, so that x is read once; fewer where
+    // that would leave half of the CUs without a workgroup, since a wave's latency is all there is
+    // then (one position, 256 -> 256 bfloat16: 13.6 us with 32 channels a wave, 27.0 with 128; 512
+    // positions, 128 -> 256 float32: 13.0 and 36.8; 4 x 1024 positions, 64 -> 64 float32: 10.7 with 32, 15.0 with 64).
+    p.mt = a.Cout > 64 && groups * ((a.Cout + 127) / 128) >= 128  ? 4
+           : a.Cout > 32 && groups * ((a.Cout + 63) / 64) >= 128 ? 2
+                                                                 : 1;
+    p.nks = (a.Cin + 15) / 16;
+    const int step = weight_parts(x_type, out_type) * p.mt * 1024;          // bytes of weights for 16 input channels
+    // 60 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
+    const bool wide = (int64_t)p.nks * step > 60 * 1024;
+    const int most = (wide ? 120 : 60) * 1024 / step, ahead = steps_ahead(x_type);
+    p.waves = wide ? 8 : 4;
+    p.chunk = p.nks <= most ? p.nks : most / ahead * ahead;
+    return p;
+}
 // By type of x; out is of out_type (x's or float32; any for float32).
 hipError_t launch_product_f32(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);
 hipError_t launch_product_bf16(const ProductArgs& a, bool last, bool out_last, int out_type, hipStream_t s);

@@ -44,15 +44,10 @@ __device__ __forceinline__ void activate(float (&z)[16], bool slope) {
 // result's type, held exactly by one (bfloat16) or two parts, and two parts of g are within 2^-18 of it.
 template <typename T, typename TO>
 struct Parts {
-    static constexpr bool g = sizeof(T) == 4 && sizeof(TO) == 2, f16g = g && __is_same(TO, f16);
-    static constexpr int x = g ? 2 : Operand<T>::parts, w = f16g ? 2 : g ? 1 : Operand<T>::parts,
+    static constexpr bool g = sizeof(T) == 4 && sizeof(TO) == 2;
+    static constexpr int x = g ? 2 : Operand<T>::parts, w = weight_parts(Operand<T>::type, Operand<TO>::type),
                          most = g ? 1 : Operand<T>::parts - 1;
 };
-
-// Steps of 16 channels that are loaded before they are used: 64 channels of 16
-// bits, 32 of 32 bits.  Chunks of staged weights are whole numbers of them.
-template <typename T>
-constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 
 // What bounds it: 64 -> 64 float32 channels first with a branch and GELU, 524288 positions,
 // 81 to 89 us, 403 MB at 4.5 to 5.0 TB/s, memory (the float32 matrix instructions alone would take 27 us at
@@ -66,7 +61,7 @@ template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
 __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_channels(ProductArgs a) {
     typedef Parts<T, TO> Q;
     typedef typename Operand<T>::V V;
-    constexpr int parts = Q::x, wparts = Q::w, ahead = kAhead<T>;
+    constexpr int parts = Q::x, wparts = Q::w, ahead = steps_ahead(Operand<T>::type);
     extern __shared__ __align__(16) unsigned char lds[];
     V* wfrag = reinterpret_cast<V*>(lds);                     // [part][mt][chunk][64]
     float* bias = reinterpret_cast<float*>(wfrag + wparts * MT * a.chunk * 64);
@@ -197,37 +192,31 @@ __global__ __launch_bounds__(kProductThreads, MT * NT <= 2 ? 3 : 2) void k_chann
 }
 
 template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
-hipError_t launch_tiles(ProductArgs a, hipStream_t s) {
+hipError_t launch_tiles(ProductArgs a, const ProductPlan& plan, hipStream_t s) {
     a.tiles_item = (int)((a.P + 32 * NT - 1) / (32 * NT));
     a.tiles = a.B * a.tiles_item;
     a.cout_tiles = (a.Cout + 32 * MT - 1) / (32 * MT);
-    a.nks = (a.Cin + 15) / 16;
-    constexpr int step = Parts<T, TO>::w * MT * 1024;           // bytes of weights for 16 input channels
-    // 60 KiB leave room for two workgroups of four waves a CU; one of eight has twice that
-    const bool wide = (int64_t)a.nks * step > 60 * 1024;
-    const int most = (wide ? 120 : 60) * 1024 / step;
-    a.chunk = a.nks <= most ? a.nks : most / kAhead<T> * kAhead<T>;
-    const int waves = wide ? 8 : 4;
+    a.nks = plan.nks;
+    a.chunk = plan.chunk;
+    const int waves = plan.waves;
     // as many waves as the CUs hold; groups of workgroups that read the same positions are dealt out in eights
     const int64_t most_groups = 256 * (MT * NT <= 2 ? 3 : 2) * 4 / waves / std::min(a.cout_tiles, 8);
     a.groups = (int)std::max<int64_t>(1, std::min<int64_t>((a.tiles + waves - 1) / waves, most_groups));
     if (a.groups > 8) a.groups = (a.groups + 7) / 8 * 8;
-    const size_t lds = (size_t)a.chunk * step + 32 * MT * sizeof(float) + (OUT_LAST ? waves * kTurnBytes : 0);
+    const size_t lds = (size_t)a.chunk * Parts<T, TO>::w * MT * 1024 + 32 * MT * sizeof(float) +
+                       (OUT_LAST ? waves * kTurnBytes : 0);
     return launch_kernel(k_channels<T, TO, LAST, OUT_LAST, MT, NT>, dim3((unsigned)(a.groups * a.cout_tiles)),
                          dim3(64 * waves), lds, s, a);
 }
 
 template <typename T, typename TO, bool LAST, bool OUT_LAST>
 hipError_t launch_couts(const ProductArgs& a, hipStream_t s) {
-    constexpr int NT = LAST && OUT_LAST ? 1 : 2;
-    // As many output channels a wave as there are, up to 128, so that x is read once; fewer where
-    // that would leave half of the CUs without a workgroup, since a wave's latency is all there is
-    // then (one position, 256 -> 256 bfloat16: 13.6 us with 32 channels a wave, 27.0 with 128; 512
-    // positions, 128 -> 256 float32: 13.0 and 36.8; 4 x 1024 positions, 64 -> 64 float32: 10.7 with 32, 15.0 with 64).
-    const int64_t groups = (a.B * ((a.P + 32 * NT - 1) / (32 * NT)) + 3) / 4;
-    if (a.Cout > 64 && groups * ((a.Cout + 127) / 128) >= 128) return launch_tiles<T, TO, LAST, OUT_LAST, 4, NT>(a, s);
-    if (a.Cout > 32 && groups * ((a.Cout + 63) / 64) >= 128) return launch_tiles<T, TO, LAST, OUT_LAST, 2, NT>(a, s);
-    return launch_tiles<T, TO, LAST, OUT_LAST, 1, NT>(a, s);
+    constexpr bool merged = LAST && OUT_LAST;
+    constexpr int NT = positions_a_wave(merged) / 32;
+    const ProductPlan plan = plan_product(a, Operand<T>::type, Operand<TO>::type, merged);
+    if (plan.mt == 4) return launch_tiles<T, TO, LAST, OUT_LAST, 4, NT>(a, plan, s);
+    if (plan.mt == 2) return launch_tiles<T, TO, LAST, OUT_LAST, 2, NT>(a, plan, s);
+    return launch_tiles<T, TO, LAST, OUT_LAST, 1, NT>(a, plan, s);
 }
 
 // all channels last: one run of positions
