@@ -476,6 +476,26 @@ __device__ __forceinline__ Frag<bf16x8, N> step_of(const T* v, int s) {
     return split<bf16x8, N>(f);
 }
 
+// What a product with the identity must not see: 0 times an infinity or NaN takes all 32 channels of a
+// position along.  Such a value of g makes its row of grad_weight and its entry of grad_bias infinite or NaN, one
+// of x its column; here it is set to zero and its channel is marked, whose sums leave as NaN.  For every tile
+// this would cost 5% of a backward pass, so it is done only where sums show such a value, in another
+// pass over their tiles.
+template <int N>
+__device__ __forceinline__ void set_apart(Frag<bf16x8, N> (&a)[2], uint32_t* marked) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool bad = !(fabsf((float)a[s].part[0][i]) < __builtin_inff());
+            __hip_atomic_fetch_or(marked + 16 * h + 8 * s + i, bad ? 1u : 0u, __ATOMIC_RELAXED,
+                                  __HIP_MEMORY_SCOPE_WORKGROUP);
+#pragma unroll
+            for (int p = 0; p < N; ++p) a[s].part[p][i] = bad ? (__bf16)0.0f : a[s].part[p][i];
+        }
+}
+
 // A 32 x 32 part of an operand, turned: lanes hold what was its steps' k.  Returns the sum of the lane's values.
 template <int N>
 __device__ __forceinline__ float turned(const Frag<bf16x8, N> (&a)[2], const bf16x8 (&one)[2],
@@ -497,11 +517,28 @@ __device__ __forceinline__ float turned(const Frag<bf16x8, N> (&a)[2], const bf1
     return sum;
 }
 
+// Whether any of a wave's sums is not finite.
+template <int MO, int MI>
+__device__ __forceinline__ bool any_not_finite(const f32x16 (&dw)[MO][MI], const float (&db)[MO]) {
+    float m[4] = {};                        // 0, or a NaN from then on
+#pragma unroll
+    for (int mo = 0; mo < MO; ++mo) {
+        m[0] = fmaf(db[mo], 0.0f, m[0]);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) m[r & 3] = fmaf(dw[mo][mi][r], 0.0f, m[r & 3]);
+    }
+    return __builtin_amdgcn_ballot_w64((m[0] + m[1]) + (m[2] + m[3]) != 0.0f) != 0;
+}
+
 // Sums of g x (and of g) that four waves of a workgroup hold, joined one after the
 // other, so in a fixed order: rows o0.., columns i0.. of part [Cout][Cin] and, of the
-// first columns' workgroup, the sums of g behind it.  join holds MO MI 1024 floats, sums 32 MO.
+// first columns' workgroup, the sums of g behind it.  join holds MO MI 1024 floats, sums 32 MO; marked_o and
+// marked_i are the marks of these rows and columns, looked at where *spoilt is not 0 (null: not).
 template <int MO, int MI>
 __device__ __forceinline__ void join_sums(const f32x16 (&dw)[MO][MI], const float (&db)[MO], float* join, float* sums,
+                                          const uint32_t* spoilt, const uint32_t* marked_o, const uint32_t* marked_i,
                                           float* part, int o0, int i0, int Cout, int Cin) {
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -522,13 +559,17 @@ __device__ __forceinline__ void join_sums(const f32x16 (&dw)[MO][MI], const floa
         }
     }
     __syncthreads();
+    const bool look = spoilt && __builtin_amdgcn_readfirstlane(*spoilt);
     for (int q = threadIdx.x; q < MO * MI * 1024; q += 256) {
         const int l = q & 63, r = (q >> 6) & 15, mi = (q >> 10) % MI, mo = (q >> 10) / MI;
-        const int o = o0 + 32 * mo + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), i = i0 + 32 * mi + (l & 31);
-        if (o < Cout && i < Cin) part[(int64_t)o * Cin + i] = join[q];
+        const int o = 32 * mo + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), i = 32 * mi + (l & 31);
+        const bool marked = look && (marked_o[o] | marked_i[i]);
+        if (o0 + o < Cout && i0 + i < Cin)
+            part[(int64_t)(o0 + o) * Cin + i0 + i] = marked ? __builtin_nanf("") : join[q];
     }
     if (i0 == 0)
-        for (int o = threadIdx.x; o < 32 * MO && o0 + o < Cout; o += 256) part[(int64_t)Cin * Cout + o0 + o] = sums[o];
+        for (int o = threadIdx.x; o < 32 * MO && o0 + o < Cout; o += 256)
+            part[(int64_t)Cin * Cout + o0 + o] = look && marked_o[o] ? __builtin_nanf("") : sums[o];
 }
 
 // ---- the product's kernel (fno_channels_kernel.hpp) ---------------------------------

@@ -45,7 +45,9 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
     float* bias = reinterpret_cast<float*>(wx + S::x * MO * MI * 128);
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    unsigned char* const turn = reinterpret_cast<unsigned char*>(bias + 32 * MO) + (threadIdx.x >> 6) * kTurnBytes;
+    uint32_t* const marked = reinterpret_cast<uint32_t*>(bias + 32 * MO);        // rows o, columns i, whether any
+    unsigned char* const turn =
+        reinterpret_cast<unsigned char*>(marked + 32 * (MO + MI + 1)) + (threadIdx.x >> 6) * kTurnBytes;
 
     const T* w = static_cast<const T*>(a.w);
     for (int q = threadIdx.x; q < MO * MI * 128; q += 256) {
@@ -73,6 +75,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
         }
     }
     for (int i = threadIdx.x; i < 32 * MO; i += 256) bias[i] = a.bias && i < a.Cout ? a.bias[i] : 0.0f;
+    for (int i = threadIdx.x; i <= 32 * (MO + MI); i += 256) marked[i] = 0;
     __syncthreads();
 
     bf16x8 one[2];
@@ -91,7 +94,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
 #pragma unroll
             for (int r = 0; r < 16; ++r) dw[mo][mi][r] = 0.0f;
     }
-    auto tile_at = [&](int64_t t) {
+    auto tile_at = [&](int64_t t) __attribute__((always_inline)) {
         Tile q;
         q.item = a.merged ? 0 : t / a.tiles_item;
         q.p0 = (a.merged ? t : t % a.tiles_item) * 32;
@@ -100,7 +103,7 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
         q.full = q.p0 + 32 <= a.P;
         return q;
     };
-    auto fetch_x = [&](Values<T> (&raw)[MI], const Tile& t) {
+    auto fetch_x = [&](Values<T> (&raw)[MI], const Tile& t) __attribute__((always_inline)) {
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
             if (32 * mi < a.Cin) {
@@ -388,14 +391,88 @@ __global__ __launch_bounds__(256, MO * MI == 1 ? 2 : 1) void k_channels_bwd(Back
     }
 
     if (!a.part) return;
+    uint32_t* const spoilt = marked + 32 * (MO + MI);
+    if (__builtin_expect(any_not_finite<MO, MI>(dw, db), 0)) {
+        *spoilt = 1;
+        // the wave's sums again, 32 output channels at a time, with what is not finite set apart
+#pragma unroll 1
+        for (int mo = 0; 32 * mo < a.Cout; ++mo) {
+            f32x16 sum[MI];
+            float sum_b = 0.0f;
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sum[mi][r] = 0.0f;
+#pragma unroll 1
+            for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tiles; t += (int64_t)a.groups * 4) {
+                const Tile tile = tile_at(t);
+                Values<T> raw[MI];
+                fetch_x(raw, tile);
+                FX x[MI][2];
+                f32x16 z;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) z[r] = bias[32 * mo + 16 * h + r];
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    raw[mi].keep(a.Cin, 32 * mi);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        x[mi][s] = step_of<S::x>(raw[mi].v, s);
+                        FX f;
+#pragma unroll
+                        for (int p = 0; p < S::x; ++p)
+                            f.part[p] = wz[(((p * MO + mo) * MI + mi) * 2 + s) * 64 + lane];
+                        z = mfma_upto<S::z>(f, x[mi][s], z);
+                    }
+                }
+                const Places<TG, OUT_LAST, 1> at(tile, a.Cout, a.P, a.B, 32 * mo);
+                Values<TG> go, br;
+                at.fetch(a.grad, 0, go);
+                go.keep(a.Cout, 32 * mo);
+                if (a.branch) {
+                    at.fetch(a.branch, 0, br);
+                    br.keep(a.Cout, 32 * mo);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] += (float)br.v[i];
+                }
+                float g[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    g[i] = (float)go.v[i];
+                    if (a.act == kActGelu) g[i] *= act_slope<kActGelu>(z[i]);
+                    if (a.act == kActSilu) g[i] *= act_slope<kActSilu>(z[i]);
+                }
+                FG gs[2], gt[2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) gs[s] = step_of<3>(g, s);
+                set_apart(gs, marked + 32 * mo);
+                sum_b += turned(gs, one, gt);
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    FX xt[2];
+                    set_apart(x[mi], marked + 32 * (MO + mi));
+                    turned(x[mi], one, xt);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) sum[mi] = mfma_upto<S::gw>(gt[s], xt[s], sum[mi]);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MO; ++m) {
+                if (m != mo) continue;
+                db[m] = sum_b;
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) dw[m][mi] = sum[mi];
+            }
+        }
+    }
     // (the weights in LDS are no longer needed)
-    join_sums<MO, MI>(dw, db, reinterpret_cast<float*>(lds), bias, a.part + (int64_t)blockIdx.x * (a.Cin + 1) * a.Cout,
-                      0, 0, a.Cout, a.Cin);
+    join_sums<MO, MI>(dw, db, reinterpret_cast<float*>(lds), bias, spoilt, marked, marked + 32 * MO,
+                      a.part + (int64_t)blockIdx.x * (a.Cin + 1) * a.Cout, 0, 0, a.Cout, a.Cin);
 }
 
 template <typename T, typename TG, bool LAST, bool OUT_LAST, int MO, int MI>
 hipError_t launch_backward_tiles(BackwardArgs a, hipStream_t s) {
-    const size_t lds = (size_t)2 * Scheme<T>::x * MO * MI * 2048 + 32 * MO * sizeof(float) +
+    const size_t lds = (size_t)2 * Scheme<T>::x * MO * MI * 2048 + 32 * (2 * MO + MI + 1) * sizeof(float) +
                        (LAST || OUT_LAST ? 4 * kTurnBytes : 0);
     return launch_kernel(k_channels_bwd<T, TG, LAST, OUT_LAST, MO, MI>, dim3((unsigned)a.groups), dim3(256), lds, s, a);
 }

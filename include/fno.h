@@ -457,7 +457,11 @@ int fno_channel_linear(const void* x, const void* weight, const float* bias, con
  * Each may be NULL, not all; they are overwritten.  grad_branch is for
  * branch_after = 0 and an activation alone: otherwise it is grad_out itself
  * (FNO_ERR_VALUE).  branch is not read with branch_after = 1.  Sums run in a
- * fixed order: equal inputs give equal bits.  `workspace`: as for fno_group_norm,
+ * fixed order: equal inputs give equal bits.  A value of g that is not finite (or is
+ * beyond bfloat16's largest finite one) makes grad_x infinite or NaN at its
+ * position, grad_weight in the row and grad_bias in the entry of its channel; one of x
+ * grad_weight in the column of its channel and, with an activation, g at its
+ * position; no others.  `workspace`: as for fno_group_norm,
  * fno_channel_linear_workspace_size bytes.
  */
 size_t fno_channel_linear_workspace_size(int B, int Cin, int Cout, int P, int act, int x_last, int out_last,
