@@ -47,9 +47,14 @@ unsigned sum_groups(const ChannelProduct& c) {
     return (unsigned)std::min<int64_t>(((int64_t)c.Cin * c.Cout + c.Cout + 63) / 64, 1 << 20);
 }
 
-// Shares of the positions: up to two workgroups a CU, each of a tile of 32 a wave or more.
+// Tiles of 32 positions that a backward pass goes through: all positions are one run where both sides are channels last.
+int64_t tiles_of(const ChannelProduct& c) {
+    return c.x_last && c.out_last ? (c.B * c.P + 31) / 32 : c.B * ((c.P + 31) / 32);
+}
+
+// Shares of the positions: up to two workgroups a CU, each of a tile a wave or more.
 int weight_splits(const ChannelProduct& c) {
-    const int64_t tiles = c.B * ((c.P + 31) / 32);
+    const int64_t tiles = tiles_of(c);
     const int64_t parts = (int64_t)((c.Cin + 63) / 64) * ((c.Cout + 63) / 64);
     return (int)std::max<int64_t>(1, std::min<int64_t>(tiles / 4, 512 / parts));
 }
@@ -69,8 +74,7 @@ bool fits(const ChannelProduct& c) { return backward_fits(c.Cin, c.Cout, c.x_typ
 
 // Workgroups of the one-kernel backward pass: one a CU, two where the registers that 32 channels take leave room.
 int backward_groups(const ChannelProduct& c) {
-    const int64_t tiles = c.x_last && c.out_last ? (c.B * c.P + 31) / 32 : c.B * ((c.P + 31) / 32);
-    return (int)std::min<int64_t>((tiles + 3) / 4, std::max(c.Cin, c.Cout) <= 32 ? 512 : 256);
+    return (int)std::min<int64_t>((tiles_of(c) + 3) / 4, std::max(c.Cin, c.Cout) <= 32 ? 512 : 256);
 }
 
 hipError_t launch_backward(const BackwardArgs& a, const ChannelProduct& c, hipStream_t s) {
