@@ -47,7 +47,7 @@ unsigned sum_groups(const ChannelProduct& c) {
     return (unsigned)std::min<int64_t>(((int64_t)c.Cin * c.Cout + c.Cout + 63) / 64, 1 << 20);
 }
 
-// Tiles of 32 positions that a backward pass goes through: all positions are one run where both sides are channels last.
+// Tiles of 32 positions that a backward pass takes: where both sides are channels last, all positions are one run.
 int64_t tiles_of(const ChannelProduct& c) {
     return c.x_last && c.out_last ? (c.B * c.P + 31) / 32 : c.B * ((c.P + 31) / 32);
 }

@@ -11,12 +11,13 @@
 // layout are read and written from registers as they lie.
 //
 // float32 values take three bfloat16 parts, each the rounding of what the ones
-// before it leave: 8 bits of fraction each, 24 together.  Of the nine products
-// of parts the six largest are formed; what the other three would add is below
-// 2^-26 of the product.  The 16-bit instructions do 16 times the float32 one's
-// work in the same time, so six of them still take 3/8 of it.  A part of an
-// infinity, or of a value above bfloat16's largest (3.39e38), is an infinity and
-// the rest then a NaN: such inputs give a NaN where float32 sums might give an infinity.
+// before it leave: a part leaves up to 2^-8 of a value, two 2^-17, three nothing.
+// Of the nine products of parts the six largest are formed; what the other three
+// would add is up to 2 2^-25 + 2^-34 of the product, which is what a float32 product's
+// rounding takes.  The 16-bit instructions do 16 times the float32 one's work in
+// the same time, so six of them still take 3/8 of it.  A part of an infinity, or of
+// a value above bfloat16's largest (3.39e38), is an infinity and the rest then a
+// NaN: such inputs give a NaN where float32 sums might give an infinity.
 #pragma once
 
 #include <algorithm>

@@ -16,9 +16,9 @@
 // Channels and positions that do not exist are zeros of both operands.
 //
 // g of a 16-bit field is three bfloat16 parts as a float32 one's is: the parameters'
-// gradients are float32 sums, in which two parts would leave 2^-18 of every g.  grad_x,
-// rounded to 16 bits, takes two of them.  x and W of float16 are two parts each,
-// which hold them exactly.
+// gradients are float32 sums, in which two parts would leave up to 2^-17 of every g.  grad_x,
+// rounded to 16 bits, takes two of them, of float16 without the second parts' product (2^-16).  x
+// and W of float16 are two parts each, which hold them exactly.
 //
 // Included by one source file for each pair of types, so that they build side by side.
 #pragma once

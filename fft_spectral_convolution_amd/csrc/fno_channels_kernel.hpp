@@ -41,7 +41,8 @@ __device__ __forceinline__ void activate(float (&z)[16], bool slope) {
 
 // Parts of x and of the weight, and the products of them that are formed (i + j up to `most`).  A
 // float32 x with a 16-bit result is the g of a 16-bit field's backward pass: the weight is of the
-// result's type, held exactly by one (bfloat16) or two parts, and two parts of g are within 2^-18 of it.
+// result's type, held exactly by one (bfloat16) or two parts.  Two parts of g are within 2^-17 of it, and a float16
+// weight's product leaves out its second part with g's, up to 2^-16: a step of the result is 2^-7 or 2^-10.
 template <typename T, typename TO>
 struct Parts {
     static constexpr bool g = sizeof(T) == 4 && sizeof(TO) == 2;

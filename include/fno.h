@@ -454,6 +454,10 @@ int fno_channel_linear(const void* x, const void* weight, const float* bias, con
  *   grad_x = weight^T g (x's layout and type),  grad_weight[o][i] = sum_{b,p} g[o] x[i],
  *   grad_bias[o] = sum_{b,p} g[o] (float32, whatever x's type),  grad_branch = g (out's)
  *
+ * Sums are float32.  float32 products are as good as float32's own, those of the
+ * parameters' gradients too; for grad_x of a 16-bit field g is taken to 2^-17 of
+ * itself, float16 products to 2^-16 besides, before the result's one rounding.
+ *
  * Each may be NULL, not all; they are overwritten.  grad_branch is for
  * branch_after = 0 and an activation alone: otherwise it is grad_out itself
  * (FNO_ERR_VALUE).  branch is not read with branch_after = 1.  Sums run in a

@@ -91,8 +91,8 @@ class Case:
         self.X, self.W = points(self.x, last), self.w.double()
         self.z = self.X @ self.W.t().contiguous()
         size = self.X.abs() @ self.W.t().abs().contiguous()
-        for t in ([self.bias.double()] if bias else []) + ([points(self.branch, out_last)] if branch == "before" else []):
-            self.z, size = self.z + t, size + t.abs()
+        for t in (self.bias.double() if bias else 0, points(self.branch, out_last) if branch == "before" else 0):
+            self.z, size = self.z + t, size + abs(t)
         products, omitted = parts(x_type)
         self.z_bound = ((products * cin + 2) * EPS + omitted) * size
 
