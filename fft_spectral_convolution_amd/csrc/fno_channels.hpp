@@ -103,8 +103,10 @@ __device__ __forceinline__ f32x16 mfma_upto(const Frag<V, NA>& a, const Frag<V, 
 // many output channels are bound by: gelu(z) = max(z, 0) - |z| Phi(-|z|), and
 // log2 Phi(-a) is a smooth function that a polynomial gives without a
 // division: least squares of the error times Phi^1/2, made level, on [0, 6]; it
-// falls on up to 12, where Phi is 2^-97 or less.  Degree 8: gelu within 8e-8, and
-// 2e-7 |z| for small z; degree 6, for results rounded to 16 bits: 2.2e-7 and 4e-7 |z|.
+// falls on up to 12, where Phi is 2^-97 or less.  Degree 8: gelu within 9e-8, and
+// of its own value within 5e-7 down to z = -1, 4e-4 down to -5.5; degree 6, for results
+// rounded to 16 bits: 2.2e-7, 1.4e-6 and 7e-4.  Below -5.5, where gelu is less than
+// 1.1e-7 in size, within 1e-10, which is not a small part of it any more.
 template <int ACT, bool FINE>
 __device__ __forceinline__ float product_act(float z) {
     if constexpr (ACT == kActGelu) {

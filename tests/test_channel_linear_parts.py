@@ -60,7 +60,7 @@ def whole(*values, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("cin,positions", [(1, 5), (1, 9000), (3, 40), (64, 129)])
 def test_forward(cin, positions):
-    """One sign, every operand at its worst: six products a channel and the bias, each addition off by EPS of the sum."""
+    """One sign, every operand at its worst: six products a channel, each addition off by EPS of the sum."""
     need_gpu()
     x = torch.full((positions, cin), WORST, dtype=F32, device=DEV)
     for cout in (1, 70):
