@@ -490,8 +490,10 @@ int fno_channel_linear_backward(const void* x, const void* weight, const float* 
  * params are float32, bfloat16, float16 or complex64; grads any of the first
  * three types (complex64 where the parameter is).  out_* may be the tensors
  * themselves (in place) or others; nothing written may overlap anything else,
- * the same tensor given twice included (FNO_ERR_ALIAS).  Arithmetic is float32
- * (8-bit moments: float64 up to the code); a 16-bit parameter is rounded once.
+ * the same tensor given twice included (FNO_ERR_ALIAS).  Arithmetic is float32;
+ * a 16-bit parameter is rounded once.  Moments of 8 bits are, up to the code,
+ * fma(beta1, m, (1 - beta1) g') and fma(beta2, v, (1 - beta2) (g' g')) in float64, g'
+ * rounded to float32: sums of short numbers often lie next to a code's border.
  * copies (NULL for none; entries may be NULL) receive p' rounded to bfloat16
  * or float16, the weights that fno_channel_linear reads beside float32
  * parameters; complex parameters have none.
