@@ -331,7 +331,7 @@ __device__ __forceinline__ void chunk8(const AdamTable& t, int i, int64_t at, in
 // A table's moments are all of 32 bits or all of 8.  67 million floats of a model with
 // spectral weights: 32 bits 335 to 340 us, 1.88 GB at 5.5 TB/s, memory (407 with one vector
 // of each field in flight and one kernel for both kinds); 8 bits 230 to 240 us, 1.09
-// GB at 4.6 TB/s beside 100 vector instructions a value, a fifth of them the random bits.  Nine
+// GB at 4.6 TB/s beside 100 vector instructions a value, a fifth of them the random bits.  11
 // small tensors: 4.9 us, a launch.
 template <int BITS>
 __global__ __launch_bounds__(kThreads, BITS == 8 ? 3 : 4) void k_adamw(AdamTable t, uint32_t nchunks, AdamOptions o) {

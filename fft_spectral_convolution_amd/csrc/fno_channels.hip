@@ -1,4 +1,4 @@
-// Channel products: which kernels a call runs, and the gradient of the weight.
+// Channel products: which kernels a call runs, and the joining of the sums of the parameters' gradients.
 #include <algorithm>
 
 #include "fno_channels.hpp"

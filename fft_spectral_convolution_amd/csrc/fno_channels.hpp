@@ -1,5 +1,5 @@
-// Device-side pieces of the channel products (fno_channels.hip,
-// fno_channels_bwd.hip): operands of the matrix instructions, the splitting of
+// Device-side pieces of the channel products (fno_channels_kernel.hpp,
+// fno_channels_bwd.hpp, fno_channels_grad.hip): operands of the matrix instructions, the splitting of
 // float32 into them, and the tiles of fields they are loaded from.
 //
 // All products run on v_mfma_f32_32x32x16_{bf16,f16}.  A lane l holds, of

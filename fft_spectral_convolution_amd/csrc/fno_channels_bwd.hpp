@@ -28,8 +28,8 @@
 namespace fno {
 namespace {
 
-// 64 -> 64 float32 channels first with a branch and GELU, 524288 positions: 178 to 190 us, 671 MB at 3.5 to 3.8
-// TB/s; 64 -> 128 bfloat16 channels last 161 us, 269 MB at 1.7 TB/s; 30 -> 50 float16, 8601 positions, 18
+// 64 -> 64 float32 channels first with a branch and GELU, 524288 positions: 184 to 190 us, 671 MB at 3.5 to 3.6
+// TB/s; 64 -> 128 bfloat16 channels last 159 to 161 us, 269 MB at 1.7 TB/s; 30 -> 50 float16, 8601 positions, 18
 // us, two launches.  One wave a SIMD (the sums, a tile's operands and the next tile's
 // fields take up to 512 registers) leaves latencies in the open: of the first case's 30 000 cycles a tile
 // and SIMD, matrix instructions take 5400, vector instructions about 11 000.  Two waves with the

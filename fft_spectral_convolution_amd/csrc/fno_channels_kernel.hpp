@@ -51,11 +51,14 @@ struct Parts {
 };
 
 // What bounds it: 64 -> 64 float32 channels first with a branch and GELU, 524288 positions,
-// 81 to 89 us, 403 MB at 4.5 to 5.0 TB/s, memory (the float32 matrix instructions alone would take 27 us at
+// 80 to 89 us, 403 MB at 4.5 to 5.0 TB/s, memory (the float32 matrix instructions alone would take 27 us at
 // their peak, the six part products 10); 3 -> 64 from channels last 27 us, 140 MB at 5.1
-// TB/s.  64 -> 256 bfloat16 with GELU 157 to 164 us, 335 MB at 2.1 TB/s: the
-// vector instructions, about 20 a value of the output with the activation, the rounding
-// and the turning; 256 -> 256 with SiLU and a residual, 65536 positions, 45 to 48 us.
+// TB/s.  64 -> 256 bfloat16 channels last with GELU 155 to 164 us, 335 MB at 2.1 TB/s, no one unit: 23
+// vector instructions a value of the output take half of the time, 45% of the waves' time is waiting.  Without the
+// activation (10 instructions) 114 us, with the output channels first as well, so not turned through LDS, 78 of a
+// floor of 66: with two waves a SIMD neither the activation nor the turning hides behind memory.  256 -> 256 with
+// SiLU and a residual, 65536 positions, 43 to 46 us, of which 12 do not grow with the positions: the staging
+// of the weight and the first loads of x behind it (262144 positions: 135 us, floor 79).
 // Two waves a SIMD with 64 or 32 channels of x on the way measured faster than three or four without
 // (64 -> 256: 164 against 208 and 268 us; 64 -> 64: 81 against 98 and 132).
 template <typename T, typename TO, bool LAST, bool OUT_LAST, int MT, int NT>
